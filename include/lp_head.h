@@ -1,0 +1,115 @@
+/*
+ * lp_head.h — C ABI of the operators a served model's head needs around the ragged
+ * log-probability path of lp_ragged.h: the final norm (with the residual's addition and
+ * an 8-bit output), the vocabulary projection with low-rank adapters, and the processing
+ * of logits (repetition, frequency and presence penalties, biases, grammar masks).
+ *
+ *     hidden -> lp_head_norm -> lp_head_project -> lp_head_process -> lp_ragged_step
+ *
+ * Conventions are those of lp_ragged.h: the caller owns every buffer and the stream, the
+ * library allocates nothing, LP_OK means "validated and enqueued", host-checked errors
+ * leave nothing enqueued, and errors found on the device set bits of the workspace's
+ * status word (bit c <=> code c; read it with lp_ragged_read_status) and never trap.
+ * These entry points only ever add bits: lp_head_clear_status (or lp_ragged_plan on the
+ * same workspace) clears the word. Strides are in elements. Row counts, sizes and ids are
+ * uint32; row strides and totals may pass 32 bits.
+ */
+#ifndef LP_HEAD_H
+#define LP_HEAD_H
+
+#include "lp_ragged.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum lp_dtype {
+    LP_F32 = 0,
+    LP_BF16 = 1,
+    LP_F16 = 2,
+    LP_E4M3 = 3 /* 8 bits: 4 exponent, 3 mantissa, largest value 448, no infinity */
+} lp_dtype;
+
+#define LP_MAX_HIDDEN 32768u /* widest row of lp_head_norm */
+#define LP_MAX_RANK 64u      /* largest adapter rank of lp_head_project */
+
+/*
+ * Bytes of scratch the calls below need: a 256-byte header with the status word, and for
+ * lp_head_project with adapters one f32 vector of `rank` values and one id a row.
+ * lp_head_norm and lp_head_process only use the header (T = rank = 0).
+ */
+size_t lp_head_workspace_size(uint32_t T, uint32_t rank);
+
+/* Enqueue the clearing of a workspace's status word. */
+lp_status lp_head_clear_status(void *workspace, lp_stream_t stream);
+
+/*
+ * Final norm. For output row o, with i = rows ? rows[o] : o,
+ *     h = x[i] + residual[i]                      (f32; h = x[i] without a residual)
+ *     y = h / sqrt(mean(h^2) + eps) * weight      (f32)
+ *     out[o] = y rounded to out_dtype, or for LP_E4M3
+ *     out_scale[o] = max(max|y| / 448, 2^-126),  out[o] = e4m3(y / out_scale[o])
+ *     residual_out[o] = h rounded to dtype        (optional)
+ * The norm reads h before its rounding.
+ *   x, residual     device, [T][H] of dtype (LP_F32, LP_BF16, LP_F16); residual may be NULL
+ *   weight          device, [H] of weight_dtype (dtype or LP_F32)
+ *   rows, n         device, uint32[n], the rows to take, or NULL (then n must equal T)
+ *   out             device out, [n][H] of out_dtype (dtype, LP_F32 or LP_E4M3)
+ *   out_scale       device out, float[n], for LP_E4M3 only
+ *   residual_out    device out, [n][H] of dtype, or NULL. Without rows, out and
+ *                   residual_out may be x or residual themselves (same type and stride).
+ *   workspace       the status word; required with rows, else may be NULL
+ * A row holding NaN or an infinity becomes NaN where the formula does (LP_E4M3: the row's
+ * scale is NaN). Device check: rows[o] < T (LP_ERR_OFFSETS; that output row gets NaN).
+ * Host checks: H in 1..LP_MAX_HIDDEN, strides >= H, pointers aligned to their type.
+ */
+lp_status lp_head_norm(const void *x, const void *residual, const void *weight, uint32_t dtype,
+                       uint32_t weight_dtype, uint32_t T, uint32_t H, uint64_t x_stride, uint64_t residual_stride,
+                       const uint32_t *rows, uint32_t n, float eps, void *out, uint32_t out_dtype,
+                       uint64_t out_stride, float *out_scale, void *residual_out, uint64_t residual_out_stride,
+                       void *workspace, size_t workspace_bytes, lp_stream_t stream);
+
+/*
+ * Processing of logits. Logits row t belongs to the request b with
+ * row_offsets[b] <= t < row_offsets[b+1] (row_offsets NULL: request t, B == T). With
+ * `seen` = the token is in the request's history, `count` = how often it is in the
+ * history's output part, every value becomes, in f32 and in this order,
+ *     x = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x
+ *     x = x - frequency[b] * count - (count > 0 ? presence[b] : 0)
+ *     x = x + bias                                  (tokens of the request's bias list)
+ *     x = -inf                                      (tokens whose mask bit is 0)
+ *   logits          device, [T][V] of dtype (LP_F32, LP_BF16, LP_F16)
+ *   out             device out, float[T][V]; may be logits itself for LP_F32 (same stride)
+ *   history         device, uint32[history_total]; request b's part is
+ *   history_offsets device, uint32[B+1]; its first prompt_lens[b] tokens are the prompt
+ *   prompt_lens     device, uint32[B], or NULL (no prompt)
+ *   repetition, frequency, presence   device, float[B] each, or NULL (1, 0, 0)
+ *   bias_tokens, bias_values, bias_offsets   device, uint32[bias_total], float[bias_total],
+ *                   uint32[B+1]: request b's biases, token ids strictly ascending; NULL: none
+ *   mask            device, uint32[mask_rows][mask_stride], bit v % 32 of word v / 32 is 1
+ *                   where token v is allowed; NULL: none
+ *   mask_index      device, int32[T]: row t's mask row, negative: row t is not masked;
+ *                   NULL: row t has mask row t (mask_rows >= T)
+ *   workspace       the status word
+ * A row whose mask allows nothing is all -inf. A masked value is -inf whatever it was.
+ * The history of a request with repetition 1 and frequency = presence = 0 is not read.
+ * Device checks, each giving the request's rows NaN: row, history and bias offsets within
+ * their totals, nondecreasing, every row in a request, mask_index < mask_rows
+ * (LP_ERR_OFFSETS); repetition positive and finite, frequency and presence finite
+ * (LP_ERR_PENALTY). A history or bias token >= V is skipped (LP_ERR_TOKEN_RANGE), bias
+ * ids not strictly ascending set LP_ERR_OFFSETS (that request's biases are unspecified).
+ */
+lp_status lp_head_process(const void *logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
+                          const uint32_t *row_offsets, uint32_t B, const uint32_t *history,
+                          const uint32_t *history_offsets, uint32_t history_total, const uint32_t *prompt_lens,
+                          const float *repetition, const float *frequency, const float *presence,
+                          const uint32_t *bias_tokens, const float *bias_values, const uint32_t *bias_offsets,
+                          uint32_t bias_total, const uint32_t *mask, uint64_t mask_stride, uint32_t mask_rows,
+                          const int32_t *mask_index, float *out, uint64_t out_stride, void *workspace,
+                          size_t workspace_bytes, lp_stream_t stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LP_HEAD_H */

@@ -18,12 +18,16 @@ from typing import Optional
 import torch
 
 from . import _build
+from . import head as _head
+from .head import (clear_status, head_workspace_size, new_head_workspace, process_logits,  # noqa: F401
+                   rms_norm)
 from .results import LogProbabilities, assemble  # noqa: F401  (host-side result assembly)
 
 __all__ = [
     "LpError", "lib_path", "load", "workspace_size", "new_workspace", "plan", "compute", "row_kernel",
     "compute_ex", "step", "read_status", "ragged_log_probs", "tuple_bytes", "shard_partials", "shard_merge",
     "gather_shard_tuples", "ragged_log_probs_vocab_parallel", "out_per_token", "STATUS_NAMES", "LogProbabilities", "assemble",
+    *_head.__all__,
 ]
 
 LP_MAX_LEVELS = 6
@@ -31,6 +35,7 @@ PAD_TOKEN = 0xFFFFFFFF
 STATUS_NAMES = {
     0: "LP_OK", 1: "LP_ERR_NULL", 2: "LP_ERR_LEVELS", 3: "LP_ERR_SHAPE", 4: "LP_ERR_OFFSETS",
     5: "LP_ERR_TOKEN_RANGE", 6: "LP_ERR_WORKSPACE", 7: "LP_ERR_CUDA", 8: "LP_ERR_TEMPERATURE",
+    9: "LP_ERR_DTYPE", 10: "LP_ERR_ADAPTER", 11: "LP_ERR_PENALTY", 12: "LP_ERR_TIMEOUT",
 }
 EXPORTS = ("lp_ragged_workspace_size", "lp_ragged_plan", "lp_ragged_compute", "lp_ragged_compute_ex",
            "lp_ragged_step", "lp_ragged_tuple_bytes", "lp_ragged_shard_partials", "lp_ragged_shard_merge",
@@ -84,6 +89,7 @@ def load() -> ctypes.CDLL:
     lib.lp_ragged_row_kernel.restype = ctypes.c_int
     lib.lp_ragged_strerror.argtypes = [ctypes.c_int]
     lib.lp_ragged_strerror.restype = ctypes.c_char_p
+    _head._declare(lib)
     _LIB = lib
     return lib
 

@@ -6,6 +6,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -13,8 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "liblp_ragged.so"
-SOURCES = ["lp_ragged.cu"]
-HEADERS = ["lp_device.cuh", "lp_kernels.cuh"]
+SOURCES = ["lp_ragged.cu", "lp_norm.cu", "lp_process.cu"]
+HEADERS = ["lp_device.cuh", "lp_kernels.cuh", "lp_head_common.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -31,7 +33,7 @@ def _nvcc() -> str:
 
 def _inputs():
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    files.append(os.path.join(INCLUDE, "lp_ragged.h"))
+    files += [os.path.join(INCLUDE, f) for f in ("lp_ragged.h", "lp_head.h")]
     files.append(os.path.abspath(__file__))
     return files
 
@@ -53,19 +55,27 @@ def build(force: bool = False, verbose: bool = False, ptxas_verbose: bool = Fals
         return out
     os.makedirs(os.path.dirname(os.path.abspath(out)), exist_ok=True)
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-O2",
-           "-I", INCLUDE, "-I", CSRC, "-o", tmp]
+    flags = [*ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC]
     if ptxas_verbose:
-        cmd += ["-Xptxas", "-v"]
-    cmd += [f"-D{d}" for d in defines]
-    cmd += [os.path.join(CSRC, f) for f in SOURCES]
-    if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+        flags += ["-Xptxas", "-v"]
+    flags += [f"-D{d}" for d in defines]
+    report = ""
+    with tempfile.TemporaryDirectory(prefix="lp_build_") as work:
+        objects = [os.path.join(work, f + ".o") for f in SOURCES]
+        commands = [[_nvcc(), *flags, "-c", os.path.join(CSRC, f), "-o", o] for f, o in zip(SOURCES, objects)]
+        commands.append([_nvcc(), *ARCH, "-shared", "-o", tmp, *objects])
+        # one compiler per source, all at once; then the link
+        for group in (commands[:-1], commands[-1:]):
+            if verbose:
+                print("\n".join(" ".join(c) for c in group), file=sys.stderr)
+            with ThreadPoolExecutor(len(group)) as pool:
+                results = list(pool.map(lambda c: subprocess.run(c, capture_output=True, text=True), group))
+            for res in results:
+                if res.returncode != 0:
+                    raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
+                report += res.stdout + res.stderr
     if verbose or ptxas_verbose:
-        sys.stderr.write(res.stdout + res.stderr)
+        sys.stderr.write(report)
     os.replace(tmp, out)
     return out
 

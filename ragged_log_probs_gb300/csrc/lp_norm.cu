@@ -1,0 +1,304 @@
+// Final norm of a model's head: residual addition, root-mean-square norm, and an output
+// in the input's type, f32, or e4m3 with one f32 scale a row (include/lp_head.h).
+//
+// One pass over the data. A row stays in registers between its two uses: h = x + residual
+// is formed in f32 while it is loaded, the row's sum of h^2 and largest |h w| are reduced
+// together (|y| is largest where |h w| is: the factor 1/rms is common to the row), and the
+// output is written from the registers. Bound by HBM: every element is read once and
+// written once. The largest LP_MAX_HIDDEN row is 1024 threads x 4 vectors of 8.
+#include "lp_head_common.h"
+
+namespace {
+
+using namespace lph;
+
+constexpr int kVec = 8;         // elements a thread handles together
+constexpr int kMaxVecs = 4;     // vectors a thread holds
+constexpr int kWarpRowVecs = 128;  // rows of up to this many vectors (1024 elements): a warp each
+constexpr int kWarpRows = 4;    // rows (warps) per CTA then
+
+struct NormParams {
+    const void* x;
+    const void* residual;
+    const void* weight;
+    const uint32_t* rows;
+    void* out;
+    float* out_scale;
+    void* residual_out;
+    uint32_t* status;
+    uint64_t x_stride, residual_stride, out_stride, residual_out_stride;
+    uint32_t T, n, H;
+    uint32_t weight_f32;  // weight is f32 whatever the rows' type
+    float eps;
+};
+
+// Eight elements from p (16-byte aligned), or the first `count` one by one, zero past them.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, int count, float (&v)[kVec]) {
+    if constexpr (VEC) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4*>(p);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(w[i], T());
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = i < count ? to_f32(p[i]) : 0.f;
+    }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8(T* p, int count, const float (&v)[kVec]) {
+    if constexpr (VEC) {
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()),
+                                                      pack2(v[4], v[5], T()), pack2(v[6], v[7], T()));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < count) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8_e4m3(uint8_t* p, int count, const float (&v)[kVec]) {
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)  // round to nearest even, saturating; NaN stays NaN
+        h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+    if constexpr (VEC) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
+    } else {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+            if (i < count) p[i] = (uint8_t)(h[i / 2] >> (8 * (i & 1)));
+    }
+}
+
+// One row by `threads` threads (a warp, or the CTA when WARP is false), this thread `tid`.
+template <typename T, typename O, bool VEC, bool WARP, int NV>
+__device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int tid, int threads, float (*red)[2]) {
+    constexpr bool kQuant = sizeof(O) == 1;
+    uint32_t i = o;
+    bool bad = false;
+    if (p.rows) {
+        i = p.rows[o];
+        bad = i >= p.T;
+        if (bad) {
+            i = 0;
+            if (tid == 0) flag(p.status, LP_ERR_OFFSETS);
+        }
+    }
+    const T* x = static_cast<const T*>(p.x) + (uint64_t)i * p.x_stride;
+    const T* r = p.residual ? static_cast<const T*>(p.residual) + (uint64_t)i * p.residual_stride : nullptr;
+    const int H = (int)p.H;
+    const auto load_weight = [&](int e, float (&g)[kVec]) {
+        if (sizeof(T) < 4 && !p.weight_f32) load8<T, VEC>(static_cast<const T*>(p.weight) + e, H - e, g);
+        else load8<float, VEC>(static_cast<const float*>(p.weight) + e, H - e, g);
+    };
+    float h[NV][kVec];
+    float sum = 0.f, top = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int e = (tid + k * threads) * kVec;
+        if (e < H) load8<T, VEC>(x + e, H - e, h[k]);
+    }
+    if (r) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int e = (tid + k * threads) * kVec;
+            float v[kVec];
+            if (e < H) {
+                load8<T, VEC>(r + e, H - e, v);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) h[k][j] += v[j];
+            }
+        }
+    }
+    if (bad) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) h[k][j] = __int_as_float(0x7fffffff);
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int e = (tid + k * threads) * kVec;
+        if (e < H) {
+#pragma unroll
+            for (int j = 0; j < kVec; ++j)
+                if (VEC || e + j < H) sum = fmaf(h[k][j], h[k][j], sum);
+            if constexpr (kQuant) {
+                float g[kVec];
+                load_weight(e, g);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (VEC || e + j < H) top = max_nan(top, fabsf(h[k][j] * g[j]));
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if constexpr (kQuant) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+    }
+    if constexpr (!WARP) {
+        const int warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
+        if (lane == 0) {
+            red[warp][0] = sum;
+            red[warp][1] = top;
+        }
+        __syncthreads();
+        sum = lane < warps ? red[lane][0] : 0.f;
+        top = lane < warps ? red[lane][1] : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            if constexpr (kQuant) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+        }
+    }
+    const float inv = rsqrtf(sum / (float)p.H + p.eps);
+    float per_scale = 1.f;  // applied after inv: their product may overflow (a row of zeros)
+    if constexpr (kQuant) {
+        const float scale = max_nan(inv * top / 448.f, 1.17549435e-38f);
+        per_scale = 1.f / scale;
+        if (tid == 0) p.out_scale[o] = scale;
+    }
+    O* out = static_cast<O*>(p.out) + (uint64_t)o * p.out_stride;
+    T* kept = p.residual_out ? static_cast<T*>(p.residual_out) + (uint64_t)o * p.residual_out_stride : nullptr;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int e = (tid + k * threads) * kVec;
+        if (e >= H) continue;
+        if (kept) store8<T, VEC>(kept + e, H - e, h[k]);
+        float g[kVec], y[kVec];
+        load_weight(e, g);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) y[j] = h[k][j] * inv * g[j] * per_scale;
+        if constexpr (kQuant)
+            store8_e4m3<VEC>(reinterpret_cast<uint8_t*>(out) + e, H - e, y);
+        else
+            store8<O, VEC>(out + e, H - e, y);
+    }
+}
+
+template <typename T, typename O, bool VEC, bool WARP, int NV>
+__global__ void __launch_bounds__(WARP ? kWarpRows * 32 : (NV == 4 ? 1024 : 512)) k_norm(NormParams p) {
+    __shared__ float red[32][2];
+    pdl_trigger();
+    pdl_wait();
+    if constexpr (WARP) {
+        const uint32_t o = blockIdx.x * kWarpRows + (threadIdx.x >> 5);
+        if (o < p.n) norm_row<T, O, VEC, true, NV>(p, o, threadIdx.x & 31, 32, nullptr);
+    } else {
+        norm_row<T, O, VEC, false, NV>(p, blockIdx.x, threadIdx.x, blockDim.x, red);
+    }
+}
+
+template <typename T, typename O, bool VEC>
+lp_status launch_norm(const NormParams& p, lp_stream_t s) {
+    const uint32_t vecs = (p.H + kVec - 1) / kVec;
+    if (vecs <= kWarpRowVecs) {
+        const dim3 grid((p.n + kWarpRows - 1) / kWarpRows);
+        if (vecs <= 32) return launch(k_norm<T, O, VEC, true, 1>, grid, kWarpRows * 32, 0, s, 1, p);
+        return launch(k_norm<T, O, VEC, true, 4>, grid, kWarpRows * 32, 0, s, 1, p);
+    }
+    const auto warps_for = [&](uint32_t nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
+    if (vecs <= 512) return launch(k_norm<T, O, VEC, false, 1>, dim3(p.n), warps_for(1), 0, s, 1, p);
+    if (vecs <= 1024) return launch(k_norm<T, O, VEC, false, 2>, dim3(p.n), warps_for(2), 0, s, 1, p);
+    return launch(k_norm<T, O, VEC, false, 4>, dim3(p.n), warps_for(4), 0, s, 1, p);
+}
+
+template <typename T>
+lp_status launch_norm(const NormParams& p, uint32_t out_dtype, uint32_t dtype, bool vec, lp_stream_t s) {
+    if (out_dtype == LP_E4M3)
+        return vec ? launch_norm<T, uint8_t, true>(p, s) : launch_norm<T, uint8_t, false>(p, s);
+    if (out_dtype == dtype) return vec ? launch_norm<T, T, true>(p, s) : launch_norm<T, T, false>(p, s);
+    return vec ? launch_norm<T, float, true>(p, s) : launch_norm<T, float, false>(p, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lp_head_workspace_size(uint32_t T, uint32_t rank) {
+    if (rank > LP_MAX_RANK) return 0;
+    const size_t ids = rank ? ((size_t)T * 4 + 255) & ~(size_t)255 : 0;
+    return lph::kHeaderBytes + ids + (size_t)T * rank * 4;
+}
+
+lp_status lp_head_clear_status(void* workspace, lp_stream_t stream) {
+    if (!workspace) return LP_ERR_WORKSPACE;
+    if (cudaMemsetAsync(workspace, 0, 4, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return LP_ERR_CUDA;
+    }
+    return LP_OK;
+}
+
+lp_status lp_head_norm(const void* x, const void* residual, const void* weight, uint32_t dtype,
+                       uint32_t weight_dtype, uint32_t T, uint32_t H, uint64_t x_stride, uint64_t residual_stride,
+                       const uint32_t* rows, uint32_t n, float eps, void* out, uint32_t out_dtype,
+                       uint64_t out_stride, float* out_scale, void* residual_out, uint64_t residual_out_stride,
+                       void* workspace, size_t workspace_bytes, lp_stream_t stream) {
+    if (!x || !weight || !out) return LP_ERR_NULL;
+    if (dtype > LP_F16 || (weight_dtype != dtype && weight_dtype != LP_F32)) return LP_ERR_DTYPE;
+    if (out_dtype != dtype && out_dtype != LP_F32 && out_dtype != LP_E4M3) return LP_ERR_DTYPE;
+    if (out_dtype == LP_E4M3 && !out_scale) return LP_ERR_NULL;
+    if (T == 0 || n == 0 || n > 0x7FFFFFFFu || H == 0 || H > LP_MAX_HIDDEN || (!rows && n != T)) return LP_ERR_SHAPE;
+    if (x_stride < H || out_stride < H || (residual && residual_stride < H) ||
+        (residual_out && residual_out_stride < H))
+        return LP_ERR_SHAPE;
+    const size_t e = dtype_bytes(dtype), eo = dtype_bytes(out_dtype), ew = dtype_bytes(weight_dtype);
+    if (!aligned_to(x, e) || !aligned_to(residual, e) || !aligned_to(residual_out, e) || !aligned_to(weight, ew) ||
+        !aligned_to(out, eo) || !aligned_to(out_scale, 4) || !aligned_to(rows, 4))
+        return LP_ERR_SHAPE;
+    if (!(eps >= 0.f) || eps > 3.0e38f) return LP_ERR_SHAPE;
+    if (rows && (!workspace || workspace_bytes < lph::kHeaderBytes)) return LP_ERR_WORKSPACE;
+    if (workspace && !aligned_to(workspace, 256)) return LP_ERR_WORKSPACE;
+    NormParams p;
+    p.x = x;
+    p.residual = residual;
+    p.weight = weight;
+    p.rows = rows;
+    p.out = out;
+    p.out_scale = out_scale;
+    p.residual_out = residual_out;
+    p.status = static_cast<uint32_t*>(workspace);
+    p.x_stride = x_stride;
+    p.residual_stride = residual_stride;
+    p.out_stride = out_stride;
+    p.residual_out_stride = residual_out_stride;
+    p.T = T;
+    p.n = n;
+    p.H = H;
+    p.eps = eps;
+    // 16-byte accesses (8 bytes for an e4m3 output) where every row starts on such a boundary
+    // and ends on a whole vector; one element at a time otherwise.
+    const auto vec_rows = [](const void* ptr, uint64_t stride, size_t size) {
+        const size_t bytes = size == 1 ? 8 : 16;
+        return !ptr || (lph::aligned_to(ptr, bytes) && stride * size % bytes == 0);
+    };
+    const bool vec = H % kVec == 0 && vec_rows(x, x_stride, e) && vec_rows(residual, residual_stride, e) &&
+                     vec_rows(out, out_stride, eo) && vec_rows(residual_out, residual_out_stride, e) &&
+                     aligned_to(weight, 16);
+    p.weight_f32 = weight_dtype == LP_F32;
+    if (dtype == LP_F32) return launch_norm<float>(p, out_dtype, dtype, vec, stream);
+    if (dtype == LP_BF16) return launch_norm<__nv_bfloat16>(p, out_dtype, dtype, vec, stream);
+    return launch_norm<__half>(p, out_dtype, dtype, vec, stream);
+}
+
+}  // extern "C"

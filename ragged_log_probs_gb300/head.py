@@ -1,0 +1,216 @@
+"""The operators of a served model's head around the ragged log-probability path: final
+norm, vocabulary projection with low-rank adapters, processing of logits.
+
+Argument marshalling only, like the package's other calls: every operator runs in the
+CUDA kernels of ``liblp_ragged.so`` behind the C ABI of ``include/lp_head.h``, whose
+comments define the operators. Matrices may have any row stride, with their last
+dimension contiguous.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+__all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "process_logits"]
+
+LP_MAX_HIDDEN = 32768
+LP_MAX_RANK = 64
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3}
+_INTS = (torch.int32, torch.uint32)
+
+
+def _declare(lib: ctypes.CDLL) -> None:
+    u32, u64, vp, sz, f32 = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
+    lib.lp_head_workspace_size.argtypes = [u32, u32]
+    lib.lp_head_workspace_size.restype = sz
+    lib.lp_head_clear_status.argtypes = [vp, vp]
+    lib.lp_head_clear_status.restype = ctypes.c_int
+    lib.lp_head_norm.argtypes = [vp, vp, vp, u32, u32, u32, u32, u64, u64, vp, u32, f32, vp, u32, u64, vp, vp, u64,
+                                 vp, sz, vp]
+    lib.lp_head_norm.restype = ctypes.c_int
+    lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
+                                    vp, u64, u32, vp, vp, u64, vp, sz, vp]
+    lib.lp_head_process.restype = ctypes.c_int
+
+
+def _pkg():
+    import ragged_log_probs_gb300 as lp
+    return lp
+
+
+def _check_device(t: torch.Tensor, name: str, device: int) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
+
+
+def _matrix(t: torch.Tensor, name: str, device: int, rows: Optional[int] = None, cols: Optional[int] = None,
+            dtype: Optional[torch.dtype] = None):
+    """Pointer and row stride of a 2-D tensor whose last dimension is contiguous."""
+    _check_device(t, name, device)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, has {t.dim()} dimensions")
+    r, c = t.shape
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{name} must be [{rows if rows is not None else r}, {cols if cols is not None else c}], "
+                         f"is [{r}, {c}]")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
+    s0, s1 = t.stride()
+    if s1 != 1 and c > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t.data_ptr(), c if r <= 1 else s0
+
+
+def _vector(t: Optional[torch.Tensor], name: str, device: int, n: Optional[int], dtypes) -> Optional[int]:
+    """Pointer of a contiguous 1-D tensor (None stays None)."""
+    if t is None:
+        return None
+    _check_device(t, name, device)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, is {t.dtype}")
+    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise ValueError(f"{name} must be contiguous 1-D" + ("" if n is None else f" with {n} elements"))
+    return t.data_ptr()
+
+
+def _scratch(workspace: Optional[torch.Tensor], device: int):
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor (see new_head_workspace)")
+    _check_device(workspace, "workspace", device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _new(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output, allocated on the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def head_workspace_size(T: int = 0, rank: int = 0) -> int:
+    """Bytes of scratch for a call: of ``project`` with adapters of that rank over T rows,
+    or (T = rank = 0) of the others, which only use the status word."""
+    n = int(_pkg().load().lp_head_workspace_size(T, rank))
+    if n == 0:
+        raise ValueError(f"rank {rank} exceeds {LP_MAX_RANK}")
+    return n
+
+
+def new_head_workspace(T: int = 0, rank: int = 0, device=None) -> torch.Tensor:
+    """A zeroed workspace (uint8). Its status word collects the bits of every call that is
+    given it, until ``clear_status``; ``read_status`` reads it."""
+    return torch.zeros(head_workspace_size(T, rank), dtype=torch.uint8,
+                       device=torch.device("cuda") if device is None else device)
+
+
+def clear_status(workspace: torch.Tensor, stream=None) -> None:
+    """Enqueue the clearing of a workspace's status word."""
+    lp = _pkg()
+    ptr, _ = _scratch(workspace, torch.cuda.current_device())
+    rc = lp.load().lp_head_clear_status(ptr, _stream(stream))
+    if rc:
+        raise lp.LpError(rc, "lp_head_clear_status")
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
+             rows: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+             out: Optional[torch.Tensor] = None, out_scale: Optional[torch.Tensor] = None,
+             residual_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Final norm: ``(x + residual) / rms * weight`` of all rows of ``x`` [T, H], or of those
+    that ``rows`` [n] names (the scored positions only).
+
+    ``out`` (or a new tensor of ``out_dtype``, default x's) is of x's type, float32, or
+    float8_e4m3fn with one float32 scale a row in ``out_scale``. ``residual_out`` receives
+    ``x + residual``. Returns ``out``, or ``(out, out_scale)`` for float8_e4m3fn. With
+    ``rows`` a workspace is needed: a row index past T sets LP_ERR_OFFSETS in its status."""
+    lp = _pkg()
+    dev = torch.cuda.current_device()
+    xp, xs = _matrix(x, "x", dev)
+    T, H = x.shape
+    dt = x.dtype
+    n = T if rows is None else rows.numel()
+    rp, rs = (None, 0) if residual is None else _matrix(residual, "residual", dev, T, H, dt)
+    wp = _vector(weight, "weight", dev, H, (dt, torch.float32))
+    if out is None:
+        out = _new((n, H), dt if out_dtype is None else out_dtype, x, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, is {out.dtype}")
+    op, os_ = _matrix(out, "out", dev, n, H)
+    quant = out.dtype == torch.float8_e4m3fn
+    if quant and out_scale is None:
+        out_scale = _new((n,), torch.float32, x, stream)
+    kp, ks = (None, 0) if residual_out is None else _matrix(residual_out, "residual_out", dev, n, H, dt)
+    sp, sn = _scratch(workspace, dev)
+    rc = lp.load().lp_head_norm(
+        xp, rp, wp, _DTYPES.get(dt, 99), _DTYPES[weight.dtype], T, H, xs, rs,
+        _vector(rows, "rows", dev, n, _INTS), n, eps, op, _DTYPES.get(out.dtype, 99), os_,
+        _vector(out_scale, "out_scale", dev, n, (torch.float32,)), kp, ks, sp, sn, _stream(stream))
+    if rc:
+        raise lp.LpError(rc, "lp_head_norm")
+    return (out, out_scale) if quant else out
+
+
+def process_logits(logits: torch.Tensor, row_offsets: Optional[torch.Tensor] = None,
+                   history: Optional[torch.Tensor] = None, history_offsets: Optional[torch.Tensor] = None,
+                   prompt_lens: Optional[torch.Tensor] = None, repetition: Optional[torch.Tensor] = None,
+                   frequency: Optional[torch.Tensor] = None, presence: Optional[torch.Tensor] = None,
+                   bias_tokens: Optional[torch.Tensor] = None, bias_values: Optional[torch.Tensor] = None,
+                   bias_offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None,
+                   mask_index: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, *,
+                   workspace: torch.Tensor, stream=None) -> torch.Tensor:
+    """Penalties for repeated tokens, biases and grammar masks on ``logits`` [T, V]; returns
+    ``out`` (float32, new by default; float32 logits may be processed in place).
+
+    ``row_offsets`` [B+1] gives each request's rows (default: one row a request). Request
+    b's ``history`` is ``history[history_offsets[b]:history_offsets[b+1]]``, its first
+    ``prompt_lens[b]`` tokens the prompt. ``bias_*`` are ragged lists too, ids strictly
+    ascending in each. ``mask`` [rows, words] int32 has a bit for each token, 1 = allowed;
+    ``mask_index`` [T] names each row's mask, negative for none. Errors found on the device
+    set bits of the workspace's status (``read_status``)."""
+    lp = _pkg()
+    dev = torch.cuda.current_device()
+    xp, xs = _matrix(logits, "logits", dev)
+    T, V = logits.shape
+    B = T if row_offsets is None else row_offsets.numel() - 1
+    f32 = (torch.float32,)
+    if (history is None) != (history_offsets is None):
+        raise ValueError("history and history_offsets come together")
+    if not ((bias_tokens is None) == (bias_values is None) == (bias_offsets is None)):
+        raise ValueError("bias_tokens, bias_values and bias_offsets come together")
+    if mask_index is not None and mask is None:
+        raise ValueError("mask_index needs a mask")
+    nb = 0 if bias_tokens is None else bias_tokens.numel()
+    mp, ms, mr = None, 0, 0
+    if mask is not None:
+        mp, ms = _matrix(mask, "mask", dev)
+        mr = mask.shape[0]
+        if mask.dtype not in _INTS or mask.shape[1] < (V + 31) // 32:
+            raise ValueError(f"mask must be int32 [rows, {(V + 31) // 32} or more]")
+    if out is None:
+        out = _new((T, V), torch.float32, logits, stream)
+    op, os_ = _matrix(out, "out", dev, T, V, torch.float32)
+    sp, sn = _scratch(workspace, dev)
+    rc = lp.load().lp_head_process(
+        xp, _DTYPES.get(logits.dtype, 99), T, V, xs, _vector(row_offsets, "row_offsets", dev, B + 1, _INTS), B,
+        _vector(history, "history", dev, None, _INTS),
+        _vector(history_offsets, "history_offsets", dev, B + 1, _INTS), 0 if history is None else history.numel(),
+        _vector(prompt_lens, "prompt_lens", dev, B, _INTS), _vector(repetition, "repetition", dev, B, f32),
+        _vector(frequency, "frequency", dev, B, f32), _vector(presence, "presence", dev, B, f32),
+        _vector(bias_tokens, "bias_tokens", dev, nb, _INTS), _vector(bias_values, "bias_values", dev, nb, f32),
+        _vector(bias_offsets, "bias_offsets", dev, B + 1, _INTS), nb, mp, ms, mr,
+        _vector(mask_index, "mask_index", dev, T, _INTS), op, os_, sp, sn, _stream(stream))
+    if rc:
+        raise lp.LpError(rc, "lp_head_process")
+    return out
