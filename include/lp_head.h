@@ -70,6 +70,37 @@ lp_status lp_head_norm(const void *x, const void *residual, const void *weight, 
                        void *workspace, size_t workspace_bytes, lp_stream_t stream);
 
 /*
+ * Projection of hidden states to logits, with low-rank adapters of many requests at once:
+ *     out[t, v] = sx[t] sw[v] sum_h x[t, h] W[v, h]  +  sum_j u[t, j] B_a[v, j]
+ *     u[t, j]   = s_a sx[t] sum_h x[t, h] A_a[j, h]
+ * with a = adapter_ids[b] for the request b of row t (rows as in lp_head_process); a
+ * negative id means no adapter. Products are exact, sums are f32, u stays f32; the result
+ * is rounded once to out_dtype.
+ *   x               device, [T][H] of dtype (LP_BF16, LP_F16, LP_E4M3)
+ *   x_scale         device, float[T], sx, for LP_E4M3 only (else NULL, and sx = 1)
+ *   weight          device, [V][H] of dtype; weight_scale: device, float[V], as x_scale
+ *   lora_a, lora_b  device, [adapters][rank][H] and [adapters][V][rank], contiguous, of
+ *                   lora_dtype: dtype, or LP_BF16 / LP_F16 where dtype is LP_E4M3
+ *   adapters        0: no adapters (the lora arguments, ids and offsets are not read)
+ *   adapter_scale   device, float[adapters], s_a, or NULL (1)
+ *   adapter_ids     device, int32[B]
+ *   row_offsets, B  device, uint32[B+1], or NULL (request t has row t, B == T)
+ *   out             device out, [T][V] of out_dtype (LP_F32, LP_BF16, LP_F16)
+ *   workspace       lp_head_workspace_size(T, rank) bytes (T = rank = 0 without adapters)
+ * Requests may hold adapters in any order; rows of one adapter that stand together share
+ * its B. Host checks: 1 <= rank <= LP_MAX_RANK; x, weight, lora_a, lora_b 16-byte aligned;
+ * H and the strides of x and weight whole multiples of 16 bytes. Device checks: every row
+ * in a request (LP_ERR_OFFSETS), ids below `adapters` (LP_ERR_ADAPTER); such a row's
+ * logits are NaN. LP_ERR_TIMEOUT: a wait inside the kernel ran out (out is not complete).
+ */
+lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H, uint64_t x_stride,
+                          const float *x_scale, const void *weight, uint32_t V, uint64_t weight_stride,
+                          const float *weight_scale, const void *lora_a, const void *lora_b, uint32_t lora_dtype,
+                          uint32_t adapters, uint32_t rank, const float *adapter_scale, const int32_t *adapter_ids,
+                          const uint32_t *row_offsets, uint32_t B, void *out, uint32_t out_dtype, uint64_t out_stride,
+                          void *workspace, size_t workspace_bytes, lp_stream_t stream);
+
+/*
  * Processing of logits. Logits row t belongs to the request b with
  * row_offsets[b] <= t < row_offsets[b+1] (row_offsets NULL: request t, B == T). With
  * `seen` = the token is in the request's history, `count` = how often it is in the

@@ -14,7 +14,7 @@ from typing import Optional
 
 import torch
 
-__all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "process_logits"]
+__all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "project", "process_logits"]
 
 LP_MAX_HIDDEN = 32768
 LP_MAX_RANK = 64
@@ -31,6 +31,9 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.lp_head_norm.argtypes = [vp, vp, vp, u32, u32, u32, u32, u64, u64, vp, u32, f32, vp, u32, u64, vp, vp, u64,
                                  vp, sz, vp]
     lib.lp_head_norm.restype = ctypes.c_int
+    lib.lp_head_project.argtypes = [vp, u32, u32, u32, u64, vp, vp, u32, u64, vp, vp, vp, u32, u32, u32, vp, vp, vp,
+                                    u32, vp, u32, u64, vp, sz, vp]
+    lib.lp_head_project.restype = ctypes.c_int
     lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
                                     vp, u64, u32, vp, vp, u64, vp, sz, vp]
     lib.lp_head_process.restype = ctypes.c_int
@@ -160,6 +163,62 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     if rc:
         raise lp.LpError(rc, "lp_head_norm")
     return (out, out_scale) if quant else out
+
+
+def project(x: torch.Tensor, weight: torch.Tensor, x_scale: Optional[torch.Tensor] = None,
+            weight_scale: Optional[torch.Tensor] = None, lora_a: Optional[torch.Tensor] = None,
+            lora_b: Optional[torch.Tensor] = None, adapter_scale: Optional[torch.Tensor] = None,
+            adapter_ids: Optional[torch.Tensor] = None, row_offsets: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, *, workspace: torch.Tensor,
+            stream=None) -> torch.Tensor:
+    """Logits ``x @ weight.T`` [T, V] of hidden states ``x`` [T, H], plus each request's
+    low-rank adapter ``adapter_scale[a] * (x @ lora_a[a].T) @ lora_b[a].T``.
+
+    ``x`` and ``weight`` [V, H] are bfloat16, float16, or float8_e4m3fn with ``x_scale`` [T]
+    and ``weight_scale`` [V]. ``lora_a`` [A, rank, H], ``lora_b`` [A, V, rank];
+    ``adapter_ids`` [B] int32 names each request's adapter (negative: none), ``row_offsets``
+    [B+1] its rows (default: one row a request). Returns ``out`` (new by default, of
+    ``out_dtype``, float32 by default). ``workspace``: see ``new_head_workspace(T, rank)``."""
+    lp = _pkg()
+    dev = torch.cuda.current_device()
+    xp, xs = _matrix(x, "x", dev)
+    T, H = x.shape
+    dt = x.dtype
+    wp, ws = _matrix(weight, "weight", dev, None, H, dt)
+    V = weight.shape[0]
+    f32 = (torch.float32,)
+    ap = bp = ip = rp = sp = None
+    A = rank = B = 0
+    at = dt
+    if lora_a is not None:
+        if lora_b is None or adapter_ids is None:
+            raise ValueError("lora_a needs lora_b and adapter_ids")
+        A, rank = lora_a.shape[:2]
+        B = T if row_offsets is None else row_offsets.numel() - 1
+        at = lora_a.dtype
+        for t, name, shape in ((lora_a, "lora_a", (A, rank, H)), (lora_b, "lora_b", (A, V, rank))):
+            _check_device(t, name, dev)
+            if t.shape != shape or not t.is_contiguous() or t.dtype != at:
+                raise ValueError(f"{name} must be contiguous {shape} of {at}, is {tuple(t.shape)} of {t.dtype}")
+        ap, bp = lora_a.data_ptr(), lora_b.data_ptr()
+        ip = _vector(adapter_ids, "adapter_ids", dev, B, (torch.int32,))
+        rp = _vector(row_offsets, "row_offsets", dev, B + 1, _INTS)
+        sp = _vector(adapter_scale, "adapter_scale", dev, A, f32)
+    elif lora_b is not None or adapter_ids is not None or adapter_scale is not None:
+        raise ValueError("lora_b, adapter_ids and adapter_scale need lora_a")
+    if out is None:
+        out = _new((T, V), torch.float32 if out_dtype is None else out_dtype, x, stream)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, is {out.dtype}")
+    op, os_ = _matrix(out, "out", dev, T, V)
+    kp, kn = _scratch(workspace, dev)
+    rc = lp.load().lp_head_project(
+        xp, _DTYPES.get(dt, 99), T, H, xs, _vector(x_scale, "x_scale", dev, T, f32), wp, V, ws,
+        _vector(weight_scale, "weight_scale", dev, V, f32), ap, bp, _DTYPES.get(at, 99), A, rank, sp, ip, rp, B, op,
+        _DTYPES.get(out.dtype, 99), os_, kp, kn, _stream(stream))
+    if rc:
+        raise lp.LpError(rc, "lp_head_project")
+    return out
 
 
 def process_logits(logits: torch.Tensor, row_offsets: Optional[torch.Tensor] = None,

@@ -24,7 +24,7 @@ def lib():
 def test_every_declared_symbol_is_exported_and_bound(lib):
     text = open(os.path.join(ROOT, "include", "lp_head.h")).read()
     names = set(re.findall(r"^\s*(?:lp_status|size_t)\s+(lp_\w+)\s*\(", text, flags=re.M))
-    assert names >= {"lp_head_workspace_size", "lp_head_clear_status", "lp_head_norm", "lp_head_process"}
+    assert names >= {"lp_head_workspace_size", "lp_head_clear_status", "lp_head_norm", "lp_head_project", "lp_head_process"}
     for name in names:
         assert getattr(lib, name).argtypes, name
 
@@ -85,6 +85,34 @@ def test_process_refusals(lib):
     assert _process(lib, x=FAKE + 2) == SHAPE and _process(lib, out=FAKE + 2) == SHAPE
     assert _process(lib, out=FAKE, dtype=BF16) == SHAPE          # in place only in float32
     assert _process(lib, out=FAKE, os_=104) == SHAPE             # and with one stride
+
+
+def _project(lib, x=FAKE, dtype=BF16, T=4, H=64, xs=64, sx=None, w=FAKE, V=100, wstr=64, sw=None, la=None, lb=None,
+             lt=BF16, A=0, rank=0, scale=None, ids=None, off=None, B=0, out=FAKE, odtype=F32, os_=100, ws=FAKE,
+             wsb=1 << 20):
+    return lib.lp_head_project(x, dtype, T, H, xs, sx, w, V, wstr, sw, la, lb, lt, A, rank, scale, ids, off, B, out,
+                               odtype, os_, ws, wsb, None)
+
+
+def test_project_refusals(lib):
+    assert _project(lib, x=None) == NULL and _project(lib, w=None) == NULL and _project(lib, out=None) == NULL
+    assert _project(lib, dtype=F32) == DTYPE and _project(lib, odtype=E4M3) == DTYPE
+    assert _project(lib, dtype=E4M3) == NULL and _project(lib, dtype=E4M3, sx=FAKE) == NULL     # needs both scales
+    assert _project(lib, sx=FAKE) == DTYPE                       # bf16 has none
+    assert _project(lib, T=0) == SHAPE and _project(lib, H=0) == SHAPE and _project(lib, V=0) == SHAPE
+    assert _project(lib, H=60) == SHAPE                          # 120 bytes
+    assert _project(lib, xs=68) == SHAPE and _project(lib, wstr=68) == SHAPE and _project(lib, xs=56) == SHAPE
+    assert _project(lib, x=FAKE + 8) == SHAPE and _project(lib, w=FAKE + 8) == SHAPE and _project(lib, out=FAKE + 2) == SHAPE
+    assert _project(lib, os_=99) == SHAPE
+    a = dict(la=FAKE, lb=FAKE, A=2, rank=8, ids=FAKE, B=4)
+    for missing in ("la", "lb", "ids"):
+        assert _project(lib, **dict(a, **{missing: None})) == NULL
+    assert _project(lib, **dict(a, rank=0)) == SHAPE and _project(lib, **dict(a, rank=65)) == SHAPE
+    assert _project(lib, **dict(a, B=3)) == SHAPE and _project(lib, **dict(a, B=0)) == SHAPE
+    assert _project(lib, **dict(a, lt=F16)) == DTYPE and _project(lib, **dict(a, lt=E4M3)) == DTYPE
+    assert _project(lib, **dict(a, la=FAKE + 2)) == SHAPE
+    assert _project(lib, ws=None) == WORKSPACE and _project(lib, ws=FAKE + 128) == WORKSPACE
+    assert _project(lib, wsb=255) == WORKSPACE and _project(lib, **dict(a, wsb=256)) == WORKSPACE
 
 
 def test_binding_refuses_host_tensors():
