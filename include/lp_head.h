@@ -35,7 +35,7 @@ typedef enum lp_dtype {
 
 /*
  * Bytes of scratch the calls below need: a 256-byte header with the status word, and for
- * lp_head_project with adapters one f32 vector of `rank` values and one id a row.
+ * lp_head_project with adapters, one f32 vector of `rank` values a row and the rows' order.
  * lp_head_norm and lp_head_process only use the header (T = rank = 0).
  */
 size_t lp_head_workspace_size(uint32_t T, uint32_t rank);

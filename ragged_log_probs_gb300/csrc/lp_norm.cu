@@ -236,8 +236,9 @@ extern "C" {
 
 size_t lp_head_workspace_size(uint32_t T, uint32_t rank) {
     if (rank > LP_MAX_RANK) return 0;
-    const size_t ids = rank ? ((size_t)T * 4 + 255) & ~(size_t)255 : 0;
-    return lph::kHeaderBytes + ids + (size_t)T * rank * 4;
+    if (rank == 0) return lph::kHeaderBytes;
+    // lp_head_project: a page for each 256 rows, and a vector of the padded rank a row
+    return lph::kHeaderBytes + ((size_t)T + 255) / 256 * 4096 + (size_t)T * ((rank + 15) & ~15u) * 4;
 }
 
 lp_status lp_head_clear_status(void* workspace, lp_stream_t stream) {

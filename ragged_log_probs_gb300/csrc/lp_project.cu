@@ -20,35 +20,60 @@ namespace {
 
 using namespace lph;
 
-constexpr uint32_t kTileV = 128;                  // vocabulary rows of a tile (accumulator lanes)
+constexpr uint32_t kTileV = 128;                  // vocabulary rows of a CTA's tile (accumulator lanes)
 constexpr uint32_t kMaxTileT = 256;               // rows of x of a tile
 constexpr uint32_t kSliceBytes = 128;             // bytes of the contracted dimension per stage
 constexpr uint32_t kStageW = kTileV * kSliceBytes;
 constexpr uint32_t kMaxStages = 12;
+constexpr uint32_t kMaxSlots = 8;                 // buffers for tiles of the adapters' B
+constexpr uint32_t kSlotsBytes = 32 * 1024;
 constexpr uint32_t kEpilogueWarps = 8;
 constexpr uint32_t kFirstEpilogueWarp = 4;
 constexpr uint32_t kThreads = (kFirstEpilogueWarp + kEpilogueWarps) * 32;
 constexpr uint32_t kSmemBudget = 227 * 1024;
-constexpr uint32_t kControlBytes = 1024 + 256;    // barriers and words, and the alignment of the ring
+constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the alignment of the ring
+constexpr uint32_t kPromoteSlices = 4;            // slices summed in the tensor core before an f32 addition
+
+// What the product kernel needs to know about the adapters of one tile of rows: the rows
+// grouped by adapter (those without one last), and the groups. Written by k_shrink.
+struct TileGroups {
+    uint32_t order[kMaxTileT];      // row within the tile
+    int32_t id[kMaxTileT];          // adapter of group k, negative for the rows without one
+    uint32_t start[kMaxTileT + 1];  // group k holds order[start[k], start[k + 1])
+    uint32_t groups;
+    uint32_t unused[254];
+};
+static_assert(sizeof(TileGroups) == 4096, "one page a tile of rows");
 
 struct ProjectParams {
     const float* x_scale;
     const float* w_scale;
-    const void* lora_b;      // [A][V][rank]
-    const float* u;          // [T][rank]
-    const int32_t* ids;      // [T] adapter of each row, negative: none
+    const void* lora_b;         // [A][V][rank]
+    const float* u;             // [T][u_cols]
+    const TileGroups* groups;   // [tiles_t]
     void* out;
     uint32_t* status;
     uint64_t out_stride;
     uint32_t T, V, rank;
-    uint32_t tile_t;         // N
+    uint32_t u_cols;            // rank rounded up to 16
+    uint32_t b_cols;            // columns of a B buffer: 16, 32 or 64
+    uint32_t slots;             // B buffers
+    uint32_t tile_t;            // N
     uint32_t tiles_t, tiles, slices, stages;
-    uint32_t acc_cols;       // TMEM columns of one accumulator
+    uint32_t chunk;             // slices summed in one accumulator pass
+    uint32_t acc_cols;          // TMEM columns of one accumulator
     uint32_t idesc;
-    uint32_t lora_f16;       // lora_b is f16 (else bf16)
-    uint32_t early;          // the inputs are complete when this kernel starts (u may not be)
+    uint32_t lora_f16;          // lora_b is f16 (else bf16)
+    uint32_t lora_tma;          // lora_b's rows are whole 16-byte pieces (TMA fills the buffers)
+    uint32_t early;             // the inputs are complete when this kernel starts (u may not be)
 };
 
+constexpr uint32_t kGroupWords = 772;             // words of TileGroups in use, rounded up to 16 bytes
+constexpr uint32_t kBarriers = 2 * kMaxStages + 2 * kMaxSlots + 6;
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ uint64_t now_ns() {
     uint64_t t;
@@ -64,9 +89,19 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Arrive on the barrier at the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done != 0;
 }
@@ -90,10 +125,17 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, vo
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_word));
 }
 
+// `bar` is a cluster address: with CTA pairs the even CTA's barrier counts both CTAs' bytes.
+template <int CG>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
-        "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+    if constexpr (CG == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
 }
 
 // Shared-memory matrix descriptor: rows of 128 bytes, 128-byte swizzle, groups of 8 rows
@@ -102,19 +144,26 @@ __device__ __forceinline__ uint64_t matrix_desc(uint32_t addr) {
     return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
-template <bool FP8>
+template <bool FP8, int CG>
 __device__ __forceinline__ void mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    if constexpr (FP8)
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem), "l"(a), "l"(b),
-                     "r"(idesc), "r"(accumulate) : "memory");
-    else
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem), "l"(a), "l"(b),
-                     "r"(idesc), "r"(accumulate) : "memory");
+#define LPH_MMA(GROUP, KIND)                                                                       \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"                               \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem), \
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory")
+    if constexpr (FP8 && CG == 2) LPH_MMA("2", "f8f6f4");
+    else if constexpr (FP8) LPH_MMA("1", "f8f6f4");
+    else if constexpr (CG == 2) LPH_MMA("2", "f16");
+    else LPH_MMA("1", "f16");
+#undef LPH_MMA
 }
+// Arrive on the barrier (of both CTAs of a pair) when every product issued so far is done.
+template <int CG>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (CG == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                     ::"r"(bar), "h"((uint16_t)3) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
     uint32_t r[32];
@@ -130,50 +179,88 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr) : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// Sixteen values of row v of an adapter's B, from j0 on (zero past the rank).
-__device__ __forceinline__ void load_b(const ProjectParams& p, uint32_t a, uint32_t v, uint32_t j0, float (&b)[16]) {
-    const uint16_t* row = static_cast<const uint16_t*>(p.lora_b) + ((uint64_t)a * p.V + v) * p.rank + j0;
-    const uint32_t left = p.rank - j0;
-    uint32_t w[8];
-    if (left >= 16 && p.rank % 8 == 0) {
-        const uint4 lo = *reinterpret_cast<const uint4*>(row), hi = *reinterpret_cast<const uint4*>(row + 8);
-        w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
-        w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
-    } else {
+// Eight columns cols[0..8) of the accumulator, one by one.
+__device__ __forceinline__ void tmem_load8(uint32_t base, const uint32_t (&col)[8], float (&v)[8]) {
+    uint32_t r[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t l = 2 * i < left ? row[2 * i] : 0u, h = 2 * i + 1 < left ? row[2 * i + 1] : 0u;
-            w[i] = l | (h << 16);
-        }
-    }
+    for (int i = 0; i < 8; ++i)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[i]) : "r"(base + col[i]) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 ::"memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 f = p.lora_f16 ? unpack2(w[i], __half()) : unpack2(w[i], __nv_bfloat16());
-        b[2 * i] = f.x;
-        b[2 * i + 1] = f.y;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+          "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+          "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+          "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(addr) : "memory");
 }
 
-template <bool FP8, typename OUT>
+// Two f32 at a time: a * b + c.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float2 f) {
+    return (uint64_t)__float_as_uint(f.x) | ((uint64_t)__float_as_uint(f.y) << 32);
+}
+
+// Byte offset of 16-byte piece `piece` of row `row` in a B buffer of `cols` columns: rows of
+// 32, 64 or 128 bytes, the pieces swizzled as TMA writes them, so that the 32 rows that a
+// warp reads spread over the banks.
+__device__ __forceinline__ uint32_t b_offset(uint32_t row, uint32_t piece, uint32_t cols) {
+    const uint32_t off = row * cols * 2 + piece * 16;
+    return off ^ ((off >> 3) & (cols * 2 - 16));
+}
+
+// PROMOTE: f32 logits of 16-bit inputs. The tensor core's f32 accumulator drops the bits
+// below its last place at every step, always towards zero: over a contraction of 4096 that
+// adds up to 2.8e-6 of the result, against 6e-7 of rounded f32 sums. So the accumulator is
+// emptied into registers every kPromoteSlices slices (256 products), and those are summed
+// with rounding. Rounded outputs (16 bits) and e4m3 products (few bits) do not need it.
+template <bool FP8, typename OUT, int CG, bool PROMOTE>
 __global__ void __launch_bounds__(kThreads, 1)
-k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x, const ProjectParams p) {
+k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+          const __grid_constant__ CUtensorMap map_b, const ProjectParams p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* ring = smem_raw + (base - smem_u32(smem_raw));
-    const uint32_t N = p.tile_t, stage_bytes = kStageW + N * kSliceBytes;
-    const uint32_t rp = (p.rank + 15) & ~15u;  // rank, padded with zeros
-    float* s_u = reinterpret_cast<float*>(ring + p.stages * stage_bytes);       // [N][rp]
-    float* s_scale = s_u + N * rp;                                              // [N]
-    int32_t* s_id = reinterpret_cast<int32_t*>(s_scale + N);                    // [N]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_id + N);
-    volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + 2 * kMaxStages + 6);
+    const uint32_t N = p.tile_t, stage_bytes = kStageW + N / CG * kSliceBytes;
+    const uint32_t uc = p.u_cols, slot_bytes = kTileV * p.b_cols * 2;
+    unsigned char* s_b = ring + p.stages * stage_bytes;                         // [slots][128][b_cols]
+    float* s_u = reinterpret_cast<float*>(s_b + p.slots * slot_bytes);          // [N][uc]
+    float* s_scale = s_u + N * uc;                                              // [N]
+    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_scale + N);          // without its padding
+    uint64_t* bars = reinterpret_cast<uint64_t*>(s_scale + N + (p.rank ? kGroupWords : 0));
+    volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + kBarriers);
     uint32_t* s_tmem = const_cast<uint32_t*>(s_abort) + 1;
-    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, acc_full0 = empty0 + 8 * kMaxStages,
+    const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, b_full0 = empty0 + 8 * kMaxStages,
+                   b_empty0 = b_full0 + 8 * kMaxSlots, acc_full0 = b_empty0 + 8 * kMaxSlots,
                    acc_empty0 = acc_full0 + 16, drain = acc_empty0 + 16, staging = drain + 8;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank = 0;
+    if constexpr (CG == 2) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;  // tiles of this CTA (pair)
 
     pdl_trigger();
     if (threadIdx.x == 0) {
@@ -181,9 +268,13 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
+        for (uint32_t i = 0; i < p.slots; ++i) {
+            mbar_init(b_full0 + 8 * i, p.lora_tma ? 1 : 32);
+            mbar_init(b_empty0 + 8 * i, kEpilogueWarps);
+        }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(acc_full0 + 8 * i, 1);
-            mbar_init(acc_empty0 + 8 * i, kEpilogueWarps);
+            mbar_init(acc_empty0 + 8 * i, kEpilogueWarps * CG);
         }
         mbar_init(drain, 1);
         mbar_init(staging, kEpilogueWarps);
@@ -192,16 +283,24 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
-                     "r"(2 * p.acc_cols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (CG == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                         "r"(2 * p.acc_cols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
+                         "r"(2 * p.acc_cols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are ready too
     fence_after();
     const uint32_t tmem = *s_tmem;
 
-    uint32_t issued = 0;  // stages the producer has started copies into
+    uint32_t issued = 0;    // stages the producer has started copies into
+    uint32_t b_issued = 0;  // B buffers the loader has started copies into
     if (warp == 0) {
         if (lane == 0) {
             if (!p.early) pdl_wait();
@@ -212,48 +311,93 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t slice_elems = FP8 ? kSliceBytes : kSliceBytes / 2;
             uint32_t s = 0, phase = 0;
             bool ok = true;
-            for (uint32_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x) {
+            for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
+                const int v0 = (int)((tv * CG + rank) * kTileV), t0 = (int)(tt * N + rank * (N / CG));
                 for (uint32_t k = 0; k < p.slices; ++k) {
                     if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
-                    const uint32_t dst = base + s * stage_bytes, bar = full0 + 8 * s;
-                    mbar_expect(bar, stage_bytes);
-                    tma_2d(dst, &map_w, (int)(k * slice_elems), (int)(tv * kTileV), bar, w_policy);
-                    tma_2d(dst + kStageW, &map_x, (int)(k * slice_elems), (int)(tt * N), bar, keep);
+                    const uint32_t dst = base + s * stage_bytes;
+                    const uint32_t bar = CG == 2 ? map_to(full0 + 8 * s, 0) : full0 + 8 * s;
+                    if (rank == 0) mbar_expect(full0 + 8 * s, CG * stage_bytes);
+                    tma_2d<CG>(dst, &map_w, (int)(k * slice_elems), v0, bar, w_policy);
+                    tma_2d<CG>(dst + kStageW, &map_x, (int)(k * slice_elems), t0, bar, keep);
                     ++issued;
                     if (++s == p.stages) { s = 0; phase ^= 1; }
                 }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
-            for (uint32_t tile = blockIdx.x; ok && tile < p.tiles; tile += gridDim.x, ++n) {
-                const uint32_t acc = n & 1, acc_phase = (n >> 1) & 1;
-                if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase ^ 1, s_abort)) break;
-                fence_after();
-                for (uint32_t k = 0; k < p.slices; ++k) {
-                    if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+            for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
+                for (uint32_t k0 = 0; ok && k0 < p.slices; k0 += p.chunk, ++n) {
+                    const uint32_t acc = n & 1, acc_phase = (n >> 1) & 1, k1 = min(k0 + p.chunk, p.slices);
+                    if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase ^ 1, s_abort)) { ok = false; break; }
                     fence_after();
-                    const uint64_t a = matrix_desc(base + s * stage_bytes);
-                    const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
+                    for (uint32_t k = k0; k < k1; ++k) {
+                        if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+                        fence_after();
+                        const uint64_t a = matrix_desc(base + s * stage_bytes);
+                        const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
 #pragma unroll
-                    for (uint32_t i = 0; i < kSliceBytes / 32; ++i)  // 32 bytes of the contracted dimension each
-                        mma<FP8>(tmem + acc * p.acc_cols, a + 2 * i, b + 2 * i, p.idesc, k | i);
-                    mma_commit(empty0 + 8 * s);
-                    if (++s == p.stages) { s = 0; phase ^= 1; }
+                        for (uint32_t i = 0; i < kSliceBytes / 32; ++i)  // 32 bytes of the contracted dimension each
+                            mma<FP8, CG>(tmem + acc * p.acc_cols, a + 2 * i, b + 2 * i, p.idesc, (k - k0) | i);
+                        mma_commit<CG>(empty0 + 8 * s);
+                        if (++s == p.stages) { s = 0; phase ^= 1; }
+                    }
+                    if (ok) mma_commit<CG>(acc_full0 + 8 * acc);
                 }
-                if (ok) mma_commit(acc_full0 + 8 * acc);
             }
-            mma_commit(drain);  // arrives once every product issued above has finished
+            mma_commit<CG>(drain);  // arrives once every product issued above has finished
+        }
+    } else if (warp == 2) {
+        // Tiles of the adapters' B, in the order the epilogue takes them.
+        if (p.rank) {
+            pdl_wait();
+            uint64_t once;
+            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+            uint32_t s = 0, phase = 0;
+            bool ok = true;
+            for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
+                const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
+                const uint32_t v0 = (tv * CG + rank) * kTileV;
+                const TileGroups* g = p.groups + tt;
+                const uint32_t groups = g->groups;
+                for (uint32_t k = 0; k < groups; ++k) {
+                    const int32_t a = g->id[k];
+                    if (a < 0 || v0 >= p.V) continue;
+                    if (!mbar_wait_warp(b_empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
+                    const uint32_t bar = b_full0 + 8 * s;
+                    if (p.lora_tma) {
+                        if (lane == 0) {
+                            mbar_expect(bar, slot_bytes);
+                            tma_2d<1>(smem_u32(s_b) + s * slot_bytes, &map_b, 0, (int)((uint32_t)a * p.V + v0), bar, once);
+                        }
+                        __syncwarp();
+                        ++b_issued;
+                    } else {
+                        const uint16_t* src = static_cast<const uint16_t*>(p.lora_b) + ((uint64_t)a * p.V + v0) * p.rank;
+                        unsigned char* dst = s_b + s * slot_bytes;
+                        const uint32_t rows = min(kTileV, p.V - v0);
+                        for (uint32_t i = lane; i < kTileV * p.b_cols; i += 32) {
+                            const uint32_t r = i / p.b_cols, j = i - r * p.b_cols;
+                            *reinterpret_cast<uint16_t*>(dst + b_offset(r, j >> 3, p.b_cols) + (j & 7) * 2) =
+                                r < rows && j < p.rank ? src[r * p.rank + j] : (uint16_t)0;
+                        }
+                        mbar_arrive(bar);
+                    }
+                    if (++s == p.slots) { s = 0; phase ^= 1; }
+                }
+            }
         }
     } else if (warp >= kFirstEpilogueWarp) {
-        // Quadrant of lanes this warp may read, and which 32-column groups it takes.
+        // The quadrant of lanes this warp may read; `half` tells apart the two warps of one.
         const uint32_t quad = warp & 3, half = (warp - kFirstEpilogueWarp) >> 2;
         const uint32_t et = threadIdx.x - kFirstEpilogueWarp * 32;
         OUT* out = static_cast<OUT*>(p.out);
-        uint32_t n = 0, staged = 0xFFFFFFFFu, staging_phase = 0;
+        uint32_t n = 0, staged = 0xFFFFFFFFu, staging_phase = 0, b_slot = 0, b_phase = 0;
+        const uint32_t acc_empty_at = CG == 2 ? map_to(acc_empty0, 0) : acc_empty0;
         // all epilogue warps have come here (a bounded wait, as everywhere: no warp can be
         // left behind by one that gave up)
         const auto meet = [&]() {
@@ -263,92 +407,184 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             staging_phase ^= 1;
             return ok;
         };
+        const auto release = [&](uint32_t acc) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_at(acc_empty_at + 8 * acc);
+                else mbar_arrive(acc_empty0 + 8 * acc);
+            }
+        };
         pdl_wait();
-        for (uint32_t tile = blockIdx.x; tile < p.tiles; tile += gridDim.x, ++n) {
-            const uint32_t acc = n & 1, acc_phase = (n >> 1) & 1;
+        for (uint32_t tile = first; tile < p.tiles; tile += step) {
             const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t, t0 = tt * N;
-            const uint32_t v = tv * kTileV + quad * 32 + lane;
-            if (tt != staged) {  // the rows' adapters, u and scales
+            const uint32_t v0 = (tv * CG + rank) * kTileV, v = v0 + quad * 32 + lane;
+            if ((FP8 || p.rank) && tt != staged) {  // the rows' scales, u and groups
                 if (!meet()) break;
-                for (uint32_t i = et; i < N; i += kEpilogueWarps * 32) {
-                    s_id[i] = p.rank && t0 + i < p.T ? p.ids[t0 + i] : -1;
-                    s_scale[i] = FP8 && t0 + i < p.T ? p.x_scale[t0 + i] : 1.f;
+                if constexpr (FP8) {
+                    for (uint32_t i = et; i < N; i += kEpilogueWarps * 32)
+                        s_scale[i] = t0 + i < p.T ? p.x_scale[t0 + i] : 0.f;
                 }
-                for (uint32_t i = et; i < N * rp; i += kEpilogueWarps * 32) {
-                    const uint32_t c = i / rp, j = i - c * rp;
-                    s_u[i] = t0 + c < p.T && j < p.rank ? p.u[(uint64_t)(t0 + c) * p.rank + j] : 0.f;
+                if (p.rank) {
+                    const uint32_t rows = min(N, p.T - t0);
+                    const float4* src = reinterpret_cast<const float4*>(p.u + (uint64_t)t0 * uc);
+                    for (uint32_t i = et; i < rows * uc / 4; i += kEpilogueWarps * 32)
+                        reinterpret_cast<float4*>(s_u)[i] = src[i];
+                    const uint32_t* words = reinterpret_cast<const uint32_t*>(p.groups + tt);
+                    for (uint32_t i = et; i < kGroupWords; i += kEpilogueWarps * 32)
+                        reinterpret_cast<uint32_t*>(s_groups)[i] = words[i];
                 }
                 if (!meet()) break;
                 staged = tt;
             }
             const float sw = FP8 && v < p.V ? p.w_scale[v] : 1.f;
-            if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase, s_abort)) break;
-            fence_after();
-            for (uint32_t c0 = half * 32; c0 < N; c0 += 64) {
-                float y[32];
-                tmem_load32(tmem + ((quad * 32) << 16) + acc * p.acc_cols + c0, y);
-                if constexpr (FP8) {
+            uint32_t acc = n & 1;
+            const uint32_t lanes = (quad * 32) << 16;
+            if constexpr (PROMOTE) {
+                // this warp's columns: groups of 32 at half * 32 + 64 g
+                float sum[kMaxTileT / 64][32];
+                bool ok = true;
+                for (uint32_t k0 = 0; k0 < p.slices; k0 += p.chunk, ++n) {
+                    acc = n & 1;
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) { ok = false; break; }
+                    fence_after();
+                    const bool last = k0 + p.chunk >= p.slices;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
+                    for (uint32_t g = 0; g < kMaxTileT / 64; ++g) {
+                        const uint32_t c0 = half * 32 + 64 * g;
+                        if (c0 >= N) continue;
+                        const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
+#pragma unroll
+                        for (int q = 0; q < 32; q += 16) {
+                            float y[16];
+                            tmem_load16(at + q, y);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) sum[g][q + c] = k0 ? sum[g][q + c] + y[c] : y[c];
+                        }
+                        if (last) tmem_store32(at, sum[g]);
+                    }
+                    if (!last) release(acc);
                 }
+                if (!ok) break;
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                // (the groups below are read by either warp of the quadrant)
                 if (p.rank) {
-                    const int32_t id = c0 + lane < N ? s_id[c0 + lane] : -1;
-                    uint32_t todo = __ballot_sync(0xFFFFFFFFu, id >= 0);
-                    while (todo) {  // the group's rows of one adapter together
-                        const int32_t a = __shfl_sync(0xFFFFFFFFu, id, __ffs(todo) - 1);
-                        const uint32_t mine = __ballot_sync(0xFFFFFFFFu, id == a);
-                        todo &= ~mine;
-                        for (uint32_t j0 = 0; j0 < rp; j0 += 16) {
-                            float b[16];
-                            load_b(p, (uint32_t)a, v < p.V ? v : p.V - 1, j0, b);
+                    fence_before();
+                    if (!meet()) break;
+                    fence_after();
+                }
+            } else {
+                if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) break;
+                fence_after();
+                ++n;
+            }
+            const uint32_t columns = tmem + lanes + acc * p.acc_cols;
+            if (!p.rank) {
+                for (uint32_t c0 = half * 32; c0 < N; c0 += 64) {
+                    float y[32];
+                    tmem_load32(columns + c0, y);
+                    if constexpr (FP8) {
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                if (mine >> c & 1) {
-                                    const float4* u4 = reinterpret_cast<const float4*>(s_u + (c0 + c) * rp + j0);
+                        for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
+                    }
+                    if (v < p.V) {
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float4 u = u4[i];
-                                        y[c] = fmaf(u.x, b[4 * i], y[c]);
-                                        y[c] = fmaf(u.y, b[4 * i + 1], y[c]);
-                                        y[c] = fmaf(u.z, b[4 * i + 2], y[c]);
-                                        y[c] = fmaf(u.w, b[4 * i + 3], y[c]);
+                        for (int c = 0; c < 32; ++c)
+                            if (c0 + c < N && t0 + c0 + c < p.T)
+                                out[(uint64_t)(t0 + c0 + c) * p.out_stride + v] = from_f32<OUT>(y[c]);
+                    }
+                }
+            } else if (v0 < p.V) {
+                // Group by group: the lane's row of B_a from the buffer, the group's rows of u
+                // (the same for every lane), eight rows at a time.
+                bool ok = true;
+                const uint32_t groups = s_groups->groups;
+                for (uint32_t k = 0; k < groups; ++k) {
+                    const int32_t a = s_groups->id[k];
+                    const uint32_t end = s_groups->start[k + 1];
+                    const unsigned char* b_tile = s_b + b_slot * slot_bytes;
+                    if (a >= 0 && !mbar_wait_warp(b_full0 + 8 * b_slot, b_phase, s_abort)) { ok = false; break; }
+                    for (uint32_t i = s_groups->start[k] + 8 * half; i < end; i += 16) {
+                        uint32_t c[8];
+                        float y[8];
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) c[r] = s_groups->order[min(i + r, end - 1)];
+                        tmem_load8(columns, c, y);
+                        if constexpr (FP8) {
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) y[r] *= sw * s_scale[c[r]];
+                        }
+                        if (a >= 0) {
+                            uint64_t y2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                            for (uint32_t j0 = 0; j0 < uc; j0 += 16) {
+                                uint64_t b2[8];
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    const uint4 w = *reinterpret_cast<const uint4*>(
+                                        b_tile + b_offset(quad * 32 + lane, j0 / 8 + q, p.b_cols));
+                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e)
+                                        b2[4 * q + e] = pair(p.lora_f16 ? unpack2(ws[e], __half())
+                                                                        : unpack2(ws[e], __nv_bfloat16()));
+                                }
+#pragma unroll
+                                for (int r = 0; r < 8; ++r) {
+                                    const ulonglong2* u = reinterpret_cast<const ulonglong2*>(s_u + c[r] * uc + j0);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const ulonglong2 u2 = u[e];
+                                        y2[r] = fma2(u2.x, b2[2 * e], y2[r]);
+                                        y2[r] = fma2(u2.y, b2[2 * e + 1], y2[r]);
                                     }
                                 }
                             }
+#pragma unroll
+                            for (int r = 0; r < 8; ++r)
+                                y[r] += __uint_as_float((uint32_t)y2[r]) + __uint_as_float((uint32_t)(y2[r] >> 32));
                         }
+#pragma unroll
+                        for (int r = 0; r < 8; ++r)
+                            if (i + r < end && v < p.V)
+                                out[(uint64_t)(t0 + c[r]) * p.out_stride + v] = from_f32<OUT>(y[r]);
+                    }
+                    if (a >= 0) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(b_empty0 + 8 * b_slot);
+                        if (++b_slot == p.slots) { b_slot = 0; b_phase ^= 1; }
                     }
                 }
-                if (v < p.V) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c)
-                        if (c0 + c < N && t0 + c0 + c < p.T)
-                            out[(uint64_t)(t0 + c0 + c) * p.out_stride + v] = from_f32<OUT>(y[c]);
-                }
+                if (!ok) break;
             }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acc_empty0 + 8 * acc);
+            release(acc);
         }
     }
     // Everything issued is finished before shared memory and TMEM go: in a normal run the
     // epilogue has seen every tile; after an abort the copies and products in flight end by
     // themselves, and these waits are bounded like the others.
-    if (warp == 1 && lane == 0) {
+    if (warp == 1 && lane == 0) {  // (in both CTAs of a pair: the commit arrives in both)
         uint32_t dummy = 0;
         (void)mbar_wait(drain, 0, &dummy);
     }
-    if (warp == 0 && lane == 0 && *s_abort) {
-        for (uint32_t i = issued < p.stages ? 0 : issued - p.stages; i < issued; ++i) {
-            uint32_t dummy = 0;
-            (void)mbar_wait(full0 + 8 * (i % p.stages), (i / p.stages) & 1, &dummy);
-        }
+    if (lane == 0 && *s_abort) {
+        uint32_t dummy = 0;
+        if (rank == 0)  // (the even CTA's barriers count the pair's copies)
+            for (uint32_t i = issued < p.stages ? 0 : issued - p.stages; i < issued; ++i)
+                (void)mbar_wait(full0 + 8 * (i % p.stages), (i / p.stages) & 1, &dummy);
+        for (uint32_t i = b_issued < p.slots ? 0 : b_issued - p.slots; i < b_issued; ++i)
+            (void)mbar_wait(b_full0 + 8 * (i % p.slots), (i / p.slots) & 1, &dummy);
     }
     __syncwarp();
     fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // neither CTA leaves while the other may write to it
     fence_after();
-    if (warp == 1)
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
+    if (warp == 1) {
+        if constexpr (CG == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
+    }
     if (threadIdx.x == 0 && *s_abort) flag(p.status, LP_ERR_TIMEOUT);
 }
 
@@ -362,10 +598,11 @@ struct ShrinkParams {
     const int32_t* adapter_ids;    // [B]
     const uint32_t* row_offsets;   // [B+1] or NULL
     float* u;
-    int32_t* ids;
+    TileGroups* groups;
     uint32_t* status;
     uint64_t x_stride;
-    uint32_t T, H, B, adapters, rank;
+    uint32_t T, H, B, adapters, rank, u_cols;
+    uint32_t tile_t;
 };
 
 constexpr uint32_t kShrinkWarps = 8;
@@ -402,36 +639,90 @@ __device__ __forceinline__ void load_x8(const __nv_fp8_e4m3* p, float (&v)[8]) {
     }
 }
 
+// The adapter of row t (negative: none); a bad id or a row of no request: adapter 0 and *bad.
+__device__ __forceinline__ int32_t adapter_of(const ShrinkParams& p, uint32_t t, bool* bad, uint32_t* code) {
+    const int b = request_of(p.row_offsets, p.B, t);
+    const int32_t a = b < 0 ? 0 : p.adapter_ids[b];
+    *bad = b < 0 || a >= (int32_t)p.adapters;
+    *code = b < 0 ? LP_ERR_OFFSETS : LP_ERR_ADAPTER;
+    return *bad ? 0 : a;
+}
+
+// The groups of one tile of rows (a thread a row): rows ordered by the first row of their
+// adapter, then by their own place.
+__device__ void group_rows(const ShrinkParams& p, uint32_t tile) {
+    __shared__ int32_t id[kMaxTileT];
+    __shared__ uint32_t key[kMaxTileT];
+    const uint32_t c = threadIdx.x, t0 = tile * p.tile_t, rows = min(p.tile_t, p.T - t0);
+    bool bad;
+    uint32_t code;
+    if (c < rows) id[c] = max(adapter_of(p, t0 + c, &bad, &code), -1);
+    __syncthreads();
+    if (c < rows) {
+        uint32_t k = kMaxTileT;  // rows without an adapter come last
+        if (id[c] >= 0)
+            for (k = 0; id[k] != id[c]; ++k) {}
+        key[c] = k;
+    }
+    __syncthreads();
+    TileGroups* g = p.groups + tile;
+    if (c < rows) {
+        uint32_t place = 0, group = 0, same_before = 0;
+        for (uint32_t i = 0; i < rows; ++i) {
+            place += key[i] < key[c] || (key[i] == key[c] && i < c);
+            same_before += key[i] == key[c] && i < c;
+            group += key[i] == i && key[i] < key[c];  // groups that begin before this row's
+        }
+        g->order[place] = c;
+        if (same_before == 0) {
+            g->id[group] = id[c];
+            g->start[group] = place;
+        }
+        if (place == rows - 1) {
+            g->groups = group + 1;
+            g->start[group + 1] = rows;
+        }
+    }
+}
+
+// grid: T blocks, one a row, then one a tile of rows for its groups.
 template <typename X, typename A>
 __global__ void __launch_bounds__(kShrinkWarps * 32) k_shrink(ShrinkParams p) {
     pdl_wait();
     pdl_trigger();  // after the wait: the product kernel may read x, which is complete now
-    const uint32_t t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = request_of(p.row_offsets, p.B, t);
-    int32_t a = b < 0 ? 0 : p.adapter_ids[b];
-    const bool bad = b < 0 || a >= (int32_t)p.adapters;
-    if (bad) {
-        a = 0;
-        if (threadIdx.x == 0) flag(p.status, b < 0 ? LP_ERR_OFFSETS : LP_ERR_ADAPTER);
+    if (blockIdx.x >= p.T) {
+        group_rows(p, blockIdx.x - p.T);
+        return;
     }
-    if (threadIdx.x == 0) p.ids[t] = a;
-    if (a < 0) return;
+    const uint32_t t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    bool bad;
+    uint32_t code;
+    const int32_t a = adapter_of(p, t, &bad, &code);
+    if (bad && threadIdx.x == 0) flag(p.status, code);
+    float* u = p.u + (uint64_t)t * p.u_cols;
+    if (a < 0) {
+        for (uint32_t j = threadIdx.x; j < p.u_cols; j += kShrinkWarps * 32) u[j] = 0.f;
+        return;
+    }
     const X* x = static_cast<const X*>(p.x) + (uint64_t)t * p.x_stride;
     float scale = p.adapter_scale ? p.adapter_scale[a] : 1.f;
     if (p.x_scale) scale *= p.x_scale[t];
-    for (uint32_t j = warp; j < p.rank; j += kShrinkWarps) {
-        const A* row = static_cast<const A*>(p.lora_a) + ((uint64_t)a * p.rank + j) * p.H;
+    for (uint32_t j = warp; j < p.u_cols; j += kShrinkWarps) {
         float sum = 0.f;
-        for (uint32_t h = lane * 8; h < p.H; h += 256) {
-            float xv[8], av[8];
-            load_x8(x + h, xv);
-            load_x8(row + h, av);
+        if (j < p.rank) {
+            const A* row = static_cast<const A*>(p.lora_a) + ((uint64_t)a * p.rank + j) * p.H;
+            for (uint32_t h = lane * 8; h < p.H; h += 256) {
+                float xv[8], av[8];
+                load_x8(x + h, xv);
+                load_x8(row + h, av);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(xv[i], av[i], sum);
+                for (int i = 0; i < 8; ++i) sum = fmaf(xv[i], av[i], sum);
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            sum = bad ? __int_as_float(0x7fffffff) : sum * scale;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (lane == 0) p.u[(uint64_t)t * p.rank + j] = bad ? __int_as_float(0x7fffffff) : sum * scale;
+        if (lane == 0) u[j] = sum;
     }
 }
 
@@ -458,9 +749,10 @@ EncodeFn encode_fn() {
     return f;
 }
 
-// Map of a row-major matrix [rows][cols], read in boxes of 128 bytes by box_rows rows.
+// Map of a row-major matrix [rows][cols], read in boxes of box_cols columns (of 32, 64 or
+// 128 bytes, swizzled over that width) by box_rows rows.
 bool encode(CUtensorMap* map, const void* ptr, uint32_t dtype, uint64_t rows, uint64_t cols, uint64_t stride,
-            uint32_t box_rows) {
+            uint32_t box_rows, uint32_t box_cols) {
     const EncodeFn f = encode_fn();
     if (!f) return false;
     const CUtensorMapDataType type = dtype == LP_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
@@ -468,32 +760,38 @@ bool encode(CUtensorMap* map, const void* ptr, uint32_t dtype, uint64_t rows, ui
                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const uint64_t e = dtype_bytes(dtype);
     const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride * e};
-    const cuuint32_t box[2] = {(cuuint32_t)(kSliceBytes / e), box_rows}, step[2] = {1, 1};
-    return f(map, type, 2, const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+    const cuuint32_t box[2] = {box_cols, box_rows}, step[2] = {1, 1};
+    const CUtensorMapSwizzle swizzle = box_cols * e == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                       : box_cols * e == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                            : CU_TENSOR_MAP_SWIZZLE_32B;
+    return f(map, type, 2, const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-std::atomic<uint64_t> g_smem_set[2][3];
+struct ProjectLaunch {
+    CUtensorMap w, x, b;
+    ProjectParams p;
+    size_t smem;
+    unsigned grid;
+};
 
-template <bool FP8, typename OUT>
-lp_status launch_project(const CUtensorMap& w, const CUtensorMap& x, const ProjectParams& p, unsigned grid, size_t smem,
-                         int out_index, lp_stream_t stream) {
-    auto kernel = k_project<FP8, OUT>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), kSmemBudget, &g_smem_set[FP8][out_index])) return LP_ERR_CUDA;
-    return launch(kernel, dim3(grid), kThreads, smem, stream, 1, w, x, p);
+template <bool FP8, typename OUT, int CG, bool PROMOTE>
+lp_status launch_project(const ProjectLaunch& l, lp_stream_t stream) {
+    static std::atomic<uint64_t> smem_set;
+    auto kernel = k_project<FP8, OUT, CG, PROMOTE>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), kSmemBudget, &smem_set)) return LP_ERR_CUDA;
+    return launch(kernel, dim3(l.grid), kThreads, l.smem, stream, CG, l.w, l.x, l.b, l.p);
 }
 
-template <bool FP8>
-lp_status launch_project(const CUtensorMap& w, const CUtensorMap& x, const ProjectParams& p, unsigned grid, size_t smem,
-                         uint32_t out_dtype, lp_stream_t stream) {
-    if (out_dtype == LP_F32) return launch_project<FP8, float>(w, x, p, grid, smem, 0, stream);
-    if (out_dtype == LP_BF16) return launch_project<FP8, __nv_bfloat16>(w, x, p, grid, smem, 1, stream);
-    return launch_project<FP8, __half>(w, x, p, grid, smem, 2, stream);
+template <bool FP8, int CG>
+lp_status launch_project(const ProjectLaunch& l, uint32_t out_dtype, lp_stream_t s) {
+    if (out_dtype == LP_F32) return launch_project<FP8, float, CG, !FP8>(l, s);
+    if (out_dtype == LP_BF16) return launch_project<FP8, __nv_bfloat16, CG, false>(l, s);
+    return launch_project<FP8, __half, CG, false>(l, s);
 }
 
 lp_status launch_shrink(const ShrinkParams& p, uint32_t dtype, uint32_t lora_dtype, lp_stream_t s) {
-    const dim3 grid(p.T);
+    const dim3 grid(p.T + (p.T + p.tile_t - 1) / p.tile_t);
     const unsigned block = kShrinkWarps * 32;
     if (dtype == LP_BF16) return launch(k_shrink<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, s, 1, p);
     if (dtype == LP_F16) return launch(k_shrink<__half, __half>, grid, block, 0, s, 1, p);
@@ -540,40 +838,55 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     if (sms == 0) return LP_ERR_CUDA;
 
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    ProjectParams p = {};
+    ProjectLaunch l = {};
+    ProjectParams& p = l.p;
     p.status = reinterpret_cast<uint32_t*>(ws);
     p.x_scale = x_scale;
     p.w_scale = weight_scale;
     p.lora_b = lora_b;
-    p.ids = reinterpret_cast<int32_t*>(ws + kHeaderBytes);
-    p.u = reinterpret_cast<float*>(ws + kHeaderBytes + (((size_t)T * 4 + 255) & ~(size_t)255));
+    // the workspace: header, the groups of each tile of rows, u
+    const uint32_t tiles_256 = (T + kMaxTileT - 1) / kMaxTileT;
+    p.groups = reinterpret_cast<TileGroups*>(ws + kHeaderBytes);
+    p.u = reinterpret_cast<float*>(ws + kHeaderBytes + (size_t)tiles_256 * sizeof(TileGroups));
     p.out = out;
     p.out_stride = out_stride;
     p.T = T;
     p.V = V;
     p.rank = rank;
+    p.u_cols = (rank + 15) & ~15u;
+    p.b_cols = rank <= 16 ? 16 : rank <= 32 ? 32 : 64;
     p.lora_f16 = lora_dtype == LP_F16;
+    p.lora_tma = rank % 8 == 0 && (uint64_t)adapters * V <= 0x7FFFFFFFu;
     p.early = rank != 0;
-    // Rows of x in even tiles of at most 256, a multiple of 16.
-    p.tiles_t = (T + kMaxTileT - 1) / kMaxTileT;
-    p.tile_t = ((T + p.tiles_t - 1) / p.tiles_t + 15) & ~15u;
-    const uint64_t tiles = (uint64_t)((V + kTileV - 1) / kTileV) * p.tiles_t;
+    // Rows of x in even tiles of at most 256, a multiple of 16 (of 32 for a pair of CTAs). A
+    // pair halves what each SM reads of x, which pays from 129 rows on.
+    const uint32_t cg = T > 128 ? 2 : 1;
+    p.tiles_t = tiles_256;
+    p.tile_t = ((T + p.tiles_t - 1) / p.tiles_t + 16 * cg - 1) / (16 * cg) * (16 * cg);
+    const uint64_t tiles = (uint64_t)((V + cg * kTileV - 1) / (cg * kTileV)) * p.tiles_t;
     if (tiles > 0x7FFFFFFFu) return LP_ERR_SHAPE;
     p.tiles = (uint32_t)tiles;
     p.slices = (uint32_t)((H * e + kSliceBytes - 1) / kSliceBytes);
+    p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : p.slices;
     for (p.acc_cols = 32; p.acc_cols < p.tile_t; p.acc_cols *= 2) {}
-    // instruction: f32 accumulator, K-major operands, M = 128, N = tile_t
+    // instruction: f32 accumulator, K-major operands, M = 128 lanes a CTA, N = tile_t
     const uint32_t type = dtype == LP_BF16 ? 1u : 0u;  // kind::f16: 0 f16, 1 bf16; kind::f8f6f4: 0 e4m3
-    p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((kTileV >> 4) << 24);
-    const uint32_t rp = (rank + 15) & ~15u, stage_bytes = kStageW + p.tile_t * kSliceBytes;
-    const uint32_t rows_bytes = p.tile_t * (rp * 4 + 8);
+    p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((cg * kTileV >> 4) << 24);
+    const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
+    p.slots = rank ? kSlotsBytes / slot_bytes : 0;
+    const uint32_t rows_bytes = p.tile_t * (p.u_cols * 4 + 4) + p.slots * slot_bytes + (rank ? kGroupWords * 4 : 0);
     p.stages = (kSmemBudget - kControlBytes - rows_bytes) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    const size_t smem = kControlBytes + rows_bytes + p.stages * stage_bytes;
-    CUtensorMap map_w, map_x;
-    if (!encode(&map_w, weight, dtype, V, H, weight_stride, kTileV) ||
-        !encode(&map_x, x, dtype, T, H, x_stride, p.tile_t))
+    l.smem = kControlBytes + rows_bytes + p.stages * stage_bytes;
+    const uint32_t slice_cols = kSliceBytes / (uint32_t)e;
+    if (!encode(&l.w, weight, dtype, V, H, weight_stride, kTileV, slice_cols) ||
+        !encode(&l.x, x, dtype, T, H, x_stride, p.tile_t / cg, slice_cols))
         return LP_ERR_CUDA;
+    if (rank && p.lora_tma) {
+        if (!encode(&l.b, lora_b, lora_dtype, (uint64_t)adapters * V, rank, rank, kTileV, p.b_cols)) return LP_ERR_CUDA;
+    } else {
+        l.b = l.w;  // not used
+    }
     if (rank) {
         ShrinkParams q = {};
         q.x = x;
@@ -583,7 +896,9 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         q.adapter_ids = adapter_ids;
         q.row_offsets = row_offsets;
         q.u = const_cast<float*>(p.u);
-        q.ids = const_cast<int32_t*>(p.ids);
+        q.groups = const_cast<TileGroups*>(p.groups);
+        q.u_cols = p.u_cols;
+        q.tile_t = p.tile_t;
         q.status = p.status;
         q.x_stride = x_stride;
         q.T = T;
@@ -594,7 +909,8 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         const lp_status st = launch_shrink(q, dtype, lora_dtype, stream);
         if (st != LP_OK) return st;
     }
-    const unsigned grid = p.tiles < (uint32_t)sms ? p.tiles : (unsigned)sms;
-    return fp8 ? launch_project<true>(map_w, map_x, p, grid, smem, out_dtype, stream)
-               : launch_project<false>(map_w, map_x, p, grid, smem, out_dtype, stream);
+    const uint32_t units = (uint32_t)sms / cg;  // CTAs, or pairs
+    l.grid = cg * (p.tiles < units ? p.tiles : units);
+    if (cg == 2) return fp8 ? launch_project<true, 2>(l, out_dtype, stream) : launch_project<false, 2>(l, out_dtype, stream);
+    return fp8 ? launch_project<true, 1>(l, out_dtype, stream) : launch_project<false, 1>(l, out_dtype, stream);
 }
