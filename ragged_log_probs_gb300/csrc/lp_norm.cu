@@ -238,7 +238,7 @@ size_t lp_head_workspace_size(uint32_t T, uint32_t rank) {
     if (rank > LP_MAX_RANK) return 0;
     if (rank == 0) return lph::kHeaderBytes;
     // lp_head_project: a page for each 256 rows, and a vector of the padded rank a row
-    return lph::kHeaderBytes + ((size_t)T + 255) / 256 * 4096 + (size_t)T * ((rank + 15) & ~15u) * 4;
+    return lph::kHeaderBytes + ((size_t)T + 255) / 256 * 2048 + (size_t)T * ((rank + 15) & ~15u) * 4;
 }
 
 lp_status lp_head_clear_status(void* workspace, lp_stream_t stream) {

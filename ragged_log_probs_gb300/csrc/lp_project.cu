@@ -27,7 +27,7 @@ constexpr uint32_t kStageW = kTileV * kSliceBytes;
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kMaxSlots = 8;                 // buffers for tiles of the adapters' B
 constexpr uint32_t kSlotsBytes = 32 * 1024;
-constexpr uint32_t kEpilogueWarps = 8;
+constexpr uint32_t kEpilogueWarps = 16;
 constexpr uint32_t kFirstEpilogueWarp = 4;
 constexpr uint32_t kThreads = (kFirstEpilogueWarp + kEpilogueWarps) * 32;
 constexpr uint32_t kSmemBudget = 227 * 1024;
@@ -35,22 +35,28 @@ constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the
 constexpr uint32_t kPromoteSlices = 4;            // slices summed in the tensor core before an f32 addition
 
 // What the product kernel needs to know about the adapters of one tile of rows: the rows
-// grouped by adapter (those without one last), and the groups. Written by k_shrink.
+// grouped by adapter (those without one last), cut into items of at most kItemRows rows of
+// one adapter. Written by k_shrink.
+constexpr uint32_t kItemRows = 32;
+constexpr uint32_t kMaxItems = kMaxTileT + kMaxTileT / kItemRows;
 struct TileGroups {
-    uint32_t order[kMaxTileT];      // row within the tile
-    int32_t id[kMaxTileT];          // adapter of group k, negative for the rows without one
-    uint32_t start[kMaxTileT + 1];  // group k holds order[start[k], start[k + 1])
-    uint32_t groups;
-    uint32_t unused[254];
+    uint32_t items;
+    uint32_t unused[3];
+    uint32_t item[kMaxItems + 4];  // adapter of item k, kNoAdapter for rows without one
+    uint8_t start[kMaxItems];      // item k holds order[start[k] ... start[k] + size[k] - 1]
+    uint8_t size[kMaxItems];
+    uint8_t order[kMaxTileT];      // row within the tile
 };
-static_assert(sizeof(TileGroups) == 4096, "one page a tile of rows");
+constexpr uint32_t kGroupBytes = 2048;  // of one tile in the workspace
+static_assert(sizeof(TileGroups) % 16 == 0 && sizeof(TileGroups) <= kGroupBytes, "read as 16-byte words");
+constexpr uint32_t kNoAdapter = 0xFFFFFFFFu;
 
 struct ProjectParams {
     const float* x_scale;
     const float* w_scale;
     const void* lora_b;         // [A][V][rank]
     const float* u;             // [T][u_cols]
-    const TileGroups* groups;   // [tiles_t]
+    const unsigned char* groups;  // [tiles_t] TileGroups, kGroupBytes apart
     void* out;
     uint32_t* status;
     uint64_t out_stride;
@@ -68,7 +74,6 @@ struct ProjectParams {
     uint32_t early;             // the inputs are complete when this kernel starts (u may not be)
 };
 
-constexpr uint32_t kGroupWords = 772;             // words of TileGroups in use, rounded up to 16 bytes
 constexpr uint32_t kBarriers = 2 * kMaxStages + 2 * kMaxSlots + 6;
 
 __device__ __forceinline__ void cluster_sync() {
@@ -96,11 +101,11 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
     return r;
 }
 __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t done;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}"
                  : "=r"(done) : "r"(bar), "r"(parity) : "memory");
     return done != 0;
@@ -109,17 +114,18 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // gives up (the host reads LP_ERR_TIMEOUT).
 constexpr uint64_t kWaitNs = 2000000000ull;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile uint32_t* abort_word) {
-    if (mbar_try(bar, parity)) return true;
-    const uint64_t t0 = now_ns();
-    for (uint32_t n = 0; n < (1u << 30); ++n) {
+    for (int n = 0; n < 256; ++n)
         if (mbar_try(bar, parity)) return true;
+    const uint64_t t0 = now_ns();
+    for (uint32_t n = 0; n < (1u << 26); ++n) {
+        for (int m = 0; m < 32; ++m)
+            if (mbar_try(bar, parity)) return true;
         if (*abort_word) return false;
         if (now_ns() - t0 > kWaitNs) break;
     }
     *abort_word = 1;
     return false;
 }
-
 // The same for a whole warp: every lane gets the same answer.
 __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, volatile uint32_t* abort_word) {
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_word));
@@ -193,8 +199,18 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-// Eight columns cols[0..8) of the accumulator, one by one.
-__device__ __forceinline__ void tmem_load8(uint32_t base, const uint32_t (&col)[8], float (&v)[8]) {
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+        ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+          "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+          "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+          "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(addr) : "memory");
+}
+
+// Eight columns of the accumulator, one by one.
+__device__ __forceinline__ void tmem_load_columns(uint32_t base, const uint32_t (&col)[8], float (&v)[8]) {
     uint32_t r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -204,15 +220,6 @@ __device__ __forceinline__ void tmem_load8(uint32_t base, const uint32_t (&col)[
                  ::"memory");
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-        ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-          "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
-          "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
-          "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(addr) : "memory");
 }
 
 // Two f32 at a time: a * b + c.
@@ -251,7 +258,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     float* s_u = reinterpret_cast<float*>(s_b + p.slots * slot_bytes);          // [N][uc]
     float* s_scale = s_u + N * uc;                                              // [N]
     TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_scale + N);          // without its padding
-    uint64_t* bars = reinterpret_cast<uint64_t*>(s_scale + N + (p.rank ? kGroupWords : 0));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(s_groups) +
+                                                 (p.rank ? sizeof(TileGroups) : 0));
     volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + kBarriers);
     uint32_t* s_tmem = const_cast<uint32_t*>(s_abort) + 1;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, b_full0 = empty0 + 8 * kMaxStages,
@@ -362,17 +370,17 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
                 const uint32_t v0 = (tv * CG + rank) * kTileV;
-                const TileGroups* g = p.groups + tt;
-                const uint32_t groups = g->groups;
-                for (uint32_t k = 0; k < groups; ++k) {
-                    const int32_t a = g->id[k];
-                    if (a < 0 || v0 >= p.V) continue;
+                const TileGroups* g = reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
+                const uint32_t items = v0 < p.V ? g->items : 0u;
+                for (uint32_t k = 0; k < items; ++k) {
+                    const uint32_t a = g->item[k];
+                    if (a == kNoAdapter) break;
                     if (!mbar_wait_warp(b_empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
                     const uint32_t bar = b_full0 + 8 * s;
                     if (p.lora_tma) {
                         if (lane == 0) {
                             mbar_expect(bar, slot_bytes);
-                            tma_2d<1>(smem_u32(s_b) + s * slot_bytes, &map_b, 0, (int)((uint32_t)a * p.V + v0), bar, once);
+                            tma_2d<1>(smem_u32(s_b) + s * slot_bytes, &map_b, 0, (int)(a * p.V + v0), bar, once);
                         }
                         __syncwarp();
                         ++b_issued;
@@ -392,8 +400,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             }
         }
     } else if (warp >= kFirstEpilogueWarp) {
-        // The quadrant of lanes this warp may read; `half` tells apart the two warps of one.
-        const uint32_t quad = warp & 3, half = (warp - kFirstEpilogueWarp) >> 2;
+        // The quadrant of lanes this warp may read, and its share of the columns: the blocks
+        // of 32 whose number is `share` modulo 4. A warp only ever touches its own.
+        const uint32_t quad = warp & 3, share = (warp - kFirstEpilogueWarp) >> 2;
         const uint32_t et = threadIdx.x - kFirstEpilogueWarp * 32;
         OUT* out = static_cast<OUT*>(p.out);
         uint32_t n = 0, staged = 0xFFFFFFFFu, staging_phase = 0, b_slot = 0, b_phase = 0;
@@ -421,18 +430,18 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t v0 = (tv * CG + rank) * kTileV, v = v0 + quad * 32 + lane;
             if ((FP8 || p.rank) && tt != staged) {  // the rows' scales, u and groups
                 if (!meet()) break;
+                const uint32_t rows = min(N, p.T - t0);
                 if constexpr (FP8) {
                     for (uint32_t i = et; i < N; i += kEpilogueWarps * 32)
-                        s_scale[i] = t0 + i < p.T ? p.x_scale[t0 + i] : 0.f;
+                        s_scale[i] = i < rows ? p.x_scale[t0 + i] : 0.f;
                 }
                 if (p.rank) {
-                    const uint32_t rows = min(N, p.T - t0);
                     const float4* src = reinterpret_cast<const float4*>(p.u + (uint64_t)t0 * uc);
-                    for (uint32_t i = et; i < rows * uc / 4; i += kEpilogueWarps * 32)
-                        reinterpret_cast<float4*>(s_u)[i] = src[i];
-                    const uint32_t* words = reinterpret_cast<const uint32_t*>(p.groups + tt);
-                    for (uint32_t i = et; i < kGroupWords; i += kEpilogueWarps * 32)
-                        reinterpret_cast<uint32_t*>(s_groups)[i] = words[i];
+                    for (uint32_t i = et; i < N * uc / 4; i += kEpilogueWarps * 32)
+                        reinterpret_cast<float4*>(s_u)[i] = i < rows * uc / 4 ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const uint4* words = reinterpret_cast<const uint4*>(p.groups + (size_t)tt * kGroupBytes);
+                    for (uint32_t i = et; i < sizeof(TileGroups) / 16; i += kEpilogueWarps * 32)
+                        reinterpret_cast<uint4*>(s_groups)[i] = words[i];
                 }
                 if (!meet()) break;
                 staged = tt;
@@ -441,8 +450,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t acc = n & 1;
             const uint32_t lanes = (quad * 32) << 16;
             if constexpr (PROMOTE) {
-                // this warp's columns: groups of 32 at half * 32 + 64 g
-                float sum[kMaxTileT / 64][32];
+                float sum[kMaxTileT / 128][32];
                 bool ok = true;
                 for (uint32_t k0 = 0; k0 < p.slices; k0 += p.chunk, ++n) {
                     acc = n & 1;
@@ -450,8 +458,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     fence_after();
                     const bool last = k0 + p.chunk >= p.slices;
 #pragma unroll
-                    for (uint32_t g = 0; g < kMaxTileT / 64; ++g) {
-                        const uint32_t c0 = half * 32 + 64 * g;
+                    for (uint32_t i = 0; i < kMaxTileT / 128; ++i) {
+                        const uint32_t c0 = share * 32 + 128 * i;
                         if (c0 >= N) continue;
                         const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
 #pragma unroll
@@ -459,20 +467,14 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             float y[16];
                             tmem_load16(at + q, y);
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) sum[g][q + c] = k0 ? sum[g][q + c] + y[c] : y[c];
+                            for (int c = 0; c < 16; ++c) sum[i][q + c] = k0 ? sum[i][q + c] + y[c] : y[c];
                         }
-                        if (last) tmem_store32(at, sum[g]);
+                        if (last) tmem_store32(at, sum[i]);
                     }
                     if (!last) release(acc);
                 }
                 if (!ok) break;
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                // (the groups below are read by either warp of the quadrant)
-                if (p.rank) {
-                    fence_before();
-                    if (!meet()) break;
-                    fence_after();
-                }
             } else {
                 if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) break;
                 fence_after();
@@ -480,7 +482,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             }
             const uint32_t columns = tmem + lanes + acc * p.acc_cols;
             if (!p.rank) {
-                for (uint32_t c0 = half * 32; c0 < N; c0 += 64) {
+                for (uint32_t c0 = share * 32; c0 < N; c0 += 128) {
                     float y[32];
                     tmem_load32(columns + c0, y);
                     if constexpr (FP8) {
@@ -488,33 +490,43 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                         for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
                     }
                     if (v < p.V) {
+                        const uint32_t rows = min(N, p.T - t0);
+                        OUT* o = out + (uint64_t)(t0 + c0) * p.out_stride + v;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (c0 + c < N && t0 + c0 + c < p.T)
-                                out[(uint64_t)(t0 + c0 + c) * p.out_stride + v] = from_f32<OUT>(y[c]);
+                        for (int c = 0; c < 32; ++c) {
+                            if (c0 + c < rows) *o = from_f32<OUT>(y[c]);
+                            o += p.out_stride;
+                        }
                     }
                 }
             } else if (v0 < p.V) {
-                // Group by group: the lane's row of B_a from the buffer, the group's rows of u
-                // (the same for every lane), eight rows at a time.
+                if constexpr (PROMOTE) {  // an item's columns may have been written by another share
+                    fence_before();
+                    if (!meet()) break;
+                    fence_after();
+                }
+                // Item by item: the lane's row of B_a from its buffer, the item's rows of u (the
+                // same for every lane), eight rows at a time.
                 bool ok = true;
-                const uint32_t groups = s_groups->groups;
-                for (uint32_t k = 0; k < groups; ++k) {
-                    const int32_t a = s_groups->id[k];
-                    const uint32_t end = s_groups->start[k + 1];
+                const uint32_t items = s_groups->items;
+                for (uint32_t k = 0; k < items; ++k) {
+                    // Items go round the shares. Every warp passes every buffer's barriers, so that
+                    // none falls behind by two phases.
+                    const uint32_t a = s_groups->item[k];
+                    if (a != kNoAdapter && !mbar_wait_warp(b_full0 + 8 * b_slot, b_phase, s_abort)) { ok = false; break; }
                     const unsigned char* b_tile = s_b + b_slot * slot_bytes;
-                    if (a >= 0 && !mbar_wait_warp(b_full0 + 8 * b_slot, b_phase, s_abort)) { ok = false; break; }
-                    for (uint32_t i = s_groups->start[k] + 8 * half; i < end; i += 16) {
+                    const uint32_t begin = s_groups->start[k], end = (k & 3) == share ? begin + s_groups->size[k] : 0;
+                    for (uint32_t i = begin; i < end; i += 8) {
                         uint32_t c[8];
                         float y[8];
 #pragma unroll
                         for (int r = 0; r < 8; ++r) c[r] = s_groups->order[min(i + r, end - 1)];
-                        tmem_load8(columns, c, y);
+                        tmem_load_columns(columns, c, y);
                         if constexpr (FP8) {
 #pragma unroll
                             for (int r = 0; r < 8; ++r) y[r] *= sw * s_scale[c[r]];
                         }
-                        if (a >= 0) {
+                        if (a != kNoAdapter) {
                             uint64_t y2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                             for (uint32_t j0 = 0; j0 < uc; j0 += 16) {
                                 uint64_t b2[8];
@@ -548,7 +560,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             if (i + r < end && v < p.V)
                                 out[(uint64_t)(t0 + c[r]) * p.out_stride + v] = from_f32<OUT>(y[r]);
                     }
-                    if (a >= 0) {
+                    if (a != kNoAdapter) {
                         __syncwarp();
                         if (lane == 0) mbar_arrive(b_empty0 + 8 * b_slot);
                         if (++b_slot == p.slots) { b_slot = 0; b_phase ^= 1; }
@@ -598,7 +610,7 @@ struct ShrinkParams {
     const int32_t* adapter_ids;    // [B]
     const uint32_t* row_offsets;   // [B+1] or NULL
     float* u;
-    TileGroups* groups;
+    unsigned char* groups;
     uint32_t* status;
     uint64_t x_stride;
     uint32_t T, H, B, adapters, rank, u_cols;
@@ -648,39 +660,48 @@ __device__ __forceinline__ int32_t adapter_of(const ShrinkParams& p, uint32_t t,
     return *bad ? 0 : a;
 }
 
-// The groups of one tile of rows (a thread a row): rows ordered by the first row of their
-// adapter, then by their own place.
+// The items of one tile of rows (a thread a row): rows ordered by the first row of their
+// adapter, then by their own place; each adapter's rows cut into items.
 __device__ void group_rows(const ShrinkParams& p, uint32_t tile) {
     __shared__ int32_t id[kMaxTileT];
-    __shared__ uint32_t key[kMaxTileT];
+    __shared__ uint32_t head[kMaxTileT];  // the first row with the same adapter
     const uint32_t c = threadIdx.x, t0 = tile * p.tile_t, rows = min(p.tile_t, p.T - t0);
     bool bad;
     uint32_t code;
     if (c < rows) id[c] = max(adapter_of(p, t0 + c, &bad, &code), -1);
     __syncthreads();
     if (c < rows) {
-        uint32_t k = kMaxTileT;  // rows without an adapter come last
+        uint32_t h = kMaxTileT;  // rows without an adapter come last
         if (id[c] >= 0)
-            for (k = 0; id[k] != id[c]; ++k) {}
-        key[c] = k;
+            for (h = 0; id[h] != id[c]; ++h) {}
+        head[c] = h;
     }
     __syncthreads();
-    TileGroups* g = p.groups + tile;
+    // place of this row, its place among its adapter's, and whether it begins an item
+    uint32_t place = 0, among = 0;
     if (c < rows) {
-        uint32_t place = 0, group = 0, same_before = 0;
         for (uint32_t i = 0; i < rows; ++i) {
-            place += key[i] < key[c] || (key[i] == key[c] && i < c);
-            same_before += key[i] == key[c] && i < c;
-            group += key[i] == i && key[i] < key[c];  // groups that begin before this row's
+            place += head[i] < head[c] || (head[i] == head[c] && i < c);
+            among += head[i] == head[c] && i < c;
         }
-        g->order[place] = c;
-        if (same_before == 0) {
-            g->id[group] = id[c];
-            g->start[group] = place;
-        }
-        if (place == rows - 1) {
-            g->groups = group + 1;
-            g->start[group + 1] = rows;
+    }
+    const bool begins = c < rows && among % kItemRows == 0;
+    __shared__ uint8_t begins_at[kMaxTileT];  // by place
+    begins_at[c] = 0;
+    __syncthreads();
+    if (begins) begins_at[place] = 1;
+    __syncthreads();
+    TileGroups* g = reinterpret_cast<TileGroups*>(p.groups + (size_t)tile * kGroupBytes);
+    if (c < rows) {
+        g->order[place] = (uint8_t)c;
+        if (begins) {
+            uint32_t item = 0, size = 1;
+            for (uint32_t i = 0; i < place; ++i) item += begins_at[i];
+            while (place + size < rows && !begins_at[place + size]) ++size;
+            g->item[item] = id[c] < 0 ? kNoAdapter : (uint32_t)id[c];
+            g->start[item] = (uint8_t)place;
+            g->size[item] = (uint8_t)size;
+            if (place + size == rows) g->items = item + 1;
         }
     }
 }
@@ -846,8 +867,8 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.lora_b = lora_b;
     // the workspace: header, the groups of each tile of rows, u
     const uint32_t tiles_256 = (T + kMaxTileT - 1) / kMaxTileT;
-    p.groups = reinterpret_cast<TileGroups*>(ws + kHeaderBytes);
-    p.u = reinterpret_cast<float*>(ws + kHeaderBytes + (size_t)tiles_256 * sizeof(TileGroups));
+    p.groups = ws + kHeaderBytes;
+    p.u = reinterpret_cast<float*>(ws + kHeaderBytes + (size_t)tiles_256 * kGroupBytes);
     p.out = out;
     p.out_stride = out_stride;
     p.T = T;
@@ -874,7 +895,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((cg * kTileV >> 4) << 24);
     const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
     p.slots = rank ? kSlotsBytes / slot_bytes : 0;
-    const uint32_t rows_bytes = p.tile_t * (p.u_cols * 4 + 4) + p.slots * slot_bytes + (rank ? kGroupWords * 4 : 0);
+    const uint32_t rows_bytes = p.tile_t * (p.u_cols * 4 + 4) + p.slots * slot_bytes + (rank ? (uint32_t)sizeof(TileGroups) : 0);
     p.stages = (kSmemBudget - kControlBytes - rows_bytes) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     l.smem = kControlBytes + rows_bytes + p.stages * stage_bytes;
@@ -896,7 +917,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         q.adapter_ids = adapter_ids;
         q.row_offsets = row_offsets;
         q.u = const_cast<float*>(p.u);
-        q.groups = const_cast<TileGroups*>(p.groups);
+        q.groups = const_cast<unsigned char*>(p.groups);
         q.u_cols = p.u_cols;
         q.tile_t = p.tile_t;
         q.status = p.status;
