@@ -15,8 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "liblp_ragged.so"
-SOURCES = ["lp_ragged.cu", "lp_norm.cu", "lp_process.cu", "lp_project.cu"]
-HEADERS = ["lp_device.cuh", "lp_kernels.cuh", "lp_head_common.h"]
+SOURCES = ["lp_ragged.cu", "lp_norm.cu", "lp_process.cu", "lp_project.cu", "lp_adapters.cu"]
+HEADERS = ["lp_device.cuh", "lp_kernels.cuh", "lp_head_common.h", "lp_adapters.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -234,13 +234,6 @@ lp_status launch_norm(const NormParams& p, uint32_t out_dtype, uint32_t dtype, b
 
 extern "C" {
 
-size_t lp_head_workspace_size(uint32_t T, uint32_t rank) {
-    if (rank > LP_MAX_RANK) return 0;
-    if (rank == 0) return lph::kHeaderBytes;
-    // lp_head_project: a page for each 256 rows, and a vector of the padded rank a row
-    return lph::kHeaderBytes + ((size_t)T + 255) / 256 * 2048 + (size_t)T * ((rank + 15) & ~15u) * 4;
-}
-
 lp_status lp_head_clear_status(void* workspace, lp_stream_t stream) {
     if (!workspace) return LP_ERR_WORKSPACE;
     if (cudaMemsetAsync(workspace, 0, 4, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {

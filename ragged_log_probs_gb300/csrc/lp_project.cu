@@ -14,14 +14,13 @@
 // and waits for it only before its first epilogue, which adds the adapters' part in f32.
 #include <cuda.h>
 
-#include "lp_head_common.h"
+#include "lp_adapters.h"
 
 namespace {
 
 using namespace lph;
 
 constexpr uint32_t kTileV = 128;                  // vocabulary rows of a CTA's tile (accumulator lanes)
-constexpr uint32_t kMaxTileT = 256;               // rows of x of a tile
 constexpr uint32_t kSliceBytes = 128;             // bytes of the contracted dimension per stage
 constexpr uint32_t kStageW = kTileV * kSliceBytes;
 constexpr uint32_t kMaxStages = 12;
@@ -34,44 +33,33 @@ constexpr uint32_t kSmemBudget = 227 * 1024;
 constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the alignment of the ring
 constexpr uint32_t kPromoteSlices = 4;            // slices summed in the tensor core before an f32 addition
 
-// What the product kernel needs to know about the adapters of one tile of rows: the rows
-// grouped by adapter (those without one last), cut into items of at most kItemRows rows of
-// one adapter. Written by k_shrink.
-constexpr uint32_t kItemRows = 32;
-constexpr uint32_t kMaxItems = kMaxTileT + kMaxTileT / kItemRows;
-struct TileGroups {
-    uint32_t items;
-    uint32_t unused[3];
-    uint32_t item[kMaxItems + 4];  // adapter of item k, kNoAdapter for rows without one
-    uint8_t start[kMaxItems];      // item k holds order[start[k] ... start[k] + size[k] - 1]
-    uint8_t size[kMaxItems];
-    uint8_t order[kMaxTileT];      // row within the tile
-};
-constexpr uint32_t kGroupBytes = 2048;  // of one tile in the workspace
-static_assert(sizeof(TileGroups) % 16 == 0 && sizeof(TileGroups) <= kGroupBytes, "read as 16-byte words");
-constexpr uint32_t kNoAdapter = 0xFFFFFFFFu;
-
 struct ProjectParams {
     const float* x_scale;
     const float* w_scale;
-    const void* lora_b;         // [A][V][rank]
-    const float* u;             // [T][u_cols]
-    const unsigned char* groups;  // [tiles_t] TileGroups, kGroupBytes apart
+    const void* lora_b;            // [A][V][rank]
+    const float* u;                // [T][u_cols]
+    const float* factor;           // [T]
+    const unsigned char* groups;   // [tiles_t] TileGroups, kGroupBytes apart
     void* out;
     uint32_t* status;
     uint64_t out_stride;
     uint32_t T, V, rank;
-    uint32_t u_cols;            // rank rounded up to 16
-    uint32_t b_cols;            // columns of a B buffer: 16, 32 or 64
-    uint32_t slots;             // B buffers
-    uint32_t tile_t;            // N
+    uint32_t u_cols;               // rank rounded up to 16
+    uint32_t b_cols;               // columns of a B buffer: 16, 32 or 64
+    uint32_t slots;                // B buffers
+    uint32_t u_smem;               // a tile's u is staged in shared memory (else read from global)
+    uint32_t part_stride;          // rows of u's parts
+    uint32_t tile_t;               // N
     uint32_t tiles_t, tiles, slices, stages;
-    uint32_t chunk;             // slices summed in one accumulator pass
-    uint32_t acc_cols;          // TMEM columns of one accumulator
-    uint32_t idesc;
-    uint32_t lora_f16;          // lora_b is f16 (else bf16)
-    uint32_t lora_tma;          // lora_b's rows are whole 16-byte pieces (TMA fills the buffers)
-    uint32_t early;             // the inputs are complete when this kernel starts (u may not be)
+    uint32_t chunk;                // slices summed in one accumulator pass
+    uint32_t acc_cols;             // TMEM columns of one accumulator
+    uint32_t idesc, lora_idesc;    // instruction descriptors: of x W^T, of the adapters' part
+    uint32_t tensor;               // blocks of rows with one adapter run on the tensor cores
+    uint32_t apart;                // with an accumulator of their own: their sum has another scale
+                                   // (e4m3), a factor a row (f16), or x W^T comes in chunks (f32)
+    uint32_t lora_f16;             // lora_b is f16 (else bf16)
+    uint32_t lora_tma;             // lora_b's rows are whole 16-byte pieces (TMA fills the buffers)
+    uint32_t early;                // the inputs are complete when this kernel starts (u may not be)
 };
 
 constexpr uint32_t kBarriers = 2 * kMaxStages + 2 * kMaxSlots + 6;
@@ -240,15 +228,26 @@ __device__ __forceinline__ uint32_t b_offset(uint32_t row, uint32_t piece, uint3
     return off ^ ((off >> 3) & (cols * 2 - 16));
 }
 
+// How many blocks from b0 on have the same entry (the adapter of a run), of `blocks`.
+__device__ __forceinline__ uint32_t run_length(const TileGroups* g, uint32_t b0, uint32_t blocks) {
+    uint32_t n = 1;
+    while (b0 + n < blocks && g->block[b0 + n] == g->block[b0]) ++n;
+    return n;
+}
+__device__ __forceinline__ const TileGroups* tile_groups(const ProjectParams& p, uint32_t tt) {
+    return reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
+}
+
 // PROMOTE: f32 logits of 16-bit inputs. The tensor core's f32 accumulator drops the bits
 // below its last place at every step, always towards zero: over a contraction of 4096 that
 // adds up to 2.8e-6 of the result, against 6e-7 of rounded f32 sums. So the accumulator is
 // emptied into registers every kPromoteSlices slices (256 products), and those are summed
 // with rounding. Rounded outputs (16 bits) and e4m3 products (few bits) do not need it.
-template <bool FP8, typename OUT, int CG, bool PROMOTE>
+template <bool FP8, typename OUT, int CG, bool PROMOTE, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
 k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
-          const __grid_constant__ CUtensorMap map_b, const ProjectParams p) {
+          const __grid_constant__ CUtensorMap map_b, const __grid_constant__ CUtensorMap map_lora_b,
+          const __grid_constant__ CUtensorMap map_parts, const ProjectParams p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     unsigned char* ring = smem_raw + (base - smem_u32(smem_raw));
@@ -256,10 +255,11 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     const uint32_t uc = p.u_cols, slot_bytes = kTileV * p.b_cols * 2;
     unsigned char* s_b = ring + p.stages * stage_bytes;                         // [slots][128][b_cols]
     float* s_u = reinterpret_cast<float*>(s_b + p.slots * slot_bytes);          // [N][uc]
-    float* s_scale = s_u + N * uc;                                              // [N]
-    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_scale + N);          // without its padding
+    float* s_scale = s_u + (LORA && p.u_smem ? N * uc : 0);                     // [N]
+    float* s_factor = s_scale + N;                                              // [N]
+    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_factor + N);         // without its padding
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(s_groups) +
-                                                 (p.rank ? sizeof(TileGroups) : 0));
+                                                 (LORA ? sizeof(TileGroups) : 0));
     volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + kBarriers);
     uint32_t* s_tmem = const_cast<uint32_t*>(s_abort) + 1;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, b_full0 = empty0 + 8 * kMaxStages,
@@ -332,6 +332,30 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     ++issued;
                     if (++s == p.stages) { s = 0; phase ^= 1; }
                 }
+                if constexpr (LORA && CG == 2) {
+                    if (!ok || !p.tensor) continue;
+                    if (tile == first) pdl_wait();
+                    // runs of blocks with one adapter: B_a in W's place, the parts of u in x's
+                    const TileGroups* g = tile_groups(p, tt);
+                    for (uint32_t b0 = 0, n; ok && b0 < N / kBlock; b0 += n) {
+                        const uint32_t a = g->block[b0];
+                        n = run_length(g, b0, N / kBlock);
+                        if (a >= kMixed) continue;
+                        for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                            if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
+                            const uint32_t dst = base + s * stage_bytes, bar = map_to(full0 + 8 * s, 0);
+                            constexpr uint32_t kHalf = kBlock / CG;  // rows of a block that a CTA holds
+                            if (rank == 0) mbar_expect(full0 + 8 * s, CG * (kStageW + n * kHalf * kSliceBytes));
+                            tma_2d<CG>(dst, &map_lora_b, 0, (int)(a * p.V) + v0, bar, keep);
+                            for (uint32_t i = 0; i < n; ++i)
+                                tma_2d<CG>(dst + kStageW + i * kHalf * kSliceBytes, &map_parts, 0,
+                                           (int)(line * p.part_stride + tt * N + b0 * kBlock + (rank * n + i) * kHalf), bar,
+                                           keep);
+                            ++issued;
+                            if (++s == p.stages) { s = 0; phase ^= 1; }
+                        }
+                    }
+                }
             }
         }
     } else if (warp == 1) {
@@ -339,29 +363,70 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
-                for (uint32_t k0 = 0; ok && k0 < p.slices; k0 += p.chunk, ++n) {
-                    const uint32_t acc = n & 1, acc_phase = (n >> 1) & 1, k1 = min(k0 + p.chunk, p.slices);
-                    if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase ^ 1, s_abort)) { ok = false; break; }
-                    fence_after();
-                    for (uint32_t k = k0; k < k1; ++k) {
-                        if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
-                        fence_after();
-                        const uint64_t a = matrix_desc(base + s * stage_bytes);
-                        const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
-#pragma unroll
-                        for (uint32_t i = 0; i < kSliceBytes / 32; ++i)  // 32 bytes of the contracted dimension each
-                            mma<FP8, CG>(tmem + acc * p.acc_cols, a + 2 * i, b + 2 * i, p.idesc, (k - k0) | i);
-                        mma_commit<CG>(empty0 + 8 * s);
-                        if (++s == p.stages) { s = 0; phase ^= 1; }
+                uint32_t in_chunk = 0;
+                bool open = false;  // an accumulator is being filled: number n
+                const auto next_stage = [&]() {
+                    mma_commit<CG>(empty0 + 8 * s);
+                    if (++s == p.stages) { s = 0; phase ^= 1; }
+                };
+                const auto close = [&]() {
+                    mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                    open = false;
+                    ++n;
+                };
+                const auto ready = [&]() {  // an accumulator and the next stage
+                    if (!open) {
+                        if (!mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort)) return false;
+                        open = true;
+                        in_chunk = 0;
                     }
-                    if (ok) mma_commit<CG>(acc_full0 + 8 * acc);
+                    if (!mbar_wait(full0 + 8 * s, phase, s_abort)) return false;
+                    fence_after();
+                    return true;
+                };
+                for (uint32_t k = 0; k < p.slices; ++k) {
+                    if (!ready()) { ok = false; break; }
+                    const uint64_t a = matrix_desc(base + s * stage_bytes);
+                    const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
+#pragma unroll
+                    for (uint32_t i = 0; i < kSliceBytes / 32; ++i)  // 32 bytes of the contracted dimension each
+                        mma<FP8, CG>(tmem + (n & 1) * p.acc_cols, a + 2 * i, b + 2 * i, p.idesc, in_chunk | i);
+                    next_stage();
+                    if (++in_chunk == p.chunk) close();
                 }
+                if constexpr (LORA && CG == 2) {
+                    if (ok && p.tensor) {
+                        if (tile == first) pdl_wait();
+                        const TileGroups* g = tile_groups(p, tile % p.tiles_t);
+                        if (p.apart && open) close();
+                        for (uint32_t b0 = 0, blocks; ok && b0 < N / kBlock; b0 += blocks) {
+                            blocks = run_length(g, b0, N / kBlock);
+                            if (g->block[b0] >= kMixed) continue;
+                            const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
+                            for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                                if (!ready()) { ok = false; break; }
+                                const uint64_t a = matrix_desc(base + s * stage_bytes);
+                                const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
+                                // 16 columns of the parts a step; B_a's start again with each part
+                                for (uint32_t i = 0; i < 4; ++i) {
+                                    const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
+                                                   j = column - part * p.b_cols;
+                                    if (part < 3 && j < uc)
+                                        mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i, idesc,
+                                                       p.apart ? (line | i) : 1u);
+                                }
+                                next_stage();
+                            }
+                        }
+                    }
+                }
+                if (ok && open) close();
             }
             mma_commit<CG>(drain);  // arrives once every product issued above has finished
         }
     } else if (warp == 2) {
         // Tiles of the adapters' B, in the order the epilogue takes them.
-        if (p.rank) {
+        if constexpr (LORA) {
             pdl_wait();
             uint64_t once;
             asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
@@ -370,7 +435,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
                 const uint32_t v0 = (tv * CG + rank) * kTileV;
-                const TileGroups* g = reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
+                const TileGroups* g = tile_groups(p, tt);
                 const uint32_t items = v0 < p.V ? g->items : 0u;
                 for (uint32_t k = 0; k < items; ++k) {
                     const uint32_t a = g->item[k];
@@ -428,23 +493,32 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         for (uint32_t tile = first; tile < p.tiles; tile += step) {
             const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t, t0 = tt * N;
             const uint32_t v0 = (tv * CG + rank) * kTileV, v = v0 + quad * 32 + lane;
-            if ((FP8 || p.rank) && tt != staged) {  // the rows' scales, u and groups
+            const uint32_t rows = min(N, p.T - t0);
+            if ((FP8 || LORA) && tt != staged) {  // the rows' scales or factors, groups and u
                 if (!meet()) break;
-                const uint32_t rows = min(N, p.T - t0);
-                if constexpr (FP8) {
-                    for (uint32_t i = et; i < N; i += kEpilogueWarps * 32)
-                        s_scale[i] = i < rows ? p.x_scale[t0 + i] : 0.f;
-                }
-                if (p.rank) {
-                    const float4* src = reinterpret_cast<const float4*>(p.u + (uint64_t)t0 * uc);
-                    for (uint32_t i = et; i < N * uc / 4; i += kEpilogueWarps * 32)
-                        reinterpret_cast<float4*>(s_u)[i] = i < rows * uc / 4 ? src[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-                    const uint4* words = reinterpret_cast<const uint4*>(p.groups + (size_t)tt * kGroupBytes);
+                if constexpr (LORA) {
+                    const uint4* words = reinterpret_cast<const uint4*>(tile_groups(p, tt));
                     for (uint32_t i = et; i < sizeof(TileGroups) / 16; i += kEpilogueWarps * 32)
                         reinterpret_cast<uint4*>(s_groups)[i] = words[i];
+                    if (p.u_smem && tile_groups(p, tt)->items) {
+                        const float4* src = reinterpret_cast<const float4*>(p.u + (uint64_t)t0 * uc);
+                        for (uint32_t i = et; i < rows * uc / 4; i += kEpilogueWarps * 32)
+                            reinterpret_cast<float4*>(s_u)[i] = src[i];
+                    }
+                }
+                for (uint32_t i = et; i < N; i += kEpilogueWarps * 32) {
+                    if (FP8) s_scale[i] = i < rows ? p.x_scale[t0 + i] : 0.f;
+                    if (LORA && p.tensor) s_factor[i] = i < rows ? p.factor[t0 + i] : 0.f;
                 }
                 if (!meet()) break;
                 staged = tt;
+            }
+            const uint32_t items = LORA ? s_groups->items : 0u;
+            // blocks whose adapters' part has an accumulator of its own
+            uint32_t apart = 0;
+            if constexpr (LORA && CG == 2) {
+                if (p.tensor && p.apart)
+                    apart = __ballot_sync(0xFFFFFFFFu, lane < N / kBlock && s_groups->block[lane < N / kBlock ? lane : 0] < kMixed);
             }
             const float sw = FP8 && v < p.V ? p.w_scale[v] : 1.f;
             uint32_t acc = n & 1;
@@ -481,16 +555,34 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 ++n;
             }
             const uint32_t columns = tmem + lanes + acc * p.acc_cols;
-            if (!p.rank) {
+            const uint32_t acc2 = n & 1;
+            if (apart) {
+                if (!mbar_wait_warp(acc_full0 + 8 * acc2, (n >> 1) & 1, s_abort)) break;
+                fence_after();
+                ++n;
+            }
+            if (!LORA || v0 < p.V) {
                 for (uint32_t c0 = share * 32; c0 < N; c0 += 128) {
+                    if (LORA && s_groups->block[c0 / kBlock] == kMixed) continue;
                     float y[32];
                     tmem_load32(columns + c0, y);
                     if constexpr (FP8) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
                     }
+                    if constexpr (LORA && CG == 2) {
+                        if (apart >> (c0 / kBlock) & 1) {
+#pragma unroll
+                            for (int h = 0; h < 32; h += 16) {
+                                float z[16];
+                                tmem_load16(tmem + lanes + acc2 * p.acc_cols + c0 + h, z);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c)
+                                    y[h + c] = fmaf(c0 + h + c < N ? s_factor[c0 + h + c] : 0.f, z[c], y[h + c]);
+                            }
+                        }
+                    }
                     if (v < p.V) {
-                        const uint32_t rows = min(N, p.T - t0);
                         OUT* o = out + (uint64_t)(t0 + c0) * p.out_stride + v;
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
@@ -499,7 +591,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                         }
                     }
                 }
-            } else if (v0 < p.V) {
+            }
+            if (LORA && items && v0 < p.V) {
                 if constexpr (PROMOTE) {  // an item's columns may have been written by another share
                     fence_before();
                     if (!meet()) break;
@@ -508,7 +601,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 // Item by item: the lane's row of B_a from its buffer, the item's rows of u (the
                 // same for every lane), eight rows at a time.
                 bool ok = true;
-                const uint32_t items = s_groups->items;
                 for (uint32_t k = 0; k < items; ++k) {
                     // Items go round the shares. Every warp passes every buffer's barriers, so that
                     // none falls behind by two phases.
@@ -542,7 +634,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                 }
 #pragma unroll
                                 for (int r = 0; r < 8; ++r) {
-                                    const ulonglong2* u = reinterpret_cast<const ulonglong2*>(s_u + c[r] * uc + j0);
+                                    const ulonglong2* u = reinterpret_cast<const ulonglong2*>(
+                                        (p.u_smem ? s_u : p.u + (uint64_t)t0 * uc) + c[r] * uc + j0);
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) {
                                         const ulonglong2 u2 = u[e];
@@ -569,6 +662,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 if (!ok) break;
             }
             release(acc);
+            if (apart) release(acc2);
         }
     }
     // Everything issued is finished before shared memory and TMEM go: in a normal run the
@@ -598,153 +692,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
     }
     if (threadIdx.x == 0 && *s_abort) flag(p.status, LP_ERR_TIMEOUT);
-}
-
-// ------------------------------------------------------------------ u = s_a sx (x A_a^T)
-
-struct ShrinkParams {
-    const void* x;
-    const float* x_scale;
-    const void* lora_a;            // [A][rank][H]
-    const float* adapter_scale;    // [A] or NULL
-    const int32_t* adapter_ids;    // [B]
-    const uint32_t* row_offsets;   // [B+1] or NULL
-    float* u;
-    unsigned char* groups;
-    uint32_t* status;
-    uint64_t x_stride;
-    uint32_t T, H, B, adapters, rank, u_cols;
-    uint32_t tile_t;
-};
-
-constexpr uint32_t kShrinkWarps = 8;
-
-__device__ __forceinline__ void load_x8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2(w[i], __nv_bfloat16());
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void load_x8(const __half* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2(w[i], __half());
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-__device__ __forceinline__ void load_x8(const __nv_fp8_e4m3* p, float (&v)[8]) {
-    const uint2 a = *reinterpret_cast<const uint2*>(p);
-    const uint32_t w[2] = {a.x, a.y};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((uint16_t)(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
-// The adapter of row t (negative: none); a bad id or a row of no request: adapter 0 and *bad.
-__device__ __forceinline__ int32_t adapter_of(const ShrinkParams& p, uint32_t t, bool* bad, uint32_t* code) {
-    const int b = request_of(p.row_offsets, p.B, t);
-    const int32_t a = b < 0 ? 0 : p.adapter_ids[b];
-    *bad = b < 0 || a >= (int32_t)p.adapters;
-    *code = b < 0 ? LP_ERR_OFFSETS : LP_ERR_ADAPTER;
-    return *bad ? 0 : a;
-}
-
-// The items of one tile of rows (a thread a row): rows ordered by the first row of their
-// adapter, then by their own place; each adapter's rows cut into items.
-__device__ void group_rows(const ShrinkParams& p, uint32_t tile) {
-    __shared__ int32_t id[kMaxTileT];
-    __shared__ uint32_t head[kMaxTileT];  // the first row with the same adapter
-    const uint32_t c = threadIdx.x, t0 = tile * p.tile_t, rows = min(p.tile_t, p.T - t0);
-    bool bad;
-    uint32_t code;
-    if (c < rows) id[c] = max(adapter_of(p, t0 + c, &bad, &code), -1);
-    __syncthreads();
-    if (c < rows) {
-        uint32_t h = kMaxTileT;  // rows without an adapter come last
-        if (id[c] >= 0)
-            for (h = 0; id[h] != id[c]; ++h) {}
-        head[c] = h;
-    }
-    __syncthreads();
-    // place of this row, its place among its adapter's, and whether it begins an item
-    uint32_t place = 0, among = 0;
-    if (c < rows) {
-        for (uint32_t i = 0; i < rows; ++i) {
-            place += head[i] < head[c] || (head[i] == head[c] && i < c);
-            among += head[i] == head[c] && i < c;
-        }
-    }
-    const bool begins = c < rows && among % kItemRows == 0;
-    __shared__ uint8_t begins_at[kMaxTileT];  // by place
-    begins_at[c] = 0;
-    __syncthreads();
-    if (begins) begins_at[place] = 1;
-    __syncthreads();
-    TileGroups* g = reinterpret_cast<TileGroups*>(p.groups + (size_t)tile * kGroupBytes);
-    if (c < rows) {
-        g->order[place] = (uint8_t)c;
-        if (begins) {
-            uint32_t item = 0, size = 1;
-            for (uint32_t i = 0; i < place; ++i) item += begins_at[i];
-            while (place + size < rows && !begins_at[place + size]) ++size;
-            g->item[item] = id[c] < 0 ? kNoAdapter : (uint32_t)id[c];
-            g->start[item] = (uint8_t)place;
-            g->size[item] = (uint8_t)size;
-            if (place + size == rows) g->items = item + 1;
-        }
-    }
-}
-
-// grid: T blocks, one a row, then one a tile of rows for its groups.
-template <typename X, typename A>
-__global__ void __launch_bounds__(kShrinkWarps * 32) k_shrink(ShrinkParams p) {
-    pdl_wait();
-    pdl_trigger();  // after the wait: the product kernel may read x, which is complete now
-    if (blockIdx.x >= p.T) {
-        group_rows(p, blockIdx.x - p.T);
-        return;
-    }
-    const uint32_t t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    bool bad;
-    uint32_t code;
-    const int32_t a = adapter_of(p, t, &bad, &code);
-    if (bad && threadIdx.x == 0) flag(p.status, code);
-    float* u = p.u + (uint64_t)t * p.u_cols;
-    if (a < 0) {
-        for (uint32_t j = threadIdx.x; j < p.u_cols; j += kShrinkWarps * 32) u[j] = 0.f;
-        return;
-    }
-    const X* x = static_cast<const X*>(p.x) + (uint64_t)t * p.x_stride;
-    float scale = p.adapter_scale ? p.adapter_scale[a] : 1.f;
-    if (p.x_scale) scale *= p.x_scale[t];
-    for (uint32_t j = warp; j < p.u_cols; j += kShrinkWarps) {
-        float sum = 0.f;
-        if (j < p.rank) {
-            const A* row = static_cast<const A*>(p.lora_a) + ((uint64_t)a * p.rank + j) * p.H;
-            for (uint32_t h = lane * 8; h < p.H; h += 256) {
-                float xv[8], av[8];
-                load_x8(x + h, xv);
-                load_x8(row + h, av);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) sum = fmaf(xv[i], av[i], sum);
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-            sum = bad ? __int_as_float(0x7fffffff) : sum * scale;
-        }
-        if (lane == 0) u[j] = sum;
-    }
 }
 
 // ------------------------------------------------------------------ host
@@ -790,34 +737,30 @@ bool encode(CUtensorMap* map, const void* ptr, uint32_t dtype, uint64_t rows, ui
 }
 
 struct ProjectLaunch {
-    CUtensorMap w, x, b;
+    CUtensorMap w, x, b, lora_b, parts;
     ProjectParams p;
     size_t smem;
     unsigned grid;
 };
 
-template <bool FP8, typename OUT, int CG, bool PROMOTE>
+template <bool FP8, typename OUT, int CG, bool LORA>
 lp_status launch_project(const ProjectLaunch& l, lp_stream_t stream) {
     static std::atomic<uint64_t> smem_set;
-    auto kernel = k_project<FP8, OUT, CG, PROMOTE>;
+    auto kernel = k_project<FP8, OUT, CG, !FP8 && sizeof(OUT) == 4, LORA>;
     if (!allow_smem(reinterpret_cast<const void*>(kernel), kSmemBudget, &smem_set)) return LP_ERR_CUDA;
-    return launch(kernel, dim3(l.grid), kThreads, l.smem, stream, CG, l.w, l.x, l.b, l.p);
+    return launch(kernel, dim3(l.grid), kThreads, l.smem, stream, CG, l.w, l.x, l.b, l.lora_b, l.parts, l.p);
 }
-
-template <bool FP8, int CG>
+template <bool FP8, int CG, bool LORA>
 lp_status launch_project(const ProjectLaunch& l, uint32_t out_dtype, lp_stream_t s) {
-    if (out_dtype == LP_F32) return launch_project<FP8, float, CG, !FP8>(l, s);
-    if (out_dtype == LP_BF16) return launch_project<FP8, __nv_bfloat16, CG, false>(l, s);
-    return launch_project<FP8, __half, CG, false>(l, s);
+    if (out_dtype == LP_F32) return launch_project<FP8, float, CG, LORA>(l, s);
+    if (out_dtype == LP_BF16) return launch_project<FP8, __nv_bfloat16, CG, LORA>(l, s);
+    return launch_project<FP8, __half, CG, LORA>(l, s);
 }
-
-lp_status launch_shrink(const ShrinkParams& p, uint32_t dtype, uint32_t lora_dtype, lp_stream_t s) {
-    const dim3 grid(p.T + (p.T + p.tile_t - 1) / p.tile_t);
-    const unsigned block = kShrinkWarps * 32;
-    if (dtype == LP_BF16) return launch(k_shrink<__nv_bfloat16, __nv_bfloat16>, grid, block, 0, s, 1, p);
-    if (dtype == LP_F16) return launch(k_shrink<__half, __half>, grid, block, 0, s, 1, p);
-    if (lora_dtype == LP_BF16) return launch(k_shrink<__nv_fp8_e4m3, __nv_bfloat16>, grid, block, 0, s, 1, p);
-    return launch(k_shrink<__nv_fp8_e4m3, __half>, grid, block, 0, s, 1, p);
+template <bool FP8>
+lp_status launch_project(const ProjectLaunch& l, uint32_t out_dtype, uint32_t cg, lp_stream_t s) {
+    if (cg == 2)
+        return l.p.rank ? launch_project<FP8, 2, true>(l, out_dtype, s) : launch_project<FP8, 2, false>(l, out_dtype, s);
+    return l.p.rank ? launch_project<FP8, 1, true>(l, out_dtype, s) : launch_project<FP8, 1, false>(l, out_dtype, s);
 }
 
 }  // namespace
@@ -865,37 +808,46 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.x_scale = x_scale;
     p.w_scale = weight_scale;
     p.lora_b = lora_b;
-    // the workspace: header, the groups of each tile of rows, u
-    const uint32_t tiles_256 = (T + kMaxTileT - 1) / kMaxTileT;
-    p.groups = ws + kHeaderBytes;
-    p.u = reinterpret_cast<float*>(ws + kHeaderBytes + (size_t)tiles_256 * kGroupBytes);
+    const AdapterSpace space(T, rank);
+    p.groups = ws + space.groups;
+    p.factor = reinterpret_cast<float*>(ws + space.factor);
+    p.u = reinterpret_cast<float*>(ws + space.u);
     p.out = out;
     p.out_stride = out_stride;
     p.T = T;
     p.V = V;
     p.rank = rank;
-    p.u_cols = (rank + 15) & ~15u;
-    p.b_cols = rank <= 16 ? 16 : rank <= 32 ? 32 : 64;
+    p.u_cols = rank_cols(rank);
+    p.b_cols = part_cols(rank);
     p.lora_f16 = lora_dtype == LP_F16;
     p.lora_tma = rank % 8 == 0 && (uint64_t)adapters * V <= 0x7FFFFFFFu;
     p.early = rank != 0;
     // Rows of x in even tiles of at most 256, a multiple of 16 (of 32 for a pair of CTAs). A
     // pair halves what each SM reads of x, which pays from 129 rows on.
     const uint32_t cg = T > 128 ? 2 : 1;
-    p.tiles_t = tiles_256;
+    p.tiles_t = (T + kMaxTileT - 1) / kMaxTileT;
     p.tile_t = ((T + p.tiles_t - 1) / p.tiles_t + 16 * cg - 1) / (16 * cg) * (16 * cg);
     const uint64_t tiles = (uint64_t)((V + cg * kTileV - 1) / (cg * kTileV)) * p.tiles_t;
     if (tiles > 0x7FFFFFFFu) return LP_ERR_SHAPE;
     p.tiles = (uint32_t)tiles;
     p.slices = (uint32_t)((H * e + kSliceBytes - 1) / kSliceBytes);
-    p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : p.slices;
+    // Blocks of rows with one adapter run on the tensor cores (pairs only: the tiles of fewer
+    // rows wait for memory, and the epilogue's arithmetic is hidden).
+    p.tensor = cg == 2 && p.lora_tma && rank != 0;
+    p.apart = fp8 || dtype == LP_F16 || out_dtype == LP_F32;
+    p.part_stride = (uint32_t)space.rows;
+    p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : 0xFFFFFFFFu;
     for (p.acc_cols = 32; p.acc_cols < p.tile_t; p.acc_cols *= 2) {}
     // instruction: f32 accumulator, K-major operands, M = 128 lanes a CTA, N = tile_t
     const uint32_t type = dtype == LP_BF16 ? 1u : 0u;  // kind::f16: 0 f16, 1 bf16; kind::f8f6f4: 0 e4m3
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((cg * kTileV >> 4) << 24);
+    const uint32_t lora_type = lora_dtype == LP_BF16 ? 1u : 0u;
+    p.lora_idesc = (1u << 4) | (lora_type << 7) | (lora_type << 10) | ((cg * kTileV >> 4) << 24);  // without N
     const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
     p.slots = rank ? kSlotsBytes / slot_bytes : 0;
-    const uint32_t rows_bytes = p.tile_t * (p.u_cols * 4 + 4) + p.slots * slot_bytes + (rank ? (uint32_t)sizeof(TileGroups) : 0);
+    // u of a tile in shared memory up to 24 KB, where it does not cost the ring a stage or two
+    p.u_smem = p.tile_t * p.u_cols * 4 <= 24 * 1024;
+    const uint32_t rows_bytes = p.tile_t * ((p.u_smem ? p.u_cols * 4 : 0) + 8) + p.slots * slot_bytes + (rank ? (uint32_t)sizeof(TileGroups) : 0);
     p.stages = (kSmemBudget - kControlBytes - rows_bytes) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     l.smem = kControlBytes + rows_bytes + p.stages * stage_bytes;
@@ -905,8 +857,11 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         return LP_ERR_CUDA;
     if (rank && p.lora_tma) {
         if (!encode(&l.b, lora_b, lora_dtype, (uint64_t)adapters * V, rank, rank, kTileV, p.b_cols)) return LP_ERR_CUDA;
-    } else {
-        l.b = l.w;  // not used
+    }
+    if (p.tensor) {
+        if (!encode(&l.lora_b, lora_b, lora_dtype, (uint64_t)adapters * V, rank, rank, kTileV, 64) ||
+            !encode(&l.parts, ws + space.parts, lora_dtype, part_rows(rank) * space.rows, 64, 64, kBlock / cg, 64))
+            return LP_ERR_CUDA;
     }
     if (rank) {
         ShrinkParams q = {};
@@ -917,9 +872,13 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         q.adapter_ids = adapter_ids;
         q.row_offsets = row_offsets;
         q.u = const_cast<float*>(p.u);
-        q.groups = const_cast<unsigned char*>(p.groups);
-        q.u_cols = p.u_cols;
+        q.groups = ws + space.groups;
+        q.factor = reinterpret_cast<float*>(ws + space.factor);
+        q.parts = reinterpret_cast<uint16_t*>(ws + space.parts);
         q.tile_t = p.tile_t;
+        q.tensor = p.tensor;
+        q.part_stride = p.part_stride;
+        q.lora_f16 = p.lora_f16;
         q.status = p.status;
         q.x_stride = x_stride;
         q.T = T;
@@ -932,6 +891,5 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     }
     const uint32_t units = (uint32_t)sms / cg;  // CTAs, or pairs
     l.grid = cg * (p.tiles < units ? p.tiles : units);
-    if (cg == 2) return fp8 ? launch_project<true, 2>(l, out_dtype, stream) : launch_project<false, 2>(l, out_dtype, stream);
-    return fp8 ? launch_project<true, 1>(l, out_dtype, stream) : launch_project<false, 1>(l, out_dtype, stream);
+    return fp8 ? launch_project<true>(l, out_dtype, cg, stream) : launch_project<false>(l, out_dtype, cg, stream);
 }

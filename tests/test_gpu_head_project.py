@@ -218,3 +218,58 @@ def test_chain_on_one_stream():
         assert torch.equal(two, lp.process_logits(lp.project(z, w, workspace=ws), workspace=ws))
         assert (two - want).abs().max() < 0.5
     assert lp.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,lora_dtype", [(BF16, BF16), (F16, F16), (E4M3, BF16), (E4M3, F16)])
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 40, 64])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_long_requests(dtype, lora_dtype, rank, out_dtype):
+    # whole blocks of 32 rows with one adapter, blocks of several, rows without one; two tiles
+    off = [0, 3, 130, 200, 232, 296, 330]
+    c = Case(330, 272, 300, dtype, A=3, rank=rank, ids=[0, 2, -1, 1, 1, 0], off=off, seed=14, lora_dtype=lora_dtype)
+    c.check(c.run(out_dtype))
+
+
+@pytest.mark.parametrize("scale", [1e-18, 1e18])
+def test_sizes_of_u_far_from_one(scale):
+    # float16 adapters of values whose u leaves float16's range, through adapter_scale
+    off = [0, 100, 230]
+    c = Case(230, 256, 200, F16, A=2, rank=16, ids=[0, 1], off=off, seed=15)
+    factor = torch.full((2,), scale)
+    base = Case(230, 256, 200, F16, seed=15)
+    base.x, base.w = c.x, c.w
+    zero = base.run()
+    out = c.run(adapter_scale=factor.cuda()).double().cpu()
+    xd = c.x.double()
+    for b in range(2):
+        r = slice(off[b], off[b + 1])
+        u = xd[r] @ c.la[b].double().t()
+        part = u @ c.lb[b].double().t() * scale
+        mag = (xd[r].abs() @ c.la[b].double().abs().t()) @ c.lb[b].double().abs().t() * scale
+        ref = zero.double().cpu()[r] + part
+        assert ((out[r] - ref).abs() <= (mag + zero.double().cpu()[r].abs()) * 64 * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("T,off", [(40, None), (256, None), (200, [0, 64, 130, 200])])
+def test_infinities_of_one_adapter_stay_with_its_rows(T, off):
+    B = T if off is None else len(off) - 1
+    c = Case(T, 128, 140, BF16, A=2, rank=16, ids=[b % 2 for b in range(B)], off=off, seed=16)
+    lb = c.lb.clone()
+    lb[1, 7, 3] = float("inf")
+    lb[1, 9, 0] = float("nan")
+    out = c.run(lora_b=lb.cuda())
+    mine = torch.tensor([b for b in range(B) for _ in range(1 if off is None else off[b + 1] - off[b])]) % 2 == 1
+    assert torch.isfinite(out.cpu()[~mine]).all()
+    assert not torch.isfinite(out.cpu()[mine][:, [7, 9]]).any()
+    cols = [v for v in range(140) if v not in (7, 9)]
+    assert torch.isfinite(out.cpu()[mine][:, cols]).all()
+
+
+def test_many_tiles_of_mixed_requests():
+    off = [0]
+    g = torch.Generator().manual_seed(5)
+    while off[-1] < 1500:
+        off.append(off[-1] + int(torch.randint(1, 120, (1,), generator=g)))
+    c = Case(off[-1], 128, 700, BF16, A=6, rank=32, off=off, seed=17)
+    c.check(c.run())
+    c.check(c.run(BF16))
