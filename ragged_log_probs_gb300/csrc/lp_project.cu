@@ -31,7 +31,10 @@ constexpr uint32_t kFirstEpilogueWarp = 4;
 constexpr uint32_t kThreads = (kFirstEpilogueWarp + kEpilogueWarps) * 32;
 constexpr uint32_t kSmemBudget = 227 * 1024;
 constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the alignment of the ring
-constexpr uint32_t kPromoteSlices = 4;            // slices summed in the tensor core before an f32 addition
+#ifndef LP_PROMOTE_SLICES
+#define LP_PROMOTE_SLICES 8
+#endif
+constexpr uint32_t kPromoteSlices = LP_PROMOTE_SLICES;            // slices summed in the tensor core before an f32 addition
 
 struct ProjectParams {
     const float* x_scale;
@@ -256,8 +259,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     unsigned char* s_b = ring + p.stages * stage_bytes;                         // [slots][128][b_cols]
     float* s_u = reinterpret_cast<float*>(s_b + p.slots * slot_bytes);          // [N][uc]
     float* s_scale = s_u + (LORA && p.u_smem ? N * uc : 0);                     // [N]
-    float* s_factor = s_scale + N;                                              // [N]
-    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_factor + N);         // without its padding
+    float* s_factor = s_scale + (FP8 ? N : 0);                                  // [N]
+    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_factor + (LORA && p.tensor ? N : 0));
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(s_groups) +
                                                  (LORA ? sizeof(TileGroups) : 0));
     volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + kBarriers);
@@ -363,48 +366,40 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
-                uint32_t in_chunk = 0;
-                bool open = false;  // an accumulator is being filled: number n
-                const auto next_stage = [&]() {
-                    mma_commit<CG>(empty0 + 8 * s);
-                    if (++s == p.stages) { s = 0; phase ^= 1; }
-                };
-                const auto close = [&]() {
-                    mma_commit<CG>(acc_full0 + 8 * (n & 1));
-                    open = false;
-                    ++n;
-                };
-                const auto ready = [&]() {  // an accumulator and the next stage
-                    if (!open) {
-                        if (!mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort)) return false;
-                        open = true;
-                        in_chunk = 0;
-                    }
-                    if (!mbar_wait(full0 + 8 * s, phase, s_abort)) return false;
+                for (uint32_t k0 = 0; ok && k0 < p.slices; k0 += p.chunk) {
+                    const uint32_t acc = n & 1, k1 = min(p.slices - k0, p.chunk) + k0;
+                    if (!mbar_wait(acc_empty0 + 8 * acc, ((n >> 1) & 1) ^ 1, s_abort)) { ok = false; break; }
                     fence_after();
-                    return true;
-                };
-                for (uint32_t k = 0; k < p.slices; ++k) {
-                    if (!ready()) { ok = false; break; }
-                    const uint64_t a = matrix_desc(base + s * stage_bytes);
-                    const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
+                    for (uint32_t k = k0; k < k1; ++k) {
+                        if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+                        fence_after();
+                        const uint64_t a = matrix_desc(base + s * stage_bytes);
+                        const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
 #pragma unroll
-                    for (uint32_t i = 0; i < kSliceBytes / 32; ++i)  // 32 bytes of the contracted dimension each
-                        mma<FP8, CG>(tmem + (n & 1) * p.acc_cols, a + 2 * i, b + 2 * i, p.idesc, in_chunk | i);
-                    next_stage();
-                    if (++in_chunk == p.chunk) close();
+                        for (uint32_t i = 0; i < kSliceBytes / 32; ++i)  // 32 bytes of the contracted dimension each
+                            mma<FP8, CG>(tmem + acc * p.acc_cols, a + 2 * i, b + 2 * i, p.idesc, (k - k0) | i);
+                        mma_commit<CG>(empty0 + 8 * s);
+                        if (++s == p.stages) { s = 0; phase ^= 1; }
+                    }
+                    if (!ok) break;
+                    if (LORA && CG == 2 && p.tensor && !p.apart) break;  // the adapters' part continues it
+                    mma_commit<CG>(acc_full0 + 8 * acc);
+                    ++n;
                 }
                 if constexpr (LORA && CG == 2) {
                     if (ok && p.tensor) {
                         if (tile == first) pdl_wait();
                         const TileGroups* g = tile_groups(p, tile % p.tiles_t);
-                        if (p.apart && open) close();
+                        bool open = !p.apart;
                         for (uint32_t b0 = 0, blocks; ok && b0 < N / kBlock; b0 += blocks) {
                             blocks = run_length(g, b0, N / kBlock);
                             if (g->block[b0] >= kMixed) continue;
                             const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
                             for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
-                                if (!ready()) { ok = false; break; }
+                                if (!open && !mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort)) ok = false;
+                                open = true;
+                                if (!ok || !mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+                                fence_after();
                                 const uint64_t a = matrix_desc(base + s * stage_bytes);
                                 const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
                                 // 16 columns of the parts a step; B_a's start again with each part
@@ -415,12 +410,16 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                         mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i, idesc,
                                                        p.apart ? (line | i) : 1u);
                                 }
-                                next_stage();
+                                mma_commit<CG>(empty0 + 8 * s);
+                                if (++s == p.stages) { s = 0; phase ^= 1; }
                             }
+                        }
+                        if (ok && open) {
+                            mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                            ++n;
                         }
                     }
                 }
-                if (ok && open) close();
             }
             mma_commit<CG>(drain);  // arrives once every product issued above has finished
         }
@@ -526,7 +525,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             if constexpr (PROMOTE) {
                 float sum[kMaxTileT / 128][32];
                 bool ok = true;
-                for (uint32_t k0 = 0; k0 < p.slices; k0 += p.chunk, ++n) {
+                for (uint32_t k0 = 0; k0 < p.slices; k0 += p.chunk, ++n) {  // (chunk <= slices)
                     acc = n & 1;
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) { ok = false; break; }
                     fence_after();
@@ -836,21 +835,30 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.tensor = cg == 2 && p.lora_tma && rank != 0;
     p.apart = fp8 || dtype == LP_F16 || out_dtype == LP_F32;
     p.part_stride = (uint32_t)space.rows;
-    p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : 0xFFFFFFFFu;
+    p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : p.slices;
     for (p.acc_cols = 32; p.acc_cols < p.tile_t; p.acc_cols *= 2) {}
     // instruction: f32 accumulator, K-major operands, M = 128 lanes a CTA, N = tile_t
     const uint32_t type = dtype == LP_BF16 ? 1u : 0u;  // kind::f16: 0 f16, 1 bf16; kind::f8f6f4: 0 e4m3
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((cg * kTileV >> 4) << 24);
     const uint32_t lora_type = lora_dtype == LP_BF16 ? 1u : 0u;
     p.lora_idesc = (1u << 4) | (lora_type << 7) | (lora_type << 10) | ((cg * kTileV >> 4) << 24);  // without N
+    // Shared memory: the ring's stages come first (at 256 rows, six stages instead of seven cost
+    // 15 %), then the adapters' buffers, and a tile's u where it fits into what is left (24 KB
+    // are set aside for it in single CTAs, which have stages to spare).
     const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
-    p.slots = rank ? kSlotsBytes / slot_bytes : 0;
-    // u of a tile in shared memory up to 24 KB, where it does not cost the ring a stage or two
-    p.u_smem = p.tile_t * p.u_cols * 4 <= 24 * 1024;
-    const uint32_t rows_bytes = p.tile_t * ((p.u_smem ? p.u_cols * 4 : 0) + 8) + p.slots * slot_bytes + (rank ? (uint32_t)sizeof(TileGroups) : 0);
-    p.stages = (kSmemBudget - kControlBytes - rows_bytes) / stage_bytes;
+    const uint32_t u_bytes = p.tile_t * p.u_cols * 4;
+    const uint32_t fixed = kControlBytes + (fp8 ? p.tile_t * 4 : 0) +
+                           (rank ? (uint32_t)sizeof(TileGroups) + (p.tensor ? p.tile_t * 4 : 0) : 0);
+    uint32_t set_aside = rank ? 2 * slot_bytes : 0;
+    if (rank && cg == 1) set_aside = kSlotsBytes + (u_bytes <= 24 * 1024 ? u_bytes : 0);
+    p.stages = (kSmemBudget - fixed - set_aside) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    l.smem = kControlBytes + rows_bytes + p.stages * stage_bytes;
+    uint32_t left = kSmemBudget - fixed - p.stages * stage_bytes;
+    p.u_smem = rank && left >= u_bytes + 2 * slot_bytes;
+    if (p.u_smem) left -= u_bytes;
+    p.slots = rank ? left / slot_bytes : 0;
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    l.smem = fixed + p.stages * stage_bytes + p.slots * slot_bytes + (p.u_smem ? u_bytes : 0);
     const uint32_t slice_cols = kSliceBytes / (uint32_t)e;
     if (!encode(&l.w, weight, dtype, V, H, weight_stride, kTileV, slice_cols) ||
         !encode(&l.x, x, dtype, T, H, x_stride, p.tile_t / cg, slice_cols))
