@@ -26,9 +26,12 @@ constexpr uint32_t kStageW = kTileV * kSliceBytes;
 constexpr uint32_t kMaxStages = 12;
 constexpr uint32_t kMaxSlots = 8;                 // buffers for tiles of the adapters' B
 constexpr uint32_t kSlotsBytes = 32 * 1024;
-constexpr uint32_t kEpilogueWarps = 16;
-constexpr uint32_t kFirstEpilogueWarp = 4;
-constexpr uint32_t kThreads = (kFirstEpilogueWarp + kEpilogueWarps) * 32;
+constexpr uint32_t kEpilogueWarps = 12;
+constexpr uint32_t kShares = kEpilogueWarps / 4;     // epilogue warps of one quadrant of lanes
+// Warps: the epilogue's (warp % 4 is the quadrant of lanes a warp may read), then one that
+// issues copies, one that issues products, one that fills the adapters' buffers.
+constexpr uint32_t kCopyWarp = kEpilogueWarps, kMmaWarp = kEpilogueWarps + 1, kBufferWarp = kEpilogueWarps + 2;
+constexpr uint32_t kThreads = (kEpilogueWarps + 3) * 32;
 constexpr uint32_t kSmemBudget = 227 * 1024;
 constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the alignment of the ring
 #ifndef LP_PROMOTE_SLICES
@@ -293,7 +296,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         if constexpr (CG == 2) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
                          "r"(2 * p.acc_cols) : "memory");
@@ -312,7 +315,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
 
     uint32_t issued = 0;    // stages the producer has started copies into
     uint32_t b_issued = 0;  // B buffers the loader has started copies into
-    if (warp == 0) {
+    if (warp == kCopyWarp) {
         if (lane == 0) {
             if (!p.early) pdl_wait();
             uint64_t once, keep;  // W is read once per row of tiles, x by every tile
@@ -361,7 +364,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 }
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == kMmaWarp) {
         if (lane == 0 && rank == 0) {
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
@@ -423,7 +426,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             }
             mma_commit<CG>(drain);  // arrives once every product issued above has finished
         }
-    } else if (warp == 2) {
+    } else if (warp == kBufferWarp) {
         // Tiles of the adapters' B, in the order the epilogue takes them.
         if constexpr (LORA) {
             pdl_wait();
@@ -463,11 +466,11 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 }
             }
         }
-    } else if (warp >= kFirstEpilogueWarp) {
+    } else {
         // The quadrant of lanes this warp may read, and its share of the columns: the blocks
-        // of 32 whose number is `share` modulo 4. A warp only ever touches its own.
-        const uint32_t quad = warp & 3, share = (warp - kFirstEpilogueWarp) >> 2;
-        const uint32_t et = threadIdx.x - kFirstEpilogueWarp * 32;
+        // of 32 whose number is `share` modulo kShares.
+        const uint32_t quad = warp & 3, share = warp >> 2;
+        const uint32_t et = threadIdx.x;
         OUT* out = static_cast<OUT*>(p.out);
         uint32_t n = 0, staged = 0xFFFFFFFFu, staging_phase = 0, b_slot = 0, b_phase = 0;
         const uint32_t acc_empty_at = CG == 2 ? map_to(acc_empty0, 0) : acc_empty0;
@@ -523,7 +526,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t acc = n & 1;
             const uint32_t lanes = (quad * 32) << 16;
             if constexpr (PROMOTE) {
-                float sum[kMaxTileT / 128][32];
+                float sum[(kMaxTileT / 32 + kShares - 1) / kShares][32];
                 bool ok = true;
                 for (uint32_t k0 = 0; k0 < p.slices; k0 += p.chunk, ++n) {  // (chunk <= slices)
                     acc = n & 1;
@@ -531,8 +534,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     fence_after();
                     const bool last = k0 + p.chunk >= p.slices;
 #pragma unroll
-                    for (uint32_t i = 0; i < kMaxTileT / 128; ++i) {
-                        const uint32_t c0 = share * 32 + 128 * i;
+                    for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
+                        const uint32_t c0 = (share + kShares * i) * 32;
                         if (c0 >= N) continue;
                         const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
 #pragma unroll
@@ -561,7 +564,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 ++n;
             }
             if (!LORA || v0 < p.V) {
-                for (uint32_t c0 = share * 32; c0 < N; c0 += 128) {
+                for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
                     if (LORA && s_groups->block[c0 / kBlock] == kMixed) continue;
                     float y[32];
                     tmem_load32(columns + c0, y);
@@ -606,7 +609,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     const uint32_t a = s_groups->item[k];
                     if (a != kNoAdapter && !mbar_wait_warp(b_full0 + 8 * b_slot, b_phase, s_abort)) { ok = false; break; }
                     const unsigned char* b_tile = s_b + b_slot * slot_bytes;
-                    const uint32_t begin = s_groups->start[k], end = (k & 3) == share ? begin + s_groups->size[k] : 0;
+                    const uint32_t begin = s_groups->start[k], end = k % kShares == share ? begin + s_groups->size[k] : 0;
                     for (uint32_t i = begin; i < end; i += 8) {
                         uint32_t c[8];
                         float y[8];
@@ -667,7 +670,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     // Everything issued is finished before shared memory and TMEM go: in a normal run the
     // epilogue has seen every tile; after an abort the copies and products in flight end by
     // themselves, and these waits are bounded like the others.
-    if (warp == 1 && lane == 0) {  // (in both CTAs of a pair: the commit arrives in both)
+    if (warp == kMmaWarp && lane == 0) {  // (in both CTAs of a pair: the commit arrives in both)
         uint32_t dummy = 0;
         (void)mbar_wait(drain, 0, &dummy);
     }
@@ -684,7 +687,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     __syncthreads();
     if constexpr (CG == 2) cluster_sync();  // neither CTA leaves while the other may write to it
     fence_after();
-    if (warp == 1) {
+    if (warp == kMmaWarp) {
         if constexpr (CG == 2)
             asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
         else
