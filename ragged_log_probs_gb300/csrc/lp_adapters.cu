@@ -13,10 +13,9 @@ namespace {
 
 using namespace lph;
 
-constexpr uint32_t kThreads = 256;
+constexpr uint32_t kThreads = 512;
 constexpr uint32_t kWarps = kThreads / 32;
 constexpr uint32_t kBlockRows = 16;
-static_assert(kThreads == kMaxTileT, "a thread a row of a tile");
 
 __device__ __forceinline__ void load_x8(const __nv_bfloat16* p, float (&v)[8]) {
     const uint4 a = *reinterpret_cast<const uint4*>(p);
@@ -60,17 +59,19 @@ __device__ __forceinline__ int32_t adapter_of(const ShrinkParams& p, uint32_t t,
     return *bad ? 0 : max(a, -1);
 }
 
-// The lists of one tile of rows; a thread a row.
+// The lists of one tile of rows; a thread a row (the block's first kMaxTileT).
 __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     __shared__ int32_t id[kMaxTileT];
     __shared__ uint32_t key[kMaxTileT];       // of a listed row: the first listed row with its adapter
     __shared__ uint8_t begins_at[kMaxTileT];  // by place: an item begins here
     constexpr uint32_t kUnlisted = kMaxTileT + 1;
+    if (threadIdx.x >= kMaxTileT) return;
+    const auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kMaxTileT) : "memory"); };
     const uint32_t c = threadIdx.x, t0 = tile * p.tile_t, rows = min(p.tile_t, p.T - t0);
     bool bad;
     uint32_t code;
     id[c] = c < rows ? adapter_of(p, t0 + c, &bad, &code) : -2;
-    __syncthreads();
+    sync();
     TileGroups* g = reinterpret_cast<TileGroups*>(p.groups + (size_t)tile * kGroupBytes);
     // the warp's rows are one block: rows past the last count as its first row's
     const int32_t first = __shfl_sync(0xFFFFFFFFu, id[c], 0);
@@ -79,16 +80,16 @@ __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     if (c % kBlock == 0) g->block[c / kBlock] = listed ? kMixed : first < 0 ? kNoAdapter : (uint32_t)first;
     uint32_t k = kUnlisted;
     key[c] = listed && c < rows ? 0 : kUnlisted;
-    __syncthreads();
+    sync();
     if (key[c] != kUnlisted) {
         k = kMaxTileT;  // rows without an adapter come last
         if (id[c] >= 0)
             for (k = 0; id[k] != id[c] || key[k] == kUnlisted; ++k) {}
     }
-    __syncthreads();
+    sync();
     key[c] = k;
     begins_at[c] = 0;
-    __syncthreads();
+    sync();
     // place of this row in the order by (key, own place)
     uint32_t place = 0, among = 0, total = 0;
     for (uint32_t i = 0; i < rows; ++i) {
@@ -99,7 +100,7 @@ __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     }
     const bool begins = k != kUnlisted && among % kItemRows == 0;
     if (begins) begins_at[place] = 1;
-    __syncthreads();
+    sync();
     if (k != kUnlisted) g->order[place] = (uint8_t)c;
     if (begins) {
         uint32_t item = 0, size = 1;
@@ -165,7 +166,7 @@ __device__ __forceinline__ float row_scale(const ShrinkParams& p, uint32_t t, in
 
 // grid: T blocks, one a row, then one a tile for its lists.
 template <typename X, typename A>
-__global__ void __launch_bounds__(kThreads) k_shrink_row(ShrinkParams p) {
+__global__ void __launch_bounds__(1024) k_shrink_row(ShrinkParams p) {
     __shared__ float s_u[64];
     pdl_wait();
     pdl_trigger();  // after the wait: the product kernel may read x, which is complete now
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(kThreads) k_shrink_row(ShrinkParams p) {
         list_tile(p, blockIdx.x - p.T);
         return;
     }
+    const uint32_t warps = blockDim.x >> 5;
     const uint32_t t = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool bad;
     uint32_t code;
@@ -180,10 +182,11 @@ __global__ void __launch_bounds__(kThreads) k_shrink_row(ShrinkParams p) {
     if (bad && threadIdx.x == 0) flag(p.status, code);
     const X* x = static_cast<const X*>(p.x) + (uint64_t)t * p.x_stride;
     const uint32_t cols = rank_cols(p.rank);
-    for (uint32_t j = warp; j < cols; j += kWarps) {
+    for (uint32_t j = warp; j < cols; j += warps) {
         float sum = 0.f;
         if (j < p.rank && a >= 0) {
             const A* row = static_cast<const A*>(p.lora_a) + ((uint64_t)a * p.rank + j) * p.H;
+#pragma unroll 4
             for (uint32_t h = lane * 8; h < p.H; h += 256) {
                 float xv[8], av[8];
                 load_x8(x + h, xv);
@@ -225,7 +228,7 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// grid: tiles x ceil(tile_t / 16) blocks of 16 rows, then one a tile for its lists. The eight
+// grid: tiles x ceil(tile_t / 16) blocks of 16 rows, then one a tile for its lists. The 16
 // warps split the contraction; their sums are added in the order of the warps.
 template <typename X, typename A>
 __global__ void __launch_bounds__(kThreads) k_shrink_block(ShrinkParams p) {
@@ -262,21 +265,30 @@ __global__ void __launch_bounds__(kThreads) k_shrink_block(ShrinkParams p) {
         const A* la = static_cast<const A*>(p.lora_a) + (uint64_t)a * p.rank * p.H;
         // 32 terms a step: this thread's are the 8 from h on, the first 4 in one product, the
         // others in the next (their order is the same in both factors)
-        for (uint32_t h = warp * 32 + q * 8; h - q * 8 < p.H; h += kWarps * 32) {
-            const bool in = h < p.H;
-            uint4 wa = make_uint4(0, 0, 0, 0), wb = wa;
-            if (in) {
-                wa = load_words<A>(xa + h);
-                wb = load_words<A>(xb + h);
-            }
+        uint4 wa, wb, b[8], na, nb, next[8];
+        const auto fetch = [&](uint32_t h, uint4& va, uint4& vb, uint4 (&vn)[8]) {
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            va = h < p.H ? load_words<A>(xa + h) : zero;
+            vb = h < p.H ? load_words<A>(xb + h) : zero;
+#pragma unroll
+            for (uint32_t n = 0; n < 8; ++n)
+                vn[n] = h < p.H && n * 8 + g < p.rank
+                            ? *reinterpret_cast<const uint4*>(la + (uint64_t)(n * 8 + g) * p.H + h) : zero;
+        };
+        uint32_t h = warp * 32 + q * 8;
+        fetch(h, wa, wb, b);
+        for (; h - q * 8 < p.H; h += kWarps * 32) {
+            fetch(h + kWarps * 32, na, nb, next);
 #pragma unroll
             for (uint32_t n = 0; n < 8; ++n) {
                 if (n * 8 >= p.rank) break;
-                uint4 b = make_uint4(0, 0, 0, 0);
-                if (in && n * 8 + g < p.rank) b = *reinterpret_cast<const uint4*>(la + (uint64_t)(n * 8 + g) * p.H + h);
-                mma16(sum[n], wa.x, wb.x, wa.y, wb.y, b.x, b.y, A());
-                mma16(sum[n], wa.z, wb.z, wa.w, wb.w, b.z, b.w, A());
+                mma16(sum[n], wa.x, wb.x, wa.y, wb.y, b[n].x, b[n].y, A());
+                mma16(sum[n], wa.z, wb.z, wa.w, wb.w, b[n].z, b[n].w, A());
             }
+            wa = na;
+            wb = nb;
+#pragma unroll
+            for (uint32_t n = 0; n < 8; ++n) b[n] = next[n];
         }
         float* mine = s_sum + warp * kBlockRows * 64;
 #pragma unroll
@@ -313,10 +325,17 @@ template <typename X, typename A>
 lp_status launch_shrink(const ShrinkParams& p, lp_stream_t s) {
     const uint32_t tiles = (p.T + p.tile_t - 1) / p.tile_t;
     // Blocks of 16 rows from 4 rows a request on.
-    if (p.T / p.B >= 4)
+    if (p.T / p.B >= 4) {
+        static std::atomic<uint64_t> smem_set;
+        if (!allow_smem(reinterpret_cast<const void*>(k_shrink_block<X, A>), kWarps * kBlockRows * 64 * sizeof(float),
+                        &smem_set))
+            return LP_ERR_CUDA;
         return launch(k_shrink_block<X, A>, dim3(tiles * (p.tile_t / kBlockRows) + tiles), kThreads,
                       kWarps * kBlockRows * 64 * sizeof(float), s, 1, p);
-    return launch(k_shrink_row<X, A>, dim3(p.T + tiles), kThreads, 0, s, 1, p);
+    }
+    // a warp a dot product, up to 16; the lists take kMaxTileT threads
+    const uint32_t warps = rank_cols(p.rank) < 16 ? 16 : rank_cols(p.rank) > 32 ? 32 : rank_cols(p.rank);
+    return launch(k_shrink_row<X, A>, dim3(p.T + tiles), warps * 32, 0, s, 1, p);
 }
 
 }  // namespace

@@ -24,10 +24,10 @@ constexpr uint32_t kTileV = 128;                  // vocabulary rows of a CTA's 
 constexpr uint32_t kSliceBytes = 128;             // bytes of the contracted dimension per stage
 constexpr uint32_t kStageW = kTileV * kSliceBytes;
 constexpr uint32_t kMaxStages = 12;
-constexpr uint32_t kMaxSlots = 8;                 // buffers for tiles of the adapters' B
-constexpr uint32_t kSlotsBytes = 32 * 1024;
 constexpr uint32_t kEpilogueWarps = 12;
-constexpr uint32_t kShares = kEpilogueWarps / 4;     // epilogue warps of one quadrant of lanes
+constexpr uint32_t kShares = kEpilogueWarps / 4;  // epilogue warps of one quadrant of lanes
+constexpr uint32_t kMaxDepth = 3;                 // buffers a share has for tiles of the adapters' B
+constexpr uint32_t kMaxSlots = kShares * kMaxDepth;
 // Warps: the epilogue's (warp % 4 is the quadrant of lanes a warp may read), then one that
 // issues copies, one that issues products, one that fills the adapters' buffers.
 constexpr uint32_t kCopyWarp = kEpilogueWarps, kMmaWarp = kEpilogueWarps + 1, kBufferWarp = kEpilogueWarps + 2;
@@ -52,7 +52,7 @@ struct ProjectParams {
     uint32_t T, V, rank;
     uint32_t u_cols;               // rank rounded up to 16
     uint32_t b_cols;               // columns of a B buffer: 16, 32 or 64
-    uint32_t slots;                // B buffers
+    uint32_t depth;                // B buffers of a share
     uint32_t u_smem;               // a tile's u is staged in shared memory (else read from global)
     uint32_t part_stride;          // rows of u's parts
     uint32_t tile_t;               // N
@@ -193,6 +193,13 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15};"
+        ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+          "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(addr) : "memory");
+}
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -234,6 +241,11 @@ __device__ __forceinline__ uint32_t b_offset(uint32_t row, uint32_t piece, uint3
     return off ^ ((off >> 3) & (cols * 2 - 16));
 }
 
+// Where the chunk that begins at slice k0 ends. A tile's first is twice as long: the epilogue
+// is still storing the tile before, from the other accumulator.
+__device__ __forceinline__ uint32_t chunk_end(const ProjectParams& p, uint32_t k0) {
+    return k0 + min(p.slices - k0, k0 ? p.chunk : 2 * p.chunk);
+}
 // How many blocks from b0 on have the same entry (the adapter of a run), of `blocks`.
 __device__ __forceinline__ uint32_t run_length(const TileGroups* g, uint32_t b0, uint32_t blocks) {
     uint32_t n = 1;
@@ -259,8 +271,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     unsigned char* ring = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t N = p.tile_t, stage_bytes = kStageW + N / CG * kSliceBytes;
     const uint32_t uc = p.u_cols, slot_bytes = kTileV * p.b_cols * 2;
-    unsigned char* s_b = ring + p.stages * stage_bytes;                         // [slots][128][b_cols]
-    float* s_u = reinterpret_cast<float*>(s_b + p.slots * slot_bytes);          // [N][uc]
+    unsigned char* s_b = ring + p.stages * stage_bytes;                         // [shares][depth][128][b_cols]
+    float* s_u = reinterpret_cast<float*>(s_b + kShares * p.depth * slot_bytes);  // [N][uc]
     float* s_scale = s_u + (LORA && p.u_smem ? N * uc : 0);                     // [N]
     float* s_factor = s_scale + (FP8 ? N : 0);                                  // [N]
     TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_factor + (LORA && p.tensor ? N : 0));
@@ -282,9 +294,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             mbar_init(full0 + 8 * s, 1);
             mbar_init(empty0 + 8 * s, 1);
         }
-        for (uint32_t i = 0; i < p.slots; ++i) {
+        for (uint32_t i = 0; LORA && i < kShares * p.depth; ++i) {
             mbar_init(b_full0 + 8 * i, p.lora_tma ? 1 : 32);
-            mbar_init(b_empty0 + 8 * i, kEpilogueWarps);
+            mbar_init(b_empty0 + 8 * i, 4);  // the share's warps
         }
         for (uint32_t i = 0; i < 2; ++i) {
             mbar_init(acc_full0 + 8 * i, 1);
@@ -314,7 +326,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     const uint32_t tmem = *s_tmem;
 
     uint32_t issued = 0;    // stages the producer has started copies into
-    uint32_t b_issued = 0;  // B buffers the loader has started copies into
     if (warp == kCopyWarp) {
         if (lane == 0) {
             if (!p.early) pdl_wait();
@@ -369,8 +380,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
-                for (uint32_t k0 = 0; ok && k0 < p.slices; k0 += p.chunk) {
-                    const uint32_t acc = n & 1, k1 = min(p.slices - k0, p.chunk) + k0;
+                for (uint32_t k0 = 0, k1; ok && k0 < p.slices; k0 = k1) {
+                    const uint32_t acc = n & 1;
+                    k1 = chunk_end(p, k0);
                     if (!mbar_wait(acc_empty0 + 8 * acc, ((n >> 1) & 1) ^ 1, s_abort)) { ok = false; break; }
                     fence_after();
                     for (uint32_t k = k0; k < k1; ++k) {
@@ -432,7 +444,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             pdl_wait();
             uint64_t once;
             asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-            uint32_t s = 0, phase = 0;
+            uint32_t used[kShares] = {};  // buffers of each share filled so far
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
@@ -440,8 +452,12 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 const TileGroups* g = tile_groups(p, tt);
                 const uint32_t items = v0 < p.V ? g->items : 0u;
                 for (uint32_t k = 0; k < items; ++k) {
-                    const uint32_t a = g->item[k];
+                    const uint32_t a = g->item[k], share = k % kShares;
                     if (a == kNoAdapter) break;
+                    uint32_t count = 0;
+#pragma unroll
+                    for (uint32_t i = 0; i < kShares; ++i) count = i == share ? used[i]++ : count;
+                    const uint32_t s = share * p.depth + count % p.depth, phase = count / p.depth & 1;
                     if (!mbar_wait_warp(b_empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
                     const uint32_t bar = b_full0 + 8 * s;
                     if (p.lora_tma) {
@@ -450,7 +466,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             tma_2d<1>(smem_u32(s_b) + s * slot_bytes, &map_b, 0, (int)(a * p.V + v0), bar, once);
                         }
                         __syncwarp();
-                        ++b_issued;
                     } else {
                         const uint16_t* src = static_cast<const uint16_t*>(p.lora_b) + ((uint64_t)a * p.V + v0) * p.rank;
                         unsigned char* dst = s_b + s * slot_bytes;
@@ -462,8 +477,14 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                         }
                         mbar_arrive(bar);
                     }
-                    if (++s == p.slots) { s = 0; phase ^= 1; }
                 }
+            }
+            // (every copy started ends, whether or not its tile is still taken)
+            if (*s_abort && p.lora_tma) {
+                uint32_t dummy = 0;
+                for (uint32_t i = 0; i < kShares; ++i)
+                    for (uint32_t c = used[i] < p.depth ? 0 : used[i] - p.depth; c < used[i]; ++c)
+                        (void)mbar_wait_warp(b_full0 + 8 * (i * p.depth + c % p.depth), c / p.depth & 1, &dummy);
             }
         }
     } else {
@@ -472,7 +493,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         const uint32_t quad = warp & 3, share = warp >> 2;
         const uint32_t et = threadIdx.x;
         OUT* out = static_cast<OUT*>(p.out);
-        uint32_t n = 0, staged = 0xFFFFFFFFu, staging_phase = 0, b_slot = 0, b_phase = 0;
+        uint32_t n = 0, staged = 0xFFFFFFFFu, staging_phase = 0, used = 0;
         const uint32_t acc_empty_at = CG == 2 ? map_to(acc_empty0, 0) : acc_empty0;
         // all epilogue warps have come here (a bounded wait, as everywhere: no warp can be
         // left behind by one that gave up)
@@ -528,11 +549,12 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             if constexpr (PROMOTE) {
                 float sum[(kMaxTileT / 32 + kShares - 1) / kShares][32];
                 bool ok = true;
-                for (uint32_t k0 = 0; k0 < p.slices; k0 += p.chunk, ++n) {  // (chunk <= slices)
+                for (uint32_t k0 = 0, k1; k0 < p.slices; k0 = k1, ++n) {
                     acc = n & 1;
+                    k1 = chunk_end(p, k0);
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) { ok = false; break; }
                     fence_after();
-                    const bool last = k0 + p.chunk >= p.slices;
+                    const bool last = k1 == p.slices;
 #pragma unroll
                     for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
                         const uint32_t c0 = (share + kShares * i) * 32;
@@ -556,32 +578,46 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 fence_after();
                 ++n;
             }
-            const uint32_t columns = tmem + lanes + acc * p.acc_cols;
-            const uint32_t acc2 = n & 1;
-            if (apart) {
-                if (!mbar_wait_warp(acc_full0 + 8 * acc2, (n >> 1) & 1, s_abort)) break;
-                fence_after();
-                ++n;
+            if constexpr (LORA && CG == 2) {
+                if (apart) {  // moved to the adapters' part, so that the next tile can use the first
+                    const uint32_t from = acc;
+                    acc = n & 1;
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) break;
+                    fence_after();
+                    ++n;
+                    for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
+                        const bool mine = apart >> (c0 / kBlock) & 1;
+#pragma unroll 1
+                        for (uint32_t c1 = c0; c1 < c0 + 32; c1 += 16) {
+                            const uint32_t to = tmem + lanes + acc * p.acc_cols + c1;
+                            float y[16];
+                            tmem_load16(tmem + lanes + from * p.acc_cols + c1, y);
+                            if (mine) {
+                                float z[16];
+                                tmem_load16(to, z);
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) {
+                                    if constexpr (FP8) y[c] *= sw * s_scale[c1 + c];
+                                    y[c] = fmaf(s_factor[c1 + c], z[c], y[c]);
+                                }
+                            }
+                            tmem_store16(to, y);
+                        }
+                    }
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    release(from);
+                }
             }
+            const uint32_t columns = tmem + lanes + acc * p.acc_cols;
             if (!LORA || v0 < p.V) {
                 for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
                     if (LORA && s_groups->block[c0 / kBlock] == kMixed) continue;
                     float y[32];
                     tmem_load32(columns + c0, y);
                     if constexpr (FP8) {
+                        if (!(apart >> (c0 / kBlock) & 1)) {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
-                    }
-                    if constexpr (LORA && CG == 2) {
-                        if (apart >> (c0 / kBlock) & 1) {
-#pragma unroll
-                            for (int h = 0; h < 32; h += 16) {
-                                float z[16];
-                                tmem_load16(tmem + lanes + acc2 * p.acc_cols + c0 + h, z);
-#pragma unroll
-                                for (int c = 0; c < 16; ++c)
-                                    y[h + c] = fmaf(c0 + h + c < N ? s_factor[c0 + h + c] : 0.f, z[c], y[h + c]);
-                            }
+                            for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
                         }
                     }
                     if (v < p.V) {
@@ -595,7 +631,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 }
             }
             if (LORA && items && v0 < p.V) {
-                if constexpr (PROMOTE) {  // an item's columns may have been written by another share
+                if (PROMOTE || apart) {  // an item's columns may have been written by another share
                     fence_before();
                     if (!meet()) break;
                     fence_after();
@@ -603,13 +639,12 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 // Item by item: the lane's row of B_a from its buffer, the item's rows of u (the
                 // same for every lane), eight rows at a time.
                 bool ok = true;
-                for (uint32_t k = 0; k < items; ++k) {
-                    // Items go round the shares. Every warp passes every buffer's barriers, so that
-                    // none falls behind by two phases.
+                for (uint32_t k = share; k < items; k += kShares) {  // items go round the shares
                     const uint32_t a = s_groups->item[k];
-                    if (a != kNoAdapter && !mbar_wait_warp(b_full0 + 8 * b_slot, b_phase, s_abort)) { ok = false; break; }
-                    const unsigned char* b_tile = s_b + b_slot * slot_bytes;
-                    const uint32_t begin = s_groups->start[k], end = k % kShares == share ? begin + s_groups->size[k] : 0;
+                    const uint32_t slot = share * p.depth + used % p.depth;
+                    if (a != kNoAdapter && !mbar_wait_warp(b_full0 + 8 * slot, used / p.depth & 1, s_abort)) { ok = false; break; }
+                    const unsigned char* b_tile = s_b + slot * slot_bytes;
+                    const uint32_t begin = s_groups->start[k], end = begin + s_groups->size[k];
                     for (uint32_t i = begin; i < end; i += 8) {
                         uint32_t c[8];
                         float y[8];
@@ -657,14 +692,13 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     }
                     if (a != kNoAdapter) {
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(b_empty0 + 8 * b_slot);
-                        if (++b_slot == p.slots) { b_slot = 0; b_phase ^= 1; }
+                        if (lane == 0) mbar_arrive(b_empty0 + 8 * slot);
+                        ++used;
                     }
                 }
                 if (!ok) break;
             }
             release(acc);
-            if (apart) release(acc2);
         }
     }
     // Everything issued is finished before shared memory and TMEM go: in a normal run the
@@ -679,8 +713,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         if (rank == 0)  // (the even CTA's barriers count the pair's copies)
             for (uint32_t i = issued < p.stages ? 0 : issued - p.stages; i < issued; ++i)
                 (void)mbar_wait(full0 + 8 * (i % p.stages), (i / p.stages) & 1, &dummy);
-        for (uint32_t i = b_issued < p.slots ? 0 : b_issued - p.slots; i < b_issued; ++i)
-            (void)mbar_wait(b_full0 + 8 * (i % p.slots), (i / p.slots) & 1, &dummy);
     }
     __syncwarp();
     fence_before();
@@ -845,23 +877,19 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((cg * kTileV >> 4) << 24);
     const uint32_t lora_type = lora_dtype == LP_BF16 ? 1u : 0u;
     p.lora_idesc = (1u << 4) | (lora_type << 7) | (lora_type << 10) | ((cg * kTileV >> 4) << 24);  // without N
-    // Shared memory: the ring's stages come first (at 256 rows, six stages instead of seven cost
-    // 15 %), then the adapters' buffers, and a tile's u where it fits into what is left (24 KB
-    // are set aside for it in single CTAs, which have stages to spare).
+    // Shared memory: the adapters' buffers, a tile's u where it takes 24 KB or less (or fits into
+    // what is left), and as many stages as there is room for.
     const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
     const uint32_t u_bytes = p.tile_t * p.u_cols * 4;
     const uint32_t fixed = kControlBytes + (fp8 ? p.tile_t * 4 : 0) +
                            (rank ? (uint32_t)sizeof(TileGroups) + (p.tensor ? p.tile_t * 4 : 0) : 0);
-    uint32_t set_aside = rank ? 2 * slot_bytes : 0;
-    if (rank && cg == 1) set_aside = kSlotsBytes + (u_bytes <= 24 * 1024 ? u_bytes : 0);
-    p.stages = (kSmemBudget - fixed - set_aside) / stage_bytes;
+    p.depth = rank == 0 ? 0 : rank <= 16 ? 3 : rank <= 32 ? 2 : 1;
+    const uint32_t b_bytes = kShares * p.depth * slot_bytes;
+    const uint32_t u_aside = u_bytes <= 24 * 1024 ? u_bytes : 0;
+    p.stages = (kSmemBudget - fixed - b_bytes - u_aside) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    uint32_t left = kSmemBudget - fixed - p.stages * stage_bytes;
-    p.u_smem = rank && left >= u_bytes + 2 * slot_bytes;
-    if (p.u_smem) left -= u_bytes;
-    p.slots = rank ? left / slot_bytes : 0;
-    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-    l.smem = fixed + p.stages * stage_bytes + p.slots * slot_bytes + (p.u_smem ? u_bytes : 0);
+    p.u_smem = rank && kSmemBudget - fixed - b_bytes - p.stages * stage_bytes >= u_bytes;
+    l.smem = fixed + p.stages * stage_bytes + b_bytes + (p.u_smem ? u_bytes : 0);
     const uint32_t slice_cols = kSliceBytes / (uint32_t)e;
     if (!encode(&l.w, weight, dtype, V, H, weight_stride, kTileV, slice_cols) ||
         !encode(&l.x, x, dtype, T, H, x_stride, p.tile_t / cg, slice_cols))
