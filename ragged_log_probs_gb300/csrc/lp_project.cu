@@ -246,6 +246,9 @@ __device__ __forceinline__ uint32_t b_offset(uint32_t row, uint32_t piece, uint3
 __device__ __forceinline__ uint32_t chunk_end(const ProjectParams& p, uint32_t k0) {
     return k0 + min(p.slices - k0, k0 ? p.chunk : 2 * p.chunk);
 }
+__device__ __forceinline__ uint32_t last_chunk(const ProjectParams& p) {  // where the last one begins
+    return p.slices <= 2 * p.chunk ? 0 : (p.slices - 1 - 2 * p.chunk) / p.chunk * p.chunk + 2 * p.chunk;
+}
 // How many blocks from b0 on have the same entry (the adapter of a run), of `blocks`.
 __device__ __forceinline__ uint32_t run_length(const TileGroups* g, uint32_t b0, uint32_t blocks) {
     uint32_t n = 1;
@@ -274,8 +277,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     unsigned char* s_b = ring + p.stages * stage_bytes;                         // [shares][depth][128][b_cols]
     float* s_u = reinterpret_cast<float*>(s_b + kShares * p.depth * slot_bytes);  // [N][uc]
     float* s_scale = s_u + (LORA && p.u_smem ? N * uc : 0);                     // [N]
-    float* s_factor = s_scale + (FP8 ? N : 0);                                  // [N]
-    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_factor + (LORA && p.tensor ? N : 0));
+    TileGroups* s_groups = reinterpret_cast<TileGroups*>(s_scale + (FP8 && LORA ? N : 0));
     uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(s_groups) +
                                                  (LORA ? sizeof(TileGroups) : 0));
     volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + kBarriers);
@@ -325,6 +327,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     fence_after();
     const uint32_t tmem = *s_tmem;
 
+    // The adapters' part comes after the product, or, with the product in chunks, before its
+    // last chunk: the sums outside the tensor core do not care, and the first kernel has time.
+    const uint32_t lora_at = PROMOTE ? last_chunk(p) : p.slices;
     uint32_t issued = 0;    // stages the producer has started copies into
     if (warp == kCopyWarp) {
         if (lane == 0) {
@@ -339,7 +344,33 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
                 const int v0 = (int)((tv * CG + rank) * kTileV), t0 = (int)(tt * N + rank * (N / CG));
-                for (uint32_t k = 0; k < p.slices; ++k) {
+                for (uint32_t k = 0;; ++k) {
+                    if constexpr (LORA && CG == 2) {
+                        if (p.tensor && k == lora_at) {
+                            if (tile == first) pdl_wait();
+                            // runs of blocks with one adapter: B_a in W's place, the parts of u in x's
+                            const TileGroups* g = tile_groups(p, tt);
+                            for (uint32_t b0 = 0, n; ok && b0 < N / kBlock; b0 += n) {
+                                const uint32_t a = g->block[b0];
+                                n = run_length(g, b0, N / kBlock);
+                                if (a >= kMixed) continue;
+                                for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                                    if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
+                                    const uint32_t dst = base + s * stage_bytes, bar = map_to(full0 + 8 * s, 0);
+                                    constexpr uint32_t kHalf = kBlock / CG;  // rows of a block that a CTA holds
+                                    if (rank == 0) mbar_expect(full0 + 8 * s, CG * (kStageW + n * kHalf * kSliceBytes));
+                                    tma_2d<CG>(dst, &map_lora_b, 0, (int)(a * p.V) + v0, bar, keep);
+                                    for (uint32_t i = 0; i < n; ++i)
+                                        tma_2d<CG>(dst + kStageW + i * kHalf * kSliceBytes, &map_parts, 0,
+                                                   (int)(line * p.part_stride + tt * N + b0 * kBlock + (rank * n + i) * kHalf),
+                                                   bar, keep);
+                                    ++issued;
+                                    if (++s == p.stages) { s = 0; phase ^= 1; }
+                                }
+                            }
+                        }
+                    }
+                    if (!ok || k == p.slices) break;
                     if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
                     const uint32_t dst = base + s * stage_bytes;
                     const uint32_t bar = CG == 2 ? map_to(full0 + 8 * s, 0) : full0 + 8 * s;
@@ -349,30 +380,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     ++issued;
                     if (++s == p.stages) { s = 0; phase ^= 1; }
                 }
-                if constexpr (LORA && CG == 2) {
-                    if (!ok || !p.tensor) continue;
-                    if (tile == first) pdl_wait();
-                    // runs of blocks with one adapter: B_a in W's place, the parts of u in x's
-                    const TileGroups* g = tile_groups(p, tt);
-                    for (uint32_t b0 = 0, n; ok && b0 < N / kBlock; b0 += n) {
-                        const uint32_t a = g->block[b0];
-                        n = run_length(g, b0, N / kBlock);
-                        if (a >= kMixed) continue;
-                        for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
-                            if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
-                            const uint32_t dst = base + s * stage_bytes, bar = map_to(full0 + 8 * s, 0);
-                            constexpr uint32_t kHalf = kBlock / CG;  // rows of a block that a CTA holds
-                            if (rank == 0) mbar_expect(full0 + 8 * s, CG * (kStageW + n * kHalf * kSliceBytes));
-                            tma_2d<CG>(dst, &map_lora_b, 0, (int)(a * p.V) + v0, bar, keep);
-                            for (uint32_t i = 0; i < n; ++i)
-                                tma_2d<CG>(dst + kStageW + i * kHalf * kSliceBytes, &map_parts, 0,
-                                           (int)(line * p.part_stride + tt * N + b0 * kBlock + (rank * n + i) * kHalf), bar,
-                                           keep);
-                            ++issued;
-                            if (++s == p.stages) { s = 0; phase ^= 1; }
-                        }
-                    }
-                }
             }
         }
     } else if (warp == kMmaWarp) {
@@ -380,7 +387,44 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
+                // The adapters' part: into the open accumulator, or one of its own.
+                const auto adapters = [&]() {
+                    if (tile == first) pdl_wait();
+                    const TileGroups* g = tile_groups(p, tile % p.tiles_t);
+                    bool open = !p.apart;
+                    for (uint32_t b0 = 0, blocks; ok && b0 < N / kBlock; b0 += blocks) {
+                        blocks = run_length(g, b0, N / kBlock);
+                        if (g->block[b0] >= kMixed) continue;
+                        const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
+                        for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                            if (!open && !mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort)) ok = false;
+                            open = true;
+                            if (!ok || !mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+                            fence_after();
+                            const uint64_t a = matrix_desc(base + s * stage_bytes);
+                            const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
+                            // 16 columns of the parts a step; B_a's start again with each part
+                            for (uint32_t i = 0; i < 4; ++i) {
+                                const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
+                                               j = column - part * p.b_cols;
+                                if (part < 3 && j < uc)
+                                    mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i, idesc,
+                                                   p.apart ? (line | i) : 1u);
+                            }
+                            mma_commit<CG>(empty0 + 8 * s);
+                            if (++s == p.stages) { s = 0; phase ^= 1; }
+                        }
+                    }
+                    if (ok && open) {
+                        mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                        ++n;
+                    }
+                };
                 for (uint32_t k0 = 0, k1; ok && k0 < p.slices; k0 = k1) {
+                    if constexpr (LORA && CG == 2 && PROMOTE) {
+                        if (p.tensor && k0 == lora_at) adapters();
+                        if (!ok) break;
+                    }
                     const uint32_t acc = n & 1;
                     k1 = chunk_end(p, k0);
                     if (!mbar_wait(acc_empty0 + 8 * acc, ((n >> 1) & 1) ^ 1, s_abort)) { ok = false; break; }
@@ -401,39 +445,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     mma_commit<CG>(acc_full0 + 8 * acc);
                     ++n;
                 }
-                if constexpr (LORA && CG == 2) {
-                    if (ok && p.tensor) {
-                        if (tile == first) pdl_wait();
-                        const TileGroups* g = tile_groups(p, tile % p.tiles_t);
-                        bool open = !p.apart;
-                        for (uint32_t b0 = 0, blocks; ok && b0 < N / kBlock; b0 += blocks) {
-                            blocks = run_length(g, b0, N / kBlock);
-                            if (g->block[b0] >= kMixed) continue;
-                            const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
-                            for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
-                                if (!open && !mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort)) ok = false;
-                                open = true;
-                                if (!ok || !mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
-                                fence_after();
-                                const uint64_t a = matrix_desc(base + s * stage_bytes);
-                                const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
-                                // 16 columns of the parts a step; B_a's start again with each part
-                                for (uint32_t i = 0; i < 4; ++i) {
-                                    const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
-                                                   j = column - part * p.b_cols;
-                                    if (part < 3 && j < uc)
-                                        mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i, idesc,
-                                                       p.apart ? (line | i) : 1u);
-                                }
-                                mma_commit<CG>(empty0 + 8 * s);
-                                if (++s == p.stages) { s = 0; phase ^= 1; }
-                            }
-                        }
-                        if (ok && open) {
-                            mma_commit<CG>(acc_full0 + 8 * (n & 1));
-                            ++n;
-                        }
-                    }
+                if constexpr (LORA && CG == 2 && !PROMOTE) {
+                    if (ok && p.tensor) adapters();
                 }
             }
             mma_commit<CG>(drain);  // arrives once every product issued above has finished
@@ -517,55 +530,68 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t, t0 = tt * N;
             const uint32_t v0 = (tv * CG + rank) * kTileV, v = v0 + quad * 32 + lane;
             const uint32_t rows = min(N, p.T - t0);
-            if ((FP8 || LORA) && tt != staged) {  // the rows' scales or factors, groups and u
-                if (!meet()) break;
-                if constexpr (LORA) {
-                    const uint4* words = reinterpret_cast<const uint4*>(tile_groups(p, tt));
+            uint32_t items = 0, mixed = 0, apart = 0;  // masks of blocks: see TileGroups
+            if constexpr (LORA) {
+                const TileGroups* g = tile_groups(p, tt);
+                const uint32_t block = lane < kMaxTileT / kBlock ? g->block[lane] : kNoAdapter;
+                mixed = __ballot_sync(0xFFFFFFFFu, block == kMixed);
+                if (CG == 2 && p.tensor && p.apart) apart = __ballot_sync(0xFFFFFFFFu, block < kMixed);
+                items = g->items;
+                if (items && tt != staged) {  // the lists, u and scales in shared memory
+                    if (!meet()) break;
+                    const uint4* words = reinterpret_cast<const uint4*>(g);
                     for (uint32_t i = et; i < sizeof(TileGroups) / 16; i += kEpilogueWarps * 32)
                         reinterpret_cast<uint4*>(s_groups)[i] = words[i];
-                    if (p.u_smem && tile_groups(p, tt)->items) {
+                    if (p.u_smem) {
                         const float4* src = reinterpret_cast<const float4*>(p.u + (uint64_t)t0 * uc);
                         for (uint32_t i = et; i < rows * uc / 4; i += kEpilogueWarps * 32)
                             reinterpret_cast<float4*>(s_u)[i] = src[i];
                     }
+                    if constexpr (FP8)
+                        for (uint32_t i = et; i < rows; i += kEpilogueWarps * 32) s_scale[i] = p.x_scale[t0 + i];
+                    if (!meet()) break;
+                    staged = tt;
                 }
-                for (uint32_t i = et; i < N; i += kEpilogueWarps * 32) {
-                    if (FP8) s_scale[i] = i < rows ? p.x_scale[t0 + i] : 0.f;
-                    if (LORA && p.tensor) s_factor[i] = i < rows ? p.factor[t0 + i] : 0.f;
-                }
-                if (!meet()) break;
-                staged = tt;
             }
-            const uint32_t items = LORA ? s_groups->items : 0u;
-            // blocks whose adapters' part has an accumulator of its own
-            uint32_t apart = 0;
-            if constexpr (LORA && CG == 2) {
-                if (p.tensor && p.apart)
-                    apart = __ballot_sync(0xFFFFFFFFu, lane < N / kBlock && s_groups->block[lane < N / kBlock ? lane : 0] < kMixed);
-            }
+            // of row c of a block, from the lane that holds it
+            const auto of_row = [&](const float* per_row, uint32_t c0) {
+                return c0 + lane < rows ? per_row[t0 + c0 + lane] : 0.f;
+            };
             const float sw = FP8 && v < p.V ? p.w_scale[v] : 1.f;
             uint32_t acc = n & 1;
             const uint32_t lanes = (quad * 32) << 16;
             if constexpr (PROMOTE) {
                 float sum[(kMaxTileT / 32 + kShares - 1) / kShares][32];
                 bool ok = true;
-                for (uint32_t k0 = 0, k1; k0 < p.slices; k0 = k1, ++n) {
+#pragma unroll
+                for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
+                bool lora = apart != 0;  // the adapters' accumulator is still to come
+                for (uint32_t k0 = 0; k0 < p.slices; ++n) {
                     acc = n & 1;
-                    k1 = chunk_end(p, k0);
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) { ok = false; break; }
                     fence_after();
-                    const bool last = k1 == p.slices;
+                    const bool now = lora && k0 == lora_at;
+                    if (now) lora = false;
+                    else k0 = chunk_end(p, k0);
+                    const bool last = k0 == p.slices;
 #pragma unroll
                     for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
                         const uint32_t c0 = (share + kShares * i) * 32;
-                        if (c0 >= N) continue;
+                        if (c0 >= N || (now && !(apart >> (c0 / kBlock) & 1))) continue;
                         const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
+                        const float factor = now && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
 #pragma unroll
                         for (int q = 0; q < 32; q += 16) {
                             float y[16];
                             tmem_load16(at + q, y);
+                            if (LORA && now && p.lora_f16) {
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) sum[i][q + c] = k0 ? sum[i][q + c] + y[c] : y[c];
+                                for (int c = 0; c < 16; ++c) y[c] *= __shfl_sync(0xFFFFFFFFu, factor, q + c);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
                         }
                         if (last) tmem_store32(at, sum[i]);
                     }
@@ -578,7 +604,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 fence_after();
                 ++n;
             }
-            if constexpr (LORA && CG == 2) {
+            if constexpr (LORA && CG == 2 && !PROMOTE) {
                 if (apart) {  // moved to the adapters' part, so that the next tile can use the first
                     const uint32_t from = acc;
                     acc = n & 1;
@@ -587,6 +613,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     ++n;
                     for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
                         const bool mine = apart >> (c0 / kBlock) & 1;
+                        const float factor = mine && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
+                        const float scale = FP8 && mine ? sw : 1.f, row_scale = FP8 && mine ? of_row(p.x_scale, c0) : 1.f;
 #pragma unroll 1
                         for (uint32_t c1 = c0; c1 < c0 + 32; c1 += 16) {
                             const uint32_t to = tmem + lanes + acc * p.acc_cols + c1;
@@ -597,8 +625,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                 tmem_load16(to, z);
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) {
-                                    if constexpr (FP8) y[c] *= sw * s_scale[c1 + c];
-                                    y[c] = fmaf(s_factor[c1 + c], z[c], y[c]);
+                                    if constexpr (FP8) y[c] *= scale * __shfl_sync(0xFFFFFFFFu, row_scale, c1 - c0 + c);
+                                    y[c] = fmaf(__shfl_sync(0xFFFFFFFFu, factor, c1 - c0 + c), z[c], y[c]);
                                 }
                             }
                             tmem_store16(to, y);
@@ -611,13 +639,14 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t columns = tmem + lanes + acc * p.acc_cols;
             if (!LORA || v0 < p.V) {
                 for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
-                    if (LORA && s_groups->block[c0 / kBlock] == kMixed) continue;
+                    if (mixed >> (c0 / kBlock) & 1) continue;
                     float y[32];
                     tmem_load32(columns + c0, y);
                     if constexpr (FP8) {
                         if (!(apart >> (c0 / kBlock) & 1)) {
+                            const float row_scale = of_row(p.x_scale, c0);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) y[c] *= sw * (c0 + c < N ? s_scale[c0 + c] : 0.f);
+                            for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
                         }
                     }
                     if (v < p.V) {
@@ -881,8 +910,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     // what is left), and as many stages as there is room for.
     const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
     const uint32_t u_bytes = p.tile_t * p.u_cols * 4;
-    const uint32_t fixed = kControlBytes + (fp8 ? p.tile_t * 4 : 0) +
-                           (rank ? (uint32_t)sizeof(TileGroups) + (p.tensor ? p.tile_t * 4 : 0) : 0);
+    const uint32_t fixed = kControlBytes + (rank ? (uint32_t)sizeof(TileGroups) + (fp8 ? p.tile_t * 4 : 0) : 0);
     p.depth = rank == 0 ? 0 : rank <= 16 ? 3 : rank <= 32 ? 2 : 1;
     const uint32_t b_bytes = kShares * p.depth * slot_bytes;
     const uint32_t u_aside = u_bytes <= 24 * 1024 ? u_bytes : 0;
