@@ -73,11 +73,45 @@ __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     id[c] = c < rows ? adapter_of(p, t0 + c, &bad, &code) : -2;
     sync();
     TileGroups* g = reinterpret_cast<TileGroups*>(p.groups + (size_t)tile * kGroupBytes);
-    // the warp's rows are one block: rows past the last count as its first row's
-    const int32_t first = __shfl_sync(0xFFFFFFFFu, id[c], 0);
-    const bool same = __all_sync(0xFFFFFFFFu, id[c] == first || id[c] == -2);
-    const bool listed = !(same && (first < 0 || p.tensor));
-    if (c % kBlock == 0) g->block[c / kBlock] = listed ? kMixed : first < 0 ? kNoAdapter : (uint32_t)first;
+    // the warp's rows are one block: its first adapter, its second, and whether there are more
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    const int32_t mine = id[c];
+    const uint32_t with = __ballot_sync(kAll, mine >= 0), in = __ballot_sync(kAll, c < rows);
+    const int32_t a0 = __shfl_sync(kAll, mine, with ? __ffs(with) - 1 : 0);
+    const uint32_t m0 = with ? __ballot_sync(kAll, mine == a0) : 0u, rest = with & ~m0;
+    const int32_t a1 = __shfl_sync(kAll, mine, rest ? __ffs(rest) - 1 : 0);
+    const uint32_t m1 = rest ? __ballot_sync(kAll, mine == a1) : 0u;
+    const bool listed = with && (!p.tensor || (p.split ? (rest & ~m1) != 0 : m0 != in));
+    const bool tensor = with && !listed;
+    __shared__ uint32_t adapter[3][kBlocks], listed_bits;  // of each pass
+    if (c == 0) listed_bits = 0;
+    sync();
+    if (c % kBlock == 0) {
+        const uint32_t b = c / kBlock, pass = m0 == in && !p.apart ? 0 : 1;  // of the first adapter
+        adapter[0][b] = tensor && pass == 0 ? (uint32_t)a0 : kNoAdapter;
+        adapter[1][b] = tensor && pass == 1 ? (uint32_t)a0 : kNoAdapter;
+        adapter[2][b] = tensor && rest ? (uint32_t)a1 : kNoAdapter;
+        g->rows[0][b] = m0;
+        g->rows[1][b] = m1;
+        if (listed) atomicOr(&listed_bits, 1u << b);
+    }
+    sync();
+    if (c == 0) {
+        uint32_t runs = 0;
+        for (uint32_t pass = 0; pass < 3; ++pass) {
+            uint32_t blocks = 0;
+            for (uint32_t b0 = 0, n; b0 < kBlocks; b0 += n) {
+                const uint32_t a = adapter[pass][b0];
+                for (n = 1; b0 + n < kBlocks && adapter[pass][b0 + n] == a; ++n) {}
+                if (a == kNoAdapter) continue;
+                g->run[runs++] = make_uint2(pass << 16 | b0 << 8 | n, a);
+                blocks |= ((1u << n) - 1u) << b0;
+            }
+            if (pass) g->blocks[pass - 1] = blocks;
+        }
+        g->runs = runs;
+        g->listed = listed_bits;
+    }
     uint32_t k = kUnlisted;
     key[c] = listed && c < rows ? 0 : kUnlisted;
     sync();

@@ -11,24 +11,34 @@ constexpr uint32_t kItemRows = 32;
 constexpr uint32_t kMaxItems = kMaxTileT + kMaxTileT / kItemRows;
 constexpr uint32_t kBlock = 32;      // rows of a block: what one epilogue pass takes
 constexpr uint32_t kNoAdapter = 0xFFFFFFFFu;
-constexpr uint32_t kMixed = 0xFFFFFFFEu;
 
-// One tile of rows, in blocks of 32. Where all rows of a block have the same adapter, its part
-// of the product can run on the tensor cores, as a continuation of the contraction for these
-// columns of the accumulator. The rows of the other blocks are grouped by adapter, those
-// without one last, and cut into items of at most kItemRows rows of one adapter, which the
-// epilogue adds. (Zeroing u in other adapters' rows instead would let an infinity in one
-// adapter's B become NaN, 0 x inf, in the rows of others.)
+// One tile of rows, in blocks of 32. Where all rows of a block have one adapter, its part of
+// the product runs on the tensor cores: in pass 0, which adds to the product's own accumulator,
+// or, where that cannot be, in pass 1, which has one of its own. Where sums are kept outside
+// the tensor cores anyway (`split`), passes 1 and 2 also take the two adapters of blocks that
+// have two, or rows without one: the epilogue adds the rows that have the pass's adapter. The
+// rows of other blocks are grouped by adapter, those without one last, and cut into items of at
+// most kItemRows rows of one adapter, which the epilogue multiplies itself.
+// (Zeroing u in other adapters' rows instead would let an infinity in one adapter's B become
+// NaN, 0 x inf, in the rows of others.)
+constexpr uint32_t kBlocks = kMaxTileT / kBlock;
+constexpr uint32_t kMaxRuns = 3 * kBlocks;
 struct TileGroups {
     uint32_t items;
-    uint32_t unused[3];
-    uint32_t block[kMaxTileT / kBlock];  // its adapter, kNoAdapter, or kMixed: its rows are in items
-    uint32_t item[kMaxItems];            // adapter of item k, kNoAdapter for rows without one
-    uint8_t start[kMaxItems];            // item k holds order[start[k] ... start[k] + size[k] - 1]
+    uint32_t listed;             // bit per block: its rows are in items
+    uint32_t runs;
+    uint32_t unused;
+    uint32_t blocks[2];          // bit per block: it is in pass 1, in pass 2
+    uint32_t unused2[2];
+    uint32_t rows[2][kBlocks];   // the block's rows that have the pass's adapter, a bit each
+    uint2 run[kMaxRuns];         // neighbouring blocks with one adapter in a pass, in the order of the
+                                 // passes: x = pass << 16 | first block << 8 | blocks, y = adapter
+    uint32_t item[kMaxItems];    // adapter of item k, kNoAdapter for rows without one
+    uint8_t start[kMaxItems];    // item k holds order[start[k] ... start[k] + size[k] - 1]
     uint8_t size[kMaxItems];
-    uint8_t order[kMaxTileT];            // row within the tile
+    uint8_t order[kMaxTileT];    // row within the tile
 };
-constexpr size_t kGroupBytes = 2048;  // of one tile in the workspace
+constexpr size_t kGroupBytes = 2560;  // of one tile in the workspace
 static_assert(sizeof(TileGroups) % 16 == 0 && sizeof(TileGroups) <= kGroupBytes, "read as 16-byte words");
 
 // u of a row for the tensor cores: three 16-bit parts (a value, what rounding it left, and
@@ -68,7 +78,9 @@ struct ShrinkParams {
     uint32_t T, H, B, adapters, rank;
     uint32_t tile_t;              // rows of a tile
     uint32_t part_stride;         // rows of u's parts
-    uint32_t tensor;              // blocks of one adapter run on the tensor cores (parts are wanted)
+    uint32_t tensor;              // blocks of one adapter run on the tensor cores (u's parts are wanted)
+    uint32_t apart;               // none in the product's own accumulator (pass 0)
+    uint32_t split;               // blocks of two adapters, or of one and none, too
     uint32_t lora_f16;
 };
 

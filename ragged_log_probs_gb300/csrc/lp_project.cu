@@ -63,8 +63,9 @@ struct ProjectParams {
     uint32_t tensor;               // blocks of rows with one adapter run on the tensor cores
     uint32_t apart;                // with an accumulator of their own: their sum has another scale
                                    // (e4m3), a factor a row (f16), or x W^T comes in chunks (f32)
+    uint64_t lora_bytes;           // of lora_b
     uint32_t lora_f16;             // lora_b is f16 (else bf16)
-    uint32_t lora_tma;             // lora_b's rows are whole 16-byte pieces (TMA fills the buffers)
+    uint32_t lora_tma;             // lora_b's rows are whole 16-byte pieces (swizzled tiles in the buffers)
     uint32_t early;                // the inputs are complete when this kernel starts (u may not be)
 };
 
@@ -136,6 +137,11 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
             "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+}
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar) : "memory");
 }
 
 // Shared-memory matrix descriptor: rows of 128 bytes, 128-byte swizzle, groups of 8 rows
@@ -249,15 +255,25 @@ __device__ __forceinline__ uint32_t chunk_end(const ProjectParams& p, uint32_t k
 __device__ __forceinline__ uint32_t last_chunk(const ProjectParams& p) {  // where the last one begins
     return p.slices <= 2 * p.chunk ? 0 : (p.slices - 1 - 2 * p.chunk) / p.chunk * p.chunk + 2 * p.chunk;
 }
-// How many blocks from b0 on have the same entry (the adapter of a run), of `blocks`.
-__device__ __forceinline__ uint32_t run_length(const TileGroups* g, uint32_t b0, uint32_t blocks) {
-    uint32_t n = 1;
-    while (b0 + n < blocks && g->block[b0 + n] == g->block[b0]) ++n;
-    return n;
-}
 __device__ __forceinline__ const TileGroups* tile_groups(const ProjectParams& p, uint32_t tt) {
     return reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
 }
+// A tile's runs: the count and the first four are fetched when the tile begins, long before
+// they are used.
+struct RunList {
+    const TileGroups* g;
+    uint32_t runs;
+    uint2 head[4];
+    __device__ __forceinline__ void fetch(const TileGroups* groups) {
+        g = groups;
+        runs = g->runs;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) head[i] = g->run[i];
+    }
+    __device__ __forceinline__ uint2 at(uint32_t r) const {
+        return r == 0 ? head[0] : r == 1 ? head[1] : r == 2 ? head[2] : r == 3 ? head[3] : g->run[r];
+    }
+};
 
 // PROMOTE: f32 logits of 16-bit inputs. The tensor core's f32 accumulator drops the bits
 // below its last place at every step, always towards zero: over a contraction of 4096 that
@@ -297,7 +313,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             mbar_init(empty0 + 8 * s, 1);
         }
         for (uint32_t i = 0; LORA && i < kShares * p.depth; ++i) {
-            mbar_init(b_full0 + 8 * i, p.lora_tma ? 1 : 32);
+            mbar_init(b_full0 + 8 * i, 1);
             mbar_init(b_empty0 + 8 * i, 4);  // the share's warps
         }
         for (uint32_t i = 0; i < 2; ++i) {
@@ -344,16 +360,19 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
                 const int v0 = (int)((tv * CG + rank) * kTileV), t0 = (int)(tt * N + rank * (N / CG));
+                RunList list;
+                if (LORA && CG == 2 && p.tensor && tile != first) list.fetch(tile_groups(p, tt));
                 for (uint32_t k = 0;; ++k) {
                     if constexpr (LORA && CG == 2) {
                         if (p.tensor && k == lora_at) {
-                            if (tile == first) pdl_wait();
+                            if (tile == first) {
+                                pdl_wait();
+                                list.fetch(tile_groups(p, tt));
+                            }
                             // runs of blocks with one adapter: B_a in W's place, the parts of u in x's
-                            const TileGroups* g = tile_groups(p, tt);
-                            for (uint32_t b0 = 0, n; ok && b0 < N / kBlock; b0 += n) {
-                                const uint32_t a = g->block[b0];
-                                n = run_length(g, b0, N / kBlock);
-                                if (a >= kMixed) continue;
+                            for (uint32_t r = 0; ok && r < list.runs; ++r) {
+                                const uint2 run = list.at(r);
+                                const uint32_t a = run.y, b0 = run.x >> 8 & 0xFF, n = run.x & 0xFF;
                                 for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
                                     if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
                                     const uint32_t dst = base + s * stage_bytes, bar = map_to(full0 + 8 * s, 0);
@@ -387,44 +406,56 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
-                // The adapters' part: into the open accumulator, or one of its own.
-                const auto adapters = [&]() {
-                    if (tile == first) pdl_wait();
-                    const TileGroups* g = tile_groups(p, tile % p.tiles_t);
-                    bool open = !p.apart;
-                    for (uint32_t b0 = 0, blocks; ok && b0 < N / kBlock; b0 += blocks) {
-                        blocks = run_length(g, b0, N / kBlock);
-                        if (g->block[b0] >= kMixed) continue;
-                        const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
-                        for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
-                            if (!open && !mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort)) ok = false;
-                            open = true;
-                            if (!ok || !mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
-                            fence_after();
-                            const uint64_t a = matrix_desc(base + s * stage_bytes);
-                            const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
-                            // 16 columns of the parts a step; B_a's start again with each part
-                            for (uint32_t i = 0; i < 4; ++i) {
-                                const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
-                                               j = column - part * p.b_cols;
-                                if (part < 3 && j < uc)
-                                    mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i, idesc,
-                                                   p.apart ? (line | i) : 1u);
+                RunList list;
+                if (LORA && CG == 2 && p.tensor && tile != first) list.fetch(tile_groups(p, tile % p.tiles_t));
+                for (uint32_t k0 = 0, k1; ok; k0 = k1) {
+                    if constexpr (LORA && CG == 2) {
+                        if (p.tensor && k0 == lora_at) {
+                            // The adapters' passes: pass 0 into the open accumulator, 1 and 2 into others.
+                            if (tile == first) {
+                                pdl_wait();
+                                list.fetch(tile_groups(p, tile % p.tiles_t));
                             }
-                            mma_commit<CG>(empty0 + 8 * s);
-                            if (++s == p.stages) { s = 0; phase ^= 1; }
+                            uint32_t pass = 0;
+                            bool open = !p.apart;  // the product's own accumulator
+                            for (uint32_t r = 0; ok && r < list.runs; ++r) {
+                                const uint2 run = list.at(r);
+                                const uint32_t b0 = run.x >> 8 & 0xFF, blocks = run.x & 0xFF;
+                                if (run.x >> 16 != pass) {
+                                    if (open) {
+                                        mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                                        ++n;
+                                    }
+                                    pass = run.x >> 16;
+                                    open = mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort);
+                                    if (!open) { ok = false; break; }
+                                }
+                                const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
+                                for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                                    if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+                                    fence_after();
+                                    const uint64_t a = matrix_desc(base + s * stage_bytes);
+                                    const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
+                                    // 16 columns of the parts a step; B_a's start again with each part
+                                    for (uint32_t i = 0; i < 4; ++i) {
+                                        const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
+                                                       j = column - part * p.b_cols;
+                                        if (part < 3 && j < uc)
+                                            mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i,
+                                                           idesc, pass ? (line | i) : 1u);
+                                    }
+                                    mma_commit<CG>(empty0 + 8 * s);
+                                    if (++s == p.stages) { s = 0; phase ^= 1; }
+                                }
+                            }
+                            if (!ok) break;
+                            if (open) {
+                                mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                                ++n;
+                            }
                         }
                     }
-                    if (ok && open) {
-                        mma_commit<CG>(acc_full0 + 8 * (n & 1));
-                        ++n;
-                    }
-                };
-                for (uint32_t k0 = 0, k1; ok && k0 < p.slices; k0 = k1) {
-                    if constexpr (LORA && CG == 2 && PROMOTE) {
-                        if (p.tensor && k0 == lora_at) adapters();
-                        if (!ok) break;
-                    }
+                    if (k0 >= p.slices) break;
                     const uint32_t acc = n & 1;
                     k1 = chunk_end(p, k0);
                     if (!mbar_wait(acc_empty0 + 8 * acc, ((n >> 1) & 1) ^ 1, s_abort)) { ok = false; break; }
@@ -441,12 +472,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                         if (++s == p.stages) { s = 0; phase ^= 1; }
                     }
                     if (!ok) break;
-                    if (LORA && CG == 2 && p.tensor && !p.apart) break;  // the adapters' part continues it
+                    if (LORA && CG == 2 && p.tensor && !p.apart) continue;  // pass 0 continues it
                     mma_commit<CG>(acc_full0 + 8 * acc);
                     ++n;
-                }
-                if constexpr (LORA && CG == 2 && !PROMOTE) {
-                    if (ok && p.tensor) adapters();
                 }
             }
             mma_commit<CG>(drain);  // arrives once every product issued above has finished
@@ -480,20 +508,30 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                         }
                         __syncwarp();
                     } else {
-                        const uint16_t* src = static_cast<const uint16_t*>(p.lora_b) + ((uint64_t)a * p.V + v0) * p.rank;
+                        // Rows of any length are one stretch of memory: copied as it is, from the
+                        // 16-byte boundary before it to the one after it, or to the last one within
+                        // the tensor, whose last bytes are then copied one value at a time.
+                        const uint64_t begin = ((uint64_t)a * p.V + v0) * p.rank * 2, from = begin & ~15ull;
+                        const uint64_t end = begin + (uint64_t)min(kTileV, p.V - v0) * p.rank * 2;
+                        const uint64_t limit = p.lora_bytes & ~15ull;
+                        const uint64_t upto = (end + 15) & ~15ull;
+                        const uint32_t bytes = (uint32_t)((upto < limit ? upto : limit) - from);
                         unsigned char* dst = s_b + s * slot_bytes;
-                        const uint32_t rows = min(kTileV, p.V - v0);
-                        for (uint32_t i = lane; i < kTileV * p.b_cols; i += 32) {
-                            const uint32_t r = i / p.b_cols, j = i - r * p.b_cols;
-                            *reinterpret_cast<uint16_t*>(dst + b_offset(r, j >> 3, p.b_cols) + (j & 7) * 2) =
-                                r < rows && j < p.rank ? src[r * p.rank + j] : (uint16_t)0;
+                        if (from + bytes + 2 * lane < end)
+                            *reinterpret_cast<uint16_t*>(dst + bytes + 2 * lane) = *reinterpret_cast<const uint16_t*>(
+                                static_cast<const unsigned char*>(p.lora_b) + from + bytes + 2 * lane);
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_expect(bar, bytes);
+                            if (bytes)
+                                bulk_copy(smem_u32(dst), static_cast<const unsigned char*>(p.lora_b) + from, bytes, bar);
                         }
-                        mbar_arrive(bar);
+                        __syncwarp();
                     }
                 }
             }
             // (every copy started ends, whether or not its tile is still taken)
-            if (*s_abort && p.lora_tma) {
+            if (*s_abort) {
                 uint32_t dummy = 0;
                 for (uint32_t i = 0; i < kShares; ++i)
                     for (uint32_t c = used[i] < p.depth ? 0 : used[i] - p.depth; c < used[i]; ++c)
@@ -530,13 +568,20 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t, t0 = tt * N;
             const uint32_t v0 = (tv * CG + rank) * kTileV, v = v0 + quad * 32 + lane;
             const uint32_t rows = min(N, p.T - t0);
-            uint32_t items = 0, mixed = 0, apart = 0;  // masks of blocks: see TileGroups
+            uint32_t items = 0, listed = 0;
+            uint32_t pass_blocks[2] = {0, 0};  // blocks of passes 1 and 2
+            uint32_t pass_rows[2] = {0, 0};    // lane b: block b's rows in the pass
             if constexpr (LORA) {
                 const TileGroups* g = tile_groups(p, tt);
-                const uint32_t block = lane < kMaxTileT / kBlock ? g->block[lane] : kNoAdapter;
-                mixed = __ballot_sync(0xFFFFFFFFu, block == kMixed);
-                if (CG == 2 && p.tensor && p.apart) apart = __ballot_sync(0xFFFFFFFFu, block < kMixed);
+                listed = g->listed;
                 items = g->items;
+                if (CG == 2 && p.tensor) {
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i) {
+                        pass_blocks[i] = g->blocks[i];
+                        pass_rows[i] = lane < kBlocks ? g->rows[i][lane] : 0u;
+                    }
+                }
                 if (items && tt != staged) {  // the lists, u and scales in shared memory
                     if (!meet()) break;
                     const uint4* words = reinterpret_cast<const uint4*>(g);
@@ -567,21 +612,28 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i)
 #pragma unroll
                     for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
-                bool lora = apart != 0;  // the adapters' accumulator is still to come
+                uint32_t pass = pass_blocks[0] ? 0 : pass_blocks[1] ? 1 : 2;  // the next of the adapters' (2: none)
                 for (uint32_t k0 = 0; k0 < p.slices; ++n) {
                     acc = n & 1;
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) { ok = false; break; }
                     fence_after();
-                    const bool now = lora && k0 == lora_at;
-                    if (now) lora = false;
-                    else k0 = chunk_end(p, k0);
+                    const bool now = LORA && pass < 2 && k0 == lora_at;
+                    uint32_t blocks = 0xFFFFFFFFu, rows_of = 0;
+                    if (now) {
+                        blocks = pass ? pass_blocks[1] : pass_blocks[0];
+                        rows_of = pass ? pass_rows[1] : pass_rows[0];
+                        pass = pass == 0 && pass_blocks[1] ? 1 : 2;
+                    } else {
+                        k0 = chunk_end(p, k0);
+                    }
                     const bool last = k0 == p.slices;
 #pragma unroll
                     for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
                         const uint32_t c0 = (share + kShares * i) * 32;
-                        if (c0 >= N || (now && !(apart >> (c0 / kBlock) & 1))) continue;
+                        if (c0 >= N || !(blocks >> (c0 / kBlock) & 1)) continue;
                         const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
                         const float factor = now && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
+                        const uint32_t take = now ? __shfl_sync(0xFFFFFFFFu, rows_of, c0 / kBlock) : 0xFFFFFFFFu;
 #pragma unroll
                         for (int q = 0; q < 32; q += 16) {
                             float y[16];
@@ -589,6 +641,10 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             if (LORA && now && p.lora_f16) {
 #pragma unroll
                                 for (int c = 0; c < 16; ++c) y[c] *= __shfl_sync(0xFFFFFFFFu, factor, q + c);
+                            }
+                            if (LORA && now) {
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) y[c] = take >> (q + c) & 1 ? y[c] : 0.f;
                             }
 #pragma unroll
                             for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
@@ -605,32 +661,35 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 ++n;
             }
             if constexpr (LORA && CG == 2 && !PROMOTE) {
-                if (apart) {  // moved to the adapters' part, so that the next tile can use the first
+                // With pass 1 the result moves to that pass's accumulator, so that the product's
+                // is free for the next tile's before the stores begin.
+                if (pass_blocks[0]) {
                     const uint32_t from = acc;
                     acc = n & 1;
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) break;
                     fence_after();
                     ++n;
                     for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
-                        const bool mine = apart >> (c0 / kBlock) & 1;
-                        const float factor = mine && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
-                        const float scale = FP8 && mine ? sw : 1.f, row_scale = FP8 && mine ? of_row(p.x_scale, c0) : 1.f;
-#pragma unroll 1
-                        for (uint32_t c1 = c0; c1 < c0 + 32; c1 += 16) {
-                            const uint32_t to = tmem + lanes + acc * p.acc_cols + c1;
-                            float y[16];
-                            tmem_load16(tmem + lanes + from * p.acc_cols + c1, y);
-                            if (mine) {
-                                float z[16];
-                                tmem_load16(to, z);
+                        const uint32_t to = tmem + lanes + acc * p.acc_cols + c0;
+                        float y[32];
+                        tmem_load32(tmem + lanes + from * p.acc_cols + c0, y);
+                        if (pass_blocks[0] >> (c0 / kBlock) & 1) {
+                            if constexpr (FP8) {
+                                const float row_scale = of_row(p.x_scale, c0);
 #pragma unroll
-                                for (int c = 0; c < 16; ++c) {
-                                    if constexpr (FP8) y[c] *= scale * __shfl_sync(0xFFFFFFFFu, row_scale, c1 - c0 + c);
-                                    y[c] = fmaf(__shfl_sync(0xFFFFFFFFu, factor, c1 - c0 + c), z[c], y[c]);
-                                }
+                                for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
                             }
-                            tmem_store16(to, y);
+                            float z[32];
+                            tmem_load32(to, z);
+                            if (p.lora_f16) {
+                                const float factor = of_row(p.factor, c0);
+#pragma unroll
+                                for (int c = 0; c < 32; ++c) z[c] *= __shfl_sync(0xFFFFFFFFu, factor, c);
+                            }
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) y[c] += z[c];
                         }
+                        tmem_store32(to, y);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     release(from);
@@ -639,11 +698,11 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t columns = tmem + lanes + acc * p.acc_cols;
             if (!LORA || v0 < p.V) {
                 for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
-                    if (mixed >> (c0 / kBlock) & 1) continue;
+                    if (listed >> (c0 / kBlock) & 1) continue;
                     float y[32];
                     tmem_load32(columns + c0, y);
                     if constexpr (FP8) {
-                        if (!(apart >> (c0 / kBlock) & 1)) {
+                        if (!LORA || !(pass_blocks[0] >> (c0 / kBlock) & 1)) {
                             const float row_scale = of_row(p.x_scale, c0);
 #pragma unroll
                             for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
@@ -660,7 +719,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 }
             }
             if (LORA && items && v0 < p.V) {
-                if (PROMOTE || apart) {  // an item's columns may have been written by another share
+                if (PROMOTE || pass_blocks[0]) {  // an item's columns may have been written by another share
                     fence_before();
                     if (!meet()) break;
                     fence_after();
@@ -688,16 +747,31 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             uint64_t y2[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                             for (uint32_t j0 = 0; j0 < uc; j0 += 16) {
                                 uint64_t b2[8];
+                                uint32_t ws[8];
+                                if (p.lora_tma) {
 #pragma unroll
-                                for (int q = 0; q < 2; ++q) {
-                                    const uint4 w = *reinterpret_cast<const uint4*>(
-                                        b_tile + b_offset(quad * 32 + lane, j0 / 8 + q, p.b_cols));
-                                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                                    for (int q = 0; q < 2; ++q) {
+                                        const uint4 w = *reinterpret_cast<const uint4*>(
+                                            b_tile + b_offset(quad * 32 + lane, j0 / 8 + q, p.b_cols));
+                                        ws[4 * q] = w.x;
+                                        ws[4 * q + 1] = w.y;
+                                        ws[4 * q + 2] = w.z;
+                                        ws[4 * q + 3] = w.w;
+                                    }
+                                } else {
+                                    // (the values past the rank are whatever follows: left out)
+                                    const uint16_t* row = reinterpret_cast<const uint16_t*>(
+                                        b_tile + (((uint64_t)a * p.V + v0) * p.rank * 2 & 15)) + (quad * 32 + lane) * p.rank + j0;
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        b2[4 * q + e] = pair(p.lora_f16 ? unpack2(ws[e], __half())
-                                                                        : unpack2(ws[e], __nv_bfloat16()));
+                                    for (int e = 0; e < 8; ++e) {
+                                        const uint32_t l = j0 + 2 * e < p.rank ? row[2 * e] : 0u,
+                                                       h = j0 + 2 * e + 1 < p.rank ? row[2 * e + 1] : 0u;
+                                        ws[e] = l | h << 16;
+                                    }
                                 }
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    b2[e] = pair(p.lora_f16 ? unpack2(ws[e], __half()) : unpack2(ws[e], __nv_bfloat16()));
 #pragma unroll
                                 for (int r = 0; r < 8; ++r) {
                                     const ulonglong2* u = reinterpret_cast<const ulonglong2*>(
@@ -883,6 +957,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.u_cols = rank_cols(rank);
     p.b_cols = part_cols(rank);
     p.lora_f16 = lora_dtype == LP_F16;
+    p.lora_bytes = (uint64_t)adapters * V * rank * 2;
     p.lora_tma = rank % 8 == 0 && (uint64_t)adapters * V <= 0x7FFFFFFFu;
     p.early = rank != 0;
     // Rows of x in even tiles of at most 256, a multiple of 16 (of 32 for a pair of CTAs). A
@@ -944,6 +1019,8 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         q.parts = reinterpret_cast<uint16_t*>(ws + space.parts);
         q.tile_t = p.tile_t;
         q.tensor = p.tensor;
+        q.apart = p.apart;
+        q.split = !fp8 && out_dtype == LP_F32;
         q.part_stride = p.part_stride;
         q.lora_f16 = p.lora_f16;
         q.status = p.status;

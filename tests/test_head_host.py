@@ -38,7 +38,7 @@ def test_workspace_size(lib):
     assert lib.lp_head_workspace_size(0, 0) == 256
     assert lib.lp_head_workspace_size(10, 0) == 256
     # header, a page and factors of 256 rows, u padded to 16 columns, its parts in 64
-    assert lib.lp_head_workspace_size(10, 8) == 256 + 2048 + 256 * (4 + 64 + 128)
+    assert lib.lp_head_workspace_size(10, 8) == 256 + 2560 + 256 * (4 + 64 + 128)
     assert lib.lp_head_workspace_size(1, 65) == 0
     assert lib.lp_head_workspace_size(2 ** 31, 64) > 2 ** 38
     assert lib.lp_head_clear_status(None, None) == WORKSPACE
