@@ -31,6 +31,8 @@ typedef enum lp_dtype {
 } lp_dtype;
 
 #define LP_MAX_HIDDEN 32768u /* widest row of lp_head_norm */
+#define LP_MIN_REPETITION 9.5367432e-07f /* 2^-20 */
+#define LP_MAX_REPETITION 1048576.0f     /* 2^20 */
 #define LP_MAX_RANK 64u      /* largest adapter rank of lp_head_project */
 
 /*
@@ -124,10 +126,10 @@ lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H,
  *   workspace       the status word
  * A row whose mask allows nothing is all -inf. A masked value is -inf whatever it was.
  * The history of a request with repetition 1 and frequency = presence = 0 is not read.
- * Device checks, each giving the request's rows NaN: row, history and bias offsets within
+ * Device checks, each giving the rows concerned NaN: row, history and bias offsets within
  * their totals, nondecreasing, every row in a request, mask_index < mask_rows
- * (LP_ERR_OFFSETS); repetition positive and finite, frequency and presence finite
- * (LP_ERR_PENALTY). A history or bias token >= V is skipped (LP_ERR_TOKEN_RANGE), bias
+ * (LP_ERR_OFFSETS); repetition within LP_MIN_REPETITION ... LP_MAX_REPETITION, frequency and
+ * presence finite (LP_ERR_PENALTY). A history or bias token >= V is skipped (LP_ERR_TOKEN_RANGE), bias
  * ids not strictly ascending set LP_ERR_OFFSETS (that request's biases are unspecified).
  */
 lp_status lp_head_process(const void *logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,

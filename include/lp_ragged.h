@@ -59,8 +59,8 @@ typedef enum lp_status {
     LP_ERR_TEMPERATURE = 8,  /* device: a temperature that is not a positive finite number  */
     LP_ERR_DTYPE = 9,        /* a type, or a combination of types, that the call does not take */
     LP_ERR_ADAPTER = 10,     /* device: an adapter id past the adapters                     */
-    LP_ERR_PENALTY = 11,     /* device: a repetition penalty that is not a positive finite
-                                number, or another penalty that is not finite               */
+    LP_ERR_PENALTY = 11,     /* device: a repetition penalty out of range, or another
+                                penalty that is not finite                                  */
     LP_ERR_TIMEOUT = 12      /* device: a bounded wait inside a kernel ran out              */
 } lp_status;
 

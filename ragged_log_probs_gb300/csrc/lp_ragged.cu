@@ -531,7 +531,7 @@ const char* lp_ragged_strerror(lp_status status) {
         case LP_ERR_TEMPERATURE: return "a temperature is not a positive finite number";
         case LP_ERR_DTYPE: return "a type, or a combination of types, that the call does not take";
         case LP_ERR_ADAPTER: return "an adapter id is not below the number of adapters";
-        case LP_ERR_PENALTY: return "a repetition penalty is not positive and finite, or another penalty is not finite";
+        case LP_ERR_PENALTY: return "a repetition penalty is out of range, or another penalty is not finite";
         case LP_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
         default: return "unknown lp_status";
     }

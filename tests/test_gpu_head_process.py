@@ -278,3 +278,17 @@ def test_graph_replay_and_other_stream():
     graph.replay()
     torch.cuda.synchronize()
     check(out, ref.process(c["x"], history=c["history"], rep=c["rep"]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_many_biases_and_uneven_requests(dtype):
+    # more biases in a slice than a CTA keeps, requests of 0 to 70 rows
+    V = 9000
+    c = make(90, V, 6, dtype, hist=500, seed=17)
+    c["off"] = [0, 1, 1, 5, 75, 76, 90]
+    g = torch.Generator().manual_seed(9)
+    c["bias"] = [{int(t): float(torch.randn(1, generator=g)) for t in torch.randperm(V, generator=g)[:3000].sort().values}
+                 for _ in range(6)]
+    out, status = call(c)
+    assert status == 0
+    check(out, want_of(c))
