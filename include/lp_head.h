@@ -38,7 +38,7 @@ typedef enum lp_dtype {
 /*
  * Bytes of scratch the calls below need: a 256-byte header with the status word, and for
  * lp_head_project with adapters, one f32 vector of `rank` values a row and the rows' order.
- * lp_head_norm and lp_head_process only use the header (T = rank = 0).
+ * lp_head_norm only uses the header (T = rank = 0); lp_head_process has a size of its own.
  */
 size_t lp_head_workspace_size(uint32_t T, uint32_t rank);
 
@@ -123,7 +123,8 @@ lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H,
  *                   where token v is allowed; NULL: none
  *   mask_index      device, int32[T]: row t's mask row, negative: row t is not masked;
  *                   NULL: row t has mask row t (mask_rows >= T)
- *   workspace       the status word
+ *   workspace       lp_head_process_workspace_size(B, history_total) bytes: the status word
+ *                   and, for histories of some thousand tokens, room to sort them
  * A row whose mask allows nothing is all -inf. A masked value is -inf whatever it was.
  * The history of a request with repetition 1 and frequency = presence = 0 is not read.
  * Device checks, each giving the rows concerned NaN: row, history and bias offsets within
@@ -132,6 +133,8 @@ lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H,
  * presence finite (LP_ERR_PENALTY). A history or bias token >= V is skipped (LP_ERR_TOKEN_RANGE), bias
  * ids not strictly ascending set LP_ERR_OFFSETS (that request's biases are unspecified).
  */
+size_t lp_head_process_workspace_size(uint32_t B, uint32_t history_total);
+
 lp_status lp_head_process(const void *logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
                           const uint32_t *row_offsets, uint32_t B, const uint32_t *history,
                           const uint32_t *history_offsets, uint32_t history_total, const uint32_t *prompt_lens,

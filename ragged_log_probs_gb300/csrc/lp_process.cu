@@ -1,23 +1,20 @@
 // Processing of logits before they are scored or sampled: penalties for repeated tokens,
 // biases, grammar masks (include/lp_head.h).
 //
-// A CTA takes a slice of the vocabulary of one logits row. It copies the slice from logits to
-// out, masked, and then corrects what differs from a copy, value by value: the tokens of the
-// request's history and of its biases. For the history it keeps a table in shared memory, 16
-// bits a token of the slice: the count in the output part and, in the top bit, whether the
-// prompt holds it (adds and ors of integers, so their order does not matter). A first pass over
-// the history counts; a second one, after the copy, takes each token's word out of the table
-// (the first thread to come gets it) and applies the penalties to the one value. For a request
-// whose output part could overflow 15 bits the words have 32 bits and the slice is done in two
-// halves. Every CTA of a row reads the history, from L2, so slices are long: 32768 tokens.
+// A CTA takes a slice of the vocabulary of one logits row. For the request's history it keeps a
+// table in shared memory, 16 bits a token of the slice: the count in the output part and, in
+// the top bit, whether the prompt holds it (adds and ors of integers, so their order does not
+// matter); 32 bits, and the slice in two halves, for a request whose output part could overflow
+// 15 bits. With many tokens of the slice in the table every value looks at its word while the
+// slice is copied from logits to out. With few the slice is copied first, and then each
+// token's word is taken out of the table (the first thread to come gets it) and its value
+// corrected. Biases are added last. Long histories are sorted by slices first (k_sort_history,
+// 4096 tokens a CTA, into the workspace); short ones are read by every CTA of a row.
 //
 // Bound by HBM: a row is read once and written once, and a vector whose mask bits are all 0 is
 // not read. What had to be hidden is the time before the copy (who the row belongs to, its
-// parameters, its history: a few reads that wait for each other): the slice is asked for in L2
-// at the very start (256 rows of 128256 f32 without lists: 57 -> 44 us, a plain copy takes 42).
-// Applying the penalties during the copy, from the table, costs every warp that holds one token
-// of the history the instructions for 128 values (histories to 30,000 tokens: 83 us for the same
-// rows); a cluster of CTAs that sends each token to its owner's table took 138 us.
+// parameters, its history: reads that wait for each other): the slice is asked for in L2 at
+// the very start (256 rows of 128256 f32 without lists: 57 -> 41 us, a plain copy takes 42).
 #include "lp_head_common.h"
 
 namespace {
@@ -29,7 +26,10 @@ constexpr uint32_t kMaxSlice = 32768;  // tokens of a slice: a 64 KB table, thre
 constexpr uint32_t kMinSlice = 1024;
 constexpr uint32_t kResident = 3;      // CTAs per SM
 constexpr uint32_t kBatch = 4;         // vectors a thread has in flight
-constexpr uint32_t kPrompt16 = 0x8000u, kPrompt32 = 0x80000000u;
+constexpr uint32_t kHeld = 4;          // tokens of a history that a thread keeps in registers
+constexpr uint32_t kChunk = 4096;      // tokens of a history sorted together
+constexpr uint32_t kSortFrom = 4096;   // mean length from which histories are sorted first
+constexpr uint32_t kMaxSlices = 256;
 
 struct ProcessParams {
     const void* logits;
@@ -45,6 +45,8 @@ struct ProcessParams {
     const uint32_t* bias_offsets;
     const uint32_t* mask;
     const int32_t* mask_index;
+    uint32_t* sorted;  // [history_total], NULL: histories are not sorted
+    uint32_t* bounds;  // [chunks][slices + 1]
     float* out;
     uint32_t* status;
     uint64_t stride, out_stride, mask_stride;
@@ -145,57 +147,41 @@ __device__ __forceinline__ void describe(const ProcessParams& p, uint32_t t, Row
     *row = r;
 }
 
-// Every token of h[0, n), four at a time; returns whether one of this thread's is >= limit.
-template <typename F>
-__device__ __forceinline__ bool each_token(const uint32_t* h, uint32_t n, uint32_t limit, F use) {
-    const uint32_t head = min(n, (uint32_t)(-(reinterpret_cast<uintptr_t>(h) >> 2) & 3));  // to a 16-byte boundary
-    const uint32_t quads = (n - head) / 4, last = head + 4 * quads;
-    uint32_t most = 0;
-    if (threadIdx.x < head) { const uint32_t v = h[threadIdx.x]; use(v); most = v; }
-    if (threadIdx.x < n - last) { const uint32_t v = h[last + threadIdx.x]; use(v); most = max(most, v); }
-    const uint4* h4 = reinterpret_cast<const uint4*>(h + head);
-#pragma unroll 4
-    for (uint32_t k = threadIdx.x; k < quads; k += kThreads) {
-        const uint4 v = h4[k];
-        use(v.x);
-        use(v.y);
-        use(v.z);
-        use(v.w);
-        most = max(most, max(max(v.x, v.y), max(v.z, v.w)));
+// A stretch of tokens that a CTA looks at: the request's history, or what a sorted chunk of it
+// has in the slice.
+struct Tokens {
+    const uint32_t* at;
+    uint32_t n;
+    uint32_t prompt;  // history: its first tokens are the prompt; sorted: bit 31 tells
+    bool sorted;
+    __device__ __forceinline__ uint32_t token(uint32_t entry) const { return sorted ? entry & 0x7FFFFFFFu : entry; }
+    __device__ __forceinline__ bool in_prompt(uint32_t i, uint32_t entry) const {
+        return sorted ? entry >> 31 : i < prompt;
     }
-    return most >= limit;
-}
+};
 
 // The table of tokens [lo, lo + size): a word of 16 bits (WIDE: 32) a token.
 template <bool WIDE>
 struct Table {
     uint32_t* words;
     uint32_t lo, size;
+    static constexpr uint32_t kAll = WIDE ? 0xFFFFFFFFu : 0xFFFFu;
+    static constexpr uint32_t kPrompt = WIDE ? 0x80000000u : 0x8000u;
     __device__ __forceinline__ uint32_t shift(uint32_t slot) const { return WIDE ? 0 : slot % 2 * 16; }
     __device__ __forceinline__ uint32_t* word(uint32_t slot) const { return words + (WIDE ? slot : slot / 2); }
 
-    // Count the row's history; returns whether a token was past the vocabulary.
-    __device__ __forceinline__ bool count(const ProcessParams& p, const Row& row) const {
-        const uint32_t* h = p.history + row.h0;
-        const bool in_prompt = each_token(h, row.prompt, p.V, [&](uint32_t v) {
-            if (v - lo < size) atomicOr(word(v - lo), (WIDE ? kPrompt32 : kPrompt16) << shift(v - lo));
-        });
-        const bool in_output = each_token(h + row.prompt, row.h1 - row.h0 - row.prompt, p.V, [&](uint32_t v) {
-            if (v - lo < size) atomicAdd(word(v - lo), 1u << shift(v - lo));
-        });
-        return in_prompt || in_output;
+    __device__ __forceinline__ uint32_t count(const Tokens& s, uint32_t i, uint32_t entry) const {  // 1: of the slice
+        const uint32_t slot = s.token(entry) - lo;
+        if (slot >= size) return 0;
+        if (s.in_prompt(i, entry)) atomicOr(word(slot), kPrompt << shift(slot));
+        else atomicAdd(word(slot), 1u << shift(slot));
+        return 1;
     }
-    // Give each token's word to one thread: use(token, in prompt, count). Empties the table.
-    template <typename F>
-    __device__ __forceinline__ void take(const ProcessParams& p, const Row& row, F use) const {
-        (void)each_token(p.history + row.h0, row.h1 - row.h0, p.V, [&](uint32_t v) {
-            const uint32_t slot = v - lo;
-            if (slot >= size) return;
-            const uint32_t all = WIDE ? 0xFFFFFFFFu : 0xFFFFu;
-            if (!(*static_cast<volatile uint32_t*>(word(slot)) & all << shift(slot))) return;  // taken
-            const uint32_t w = atomicAnd(word(slot), ~(all << shift(slot))) >> shift(slot) & all;
-            if (w) use(v, w & ~(WIDE ? kPrompt32 : kPrompt16));
-        });
+    // The token's word, for the first thread that asks (0 for others), which empties it.
+    __device__ __forceinline__ uint32_t take(uint32_t slot) const {
+        if (slot >= size) return 0;
+        if (!(*static_cast<volatile uint32_t*>(word(slot)) >> shift(slot) & kAll)) return 0;
+        return atomicAnd(word(slot), ~(kAll << shift(slot))) >> shift(slot) & kAll;
     }
 };
 
@@ -211,11 +197,98 @@ __device__ __forceinline__ void prefetch_slice(const T* row, uint32_t lo, uint32
     }
 }
 
+constexpr uint32_t kSortThreads = 512;
+constexpr uint32_t kSortEach = kChunk / kSortThreads;
+
+// Histories are sorted in chunks of kChunk tokens. Request b's chunk c has number
+// b + h0 / kChunk + c: no two have the same, and there are at most B + total / kChunk + 1.
+__device__ __forceinline__ uint32_t first_chunk(const ProcessParams& p, uint32_t b) {
+    return b + p.history_offsets[b] / kChunk;
+}
+
+// Sort a chunk by slices: sorted[h0 + c kChunk ...] gets its tokens (bit 31: of the prompt),
+// bounds[chunk][k] where slice k's begin. A warp takes the places of its tokens of one slice
+// together; their order within a slice is left open. grid: a CTA a chunk
+__global__ void __launch_bounds__(kSortThreads) k_sort_history(ProcessParams p) {
+    __shared__ uint32_t place[kMaxSlices + 1];
+    __shared__ uint32_t s_request;
+    pdl_wait();
+    pdl_trigger();  // after the wait: the copy may read logits, which are complete now
+    const uint32_t tid = threadIdx.x, lane = tid & 31, chunk = blockIdx.x;
+    for (uint32_t k = tid; k <= p.slices; k += kSortThreads) place[k] = 0;
+    if (tid < 32) {  // the last request whose first chunk is not past this one, 32 at a time
+        uint32_t lo = 0, n = p.B;
+        while (n > 1) {
+            const uint32_t step = (n + 31) / 32, i = lane * step;
+            const uint32_t below = __ballot_sync(0xFFFFFFFFu, i < n && first_chunk(p, lo + (i < n ? i : 0)) <= chunk);
+            const uint32_t k = 31 - __clz(below | 1u);
+            lo += k * step;
+            n = min(step, n - k * step);
+        }
+        if (lane == 0) s_request = lo;
+    }
+    __syncthreads();
+    const uint32_t b = s_request, h0 = p.history_offsets[b], h1 = p.history_offsets[b + 1];
+    const bool neutral = (!p.repetition || p.repetition[b] == 1.f) && (!p.frequency || p.frequency[b] == 0.f) &&
+                         (!p.presence || p.presence[b] == 0.f);
+    const uint32_t before = chunk - first_chunk(p, b);  // chunks of the request before this one
+    if (neutral || h0 > h1 || h1 > p.history_total || chunk < first_chunk(p, b) ||
+        (uint64_t)before * kChunk >= h1 - h0)
+        return;  // (no chunk, or not read: see describe)
+    const uint32_t from = before * kChunk, n = min(kChunk, h1 - h0 - from);
+    const uint32_t prompt = p.prompt_lens ? p.prompt_lens[b] : 0u;
+    uint32_t v[kSortEach], slice[kSortEach];
+    bool outside = false;
+#pragma unroll
+    for (uint32_t k = 0; k < kSortEach; ++k) {
+        const uint32_t i = tid + k * kSortThreads;
+        v[k] = i < n ? p.history[h0 + from + i] : 0u;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kSortEach; ++k) {
+        const uint32_t i = tid + k * kSortThreads;
+        slice[k] = i < n && v[k] < p.V ? v[k] / p.slice : 0xFFFFFFFFu;
+        outside |= i < n && v[k] >= p.V;
+        if (from + i < prompt) v[k] |= 0x80000000u;
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, slice[k]);
+        if (slice[k] != 0xFFFFFFFFu && (peers & ((1u << lane) - 1u)) == 0) atomicAdd(place + slice[k] + 1, __popc(peers));
+    }
+    __syncthreads();
+    if (tid < 32) {  // place[k]: tokens of the slices before k
+        uint32_t sum = 0;
+        for (uint32_t k0 = 0; k0 <= p.slices; k0 += 32) {
+            uint32_t x = k0 + lane <= p.slices ? place[k0 + lane] : 0u;
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+                if (lane >= d) x += y;
+            }
+            x += sum;
+            if (k0 + lane <= p.slices) {
+                place[k0 + lane] = x;
+                p.bounds[(uint64_t)chunk * (p.slices + 1) + k0 + lane] = x;
+            }
+            sum = __shfl_sync(0xFFFFFFFFu, x, 31);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t k = 0; k < kSortEach; ++k) {
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, slice[k]), rank = __popc(peers & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (slice[k] != 0xFFFFFFFFu && rank == 0) at = atomicAdd(place + slice[k], __popc(peers));
+        at = __shfl_sync(0xFFFFFFFFu, at, __ffs(peers) - 1) + rank;
+        if (slice[k] != 0xFFFFFFFFu) p.sorted[h0 + from + at] = v[k];
+    }
+    if (outside) flag(p.status, LP_ERR_TOKEN_RANGE);
+}
+
 // grid: T x slices CTAs
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p) {
     extern __shared__ __align__(16) uint32_t table[];  // slice / 2 words
     __shared__ Row s_row;
+    __shared__ uint32_t s_in_slice;
     __shared__ uint32_t s_mask[kMaxSlice / 32 + 2];    // mask words of the slice
     pdl_trigger();
     const uint32_t tid = threadIdx.x;
@@ -226,11 +299,13 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
     const float ninf = __int_as_float(0xff800000);
     if (p.history)
         for (uint32_t i = tid; i < (p.slice + 7) / 8; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
-    pdl_wait();
+    if (tid == 0) s_in_slice = 0;
+    if (!p.sorted) pdl_wait();  // (the sort has waited for what logits and the lists come from)
     if (!p.mask) prefetch_slice(in, lo, hi);
     if (tid < 32) describe(p, t, &s_row, part == 0);
     __syncthreads();
     const Row row = s_row;
+    if (p.sorted) pdl_wait();
     if (row.request < 0) {
         for (uint32_t v = lo + tid; v < hi; v += kThreads) out[v] = __int_as_float(0x7fffffff);
         return;
@@ -247,7 +322,41 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
     // 15 bits hold any count of an output part of up to 32767 tokens
     const bool wide = row.counted && row.h1 - row.h0 - row.prompt > 0x7FFFu;
     const Table<false> counts = {table, lo, hi - lo};
-    if (row.counted && !wide && counts.count(p, row) && part == 0) flag(p.status, LP_ERR_TOKEN_RANGE);
+    const uint32_t pieces = !row.counted ? 0 : p.sorted ? (row.h1 - row.h0 + kChunk - 1) / kChunk : 1;
+    const auto piece = [&](uint32_t c) -> Tokens {
+        if (!p.sorted) return {p.history + row.h0, row.h1 - row.h0, row.prompt, false};
+        const uint32_t* bounds = p.bounds + (uint64_t)(row.request + row.h0 / kChunk + c) * (p.slices + 1) + part;
+        const uint32_t limit = min(kChunk, row.h1 - row.h0 - c * kChunk);
+        const uint32_t from = min(bounds[0], limit), to = min(bounds[1], limit);
+        return {p.sorted + row.h0 + (uint64_t)c * kChunk + from, to > from ? to - from : 0u, 0u, true};
+    };
+    bool outside = false;
+    uint32_t mine = 0;  // tokens of the slice that this thread has counted
+    const auto count_all = [&](const auto& into) {
+        for (uint32_t c = 0; c < pieces; ++c) {
+            const Tokens s = piece(c);
+            for (uint32_t i0 = tid; i0 < s.n; i0 += kHeld * kThreads) {
+                uint32_t e[kHeld];
+#pragma unroll
+                for (uint32_t k = 0; k < kHeld; ++k) e[k] = i0 + k * kThreads < s.n ? s.at[i0 + k * kThreads] : 0u;
+#pragma unroll
+                for (uint32_t k = 0; k < kHeld; ++k) {
+                    if (i0 + k * kThreads >= s.n) break;
+                    outside |= s.token(e[k]) >= p.V;
+                    mine += into.count(s, i0 + k * kThreads, e[k]);
+                }
+            }
+        }
+    };
+    // Many tokens of the slice in the table (1 in 32): looked at during the copy.
+    bool dense = false;
+    if (row.counted && !wide) {
+        count_all(counts);
+        mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+        if (tid % 32 == 0 && mine) atomicAdd(&s_in_slice, mine);
+        __syncthreads();
+        dense = s_in_slice > (hi - lo) / 32;
+    }
     // this thread's first bias, long before it is needed
     const bool biased = row.b1 - row.b0 > tid;
     const uint32_t bias_at = biased ? p.bias_tokens[row.b0 + tid] : 0u;
@@ -257,8 +366,12 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
     // the copy
     const uint32_t first = VEC ? min(lo + ((-(uint32_t)(reinterpret_cast<uintptr_t>(out + lo) >> 2)) & 3u), hi) : hi;
     const uint32_t vecs = (hi - first) / 4, vec_end = first + 4 * vecs;
-    for (uint32_t v = lo + tid; v < first; v += kThreads) out[v] = allowed(v) ? to_f32(in[v]) : ninf;
-    for (uint32_t v = vec_end + tid; v < hi; v += kThreads) out[v] = allowed(v) ? to_f32(in[v]) : ninf;
+    const auto one = [&](uint32_t v) {
+        const uint32_t w = dense ? *counts.word(v - lo) >> counts.shift(v - lo) & 0xFFFFu : 0u;
+        out[v] = !allowed(v) ? ninf : w ? penalised(to_f32(in[v]), w & 0x7FFF, row.q) : to_f32(in[v]);
+    };
+    for (uint32_t v = lo + tid; v < first; v += kThreads) one(v);
+    for (uint32_t v = vec_end + tid; v < hi; v += kThreads) one(v);
     if constexpr (VEC) {
         const T* in4 = in + first;
         float4* out4 = reinterpret_cast<float4*>(out + first);
@@ -282,6 +395,16 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
                 const uint32_t i = i0 + u * kThreads;
                 if (i >= vecs) break;
                 float4 y = x[u];
+                if (dense) {
+                    // the words of 4 tokens from slot 4 i + (first - lo) on: out of two or three
+                    const uint32_t slot = first - lo + 4 * i, odd = slot % 2 * 16;
+                    const uint32_t* w = table + slot / 2;
+                    const uint32_t w0 = __funnelshift_r(w[0], w[1], odd), w1 = __funnelshift_r(w[1], w[odd ? 2 : 1], odd);
+                    if (w0 & 0xFFFF) y.x = penalised(y.x, w0 & 0x7FFF, row.q);
+                    if (w0 >> 16) y.y = penalised(y.y, w0 >> 16 & 0x7FFF, row.q);
+                    if (w1 & 0xFFFF) y.z = penalised(y.z, w1 & 0x7FFF, row.q);
+                    if (w1 >> 16) y.w = penalised(y.w, w1 >> 16 & 0x7FFF, row.q);
+                }
                 if (masked) {
                     y.x = bits[u] & 1 ? y.x : ninf;
                     y.y = bits[u] & 2 ? y.y : ninf;
@@ -293,24 +416,42 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
         }
     }
 
-    // the history's tokens
-    const auto correct = [&](uint32_t v, uint32_t count) {
-        if (allowed(v)) out[v] = penalised(out[v], count, row.q);
+    // few tokens of the history: corrected now
+    const auto correct = [&](const auto& from) {
+        for (uint32_t c = 0; c < pieces; ++c) {
+            const Tokens s = piece(c);
+            for (uint32_t i0 = tid; i0 < s.n; i0 += kHeld * kThreads) {
+                uint32_t v[kHeld], w[kHeld];
+                float x[kHeld];
+#pragma unroll
+                for (uint32_t k = 0; k < kHeld; ++k) v[k] = i0 + k * kThreads < s.n ? s.token(s.at[i0 + k * kThreads]) : p.V;
+#pragma unroll
+                for (uint32_t k = 0; k < kHeld; ++k) {
+                    w[k] = v[k] < p.V ? from.take(v[k] - from.lo) : 0u;
+                    if (w[k] && !allowed(v[k])) w[k] = 0;
+                }
+#pragma unroll
+                for (uint32_t k = 0; k < kHeld; ++k) x[k] = w[k] ? out[v[k]] : 0.f;
+#pragma unroll
+                for (uint32_t k = 0; k < kHeld; ++k)
+                    if (w[k]) out[v[k]] = penalised(x[k], w[k] & (from.kPrompt - 1), row.q);
+            }
+        }
     };
-    if (row.counted && !wide) {
+    if (row.counted && !wide && !dense) {
         __syncthreads();
-        counts.take(p, row, correct);
-    } else if (row.counted) {
+        correct(counts);
+    } else if (wide) {
         const uint32_t half = (p.slice + 7) / 8 * 4;  // (a table of 16 bits a token holds half as many of 32)
-        for (uint32_t from = lo; from < hi; from += half) {
-            const Table<true> part_counts = {table, from, min(half, hi - from)};
-            const bool outside = part_counts.count(p, row);
-            if (outside && part == 0 && from == lo) flag(p.status, LP_ERR_TOKEN_RANGE);
+        for (uint32_t first_token = lo; first_token < hi; first_token += half) {
+            const Table<true> wide_counts = {table, first_token, min(half, hi - first_token)};
+            count_all(wide_counts);
             __syncthreads();
-            part_counts.take(p, row, correct);
+            correct(wide_counts);
             __syncthreads();
         }
     }
+    if (outside && part == 0) flag(p.status, LP_ERR_TOKEN_RANGE);
     // the biases: no token has two
     if (row.b1 > row.b0) {
         __syncthreads();
@@ -334,11 +475,16 @@ std::atomic<uint64_t> g_smem_set[2];
 template <typename T>
 lp_status launch_process(const ProcessParams& p, bool vec, unsigned ctas, lp_stream_t s) {
     void (*kernel)(ProcessParams) = vec ? k_process<T, true> : k_process<T, false>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), kMaxSlice * 2, &g_smem_set<T>[vec])) return LP_ERR_CUDA;
-    return launch(kernel, dim3(ctas), kThreads, (size_t)p.slice * 2, s, 1, p);
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), kMaxSlice * 2 + 16, &g_smem_set<T>[vec])) return LP_ERR_CUDA;
+    return launch(kernel, dim3(ctas), kThreads, (size_t)p.slice * 2 + 16, s, 1, p);
 }
 
 }  // namespace
+
+extern "C" size_t lp_head_process_workspace_size(uint32_t B, uint32_t history_total) {
+    if (B == 0 || history_total / B < kSortFrom) return kHeaderBytes;
+    return kHeaderBytes + (((size_t)B + history_total / kChunk + 1) * (kMaxSlices + 1) + history_total) * 4;
+}
 
 extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
                                      const uint32_t* row_offsets, uint32_t B, const uint32_t* history,
@@ -365,7 +511,7 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     if (static_cast<const void*>(out) == logits && (dtype != LP_F32 || stride != out_stride)) return LP_ERR_SHAPE;
     const int sms = sm_count();
     if (sms == 0) return LP_ERR_CUDA;
-    ProcessParams p;
+    ProcessParams p = {};
     p.logits = logits;
     p.row_offsets = row_offsets;
     p.history = history_total ? history : nullptr;
@@ -398,6 +544,7 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     if (T * least < room) {
         const uint64_t most = (V + (uint64_t)kMinSlice - 1) / kMinSlice;
         slices = room / T < most ? room / T : most;
+        if (slices > kMaxSlices) slices = kMaxSlices;
         if (slices < least) slices = least;
     } else {
         const auto cost = [&](uint64_t n) {  // waves, by the length of a slice and a part for the history
@@ -408,6 +555,16 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     }
     p.slice = (uint32_t)(((V + slices - 1) / slices + 7) / 8 * 8);
     p.slices = (V + p.slice - 1) / p.slice;
+    // Long histories are sorted by slices first; below that, reading them in every CTA costs less
+    // than a second kernel.
+    if (p.history && history_total / B >= kSortFrom) {
+        if (workspace_bytes < lp_head_process_workspace_size(B, history_total) || p.slices > kMaxSlices) return LP_ERR_WORKSPACE;
+        p.bounds = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
+        const uint32_t chunks = B + history_total / kChunk + 1;
+        p.sorted = p.bounds + (size_t)chunks * (p.slices + 1);
+        const lp_status st = launch(k_sort_history, dim3(chunks), kSortThreads, 0, stream, 1, p);
+        if (st != LP_OK) return st;
+    }
     // 4 values at a time where logits and out have their 4-value boundaries at the same tokens
     const bool vec = stride % 4 == out_stride % 4 &&
                      (reinterpret_cast<uintptr_t>(logits) / e) % 4 == (reinterpret_cast<uintptr_t>(out) / 4) % 4;

@@ -37,6 +37,8 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
                                     vp, u64, u32, vp, vp, u64, vp, sz, vp]
     lib.lp_head_process.restype = ctypes.c_int
+    lib.lp_head_process_workspace_size.argtypes = [u32, u32]
+    lib.lp_head_process_workspace_size.restype = sz
 
 
 def _pkg():
@@ -102,19 +104,21 @@ def _new(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
-def head_workspace_size(T: int = 0, rank: int = 0) -> int:
-    """Bytes of scratch for a call: of ``project`` with adapters of that rank over T rows,
-    or (T = rank = 0) of the others, which only use the status word."""
-    n = int(_pkg().load().lp_head_workspace_size(T, rank))
+def head_workspace_size(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0) -> int:
+    """Bytes of scratch that serve every call of these sizes: ``project`` with adapters of
+    that rank over T rows, ``process_logits`` of that many requests with that many history
+    tokens in all (0: only the status word)."""
+    lib = _pkg().load()
+    n = int(lib.lp_head_workspace_size(T, rank))
     if n == 0:
         raise ValueError(f"rank {rank} exceeds {LP_MAX_RANK}")
-    return n
+    return max(n, int(lib.lp_head_process_workspace_size(requests, history)))
 
 
-def new_head_workspace(T: int = 0, rank: int = 0, device=None) -> torch.Tensor:
-    """A zeroed workspace (uint8). Its status word collects the bits of every call that is
-    given it, until ``clear_status``; ``read_status`` reads it."""
-    return torch.zeros(head_workspace_size(T, rank), dtype=torch.uint8,
+def new_head_workspace(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0, device=None) -> torch.Tensor:
+    """A zeroed workspace (uint8) of ``head_workspace_size``. Its status word collects the
+    bits of every call that is given it, until ``clear_status``; ``read_status`` reads it."""
+    return torch.zeros(head_workspace_size(T, rank, requests, history), dtype=torch.uint8,
                        device=torch.device("cuda") if device is None else device)
 
 

@@ -56,7 +56,8 @@ def make(T, V, B, dtype=torch.float32, hist=20, n_bias=3, masked=True, seed=0):
 
 def call(c, x=None, **kw):
     ws = kw.pop("workspace", None)
-    ws = lp.new_head_workspace() if ws is None else ws
+    if ws is None:
+        ws = lp.new_head_workspace(requests=len(c["off"]) - 1, history=sum(len(h) for h in c["history"]))
     f = lambda v: torch.tensor(v, dtype=torch.float32).cuda()
     args = dict(row_offsets=i32(c["off"]), history=flat(c["history"]), history_offsets=offsets(c["history"]),
                 prompt_lens=i32(c["prompt"]), repetition=f(c["rep"]), frequency=f(c["freq"]), presence=f(c["pres"]),
@@ -292,3 +293,33 @@ def test_many_biases_and_uneven_requests(dtype):
     out, status = call(c)
     assert status == 0
     check(out, want_of(c))
+
+
+@pytest.mark.parametrize("T,B,V", [(3, 3, 50000), (6, 2, 9000), (40, 40, 40000)])
+def test_long_histories_are_sorted_first(T, B, V):
+    # a mean of more than 4096 tokens; one request neutral, one with few, prompts of any length
+    c = make(T, V, B, hist=10, n_bias=30, seed=18)
+    g = torch.Generator().manual_seed(7)
+    lens = [9000 + int(torch.randint(0, 2000, (1,), generator=g)) for _ in range(B)]
+    c["history"] = [(V * torch.rand(n, generator=g) ** 3).long().clamp_max(V - 1).tolist() for n in lens]
+    c["prompt"] = [n // 3 for n in lens]
+    if B > 2:
+        c["history"][1], c["prompt"][1] = [5, 5, V - 1], 1
+    out, status = call(c)
+    assert status == 0
+    check(out, want_of(c))
+    c["history"][-1][100] = V
+    d = dict(c, history=[[t for t in h if t < V] for h in c["history"]])
+    d["prompt"] = list(c["prompt"])
+    d["prompt"][-1] -= 1
+    c["rep"][-1] = d["rep"][-1] = 1.25
+    out, status = call(c)
+    assert status == bits(5)
+    check(out, want_of(d))
+
+
+def test_workspace_for_long_histories_is_checked():
+    c = make(2, 5000, 2, seed=19)
+    c["history"], c["prompt"] = [[1, 2, 3] * 3000] * 2, [0, 0]
+    with pytest.raises(lp.LpError):
+        call(c, workspace=lp.new_head_workspace())

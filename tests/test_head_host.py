@@ -42,6 +42,8 @@ def test_workspace_size(lib):
     assert lib.lp_head_workspace_size(1, 65) == 0
     assert lib.lp_head_workspace_size(2 ** 31, 64) > 2 ** 38
     assert lib.lp_head_clear_status(None, None) == WORKSPACE
+    assert lib.lp_head_process_workspace_size(0, 0) == 256 and lib.lp_head_process_workspace_size(4, 4000) == 256
+    assert lib.lp_head_process_workspace_size(2, 2 ** 31) > 2 ** 33
 
 
 def _norm(lib, x=FAKE, residual=None, w=FAKE, dtype=BF16, wdtype=BF16, T=4, H=64, xs=64, rs=64, rows=None, n=4,
