@@ -21,10 +21,10 @@ namespace {
 
 using namespace lph;
 
-constexpr uint32_t kThreads = 512;
-constexpr uint32_t kMaxSlice = 32768;  // tokens of a slice: a 64 KB table, three CTAs per SM
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kMaxSlice = 24576;  // tokens of a slice: a 48 KB table, four CTAs per SM
 constexpr uint32_t kMinSlice = 1024;
-constexpr uint32_t kResident = 3;      // CTAs per SM
+constexpr uint32_t kResident = 4;      // CTAs per SM
 constexpr uint32_t kBatch = 4;         // vectors a thread has in flight
 constexpr uint32_t kHeld = 4;          // tokens of a history that a thread keeps in registers
 constexpr uint32_t kChunk = 4096;      // tokens of a history sorted together
@@ -197,7 +197,7 @@ __device__ __forceinline__ void prefetch_slice(const T* row, uint32_t lo, uint32
     }
 }
 
-constexpr uint32_t kSortThreads = 512;
+constexpr uint32_t kSortThreads = 256;
 constexpr uint32_t kSortEach = kChunk / kSortThreads;
 
 // Histories are sorted in chunks of kChunk tokens. Request b's chunk c has number

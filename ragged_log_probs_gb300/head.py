@@ -46,6 +46,18 @@ def _pkg():
     return lp
 
 
+# The calls below are made once a token, and a launch takes under 2 us: the checks are kept to
+# one look at each tensor, and what is wrong is worked out only once something is.
+_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_F32 = (torch.float32,)
+
+
+def _stream(stream, device: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream
+
+
 def _check_device(t: torch.Tensor, name: str, device: int) -> None:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
@@ -53,47 +65,62 @@ def _check_device(t: torch.Tensor, name: str, device: int) -> None:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{device}")
 
 
-def _matrix(t: torch.Tensor, name: str, device: int, rows: Optional[int] = None, cols: Optional[int] = None,
-            dtype: Optional[torch.dtype] = None):
-    """Pointer and row stride of a 2-D tensor whose last dimension is contiguous."""
+def _refuse_matrix(t, name: str, device: int, shape, dtype) -> None:
     _check_device(t, name, device)
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, has {t.dim()} dimensions")
-    r, c = t.shape
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{name} must be [{rows if rows is not None else r}, {cols if cols is not None else c}], "
-                         f"is [{r}, {c}]")
-    if dtype is not None and t.dtype != dtype:
+    if t.dim() != 2 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, is {t.dtype}")
-    s0, s1 = t.stride()
-    if s1 != 1 and c > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr(), c if r <= 1 else s0
+    raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
-def _vector(t: Optional[torch.Tensor], name: str, device: int, n: Optional[int], dtypes) -> Optional[int]:
-    """Pointer of a contiguous 1-D tensor (None stays None)."""
+def _matrix(t: torch.Tensor, name: str, device: int, shape, dtype: torch.dtype):
+    """Pointer and row stride of a 2-D tensor whose last dimension is contiguous."""
+    try:
+        if t.get_device() == device and t.shape == shape and t.dtype == dtype:
+            s0, s1 = t.stride()
+            if s1 == 1 or shape[1] == 1:
+                return t.data_ptr(), s0 if shape[0] > 1 else shape[1]
+    except (AttributeError, ValueError):
+        pass
+    _refuse_matrix(t, name, device, shape, dtype)
+
+
+def _shape2(t: torch.Tensor, name: str, device: int):
+    """Shape of a CUDA tensor with two dimensions."""
+    try:
+        r, c = t.shape
+        return r, c
+    except (AttributeError, ValueError):
+        _check_device(t, name, device)
+        raise ValueError(f"{name} must be 2-D, has {t.dim()} dimensions") from None
+
+
+def _vector(t: Optional[torch.Tensor], name: str, device: int, n: int, dtypes) -> Optional[int]:
+    """Pointer of a contiguous 1-D tensor of n elements (None stays None)."""
     if t is None:
         return None
+    try:
+        if t.get_device() == device and t.shape == (n,) and t.dtype in dtypes and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _check_device(t, name, device)
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, is {t.dtype}")
-    if t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n):
-        raise ValueError(f"{name} must be contiguous 1-D" + ("" if n is None else f" with {n} elements"))
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous 1-D with {n} elements")
 
 
 def _scratch(workspace: Optional[torch.Tensor], device: int):
     if workspace is None:
         return None, 0
-    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor (see new_head_workspace)")
+    try:
+        if workspace.get_device() == device and workspace.is_contiguous():
+            return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    except AttributeError:
+        pass
     _check_device(workspace, "workspace", device)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-
-
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    raise TypeError("workspace must be a contiguous CUDA tensor (see new_head_workspace)")
 
 
 def _new(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -102,6 +129,18 @@ def _new(shape, dtype: torch.dtype, like: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _output(out, shape, dtype, like, stream):
+    if out is None:
+        return _new(shape, dtype, like, stream)
+    if dtype is not None and out.dtype != dtype:
+        raise TypeError(f"out must be {dtype}, is {out.dtype}")
+    return out
+
+
+def _failed(rc: int, what: str) -> None:
+    raise _pkg().LpError(rc, what)
 
 
 def head_workspace_size(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0) -> int:
@@ -124,11 +163,10 @@ def new_head_workspace(T: int = 0, rank: int = 0, requests: int = 0, history: in
 
 def clear_status(workspace: torch.Tensor, stream=None) -> None:
     """Enqueue the clearing of a workspace's status word."""
-    lp = _pkg()
-    ptr, _ = _scratch(workspace, torch.cuda.current_device())
-    rc = lp.load().lp_head_clear_status(ptr, _stream(stream))
+    dev = _device()
+    rc = _pkg().load().lp_head_clear_status(_scratch(workspace, dev)[0], _stream(stream, dev))
     if rc:
-        raise lp.LpError(rc, "lp_head_clear_status")
+        _failed(rc, "lp_head_clear_status")
 
 
 def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: Optional[torch.Tensor] = None,
@@ -142,31 +180,35 @@ def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual:
     float8_e4m3fn with one float32 scale a row in ``out_scale``. ``residual_out`` receives
     ``x + residual``. Returns ``out``, or ``(out, out_scale)`` for float8_e4m3fn. With
     ``rows`` a workspace is needed: a row index past T sets LP_ERR_OFFSETS in its status."""
-    lp = _pkg()
-    dev = torch.cuda.current_device()
-    xp, xs = _matrix(x, "x", dev)
-    T, H = x.shape
+    dev = _device()
+    T, H = _shape2(x, "x", dev)
     dt = x.dtype
-    n = T if rows is None else rows.numel()
-    rp, rs = (None, 0) if residual is None else _matrix(residual, "residual", dev, T, H, dt)
-    wp = _vector(weight, "weight", dev, H, (dt, torch.float32))
-    if out is None:
-        out = _new((n, H), dt if out_dtype is None else out_dtype, x, stream)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out must be {out_dtype}, is {out.dtype}")
-    op, os_ = _matrix(out, "out", dev, n, H)
-    quant = out.dtype == torch.float8_e4m3fn
-    if quant and out_scale is None:
+    xp, xs = _matrix(x, "x", dev, (T, H), dt)
+    n = T
+    rp = ip = kp = sp = None
+    rs = ks = 0
+    if residual is not None:
+        rp, rs = _matrix(residual, "residual", dev, (T, H), dt)
+    if rows is not None:
+        n = rows.numel()
+        ip = _vector(rows, "rows", dev, n, _INTS)
+    if out is None or out_dtype is not None:
+        out = _output(out, (n, H), dt if out_dtype is None else out_dtype, x, stream)
+    odt = out.dtype
+    op, os_ = _matrix(out, "out", dev, (n, H), odt)
+    if odt == torch.float8_e4m3fn and out_scale is None:
         out_scale = _new((n,), torch.float32, x, stream)
-    kp, ks = (None, 0) if residual_out is None else _matrix(residual_out, "residual_out", dev, n, H, dt)
-    sp, sn = _scratch(workspace, dev)
-    rc = lp.load().lp_head_norm(
-        xp, rp, wp, _DTYPES.get(dt, 99), _DTYPES[weight.dtype], T, H, xs, rs,
-        _vector(rows, "rows", dev, n, _INTS), n, eps, op, _DTYPES.get(out.dtype, 99), os_,
-        _vector(out_scale, "out_scale", dev, n, (torch.float32,)), kp, ks, sp, sn, _stream(stream))
+    if out_scale is not None:
+        sp = _vector(out_scale, "out_scale", dev, n, _F32)
+    if residual_out is not None:
+        kp, ks = _matrix(residual_out, "residual_out", dev, (n, H), dt)
+    wp = _vector(weight, "weight", dev, H, (dt, torch.float32))
+    ws, wn = _scratch(workspace, dev)
+    rc = _pkg().load().lp_head_norm(xp, rp, wp, _DTYPES.get(dt, 99), _DTYPES[weight.dtype], T, H, xs, rs, ip, n, eps,
+                                    op, _DTYPES.get(odt, 99), os_, sp, kp, ks, ws, wn, _stream(stream, dev))
     if rc:
-        raise lp.LpError(rc, "lp_head_norm")
-    return (out, out_scale) if quant else out
+        _failed(rc, "lp_head_norm")
+    return (out, out_scale) if odt == torch.float8_e4m3fn else out
 
 
 def project(x: torch.Tensor, weight: torch.Tensor, x_scale: Optional[torch.Tensor] = None,
@@ -183,20 +225,20 @@ def project(x: torch.Tensor, weight: torch.Tensor, x_scale: Optional[torch.Tenso
     ``adapter_ids`` [B] int32 names each request's adapter (negative: none), ``row_offsets``
     [B+1] its rows (default: one row a request). Returns ``out`` (new by default, of
     ``out_dtype``, float32 by default). ``workspace``: see ``new_head_workspace(T, rank)``."""
-    lp = _pkg()
-    dev = torch.cuda.current_device()
-    xp, xs = _matrix(x, "x", dev)
-    T, H = x.shape
+    dev = _device()
+    T, H = _shape2(x, "x", dev)
     dt = x.dtype
-    wp, ws = _matrix(weight, "weight", dev, None, H, dt)
-    V = weight.shape[0]
-    f32 = (torch.float32,)
+    xp, xs = _matrix(x, "x", dev, (T, H), dt)
+    V = _shape2(weight, "weight", dev)[0]
+    wp, ws = _matrix(weight, "weight", dev, (V, H), dt)
     ap = bp = ip = rp = sp = None
     A = rank = B = 0
     at = dt
     if lora_a is not None:
         if lora_b is None or adapter_ids is None:
             raise ValueError("lora_a needs lora_b and adapter_ids")
+        if lora_a.dim() != 3:
+            raise ValueError(f"lora_a must be 3-D, has {lora_a.dim()} dimensions")
         A, rank = lora_a.shape[:2]
         B = T if row_offsets is None else row_offsets.numel() - 1
         at = lora_a.dtype
@@ -207,21 +249,20 @@ def project(x: torch.Tensor, weight: torch.Tensor, x_scale: Optional[torch.Tenso
         ap, bp = lora_a.data_ptr(), lora_b.data_ptr()
         ip = _vector(adapter_ids, "adapter_ids", dev, B, (torch.int32,))
         rp = _vector(row_offsets, "row_offsets", dev, B + 1, _INTS)
-        sp = _vector(adapter_scale, "adapter_scale", dev, A, f32)
+        sp = _vector(adapter_scale, "adapter_scale", dev, A, _F32)
     elif lora_b is not None or adapter_ids is not None or adapter_scale is not None:
         raise ValueError("lora_b, adapter_ids and adapter_scale need lora_a")
-    if out is None:
-        out = _new((T, V), torch.float32 if out_dtype is None else out_dtype, x, stream)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError(f"out must be {out_dtype}, is {out.dtype}")
-    op, os_ = _matrix(out, "out", dev, T, V)
+    if out is None or out_dtype is not None:
+        out = _output(out, (T, V), torch.float32 if out_dtype is None else out_dtype, x, stream)
+    odt = out.dtype
+    op, os_ = _matrix(out, "out", dev, (T, V), odt)
     kp, kn = _scratch(workspace, dev)
-    rc = lp.load().lp_head_project(
-        xp, _DTYPES.get(dt, 99), T, H, xs, _vector(x_scale, "x_scale", dev, T, f32), wp, V, ws,
-        _vector(weight_scale, "weight_scale", dev, V, f32), ap, bp, _DTYPES.get(at, 99), A, rank, sp, ip, rp, B, op,
-        _DTYPES.get(out.dtype, 99), os_, kp, kn, _stream(stream))
+    rc = _pkg().load().lp_head_project(
+        xp, _DTYPES.get(dt, 99), T, H, xs, _vector(x_scale, "x_scale", dev, T, _F32), wp, V, ws,
+        _vector(weight_scale, "weight_scale", dev, V, _F32), ap, bp, _DTYPES.get(at, 99), A, rank, sp, ip, rp, B, op,
+        _DTYPES.get(odt, 99), os_, kp, kn, _stream(stream, dev))
     if rc:
-        raise lp.LpError(rc, "lp_head_project")
+        _failed(rc, "lp_head_project")
     return out
 
 
@@ -240,40 +281,46 @@ def process_logits(logits: torch.Tensor, row_offsets: Optional[torch.Tensor] = N
     b's ``history`` is ``history[history_offsets[b]:history_offsets[b+1]]``, its first
     ``prompt_lens[b]`` tokens the prompt. ``bias_*`` are ragged lists too, ids strictly
     ascending in each. ``mask`` [rows, words] int32 has a bit for each token, 1 = allowed;
-    ``mask_index`` [T] names each row's mask, negative for none. Errors found on the device
-    set bits of the workspace's status (``read_status``)."""
-    lp = _pkg()
-    dev = torch.cuda.current_device()
-    xp, xs = _matrix(logits, "logits", dev)
-    T, V = logits.shape
+    ``mask_index`` [T] names each row's mask, negative for none. ``workspace``: see
+    ``new_head_workspace(requests=B, history=history.numel())``; errors found on the device set
+    bits of its status (``read_status``)."""
+    dev = _device()
+    T, V = _shape2(logits, "logits", dev)
+    dt = logits.dtype
+    xp, xs = _matrix(logits, "logits", dev, (T, V), dt)
     B = T if row_offsets is None else row_offsets.numel() - 1
-    f32 = (torch.float32,)
-    if (history is None) != (history_offsets is None):
-        raise ValueError("history and history_offsets come together")
-    if not ((bias_tokens is None) == (bias_values is None) == (bias_offsets is None)):
-        raise ValueError("bias_tokens, bias_values and bias_offsets come together")
-    if mask_index is not None and mask is None:
-        raise ValueError("mask_index needs a mask")
-    nb = 0 if bias_tokens is None else bias_tokens.numel()
-    mp, ms, mr = None, 0, 0
+    hp = ho = bt = bv = bo = mp = mi = None
+    hn = nb = ms = mr = 0
+    if history is not None or history_offsets is not None:
+        if history is None or history_offsets is None:
+            raise ValueError("history and history_offsets come together")
+        hn = history.numel()
+        hp = _vector(history, "history", dev, hn, _INTS)
+        ho = _vector(history_offsets, "history_offsets", dev, B + 1, _INTS)
+    if bias_tokens is not None or bias_values is not None or bias_offsets is not None:
+        if bias_tokens is None or bias_values is None or bias_offsets is None:
+            raise ValueError("bias_tokens, bias_values and bias_offsets come together")
+        nb = bias_tokens.numel()
+        bt = _vector(bias_tokens, "bias_tokens", dev, nb, _INTS)
+        bv = _vector(bias_values, "bias_values", dev, nb, _F32)
+        bo = _vector(bias_offsets, "bias_offsets", dev, B + 1, _INTS)
     if mask is not None:
-        mp, ms = _matrix(mask, "mask", dev)
-        mr = mask.shape[0]
-        if mask.dtype not in _INTS or mask.shape[1] < (V + 31) // 32:
+        mr, words = _shape2(mask, "mask", dev)
+        if mask.dtype not in _INTS or words < (V + 31) // 32:
             raise ValueError(f"mask must be int32 [rows, {(V + 31) // 32} or more]")
+        mp, ms = _matrix(mask, "mask", dev, (mr, words), mask.dtype)
+        mi = _vector(mask_index, "mask_index", dev, T, _INTS)
+    elif mask_index is not None:
+        raise ValueError("mask_index needs a mask")
     if out is None:
         out = _new((T, V), torch.float32, logits, stream)
-    op, os_ = _matrix(out, "out", dev, T, V, torch.float32)
+    op, os_ = _matrix(out, "out", dev, (T, V), torch.float32)
     sp, sn = _scratch(workspace, dev)
-    rc = lp.load().lp_head_process(
-        xp, _DTYPES.get(logits.dtype, 99), T, V, xs, _vector(row_offsets, "row_offsets", dev, B + 1, _INTS), B,
-        _vector(history, "history", dev, None, _INTS),
-        _vector(history_offsets, "history_offsets", dev, B + 1, _INTS), 0 if history is None else history.numel(),
-        _vector(prompt_lens, "prompt_lens", dev, B, _INTS), _vector(repetition, "repetition", dev, B, f32),
-        _vector(frequency, "frequency", dev, B, f32), _vector(presence, "presence", dev, B, f32),
-        _vector(bias_tokens, "bias_tokens", dev, nb, _INTS), _vector(bias_values, "bias_values", dev, nb, f32),
-        _vector(bias_offsets, "bias_offsets", dev, B + 1, _INTS), nb, mp, ms, mr,
-        _vector(mask_index, "mask_index", dev, T, _INTS), op, os_, sp, sn, _stream(stream))
+    rc = _pkg().load().lp_head_process(
+        xp, _DTYPES.get(dt, 99), T, V, xs, _vector(row_offsets, "row_offsets", dev, B + 1, _INTS), B, hp, ho, hn,
+        _vector(prompt_lens, "prompt_lens", dev, B, _INTS), _vector(repetition, "repetition", dev, B, _F32),
+        _vector(frequency, "frequency", dev, B, _F32), _vector(presence, "presence", dev, B, _F32), bt, bv, bo, nb,
+        mp, ms, mr, mi, op, os_, sp, sn, _stream(stream, dev))
     if rc:
-        raise lp.LpError(rc, "lp_head_process")
+        _failed(rc, "lp_head_process")
     return out

@@ -188,3 +188,21 @@ def test_on_another_stream_and_in_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     check(out, y, torch.bfloat16)
+
+
+def test_refusals_of_the_binding():
+    x, r, w = inputs(4, 64, torch.bfloat16)
+    xc, rc, wc = cuda(x, r, w)
+    for bad in (dict(residual=rc[:3]), dict(residual=rc.float()), dict(out=torch.empty(4, 65, device="cuda")),
+                dict(out=torch.empty(64, 4, device="cuda", dtype=torch.bfloat16).t()), dict(residual=r),
+                dict(out=xc, out_dtype=torch.float32), dict(out_scale=torch.empty(3, device="cuda"))):
+        with pytest.raises((ValueError, TypeError)):
+            lp.rms_norm(xc, wc, EPS, **bad)
+    with pytest.raises(ValueError):
+        lp.rms_norm(xc[0], wc, EPS)
+    with pytest.raises((ValueError, TypeError)):
+        lp.rms_norm(xc, wc[:63], EPS)
+    with pytest.raises(lp.LpError):                  # picked rows need a workspace
+        lp.rms_norm(xc, wc, EPS, rows=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    with pytest.raises(lp.LpError):
+        lp.rms_norm(xc.int(), wc.int().float(), EPS)

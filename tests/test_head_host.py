@@ -121,7 +121,9 @@ def test_project_refusals(lib):
 def test_binding_refuses_host_tensors():
     from ragged_log_probs_gb300 import head
     with pytest.raises(TypeError):
-        head._matrix(torch.zeros(2, 2), "x", 0)
+        head._matrix(torch.zeros(2, 2), "x", 0, (2, 2), torch.float32)
+    with pytest.raises(TypeError):
+        head._matrix(None, "x", 0, (2, 2), torch.float32)
     with pytest.raises(TypeError):
         head._vector(torch.zeros(2), "weight", 0, 2, (torch.float32,))
     with pytest.raises(TypeError):
