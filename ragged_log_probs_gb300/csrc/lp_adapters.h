@@ -47,13 +47,13 @@ __host__ __device__ constexpr uint32_t rank_cols(uint32_t rank) { return (rank +
 __host__ __device__ constexpr uint32_t part_cols(uint32_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : 64; }
 __host__ __device__ constexpr uint32_t part_rows(uint32_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 3; }
 
-// The workspace: header, a page a tile of rows, a factor a row, u (f32, padded to a multiple
-// of 16), and u as parts ([part_rows][rows][64]).
+// The workspace: header, a page a tile of rows (of 32 at least, or all rows), a factor a row, u
+// (f32, padded to a multiple of 16), and u as parts ([part_rows][rows][64]).
 struct AdapterSpace {
     size_t rows, groups, factor, u, parts, bytes;
     AdapterSpace(uint32_t T, uint32_t rank) {
-        const size_t tiles = ((size_t)T + kMaxTileT - 1) / kMaxTileT;
-        rows = tiles * kMaxTileT;
+        const size_t tiles = ((size_t)T + kBlock - 1) / kBlock;
+        rows = ((size_t)T + kMaxTileT - 1) / kMaxTileT * kMaxTileT;
         groups = kHeaderBytes;
         factor = groups + tiles * kGroupBytes;
         u = factor + rows * 4;

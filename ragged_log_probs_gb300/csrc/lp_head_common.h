@@ -59,12 +59,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, __half) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The request of row t: the b with off[b] <= t < off[b+1], or -1. Ends for any contents of
-// off (the interval halves each time).
+// The request of row t: the b with off[b] <= t < off[b+1], or -1. The row's own number is tried
+// first (a request a row). Ends for any contents of off (the interval halves each time).
 __device__ __forceinline__ int request_of(const uint32_t* off, uint32_t B, uint32_t t) {
     if (!off) return (int)t;
     uint32_t lo = 0, hi = B;  // off[lo] <= t is kept, off[hi] > t is kept, once checked below
-    if (off[0] > t || off[B] <= t) return -1;
+    const uint32_t guess = t < B ? t : B - 1, at = off[guess], after = off[guess + 1], begin = off[0], end = off[B];
+    if (at <= t && t < after) return (int)guess;
+    if (begin > t || end <= t) return -1;
     while (hi - lo > 1) {
         const uint32_t mid = lo + (hi - lo) / 2;
         if (off[mid] <= t) lo = mid; else hi = mid;

@@ -59,6 +59,7 @@ struct ProjectParams {
     uint32_t tiles_t, tiles, slices, stages;
     uint32_t chunk;                // slices summed in one accumulator pass
     uint32_t acc_cols;             // TMEM columns of one accumulator
+    uint32_t acc_shift;            // log2 of the number of accumulators
     uint32_t idesc, lora_idesc;    // instruction descriptors: of x W^T, of the adapters' part
     uint32_t tensor;               // blocks of rows with one adapter run on the tensor cores
     uint32_t apart;                // with an accumulator of their own: their sum has another scale
@@ -69,7 +70,8 @@ struct ProjectParams {
     uint32_t early;                // the inputs are complete when this kernel starts (u may not be)
 };
 
-constexpr uint32_t kBarriers = 2 * kMaxStages + 2 * kMaxSlots + 6;
+constexpr uint32_t kMaxAccs = 8;
+constexpr uint32_t kBarriers = 2 * kMaxStages + 2 * kMaxSlots + 2 * kMaxAccs + 2;
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
@@ -247,13 +249,14 @@ __device__ __forceinline__ uint32_t b_offset(uint32_t row, uint32_t piece, uint3
     return off ^ ((off >> 3) & (cols * 2 - 16));
 }
 
-// Where the chunk that begins at slice k0 ends. A tile's first is twice as long: the epilogue
-// is still storing the tile before, from the other accumulator.
+// Where the chunk that begins at slice k0 ends. A tile's first is half as long again: the
+// epilogue is still storing the tile before, from the other accumulator.
 __device__ __forceinline__ uint32_t chunk_end(const ProjectParams& p, uint32_t k0) {
-    return k0 + min(p.slices - k0, k0 ? p.chunk : 2 * p.chunk);
+    return k0 + min(p.slices - k0, k0 ? p.chunk : p.chunk + p.chunk / 2);
 }
 __device__ __forceinline__ uint32_t last_chunk(const ProjectParams& p) {  // where the last one begins
-    return p.slices <= 2 * p.chunk ? 0 : (p.slices - 1 - 2 * p.chunk) / p.chunk * p.chunk + 2 * p.chunk;
+    const uint32_t second = p.chunk + p.chunk / 2;
+    return p.slices <= second ? 0 : (p.slices - 1 - second) / p.chunk * p.chunk + second;
 }
 __device__ __forceinline__ const TileGroups* tile_groups(const ProjectParams& p, uint32_t tt) {
     return reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
@@ -300,11 +303,14 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     uint32_t* s_tmem = const_cast<uint32_t*>(s_abort) + 1;
     const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * kMaxStages, b_full0 = empty0 + 8 * kMaxStages,
                    b_empty0 = b_full0 + 8 * kMaxSlots, acc_full0 = b_empty0 + 8 * kMaxSlots,
-                   acc_empty0 = acc_full0 + 16, drain = acc_empty0 + 16, staging = drain + 8;
+                   acc_empty0 = acc_full0 + 8 * kMaxAccs, drain = acc_empty0 + 8 * kMaxAccs, staging = drain + 8;
     const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank = 0;
     if constexpr (CG == 2) asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;  // tiles of this CTA (pair)
+    // the n-th filling: its accumulator, and the phase of that one's barriers
+    const auto acc_of = [&](uint32_t n) { return n & ((1u << p.acc_shift) - 1); };
+    const auto acc_phase = [&](uint32_t n) { return n >> p.acc_shift & 1; };
 
     pdl_trigger();
     if (threadIdx.x == 0) {
@@ -316,7 +322,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             mbar_init(b_full0 + 8 * i, 1);
             mbar_init(b_empty0 + 8 * i, 4);  // the share's warps
         }
-        for (uint32_t i = 0; i < 2; ++i) {
+        for (uint32_t i = 0; i < 1u << p.acc_shift; ++i) {
             mbar_init(acc_full0 + 8 * i, 1);
             mbar_init(acc_empty0 + 8 * i, kEpilogueWarps * CG);
         }
@@ -329,11 +335,11 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     if (warp == kMmaWarp) {
         if constexpr (CG == 2) {
             asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
-                         "r"(2 * p.acc_cols) : "memory");
+                         "r"(p.acc_cols << p.acc_shift) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         } else {
             asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(s_tmem)),
-                         "r"(2 * p.acc_cols) : "memory");
+                         "r"(p.acc_cols << p.acc_shift) : "memory");
             asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         }
     }
@@ -423,11 +429,11 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                 const uint32_t b0 = run.x >> 8 & 0xFF, blocks = run.x & 0xFF;
                                 if (run.x >> 16 != pass) {
                                     if (open) {
-                                        mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                                        mma_commit<CG>(acc_full0 + 8 * acc_of(n));
                                         ++n;
                                     }
                                     pass = run.x >> 16;
-                                    open = mbar_wait(acc_empty0 + 8 * (n & 1), ((n >> 1) & 1) ^ 1, s_abort);
+                                    open = mbar_wait(acc_empty0 + 8 * acc_of(n), acc_phase(n) ^ 1, s_abort);
                                     if (!open) { ok = false; break; }
                                 }
                                 const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
@@ -441,7 +447,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                         const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
                                                        j = column - part * p.b_cols;
                                         if (part < 3 && j < uc)
-                                            mma<false, CG>(tmem + (n & 1) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i,
+                                            mma<false, CG>(tmem + acc_of(n) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i,
                                                            idesc, pass ? (line | i) : 1u);
                                     }
                                     mma_commit<CG>(empty0 + 8 * s);
@@ -450,15 +456,15 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             }
                             if (!ok) break;
                             if (open) {
-                                mma_commit<CG>(acc_full0 + 8 * (n & 1));
+                                mma_commit<CG>(acc_full0 + 8 * acc_of(n));
                                 ++n;
                             }
                         }
                     }
                     if (k0 >= p.slices) break;
-                    const uint32_t acc = n & 1;
+                    const uint32_t acc = acc_of(n);
                     k1 = chunk_end(p, k0);
-                    if (!mbar_wait(acc_empty0 + 8 * acc, ((n >> 1) & 1) ^ 1, s_abort)) { ok = false; break; }
+                    if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase(n) ^ 1, s_abort)) { ok = false; break; }
                     fence_after();
                     for (uint32_t k = k0; k < k1; ++k) {
                         if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
@@ -603,7 +609,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 return c0 + lane < rows ? per_row[t0 + c0 + lane] : 0.f;
             };
             const float sw = FP8 && v < p.V ? p.w_scale[v] : 1.f;
-            uint32_t acc = n & 1;
+            uint32_t acc = acc_of(n);
             const uint32_t lanes = (quad * 32) << 16;
             if constexpr (PROMOTE) {
                 float sum[(kMaxTileT / 32 + kShares - 1) / kShares][32];
@@ -614,8 +620,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
                 uint32_t pass = pass_blocks[0] ? 0 : pass_blocks[1] ? 1 : 2;  // the next of the adapters' (2: none)
                 for (uint32_t k0 = 0; k0 < p.slices; ++n) {
-                    acc = n & 1;
-                    if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) { ok = false; break; }
+                    acc = acc_of(n);
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) { ok = false; break; }
                     fence_after();
                     const bool now = LORA && pass < 2 && k0 == lora_at;
                     uint32_t blocks = 0xFFFFFFFFu, rows_of = 0;
@@ -656,7 +662,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 if (!ok) break;
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             } else {
-                if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) break;
+                if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
                 fence_after();
                 ++n;
             }
@@ -665,8 +671,8 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 // is free for the next tile's before the stores begin.
                 if (pass_blocks[0]) {
                     const uint32_t from = acc;
-                    acc = n & 1;
-                    if (!mbar_wait_warp(acc_full0 + 8 * acc, (n >> 1) & 1, s_abort)) break;
+                    acc = acc_of(n);
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
                     fence_after();
                     ++n;
                     for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
@@ -824,9 +830,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     fence_after();
     if (warp == kMmaWarp) {
         if constexpr (CG == 2)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.acc_cols << p.acc_shift));
         else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * p.acc_cols));
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.acc_cols << p.acc_shift));
     }
     if (threadIdx.x == 0 && *s_abort) flag(p.status, LP_ERR_TIMEOUT);
 }
@@ -871,6 +877,43 @@ bool encode(CUtensorMap* map, const void* ptr, uint32_t dtype, uint64_t rows, ui
                                                             : CU_TENSOR_MAP_SWIZZLE_32B;
     return f(map, type, 2, const_cast<void*>(ptr), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clocks of one SM that a cut takes, counted roughly: a stage of the ring costs its products
+// (N / 256 x 512 clocks), its bytes at 55 a clock from L2, W's at 23.5 from HBM, or 120; a tile
+// an epilogue of 8 per row and 1000, of which the last tile's is not hidden.
+struct Cut {
+    uint32_t cg, tile_t;
+};
+Cut choose_cut(uint32_t T, uint32_t V, uint32_t slices, uint32_t sms, bool adapters) {
+    Cut best = {0, 0};
+    double least = 0;
+    for (uint32_t cg = 1; cg <= 2; ++cg) {
+        const uint32_t unit = 16 * cg;
+        for (uint32_t most = kMaxTileT; most >= 32; most /= 2) {
+            if (T <= most / 2 && most > 32) continue;  // the same as a smaller one
+            const uint32_t tiles_t = (T + most - 1) / most;
+            const uint32_t tile_t = ((T + tiles_t - 1) / tiles_t + unit - 1) / unit * unit;
+            if (adapters && tile_t < 32 && T > 32) continue;  // (a page of the workspace for each 32 rows)
+            const double tiles = (double)((V + cg * kTileV - 1) / (cg * kTileV)) * ((T + tile_t - 1) / tile_t);
+            const double units = sms / cg, waves = (double)(uint64_t)((tiles + units - 1) / units);
+            const double busy = tiles < units ? tiles / units : 1.0;  // few SMs share L2's bandwidth
+            double stage = 2.0 * tile_t;
+            const double bytes = (kStageW + tile_t * kSliceBytes / cg) / 55.0 * (0.5 + 0.5 * busy);
+            const double memory = kStageW / 23.5 * busy / tiles_t;  // W from HBM
+            if (stage < bytes) stage = bytes;
+            if (stage < memory) stage = memory;
+            if (stage < 120) stage = 120;
+            const double main = slices * stage, tail = 1000 + 8.0 * tile_t;
+            const double cost = waves * (main > tail ? main : tail) + tail;
+            if (best.cg == 0 || cost < least) {
+                best = {cg, tile_t};
+                least = cost;
+            }
+            if (tiles >= units) break;  // shorter tiles would only read W more often
+        }
+    }
+    return best;
 }
 
 struct ProjectLaunch {
@@ -960,15 +1003,17 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.lora_bytes = (uint64_t)adapters * V * rank * 2;
     p.lora_tma = rank % 8 == 0 && (uint64_t)adapters * V <= 0x7FFFFFFFu;
     p.early = rank != 0;
-    // Rows of x in even tiles of at most 256, a multiple of 16 (of 32 for a pair of CTAs). A
-    // pair halves what each SM reads of x, which pays from 129 rows on.
-    const uint32_t cg = T > 128 ? 2 : 1;
-    p.tiles_t = (T + kMaxTileT - 1) / kMaxTileT;
-    p.tile_t = ((T + p.tiles_t - 1) / p.tiles_t + 16 * cg - 1) / (16 * cg) * (16 * cg);
+    // How the product is cut: the rows of x into even tiles of at most 256, a multiple of 16, for
+    // single CTAs or (a multiple of 32) for pairs, which read each row of x once for two tiles of
+    // the vocabulary. The choice is the cheapest of a few by a rough count of clocks.
+    p.slices = (uint32_t)((H * e + kSliceBytes - 1) / kSliceBytes);
+    const Cut cut = choose_cut(T, V, p.slices, (uint32_t)sms, rank != 0);
+    const uint32_t cg = cut.cg;
+    p.tile_t = cut.tile_t;
+    p.tiles_t = (T + p.tile_t - 1) / p.tile_t;
     const uint64_t tiles = (uint64_t)((V + cg * kTileV - 1) / (cg * kTileV)) * p.tiles_t;
     if (tiles > 0x7FFFFFFFu) return LP_ERR_SHAPE;
     p.tiles = (uint32_t)tiles;
-    p.slices = (uint32_t)((H * e + kSliceBytes - 1) / kSliceBytes);
     // Blocks of rows with one adapter run on the tensor cores (pairs only: the tiles of fewer
     // rows wait for memory, and the epilogue's arithmetic is hidden).
     p.tensor = cg == 2 && p.lora_tma && rank != 0;
@@ -976,22 +1021,23 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.part_stride = (uint32_t)space.rows;
     p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : p.slices;
     for (p.acc_cols = 32; p.acc_cols < p.tile_t; p.acc_cols *= 2) {}
+    for (p.acc_shift = 1; p.acc_shift < 3 && p.acc_cols << (p.acc_shift + 1) <= 512; ++p.acc_shift) {}
     // instruction: f32 accumulator, K-major operands, M = 128 lanes a CTA, N = tile_t
     const uint32_t type = dtype == LP_BF16 ? 1u : 0u;  // kind::f16: 0 f16, 1 bf16; kind::f8f6f4: 0 e4m3
     p.idesc = (1u << 4) | (type << 7) | (type << 10) | ((p.tile_t >> 3) << 17) | ((cg * kTileV >> 4) << 24);
     const uint32_t lora_type = lora_dtype == LP_BF16 ? 1u : 0u;
     p.lora_idesc = (1u << 4) | (lora_type << 7) | (lora_type << 10) | ((cg * kTileV >> 4) << 24);  // without N
-    // Shared memory: the adapters' buffers, a tile's u where it takes 24 KB or less (or fits into
-    // what is left), and as many stages as there is room for.
+    // Shared memory: the adapters' buffers, a tile's u where that leaves four stages, and as many
+    // stages as there is room for.
     const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes, slot_bytes = kTileV * p.b_cols * 2;
     const uint32_t u_bytes = p.tile_t * p.u_cols * 4;
     const uint32_t fixed = kControlBytes + (rank ? (uint32_t)sizeof(TileGroups) + (fp8 ? p.tile_t * 4 : 0) : 0);
     p.depth = rank == 0 ? 0 : rank <= 16 ? 3 : rank <= 32 ? 2 : 1;
     const uint32_t b_bytes = kShares * p.depth * slot_bytes;
-    const uint32_t u_aside = u_bytes <= 24 * 1024 ? u_bytes : 0;
+    const uint32_t u_aside = kSmemBudget - fixed - b_bytes >= u_bytes + 4 * stage_bytes ? u_bytes : 0;
     p.stages = (kSmemBudget - fixed - b_bytes - u_aside) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
-    p.u_smem = rank && kSmemBudget - fixed - b_bytes - p.stages * stage_bytes >= u_bytes;
+    p.u_smem = rank && u_aside != 0;
     l.smem = fixed + p.stages * stage_bytes + b_bytes + (p.u_smem ? u_bytes : 0);
     const uint32_t slice_cols = kSliceBytes / (uint32_t)e;
     if (!encode(&l.w, weight, dtype, V, H, weight_stride, kTileV, slice_cols) ||
