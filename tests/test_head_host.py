@@ -118,13 +118,21 @@ def test_project_refusals(lib):
     assert _project(lib, wsb=255) == WORKSPACE and _project(lib, **dict(a, wsb=256)) == WORKSPACE
 
 
-def test_binding_refuses_host_tensors():
-    from ragged_log_probs_gb300 import head
-    with pytest.raises(TypeError):
-        head._matrix(torch.zeros(2, 2), "x", 0, (2, 2), torch.float32)
-    with pytest.raises(TypeError):
-        head._matrix(None, "x", 0, (2, 2), torch.float32)
-    with pytest.raises(TypeError):
-        head._vector(torch.zeros(2), "weight", 0, 2, (torch.float32,))
-    with pytest.raises(TypeError):
-        head._scratch(torch.zeros(256, dtype=torch.uint8), 0)
+def test_binding_refuses_host_tensors(lib):
+    # before any pointer is read and without a GPU
+    import ragged_log_probs_gb300 as lp
+    x, w = torch.zeros(2, 8, dtype=torch.bfloat16), torch.ones(8, dtype=torch.bfloat16)
+    ws = torch.zeros(256, dtype=torch.uint8)
+    for call in (lambda: lp.rms_norm(x, w), lambda: lp.rms_norm(None, w), lambda: lp.project(x, x, workspace=ws),
+                 lambda: lp.process_logits(x, workspace=ws), lambda: lp.process_logits([1.0], workspace=ws),
+                 lambda: lp.clear_status(ws)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_the_binding_is_needed(monkeypatch, tmp_path, lib):
+    from ragged_log_probs_gb300 import _build, head
+    monkeypatch.setattr(head, "_native", None)
+    monkeypatch.setattr(_build, "binding_path", lambda: str(tmp_path / "missing.so"))
+    with pytest.raises(ImportError):
+        head._load()
