@@ -21,12 +21,10 @@ namespace {
 
 using namespace lph;
 
-constexpr uint32_t kThreads = 256;
 constexpr uint32_t kMaxSlice = 24576;  // tokens of a slice: a 48 KB table, four CTAs per SM
 constexpr uint32_t kMinSlice = 1024;
 constexpr uint32_t kResident = 4;      // CTAs per SM
 constexpr uint32_t kBatch = 4;         // vectors a thread has in flight
-constexpr uint32_t kHeld = 4;          // tokens of a history that a thread keeps in registers
 constexpr uint32_t kChunk = 4096;      // tokens of a history sorted together
 constexpr uint32_t kSortFrom = 4096;   // mean length from which histories are sorted first
 constexpr uint32_t kMaxSlices = 256;
@@ -187,18 +185,19 @@ struct Table {
 
 // Ask for a row's slice in L2.
 template <typename T>
-__device__ __forceinline__ void prefetch_slice(const T* row, uint32_t lo, uint32_t hi) {
+__device__ __forceinline__ void prefetch_slice(const T* row, uint32_t lo, uint32_t hi, uint32_t threads) {
     constexpr uint32_t kPiece = 4096;
     const uintptr_t from = (reinterpret_cast<uintptr_t>(row + lo) + 15) & ~(uintptr_t)15;
     const uintptr_t to = reinterpret_cast<uintptr_t>(row + hi) & ~(uintptr_t)15;
-    for (uintptr_t at = from + threadIdx.x * kPiece; at < to; at += kThreads * kPiece) {
+    for (uintptr_t at = from + threadIdx.x * kPiece; at < to; at += threads * kPiece) {
         const uint32_t bytes = to - at < kPiece ? (uint32_t)(to - at) : kPiece;
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
     }
 }
 
-constexpr uint32_t kSortThreads = 256;
+constexpr uint32_t kSortThreads = 512;
 constexpr uint32_t kSortEach = kChunk / kSortThreads;
+constexpr uint32_t kNowhere = 0xFFFF0000u;
 
 // Histories are sorted in chunks of kChunk tokens. Request b's chunk c has number
 // b + h0 / kChunk + c: no two have the same, and there are at most B + total / kChunk + 1.
@@ -209,7 +208,7 @@ __device__ __forceinline__ uint32_t first_chunk(const ProcessParams& p, uint32_t
 // Sort a chunk by slices: sorted[h0 + c kChunk ...] gets its tokens (bit 31: of the prompt),
 // bounds[chunk][k] where slice k's begin. A warp takes the places of its tokens of one slice
 // together; their order within a slice is left open. grid: a CTA a chunk
-__global__ void __launch_bounds__(kSortThreads) k_sort_history(ProcessParams p) {
+__global__ void __launch_bounds__(kSortThreads, 3) k_sort_history(ProcessParams p) {
     __shared__ uint32_t place[kMaxSlices + 1];
     __shared__ uint32_t s_request;
     pdl_wait();
@@ -237,7 +236,7 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_history(ProcessParams p) 
         return;  // (no chunk, or not read: see describe)
     const uint32_t from = before * kChunk, n = min(kChunk, h1 - h0 - from);
     const uint32_t prompt = p.prompt_lens ? p.prompt_lens[b] : 0u;
-    uint32_t v[kSortEach], slice[kSortEach];
+    uint32_t v[kSortEach], where[kSortEach];  // where: slice << 16 | place among the chunk's of the slice
     bool outside = false;
 #pragma unroll
     for (uint32_t k = 0; k < kSortEach; ++k) {
@@ -247,11 +246,13 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_history(ProcessParams p) 
 #pragma unroll
     for (uint32_t k = 0; k < kSortEach; ++k) {
         const uint32_t i = tid + k * kSortThreads;
-        slice[k] = i < n && v[k] < p.V ? v[k] / p.slice : 0xFFFFFFFFu;
+        const uint32_t slice = i < n && v[k] < p.V ? v[k] / p.slice : kNowhere >> 16;
         outside |= i < n && v[k] >= p.V;
         if (from + i < prompt) v[k] |= 0x80000000u;
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, slice[k]);
-        if (slice[k] != 0xFFFFFFFFu && (peers & ((1u << lane) - 1u)) == 0) atomicAdd(place + slice[k] + 1, __popc(peers));
+        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, slice), rank = __popc(peers & ((1u << lane) - 1u));
+        uint32_t at = 0;
+        if (slice != kNowhere >> 16 && rank == 0) at = atomicAdd(place + slice + 1, __popc(peers));
+        where[k] = slice << 16 | (__shfl_sync(0xFFFFFFFFu, at, __ffs(peers) - 1) + rank);
     }
     __syncthreads();
     if (tid < 32) {  // place[k]: tokens of the slices before k
@@ -273,26 +274,29 @@ __global__ void __launch_bounds__(kSortThreads) k_sort_history(ProcessParams p) 
     }
     __syncthreads();
 #pragma unroll
-    for (uint32_t k = 0; k < kSortEach; ++k) {
-        const uint32_t peers = __match_any_sync(0xFFFFFFFFu, slice[k]), rank = __popc(peers & ((1u << lane) - 1u));
-        uint32_t at = 0;
-        if (slice[k] != 0xFFFFFFFFu && rank == 0) at = atomicAdd(place + slice[k], __popc(peers));
-        at = __shfl_sync(0xFFFFFFFFu, at, __ffs(peers) - 1) + rank;
-        if (slice[k] != 0xFFFFFFFFu) p.sorted[h0 + from + at] = v[k];
-    }
+    for (uint32_t k = 0; k < kSortEach; ++k)
+        if (where[k] < kNowhere) p.sorted[h0 + from + place[where[k] >> 16] + (where[k] & 0xFFFF)] = v[k];
     if (outside) flag(p.status, LP_ERR_TOKEN_RANGE);
 }
 
-// grid: T x slices CTAs
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p) {
+// Threads of a CTA. With sorted histories more, which overlap better (256 x 128256 f32, histories
+// of 30000: 256 threads 69.0 us, 384 66.1); without, the registers they leave cost more (240 x
+// 152064 bf16, histories of 1000: 47.1 and 51.2 us).
+__host__ __device__ constexpr uint32_t threads(bool sorted) { return sorted ? 384 : 256; }
+
+// grid: T x slices CTAs, all rows' first slices first: a vocabulary's frequent tokens mostly have
+// its low numbers, and the CTAs with the most to count should not be the last to start (256 rows
+// with histories of 30000: 80 us row by row, 69 so).
+template <typename T, bool VEC, bool SORTED>
+__global__ void __launch_bounds__(threads(SORTED), kResident) k_process(ProcessParams p) {
+    constexpr uint32_t kThreads = threads(SORTED);
     extern __shared__ __align__(16) uint32_t table[];  // slice / 2 words
     __shared__ Row s_row;
     __shared__ uint32_t s_in_slice;
     __shared__ uint32_t s_mask[kMaxSlice / 32 + 2];    // mask words of the slice
     pdl_trigger();
     const uint32_t tid = threadIdx.x;
-    const uint32_t t = blockIdx.x / p.slices, part = blockIdx.x - t * p.slices;
+    const uint32_t part = blockIdx.x / p.T, t = blockIdx.x - part * p.T;
     const uint32_t lo = part * p.slice, hi = min(lo + p.slice, p.V);  // this CTA's tokens
     const T* in = static_cast<const T*>(p.logits) + (uint64_t)t * p.stride;
     float* out = p.out + (uint64_t)t * p.out_stride;
@@ -300,12 +304,12 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
     if (p.history)
         for (uint32_t i = tid; i < (p.slice + 7) / 8; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_in_slice = 0;
-    if (!p.sorted) pdl_wait();  // (the sort has waited for what logits and the lists come from)
-    if (!p.mask) prefetch_slice(in, lo, hi);
+    if constexpr (!SORTED) pdl_wait();  // (the sort has waited for what logits and the lists come from)
+    if (!p.mask) prefetch_slice(in, lo, hi, kThreads);
     if (tid < 32) describe(p, t, &s_row, part == 0);
     __syncthreads();
     const Row row = s_row;
-    if (p.sorted) pdl_wait();
+    if constexpr (SORTED) pdl_wait();
     if (row.request < 0) {
         for (uint32_t v = lo + tid; v < hi; v += kThreads) out[v] = __int_as_float(0x7fffffff);
         return;
@@ -316,39 +320,45 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
         for (uint32_t i = tid; i <= words; i += kThreads)  // (the last is read beside the one before)
             s_mask[i] = i < words ? p.mask[row.mask + word0 + i] : 0u;
     } else if (p.mask) {
-        prefetch_slice(in, lo, hi);
+        prefetch_slice(in, lo, hi, kThreads);
     }
     const auto allowed = [&](uint32_t v) { return !masked || ((s_mask[(v >> 5) - word0] >> (v & 31)) & 1u); };
     // 15 bits hold any count of an output part of up to 32767 tokens
     const bool wide = row.counted && row.h1 - row.h0 - row.prompt > 0x7FFFu;
     const Table<false> counts = {table, lo, hi - lo};
-    const uint32_t pieces = !row.counted ? 0 : p.sorted ? (row.h1 - row.h0 + kChunk - 1) / kChunk : 1;
+    const uint32_t pieces = !row.counted ? 0 : SORTED ? (row.h1 - row.h0 + kChunk - 1) / kChunk : 1;
     const auto piece = [&](uint32_t c) -> Tokens {
-        if (!p.sorted) return {p.history + row.h0, row.h1 - row.h0, row.prompt, false};
+        if (!SORTED) return {p.history + row.h0, row.h1 - row.h0, row.prompt, false};
         const uint32_t* bounds = p.bounds + (uint64_t)(row.request + row.h0 / kChunk + c) * (p.slices + 1) + part;
         const uint32_t limit = min(kChunk, row.h1 - row.h0 - c * kChunk);
         const uint32_t from = min(bounds[0], limit), to = min(bounds[1], limit);
         return {p.sorted + row.h0 + (uint64_t)c * kChunk + from, to > from ? to - from : 0u, 0u, true};
     };
+    // Sorted pieces side by side, a warp each with 8 tokens a lane in flight, since a piece's loads
+    // wait for each other (256 histories of 30000: 72 us; one after the other by all threads, 4 in
+    // flight: 80). A history that is not sorted is one piece, and short: 8 in flight cost it 7 %.
+    constexpr uint32_t kTeam = SORTED ? 32 : kThreads, kTeams = kThreads / kTeam, kHeld = SORTED ? 8 : 4;
+    const uint32_t my_team = SORTED ? tid >> 5 : 0, me = SORTED ? tid & 31 : tid;
     bool outside = false;
     uint32_t mine = 0;  // tokens of the slice that this thread has counted
     const auto count_all = [&](const auto& into) {
-        for (uint32_t c = 0; c < pieces; ++c) {
+        for (uint32_t c = my_team; c < pieces; c += kTeams) {
             const Tokens s = piece(c);
-            for (uint32_t i0 = tid; i0 < s.n; i0 += kHeld * kThreads) {
+            for (uint32_t i0 = me; i0 < s.n; i0 += kHeld * kTeam) {
                 uint32_t e[kHeld];
 #pragma unroll
-                for (uint32_t k = 0; k < kHeld; ++k) e[k] = i0 + k * kThreads < s.n ? s.at[i0 + k * kThreads] : 0u;
+                for (uint32_t k = 0; k < kHeld; ++k) e[k] = i0 + k * kTeam < s.n ? s.at[i0 + k * kTeam] : 0u;
 #pragma unroll
                 for (uint32_t k = 0; k < kHeld; ++k) {
-                    if (i0 + k * kThreads >= s.n) break;
+                    if (i0 + k * kTeam >= s.n) break;
                     outside |= s.token(e[k]) >= p.V;
-                    mine += into.count(s, i0 + k * kThreads, e[k]);
+                    mine += into.count(s, i0 + k * kTeam, e[k]);
                 }
             }
         }
     };
-    // Many tokens of the slice in the table (1 in 32): looked at during the copy.
+    // Many tokens of the slice in the table (1 in 32): looked at during the copy. (256 rows of
+    // 128256 with histories of 30000: 1 in 32 71.9 us, 1 in 16 73.2, 1 in 12 73.8.)
     bool dense = false;
     if (row.counted && !wide) {
         count_all(counts);
@@ -418,13 +428,13 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
 
     // few tokens of the history: corrected now
     const auto correct = [&](const auto& from) {
-        for (uint32_t c = 0; c < pieces; ++c) {
+        for (uint32_t c = my_team; c < pieces; c += kTeams) {
             const Tokens s = piece(c);
-            for (uint32_t i0 = tid; i0 < s.n; i0 += kHeld * kThreads) {
+            for (uint32_t i0 = me; i0 < s.n; i0 += kHeld * kTeam) {
                 uint32_t v[kHeld], w[kHeld];
                 float x[kHeld];
 #pragma unroll
-                for (uint32_t k = 0; k < kHeld; ++k) v[k] = i0 + k * kThreads < s.n ? s.token(s.at[i0 + k * kThreads]) : p.V;
+                for (uint32_t k = 0; k < kHeld; ++k) v[k] = i0 + k * kTeam < s.n ? s.token(s.at[i0 + k * kTeam]) : p.V;
 #pragma unroll
                 for (uint32_t k = 0; k < kHeld; ++k) {
                     w[k] = v[k] < p.V ? from.take(v[k] - from.lo) : 0u;
@@ -470,13 +480,15 @@ __global__ void __launch_bounds__(kThreads, kResident) k_process(ProcessParams p
 }
 
 template <typename T>
-std::atomic<uint64_t> g_smem_set[2];
+std::atomic<uint64_t> g_smem_set[2][2];
 
 template <typename T>
 lp_status launch_process(const ProcessParams& p, bool vec, unsigned ctas, lp_stream_t s) {
-    void (*kernel)(ProcessParams) = vec ? k_process<T, true> : k_process<T, false>;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), kMaxSlice * 2 + 16, &g_smem_set<T>[vec])) return LP_ERR_CUDA;
-    return launch(kernel, dim3(ctas), kThreads, (size_t)p.slice * 2 + 16, s, 1, p);
+    const bool sorted = p.sorted != nullptr;
+    void (*kernel)(ProcessParams) = sorted ? vec ? k_process<T, true, true> : k_process<T, false, true>
+                                           : vec ? k_process<T, true, false> : k_process<T, false, false>;
+    if (!allow_smem(reinterpret_cast<const void*>(kernel), kMaxSlice * 2 + 16, &g_smem_set<T>[vec][sorted])) return LP_ERR_CUDA;
+    return launch(kernel, dim3(ctas), threads(sorted), (size_t)p.slice * 2 + 16, s, 1, p);
 }
 
 }  // namespace
