@@ -81,7 +81,7 @@ __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     const uint32_t m0 = with ? __ballot_sync(kAll, mine == a0) : 0u, rest = with & ~m0;
     const int32_t a1 = __shfl_sync(kAll, mine, rest ? __ffs(rest) - 1 : 0);
     const uint32_t m1 = rest ? __ballot_sync(kAll, mine == a1) : 0u;
-    const bool listed = with && (!p.tensor || (p.split ? (rest & ~m1) != 0 : m0 != in));
+    const bool listed = with && (!p.tensor || (rest & ~m1) != 0);
     const bool tensor = with && !listed;
     __shared__ uint32_t adapter[3][kBlocks], listed_bits;  // of each pass
     if (c == 0) listed_bits = 0;
@@ -358,8 +358,13 @@ __global__ void __launch_bounds__(kThreads) k_shrink_block(ShrinkParams p) {
 template <typename X, typename A>
 lp_status launch_shrink(const ShrinkParams& p, lp_stream_t s) {
     const uint32_t tiles = (p.T + p.tile_t - 1) / p.tile_t;
-    // Blocks of 16 rows from 4 rows a request on.
-    if (p.T / p.B >= 4) {
+    // A block of 16 rows takes its adapters one after the other, a row a block its rank's dot
+    // products. Whole projections onto 512 tokens, us (blocks | rows), H = 4096, rank 16 and 64:
+    //     77 rows, 4 a request  50 | 32, 66 | 38    16 a request  31 | 29, 33 | 33
+    //    256 rows, 4 a request  50 | 40, 64 | 51     8 a request  36 | 38, 44 | 47
+    //   1024 rows, 2 a request  77 | 56, 101 | 107   4 a request  52 | 54, 66 | 105
+    const uint32_t sms = (uint32_t)sm_count(), rows_a_request = p.T / p.B;
+    if (p.T > sms && rows_a_request >= (p.T > 2 * sms ? 4u : 8u)) {
         static std::atomic<uint64_t> smem_set;
         if (!allow_smem(reinterpret_cast<const void*>(k_shrink_block<X, A>), kWarps * kBlockRows * 64 * sizeof(float),
                         &smem_set))

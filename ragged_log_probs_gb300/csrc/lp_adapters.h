@@ -14,11 +14,11 @@ constexpr uint32_t kNoAdapter = 0xFFFFFFFFu;
 
 // One tile of rows, in blocks of 32. Where all rows of a block have one adapter, its part of
 // the product runs on the tensor cores: in pass 0, which adds to the product's own accumulator,
-// or, where that cannot be, in pass 1, which has one of its own. Where sums are kept outside
-// the tensor cores anyway (`split`), passes 1 and 2 also take the two adapters of blocks that
-// have two, or rows without one: the epilogue adds the rows that have the pass's adapter. The
-// rows of other blocks are grouped by adapter, those without one last, and cut into items of at
-// most kItemRows rows of one adapter, which the epilogue multiplies itself.
+// or, where that cannot be (`apart`), in pass 1, which has one of its own. Passes 1 and 2 take
+// the two adapters of blocks that have two, or one and rows without: the epilogue adds the rows
+// that have the pass's adapter. The rows of other blocks are grouped by adapter, those without
+// one last, and cut into items of at most kItemRows rows of one adapter, which the epilogue
+// multiplies itself.
 // (Zeroing u in other adapters' rows instead would let an infinity in one adapter's B become
 // NaN, 0 x inf, in the rows of others.)
 constexpr uint32_t kBlocks = kMaxTileT / kBlock;
@@ -80,7 +80,6 @@ struct ShrinkParams {
     uint32_t part_stride;         // rows of u's parts
     uint32_t tensor;              // blocks of one adapter run on the tensor cores (u's parts are wanted)
     uint32_t apart;               // none in the product's own accumulator (pass 0)
-    uint32_t split;               // blocks of two adapters, or of one and none, too
     uint32_t lora_f16;
 };
 

@@ -62,8 +62,8 @@ struct ProjectParams {
     uint32_t acc_shift;            // log2 of the number of accumulators
     uint32_t idesc, lora_idesc;    // instruction descriptors: of x W^T, of the adapters' part
     uint32_t tensor;               // blocks of rows with one adapter run on the tensor cores
-    uint32_t apart;                // with an accumulator of their own: their sum has another scale
-                                   // (e4m3), a factor a row (f16), or x W^T comes in chunks (f32)
+    uint32_t apart;                // all with an accumulator of their own: their sum has another
+                                   // scale (e4m3) or a factor a row (f16)
     uint64_t lora_bytes;           // of lora_b
     uint32_t lora_f16;             // lora_b is f16 (else bf16)
     uint32_t lora_tma;             // lora_b's rows are whole 16-byte pieces (swizzled tiles in the buffers)
@@ -201,13 +201,6 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const float (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15};"
-        ::"f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-          "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "r"(addr) : "memory");
-}
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const float (&v)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -253,10 +246,6 @@ __device__ __forceinline__ uint32_t b_offset(uint32_t row, uint32_t piece, uint3
 // epilogue is still storing the tile before, from the other accumulator.
 __device__ __forceinline__ uint32_t chunk_end(const ProjectParams& p, uint32_t k0) {
     return k0 + min(p.slices - k0, k0 ? p.chunk : p.chunk + p.chunk / 2);
-}
-__device__ __forceinline__ uint32_t last_chunk(const ProjectParams& p) {  // where the last one begins
-    const uint32_t second = p.chunk + p.chunk / 2;
-    return p.slices <= second ? 0 : (p.slices - 1 - second) / p.chunk * p.chunk + second;
 }
 __device__ __forceinline__ const TileGroups* tile_groups(const ProjectParams& p, uint32_t tt) {
     return reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
@@ -349,9 +338,6 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
     fence_after();
     const uint32_t tmem = *s_tmem;
 
-    // The adapters' part comes after the product, or, with the product in chunks, before its
-    // last chunk: the sums outside the tensor core do not care, and the first kernel has time.
-    const uint32_t lora_at = PROMOTE ? last_chunk(p) : p.slices;
     uint32_t issued = 0;    // stages the producer has started copies into
     if (warp == kCopyWarp) {
         if (lane == 0) {
@@ -370,7 +356,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 if (LORA && CG == 2 && p.tensor && tile != first) list.fetch(tile_groups(p, tt));
                 for (uint32_t k = 0;; ++k) {
                     if constexpr (LORA && CG == 2) {
-                        if (p.tensor && k == lora_at) {
+                        if (p.tensor && k == p.slices) {
                             if (tile == first) {
                                 pdl_wait();
                                 list.fetch(tile_groups(p, tt));
@@ -416,7 +402,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 if (LORA && CG == 2 && p.tensor && tile != first) list.fetch(tile_groups(p, tile % p.tiles_t));
                 for (uint32_t k0 = 0, k1; ok; k0 = k1) {
                     if constexpr (LORA && CG == 2) {
-                        if (p.tensor && k0 == lora_at) {
+                        if (p.tensor && k0 == p.slices) {
                             // The adapters' passes: pass 0 into the open accumulator, 1 and 2 into others.
                             if (tile == first) {
                                 pdl_wait();
@@ -478,7 +464,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                         if (++s == p.stages) { s = 0; phase ^= 1; }
                     }
                     if (!ok) break;
-                    if (LORA && CG == 2 && p.tensor && !p.apart) continue;  // pass 0 continues it
+                    if (LORA && CG == 2 && p.tensor && !p.apart && k1 == p.slices) continue;  // pass 0 continues it
                     mma_commit<CG>(acc_full0 + 8 * acc);
                     ++n;
                 }
@@ -618,46 +604,53 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i)
 #pragma unroll
                     for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
-                uint32_t pass = pass_blocks[0] ? 0 : pass_blocks[1] ? 1 : 2;  // the next of the adapters' (2: none)
-                for (uint32_t k0 = 0; k0 < p.slices; ++n) {
+                uint32_t passes = 0;  // of the adapters' accumulators taken, after the product's chunks
+                for (uint32_t k0 = 0;; ++n) {
                     acc = acc_of(n);
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) { ok = false; break; }
                     fence_after();
-                    const bool now = LORA && pass < 2 && k0 == lora_at;
+                    const bool now = LORA && k0 == p.slices;
                     uint32_t blocks = 0xFFFFFFFFu, rows_of = 0;
                     if (now) {
-                        blocks = pass ? pass_blocks[1] : pass_blocks[0];
-                        rows_of = pass ? pass_rows[1] : pass_rows[0];
-                        pass = pass == 0 && pass_blocks[1] ? 1 : 2;
+                        blocks = passes ? pass_blocks[1] : pass_blocks[0];
+                        rows_of = passes ? pass_rows[1] : pass_rows[0];
+                        ++passes;
                     } else {
                         k0 = chunk_end(p, k0);
                     }
-                    const bool last = k0 == p.slices;
+                    // (pass 2 has some of pass 1's blocks)
+                    const bool last = k0 == p.slices && !(LORA && (passes == 0 ? pass_blocks[0] : passes == 1 && pass_blocks[1]));
 #pragma unroll
                     for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
                         const uint32_t c0 = (share + kShares * i) * 32;
-                        if (c0 >= N || !(blocks >> (c0 / kBlock) & 1)) continue;
+                        if (c0 >= N) continue;
                         const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
-                        const float factor = now && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
-                        const uint32_t take = now ? __shfl_sync(0xFFFFFFFFu, rows_of, c0 / kBlock) : 0xFFFFFFFFu;
+                        if (blocks >> (c0 / kBlock) & 1) {
+                            const float factor = now && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
+                            const uint32_t take = now ? __shfl_sync(0xFFFFFFFFu, rows_of, c0 / kBlock) : 0xFFFFFFFFu;
 #pragma unroll
-                        for (int q = 0; q < 32; q += 16) {
-                            float y[16];
-                            tmem_load16(at + q, y);
-                            if (LORA && now && p.lora_f16) {
+                            for (int q = 0; q < 32; q += 16) {
+                                float y[16];
+                                tmem_load16(at + q, y);
+                                if (LORA && now && p.lora_f16) {
 #pragma unroll
-                                for (int c = 0; c < 16; ++c) y[c] *= __shfl_sync(0xFFFFFFFFu, factor, q + c);
+                                    for (int c = 0; c < 16; ++c) y[c] *= __shfl_sync(0xFFFFFFFFu, factor, q + c);
+                                }
+                                if (LORA && now) {
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) y[c] = take >> (q + c) & 1 ? y[c] : 0.f;
+                                }
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
                             }
-                            if (LORA && now) {
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) y[c] = take >> (q + c) & 1 ? y[c] : 0.f;
-                            }
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
                         }
                         if (last) tmem_store32(at, sum[i]);
                     }
-                    if (!last) release(acc);
+                    if (last) {
+                        ++n;
+                        break;
+                    }
+                    release(acc);
                 }
                 if (!ok) break;
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -667,20 +660,23 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 ++n;
             }
             if constexpr (LORA && CG == 2 && !PROMOTE) {
-                // With pass 1 the result moves to that pass's accumulator, so that the product's
-                // is free for the next tile's before the stores begin.
-                if (pass_blocks[0]) {
+                // With pass 1 the result moves to that pass's accumulator, so that the product's is
+                // free for the next tile's before the stores begin, and from there to pass 2's.
+                bool ok = true;
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i) {
+                    if (!pass_blocks[i]) break;
                     const uint32_t from = acc;
                     acc = acc_of(n);
-                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) { ok = false; break; }
                     fence_after();
                     ++n;
                     for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
                         const uint32_t to = tmem + lanes + acc * p.acc_cols + c0;
                         float y[32];
                         tmem_load32(tmem + lanes + from * p.acc_cols + c0, y);
-                        if (pass_blocks[0] >> (c0 / kBlock) & 1) {
-                            if constexpr (FP8) {
+                        if (pass_blocks[i] >> (c0 / kBlock) & 1) {
+                            if (FP8 && i == 0) {  // (pass 2 has some of pass 1's blocks)
                                 const float row_scale = of_row(p.x_scale, c0);
 #pragma unroll
                                 for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
@@ -692,14 +688,16 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
 #pragma unroll
                                 for (int c = 0; c < 32; ++c) z[c] *= __shfl_sync(0xFFFFFFFFu, factor, c);
                             }
+                            const uint32_t take = __shfl_sync(0xFFFFFFFFu, pass_rows[i], c0 / kBlock);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) y[c] += z[c];
+                            for (int c = 0; c < 32; ++c) y[c] += take >> c & 1 ? z[c] : 0.f;
                         }
                         tmem_store32(to, y);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     release(from);
                 }
+                if (!ok) break;
             }
             const uint32_t columns = tmem + lanes + acc * p.acc_cols;
             if (!LORA || v0 < p.V) {
@@ -1017,7 +1015,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     // Blocks of rows with one adapter run on the tensor cores (pairs only: the tiles of fewer
     // rows wait for memory, and the epilogue's arithmetic is hidden).
     p.tensor = cg == 2 && p.lora_tma && rank != 0;
-    p.apart = fp8 || dtype == LP_F16 || out_dtype == LP_F32;
+    p.apart = fp8 || dtype == LP_F16;
     p.part_stride = (uint32_t)space.rows;
     p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : p.slices;
     for (p.acc_cols = 32; p.acc_cols < p.tile_t; p.acc_cols *= 2) {}
@@ -1066,7 +1064,6 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         q.tile_t = p.tile_t;
         q.tensor = p.tensor;
         q.apart = p.apart;
-        q.split = !fp8 && out_dtype == LP_F32;
         q.part_stride = p.part_stride;
         q.lora_f16 = p.lora_f16;
         q.status = p.status;
