@@ -81,37 +81,57 @@ __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     const uint32_t m0 = with ? __ballot_sync(kAll, mine == a0) : 0u, rest = with & ~m0;
     const int32_t a1 = __shfl_sync(kAll, mine, rest ? __ffs(rest) - 1 : 0);
     const uint32_t m1 = rest ? __ballot_sync(kAll, mine == a1) : 0u;
-    const bool listed = with && (!p.tensor || (rest & ~m1) != 0);
-    const bool tensor = with && !listed;
-    __shared__ uint32_t adapter[3][kBlocks], listed_bits;  // of each pass
+    const bool many = with && (!p.tensor || (rest & ~m1) != 0);
+    __shared__ uint32_t adapter[3][kBlocks], listed_bits;  // of pass 0, of pass 1: first and second
     if (c == 0) listed_bits = 0;
     sync();
     if (c % kBlock == 0) {
         const uint32_t b = c / kBlock, pass = m0 == in && !p.apart ? 0 : 1;  // of the first adapter
+        const bool tensor = with && !many;
         adapter[0][b] = tensor && pass == 0 ? (uint32_t)a0 : kNoAdapter;
         adapter[1][b] = tensor && pass == 1 ? (uint32_t)a0 : kNoAdapter;
         adapter[2][b] = tensor && rest ? (uint32_t)a1 : kNoAdapter;
         g->rows[0][b] = m0;
         g->rows[1][b] = m1;
-        if (listed) atomicOr(&listed_bits, 1u << b);
+        if (many) atomicOr(&listed_bits, 1u << b);
     }
     sync();
     if (c == 0) {
-        uint32_t runs = 0;
-        for (uint32_t pass = 0; pass < 3; ++pass) {
-            uint32_t blocks = 0;
+        uint32_t runs = 0, blocks = 0, second = 0, place = 0, taken = 0;
+        for (uint32_t b = 0; b < kBlocks; ++b)
+            if (adapter[1][b] != kNoAdapter) taken |= 1u << b;
+        for (uint32_t b = 0; b < kBlocks; ++b) {
+            if (adapter[2][b] == kNoAdapter) continue;
+            const uint32_t free = ~taken & ((1u << p.tile_t / kBlock) - 1u);
+            if (free) {
+                const uint32_t f = __ffs(free) - 1;
+                taken |= 1u << f;
+                place |= f << 4 * b;
+                second |= 1u << b;
+            } else {
+                adapter[1][b] = adapter[2][b] = kNoAdapter;
+                listed_bits |= 1u << b;
+            }
+        }
+        for (uint32_t pass = 0; pass < 2; ++pass) {
             for (uint32_t b0 = 0, n; b0 < kBlocks; b0 += n) {
                 const uint32_t a = adapter[pass][b0];
                 for (n = 1; b0 + n < kBlocks && adapter[pass][b0 + n] == a; ++n) {}
                 if (a == kNoAdapter) continue;
-                g->run[runs++] = make_uint2(pass << 16 | b0 << 8 | n, a);
-                blocks |= ((1u << n) - 1u) << b0;
+                g->run[runs++] = make_uint2(b0 << 24 | pass << 16 | b0 << 8 | n, a);
+                if (pass) blocks |= ((1u << n) - 1u) << b0;
             }
-            if (pass) g->blocks[pass - 1] = blocks;
         }
+        for (uint32_t b = 0; b < kBlocks; ++b)
+            if (second >> b & 1) g->run[runs++] = make_uint2((place >> 4 * b & 15) << 24 | 1u << 16 | b << 8 | 1u, adapter[2][b]);
+        g->blocks = blocks;
+        g->second = second;
+        g->place = place;
         g->runs = runs;
         g->listed = listed_bits;
     }
+    sync();
+    const bool listed = listed_bits >> (c / kBlock) & 1;
     uint32_t k = kUnlisted;
     key[c] = listed && c < rows ? 0 : kUnlisted;
     sync();

@@ -14,25 +14,28 @@ constexpr uint32_t kNoAdapter = 0xFFFFFFFFu;
 
 // One tile of rows, in blocks of 32. Where all rows of a block have one adapter, its part of
 // the product runs on the tensor cores: in pass 0, which adds to the product's own accumulator,
-// or, where that cannot be (`apart`), in pass 1, which has one of its own. Passes 1 and 2 take
-// the two adapters of blocks that have two, or one and rows without: the epilogue adds the rows
-// that have the pass's adapter. The rows of other blocks are grouped by adapter, those without
-// one last, and cut into items of at most kItemRows rows of one adapter, which the epilogue
-// multiplies itself.
+// or, where that cannot be (`apart`), in pass 1, which has one of its own. Pass 1 also takes the
+// two adapters of blocks that have two, or one and rows without: the epilogue adds the rows that
+// have the adapter. The second adapter's sums lie in columns of a block that is not in the pass.
+// The rows of other blocks (and where no such column is left) are grouped by adapter, those
+// without one last, and cut into items of at most kItemRows rows of one adapter, which the
+// epilogue multiplies itself.
 // (Zeroing u in other adapters' rows instead would let an infinity in one adapter's B become
 // NaN, 0 x inf, in the rows of others.)
 constexpr uint32_t kBlocks = kMaxTileT / kBlock;
-constexpr uint32_t kMaxRuns = 3 * kBlocks;
+constexpr uint32_t kMaxRuns = 2 * kBlocks;
 struct TileGroups {
     uint32_t items;
     uint32_t listed;             // bit per block: its rows are in items
     uint32_t runs;
-    uint32_t unused;
-    uint32_t blocks[2];          // bit per block: it is in pass 1, in pass 2
-    uint32_t unused2[2];
-    uint32_t rows[2][kBlocks];   // the block's rows that have the pass's adapter, a bit each
+    uint32_t blocks;             // bit per block: it is in pass 1
+    uint32_t second;             // bit per block: with two adapters
+    uint32_t place;              // 4 bits per block: the block whose columns hold the second one's sums
+    uint32_t unused[2];
+    uint32_t rows[2][kBlocks];   // the block's rows that have its first, its second adapter, a bit each
     uint2 run[kMaxRuns];         // neighbouring blocks with one adapter in a pass, in the order of the
-                                 // passes: x = pass << 16 | first block << 8 | blocks, y = adapter
+                                 // passes: x = place of the sums << 24 | pass << 16 | first block << 8
+                                 // | blocks, y = adapter
     uint32_t item[kMaxItems];    // adapter of item k, kNoAdapter for rows without one
     uint8_t start[kMaxItems];    // item k holds order[start[k] ... start[k] + size[k] - 1]
     uint8_t size[kMaxItems];

@@ -403,7 +403,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 for (uint32_t k0 = 0, k1; ok; k0 = k1) {
                     if constexpr (LORA && CG == 2) {
                         if (p.tensor && k0 == p.slices) {
-                            // The adapters' passes: pass 0 into the open accumulator, 1 and 2 into others.
+                            // The adapters' passes: pass 0 into the open accumulator, 1 into the next.
                             if (tile == first) {
                                 pdl_wait();
                                 list.fetch(tile_groups(p, tile % p.tiles_t));
@@ -412,13 +412,13 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             bool open = !p.apart;  // the product's own accumulator
                             for (uint32_t r = 0; ok && r < list.runs; ++r) {
                                 const uint2 run = list.at(r);
-                                const uint32_t b0 = run.x >> 8 & 0xFF, blocks = run.x & 0xFF;
-                                if (run.x >> 16 != pass) {
+                                const uint32_t to = run.x >> 24, blocks = run.x & 0xFF;
+                                if ((run.x >> 16 & 0xFF) != pass) {
                                     if (open) {
                                         mma_commit<CG>(acc_full0 + 8 * acc_of(n));
                                         ++n;
                                     }
-                                    pass = run.x >> 16;
+                                    pass = 1;
                                     open = mbar_wait(acc_empty0 + 8 * acc_of(n), acc_phase(n) ^ 1, s_abort);
                                     if (!open) { ok = false; break; }
                                 }
@@ -433,7 +433,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                         const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
                                                        j = column - part * p.b_cols;
                                         if (part < 3 && j < uc)
-                                            mma<false, CG>(tmem + acc_of(n) * p.acc_cols + b0 * kBlock, a + j / 8, b + 2 * i,
+                                            mma<false, CG>(tmem + acc_of(n) * p.acc_cols + to * kBlock, a + j / 8, b + 2 * i,
                                                            idesc, pass ? (line | i) : 1u);
                                     }
                                     mma_commit<CG>(empty0 + 8 * s);
@@ -560,20 +560,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
             const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t, t0 = tt * N;
             const uint32_t v0 = (tv * CG + rank) * kTileV, v = v0 + quad * 32 + lane;
             const uint32_t rows = min(N, p.T - t0);
-            uint32_t items = 0, listed = 0;
-            uint32_t pass_blocks[2] = {0, 0};  // blocks of passes 1 and 2
-            uint32_t pass_rows[2] = {0, 0};    // lane b: block b's rows in the pass
+            [[maybe_unused]] const TileGroups* g = LORA ? tile_groups(p, tt) : nullptr;
             if constexpr (LORA) {
-                const TileGroups* g = tile_groups(p, tt);
-                listed = g->listed;
-                items = g->items;
-                if (CG == 2 && p.tensor) {
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        pass_blocks[i] = g->blocks[i];
-                        pass_rows[i] = lane < kBlocks ? g->rows[i][lane] : 0u;
-                    }
-                }
+                const uint32_t items = g->items;
                 if (items && tt != staged) {  // the lists, u and scales in shared memory
                     if (!meet()) break;
                     const uint4* words = reinterpret_cast<const uint4*>(g);
@@ -604,100 +593,130 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i)
 #pragma unroll
                     for (int c = 0; c < 32; ++c) sum[i][c] = 0.f;
-                uint32_t passes = 0;  // of the adapters' accumulators taken, after the product's chunks
-                for (uint32_t k0 = 0;; ++n) {
+                for (uint32_t k0 = 0;;) {
                     acc = acc_of(n);
                     if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) { ok = false; break; }
+                    ++n;
                     fence_after();
-                    const bool now = LORA && k0 == p.slices;
-                    uint32_t blocks = 0xFFFFFFFFu, rows_of = 0;
-                    if (now) {
-                        blocks = passes ? pass_blocks[1] : pass_blocks[0];
-                        rows_of = passes ? pass_rows[1] : pass_rows[0];
-                        ++passes;
-                    } else {
-                        k0 = chunk_end(p, k0);
-                    }
-                    // (pass 2 has some of pass 1's blocks)
-                    const bool last = k0 == p.slices && !(LORA && (passes == 0 ? pass_blocks[0] : passes == 1 && pass_blocks[1]));
+                    k0 = chunk_end(p, k0);
 #pragma unroll
                     for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
                         const uint32_t c0 = (share + kShares * i) * 32;
                         if (c0 >= N) continue;
                         const uint32_t at = tmem + lanes + acc * p.acc_cols + c0;
-                        if (blocks >> (c0 / kBlock) & 1) {
-                            const float factor = now && p.lora_f16 ? of_row(p.factor, c0) : 1.f;
-                            const uint32_t take = now ? __shfl_sync(0xFFFFFFFFu, rows_of, c0 / kBlock) : 0xFFFFFFFFu;
 #pragma unroll
-                            for (int q = 0; q < 32; q += 16) {
-                                float y[16];
-                                tmem_load16(at + q, y);
-                                if (LORA && now && p.lora_f16) {
+                        for (int q = 0; q < 32; q += 16) {
+                            float y[16];
+                            tmem_load16(at + q, y);
 #pragma unroll
-                                    for (int c = 0; c < 16; ++c) y[c] *= __shfl_sync(0xFFFFFFFFu, factor, q + c);
-                                }
-                                if (LORA && now) {
-#pragma unroll
-                                    for (int c = 0; c < 16; ++c) y[c] = take >> (q + c) & 1 ? y[c] : 0.f;
-                                }
-#pragma unroll
-                                for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
-                            }
+                            for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
                         }
-                        if (last) tmem_store32(at, sum[i]);
                     }
-                    if (last) {
-                        ++n;
-                        break;
-                    }
+                    if (k0 == p.slices) break;
                     release(acc);
                 }
                 if (!ok) break;
+                const uint32_t blocks = LORA && CG == 2 && p.tensor ? g->blocks : 0u;
+                if (blocks) {  // pass 1
+                    release(acc);
+                    acc = acc_of(n);
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
+                    ++n;
+                    fence_after();
+                    const uint32_t columns = tmem + lanes + acc * p.acc_cols;
+#pragma unroll
+                    for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
+                        const uint32_t b = share + kShares * i, c0 = b * 32;
+                        if (c0 >= N || !(blocks >> b & 1)) continue;
+                        const float factor = p.lora_f16 ? of_row(p.factor, c0) : 1.f;
+                        const uint32_t adapters = 1 + (g->second >> b & 1);
+                        for (uint32_t k = 0; k < adapters; ++k) {
+                            const uint32_t take = g->rows[k][b], from = k ? (g->place >> 4 * b & 15) * 32 : c0;
+#pragma unroll
+                            for (int q = 0; q < 32; q += 16) {
+                                float y[16];
+                                tmem_load16(columns + from + q, y);
+                                if (p.lora_f16) {
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) y[c] *= __shfl_sync(0xFFFFFFFFu, factor, q + c);
+                                }
+#pragma unroll
+                                for (int c = 0; c < 16; ++c) sum[i][q + c] += take >> (q + c) & 1 ? y[c] : 0.f;
+                            }
+                        }
+                    }
+                    // (a block's columns may hold another's second sums)
+                    fence_before();
+                    if (!meet()) break;
+                    fence_after();
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < (kMaxTileT / 32 + kShares - 1) / kShares; ++i) {
+                    const uint32_t c0 = (share + kShares * i) * 32;
+                    if (c0 < N) tmem_store32(tmem + lanes + acc * p.acc_cols + c0, sum[i]);
+                }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             } else {
                 if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
                 fence_after();
                 ++n;
             }
+            const uint32_t listed = LORA ? g->listed : 0u, items = LORA ? g->items : 0u;
+            const uint32_t blocks = LORA && CG == 2 && p.tensor ? g->blocks : 0u;
             if constexpr (LORA && CG == 2 && !PROMOTE) {
-                // With pass 1 the result moves to that pass's accumulator, so that the product's is
-                // free for the next tile's before the stores begin, and from there to pass 2's.
-                bool ok = true;
-#pragma unroll
-                for (uint32_t i = 0; i < 2; ++i) {
-                    if (!pass_blocks[i]) break;
-                    const uint32_t from = acc;
+                // With pass 1 the result moves to that pass's accumulator, so that the product's
+                // is free for the next tile's before the stores begin.
+                if (blocks) {
+                    const uint32_t from = tmem + lanes + acc * p.acc_cols;
+                    const uint32_t main = acc, second = g->second;
                     acc = acc_of(n);
-                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) { ok = false; break; }
+                    if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
                     fence_after();
                     ++n;
-                    for (uint32_t c0 = share * 32; c0 < N; c0 += kShares * 32) {
-                        const uint32_t to = tmem + lanes + acc * p.acc_cols + c0;
-                        float y[32];
-                        tmem_load32(tmem + lanes + from * p.acc_cols + c0, y);
-                        if (pass_blocks[i] >> (c0 / kBlock) & 1) {
-                            if (FP8 && i == 0) {  // (pass 2 has some of pass 1's blocks)
-                                const float row_scale = of_row(p.x_scale, c0);
+                    const uint32_t to = tmem + lanes + acc * p.acc_cols;
+                    // the product of block b in y, e4m3's with its scales
+                    const auto load_product = [&](uint32_t b, bool scaled, float (&y)[32]) {
+                        tmem_load32(from + b * 32, y);
+                        if (FP8 && scaled) {
+                            const float row_scale = of_row(p.x_scale, b * 32);
 #pragma unroll
-                                for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
-                            }
-                            float z[32];
-                            tmem_load32(to, z);
-                            if (p.lora_f16) {
-                                const float factor = of_row(p.factor, c0);
-#pragma unroll
-                                for (int c = 0; c < 32; ++c) z[c] *= __shfl_sync(0xFFFFFFFFu, factor, c);
-                            }
-                            const uint32_t take = __shfl_sync(0xFFFFFFFFu, pass_rows[i], c0 / kBlock);
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) y[c] += take >> c & 1 ? z[c] : 0.f;
+                            for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
                         }
-                        tmem_store32(to, y);
+                    };
+                    // and block b's sums at block `at` of the pass, of the rows in `take`
+                    const auto add_sums = [&](uint32_t b, uint32_t at, uint32_t take, float (&y)[32]) {
+                        float z[32];
+                        tmem_load32(to + at * 32, z);
+                        if (p.lora_f16) {
+                            const float factor = of_row(p.factor, b * 32);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) z[c] *= __shfl_sync(0xFFFFFFFFu, factor, c);
+                        }
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) y[c] += take >> c & 1 ? z[c] : 0.f;
+                    };
+                    if (second) {  // those lie where other blocks' results go
+                        for (uint32_t b = share; b < N / 32; b += kShares) {
+                            if (!(second >> b & 1)) continue;
+                            float y[32];
+                            load_product(b, true, y);
+                            add_sums(b, g->place >> 4 * b & 15, g->rows[1][b], y);
+                            tmem_store32(from + b * 32, y);
+                        }
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                        fence_before();
+                        if (!meet()) break;
+                        fence_after();
+                    }
+                    for (uint32_t b = share; b * 32 < N; b += kShares) {
+                        float y[32];
+                        load_product(b, (blocks & ~second) >> b & 1, y);
+                        if (blocks >> b & 1) add_sums(b, b, g->rows[0][b], y);
+                        tmem_store32(to + b * 32, y);
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    release(from);
+                    release(main);
                 }
-                if (!ok) break;
             }
             const uint32_t columns = tmem + lanes + acc * p.acc_cols;
             if (!LORA || v0 < p.V) {
@@ -706,7 +725,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                     float y[32];
                     tmem_load32(columns + c0, y);
                     if constexpr (FP8) {
-                        if (!LORA || !(pass_blocks[0] >> (c0 / kBlock) & 1)) {
+                        if (!LORA || !(blocks >> (c0 / kBlock) & 1)) {
                             const float row_scale = of_row(p.x_scale, c0);
 #pragma unroll
                             for (int c = 0; c < 32; ++c) y[c] *= sw * __shfl_sync(0xFFFFFFFFu, row_scale, c);
@@ -723,7 +742,7 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                 }
             }
             if (LORA && items && v0 < p.V) {
-                if (PROMOTE || pass_blocks[0]) {  // an item's columns may have been written by another share
+                if (PROMOTE || blocks) {  // an item's columns may have been written by another share
                     fence_before();
                     if (!meet()) break;
                     fence_after();
