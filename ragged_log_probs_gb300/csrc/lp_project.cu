@@ -250,6 +250,13 @@ __device__ __forceinline__ uint32_t chunk_end(const ProjectParams& p, uint32_t k
 __device__ __forceinline__ const TileGroups* tile_groups(const ProjectParams& p, uint32_t tt) {
     return reinterpret_cast<const TileGroups*>(p.groups + (size_t)tt * kGroupBytes);
 }
+// Lines of u's parts that a stage holds for a run of `blocks` blocks beside B_a: all that it has,
+// where the rows of x in a stage leave the room (a short run has little to compute, and with a
+// stage a line the copies of the product's next slices started too late for it: 2048 x 32000
+// with ragged adapters of rank 64: 441 us so, 436 with all in one), or one.
+__device__ __forceinline__ uint32_t lines_a_stage(uint32_t lines, uint32_t blocks, uint32_t N) {
+    return lines * blocks * kBlock <= N ? lines : 1;
+}
 // A tile's runs: the count and the first four are fetched when the tile begins, long before
 // they are used.
 struct RunList {
@@ -365,16 +372,19 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                             for (uint32_t r = 0; ok && r < list.runs; ++r) {
                                 const uint2 run = list.at(r);
                                 const uint32_t a = run.y, b0 = run.x >> 8 & 0xFF, n = run.x & 0xFF;
-                                for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                                constexpr uint32_t kHalf = kBlock / CG;  // rows of a block that a CTA holds
+                                const uint32_t lines = part_rows(p.rank), group = lines_a_stage(lines, n, N);
+                                for (uint32_t l0 = 0; l0 < lines; l0 += group) {
                                     if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
                                     const uint32_t dst = base + s * stage_bytes, bar = map_to(full0 + 8 * s, 0);
-                                    constexpr uint32_t kHalf = kBlock / CG;  // rows of a block that a CTA holds
-                                    if (rank == 0) mbar_expect(full0 + 8 * s, CG * (kStageW + n * kHalf * kSliceBytes));
+                                    if (rank == 0) mbar_expect(full0 + 8 * s, CG * (kStageW + group * n * kHalf * kSliceBytes));
                                     tma_2d<CG>(dst, &map_lora_b, 0, (int)(a * p.V) + v0, bar, keep);
-                                    for (uint32_t i = 0; i < n; ++i)
+                                    for (uint32_t i = 0; i < group * n; ++i) {
+                                        const uint32_t line = l0 + i / n, block = i % n;
                                         tma_2d<CG>(dst + kStageW + i * kHalf * kSliceBytes, &map_parts, 0,
-                                                   (int)(line * p.part_stride + tt * N + b0 * kBlock + (rank * n + i) * kHalf),
+                                                   (int)(line * p.part_stride + tt * N + b0 * kBlock + (rank * n + block) * kHalf),
                                                    bar, keep);
+                                    }
                                     ++issued;
                                     if (++s == p.stages) { s = 0; phase ^= 1; }
                                 }
@@ -423,18 +433,22 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
                                     if (!open) { ok = false; break; }
                                 }
                                 const uint32_t idesc = p.lora_idesc | ((blocks * kBlock >> 3) << 17);
-                                for (uint32_t line = 0; line < part_rows(p.rank); ++line) {
+                                const uint32_t lines = part_rows(p.rank), group = lines_a_stage(lines, blocks, N);
+                                for (uint32_t l0 = 0; l0 < lines; l0 += group) {
                                     if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
                                     fence_after();
                                     const uint64_t a = matrix_desc(base + s * stage_bytes);
-                                    const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW);
-                                    // 16 columns of the parts a step; B_a's start again with each part
-                                    for (uint32_t i = 0; i < 4; ++i) {
-                                        const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
-                                                       j = column - part * p.b_cols;
-                                        if (part < 3 && j < uc)
-                                            mma<false, CG>(tmem + acc_of(n) * p.acc_cols + to * kBlock, a + j / 8, b + 2 * i,
-                                                           idesc, pass ? (line | i) : 1u);
+                                    for (uint32_t line = l0; line < l0 + group; ++line) {
+                                        const uint64_t b = matrix_desc(base + s * stage_bytes + kStageW +
+                                                                       (line - l0) * blocks * (kBlock / CG) * kSliceBytes);
+                                        // 16 columns of the parts a step; B_a's start again with each part
+                                        for (uint32_t i = 0; i < 4; ++i) {
+                                            const uint32_t column = line * 64 + i * 16, part = column / p.b_cols,
+                                                           j = column - part * p.b_cols;
+                                            if (part < 3 && j < uc)
+                                                mma<false, CG>(tmem + acc_of(n) * p.acc_cols + to * kBlock, a + j / 8, b + 2 * i,
+                                                               idesc, pass ? (line | i) : 1u);
+                                        }
                                     }
                                     mma_commit<CG>(empty0 + 8 * s);
                                     if (++s == p.stages) { s = 0; phase ^= 1; }
