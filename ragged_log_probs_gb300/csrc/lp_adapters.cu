@@ -5,8 +5,9 @@
 // rows of its adapter's A, so it suits rows with adapters of their own (decode). A block of 16
 // rows, which multiplies them by the A of every adapter among them on the tensor cores
 // (mma.sync: the work is too small and too ragged for a pipeline of its own): long requests,
-// where 16 rows have one adapter or two. Measured for 2048 rows of 8 requests, rank 64,
-// H = 4096: see launch_shrink.
+// where 16 rows have one adapter or two (launch_shrink has both sides' times). Bound by latency:
+// 2048 rows of 8 requests, rank 64, H = 4096 take 30 us, of which x and A at HBM's rate would be
+// 3; the product runs meanwhile and asks for u at the end of its first tile.
 #include "lp_adapters.h"
 
 namespace {

@@ -11,17 +11,23 @@
 // corrected. Biases are added last. Long histories are sorted by slices first (k_sort_history,
 // 4096 tokens a CTA, into the workspace); short ones are read by every CTA of a row.
 //
-// Bound by HBM: a row is read once and written once, and a vector whose mask bits are all 0 is
-// not read. What had to be hidden is the time before the copy (who the row belongs to, its
-// parameters, its history: reads that wait for each other): the slice is asked for in L2 at
-// the very start (256 rows of 128256 f32 without lists: 57 -> 41 us, a plain copy takes 42).
+// A row is read once and written once, and a vector whose mask bits are all 0 is not read; HBM
+// would take 41 us for 256 rows of 128256 f32, and without lists this takes that. What costs is
+// the time before the copy (who the row belongs to, its parameters, its history: reads that wait
+// for each other, about 6 of a CTA's 17 us), and the copy's look at the table (8 against 4 us).
+// So the slice is asked for in L2 at the very start (57 -> 41 us), the histories are sorted while
+// the first CTAs begin, and four CTAs share an SM. With histories of up to 30000: 66 us.
+// Slices held in shared memory as values, loaded and stored by bulk copies, were measured too:
+// 36000 tokens per SM at a time instead of 98000 hide less of those waits (85 us).
 #include "lp_head_common.h"
 
 namespace {
 
 using namespace lph;
 
-constexpr uint32_t kMaxSlice = 24576;  // tokens of a slice: a 48 KB table, four CTAs per SM
+// Tokens of a slice: a 48 KB table, four CTAs per SM (256 rows of 128256 f32 with histories of up
+// to 30000, 240 rows of 152064 bf16 with up to 3000: 69 and 47 us; 16384, five CTAs: 71 and 54).
+constexpr uint32_t kMaxSlice = 24576;
 constexpr uint32_t kMinSlice = 1024;
 constexpr uint32_t kResident = 4;      // CTAs per SM
 constexpr uint32_t kBatch = 4;         // vectors a thread has in flight
@@ -568,9 +574,12 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     p.slice = (uint32_t)(((V + slices - 1) / slices + 7) / 8 * 8);
     p.slices = (V + p.slice - 1) / p.slice;
     // Long histories are sorted by slices first; below that, reading them in every CTA costs less
-    // than a second kernel.
-    if (p.history && history_total / B >= kSortFrom) {
-        if (workspace_bytes < lp_head_process_workspace_size(B, history_total) || p.slices > kMaxSlices) return LP_ERR_WORKSPACE;
+    // than a second kernel. Rows of 128256 f32, all histories of one length, us (sorted | not):
+    //     256 rows  2000: 60 | 59    4000: 64 | 70    8000: 72 | 89   16000: 78 | 113
+    //      32 rows  2000: 21 | 17    4000: 27 | 21    8000: 27 | 27   16000: 29 | 36
+    //       4 rows  2000: 17 | 13    4000: 21 | 15    8000: 21 | 17   16000: 21 | 25
+    if (p.history && history_total / B >= kSortFrom && p.slices <= kMaxSlices) {
+        if (workspace_bytes < lp_head_process_workspace_size(B, history_total)) return LP_ERR_WORKSPACE;
         p.bounds = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
         const uint32_t chunks = B + history_total / kChunk + 1;
         p.sorted = p.bounds + (size_t)chunks * (p.slices + 1);

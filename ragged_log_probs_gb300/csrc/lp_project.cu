@@ -3,15 +3,23 @@
 //     u[t, j]   = s_a sx[t] sum_h x[t, h] A_a[j, h],   a = adapter of row t's request.
 //
 // The product runs on the tensor cores with the vocabulary on the accumulator's lanes: a
-// tile is 128 vocabulary rows by N rows of x (N = the row count rounded up to 16, at most
-// 256), so that a decode step reads W once and pads little, and a warp's 32 lanes hold 32
-// neighbouring logits of one output row (coalesced stores without a transpose). One thread
-// issues TMA copies of 128-byte-wide slices of W and x into a ring of stages, one issues
-// tcgen05.mma from them into one of two accumulators in TMEM, and eight warps empty the
-// other accumulator meanwhile. Kernels are persistent; consecutive tiles share their W rows.
+// tile is 128 vocabulary rows (256 of a pair of CTAs) by N rows of x (at most 256), so that a
+// decode step reads W once and pads little, and a warp's 32 lanes hold 32 neighbouring logits of
+// one output row (coalesced stores without a transpose). One thread issues TMA copies of
+// 128-byte-wide slices of W and x into a ring of stages, one issues tcgen05.mma from them into
+// one of two to eight accumulators in TMEM (what 512 columns hold), and twelve warps empty the
+// others meanwhile. Kernels are persistent; consecutive tiles share their W rows.
 //
-// u is computed first, by its own small kernel; the product starts while that still runs
-// and waits for it only before its first epilogue, which adds the adapters' part in f32.
+// u is computed first, by its own small kernel (lp_adapters.cu); the product starts while that
+// still runs and waits for it only at the end of its first tile. Where 32 rows of a tile have
+// one adapter or two, u B_a^T is a product on the tensor cores as well, with u as three 16-bit
+// parts (24 bits, what f32 has); other rows, and tiles of single CTAs, are multiplied by the
+// epilogue in f32, adapter by adapter, with tiles of B_a copied ahead of it.
+//
+// Bound by HBM (W) up to about 128 rows, by the tensor cores above. Measured, us (W at HBM's
+// measured rate, or the products at a large library product's): one row, V = 128256, H = 4096
+// bf16 162 (155); 256 rows 183 (144); 2048 rows, V = 32000 bf16 286 and f32 327 (287); e4m3 48
+// rows of V = 152064 with 12 adapters of rank 32 134 (114).
 #include <cuda.h>
 
 #include "lp_adapters.h"
@@ -276,9 +284,10 @@ struct RunList {
 
 // PROMOTE: f32 logits of 16-bit inputs. The tensor core's f32 accumulator drops the bits
 // below its last place at every step, always towards zero: over a contraction of 4096 that
-// adds up to 2.8e-6 of the result, against 6e-7 of rounded f32 sums. So the accumulator is
-// emptied into registers every kPromoteSlices slices (256 products), and those are summed
-// with rounding. Rounded outputs (16 bits) and e4m3 products (few bits) do not need it.
+// adds up to 4.4e-6 of the result, against 6e-7 of rounded f32 sums. So the accumulator is
+// emptied into registers every kPromoteSlices slices (8, 512 products; the first time after
+// half as many again), and those are summed with rounding: 4.8e-7 (4 slices 2.4e-7, 16 1.0e-6).
+// It costs 2048 rows on V = 32000 327 us instead of 286. Rounded outputs (16 bits) and e4m3 products (few bits) do not need it.
 template <bool FP8, typename OUT, int CG, bool PROMOTE, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
 k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
