@@ -13,7 +13,6 @@ namespace {
 using namespace lph;
 
 constexpr int kVec = 8;         // elements a thread handles together
-constexpr int kMaxVecs = 4;     // vectors a thread holds
 constexpr int kWarpRowVecs = 128;  // rows of up to this many vectors (1024 elements): a warp each
 constexpr int kWarpRows = 4;    // rows (warps) per CTA then
 
@@ -28,39 +27,88 @@ struct NormParams {
     uint32_t* status;
     uint64_t x_stride, residual_stride, out_stride, residual_out_stride;
     uint32_t T, n, H;
+    uint32_t shift;       // groups of eight follow the output's boundaries (kShifted)
     uint32_t weight_f32;  // weight is f32 whatever the rows' type
     float eps;
 };
 
-// Eight elements: neighbours from e on (16-byte aligned), or every `step`-th from e on, one by
-// one, zero from H on (so that a warp's lanes read neighbours).
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int e, int step, int H, float (&v)[kVec]) {
-    if constexpr (VEC) {
-        p += e;
-        if constexpr (sizeof(T) == 4) {
-            const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = *reinterpret_cast<const uint4*>(p);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Where a thread's eight elements lie. kAligned: neighbours, all in the row, on a 16-byte
+// boundary. Rows at other boundaries: kShifted, neighbours from any element on, also before the
+// row's first, or kStrided, every `step`-th, so that a warp's lanes read neighbours. The first
+// reads the aligned 16-byte words that hold the eight and shifts, which takes fewer loads and
+// costs more at a row's ends: 333 rows of 5001 f16 7.3 us, strided 9.0; 10757 of 6622 bf16 92 and
+// 107; but 8746 of 390, a warp each, 14.5 and 10.5.
+enum Layout { kAligned, kShifted, kStrided };
+
+// Eight elements out of their words.
+__device__ __forceinline__ void widen(const uint32_t (&w)[8], float (&v)[kVec], float) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack2(w[i], T());
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
+    for (int i = 0; i < kVec; ++i) v[i] = __uint_as_float(w[i]);
+}
+template <typename T>
+__device__ __forceinline__ void widen(const uint32_t (&w)[8], float (&v)[kVec], T) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2(w[i], T());
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+__device__ __forceinline__ void read16(const void* p, uint32_t* w) {
+    const uint4 a = *static_cast<const uint4*>(p);
+    w[0] = a.x;
+    w[1] = a.y;
+    w[2] = a.z;
+    w[3] = a.w;
+}
+
+// The eight elements from e on, zero where the row of H has none.
+template <typename T, Layout L>
+__device__ __forceinline__ void load8(const T* p, int e, int step, int H, float (&v)[kVec]) {
+    constexpr int kIn16 = 16 / sizeof(T), kWords = 2 * sizeof(T);  // 32-bit words of the eight
+    const int m = L == kShifted ? (int)((reinterpret_cast<uintptr_t>(p + e) & 15) / sizeof(T)) : 0;
+    if (L == kAligned || (L == kShifted && e - m >= 0 && e - m + kVec + (m ? kIn16 : 0) <= H)) {
+        uint32_t w[12];
+        const T* q = p + e - m;
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) read16(q + i * kIn16, w + 4 * i);
+        if (m) {
+            read16(q + kVec, w + kWords);
+            if (sizeof(T) == 2) {
+                if (m & 4)
+#pragma unroll
+                    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+                if (m & 2)
+#pragma unroll
+                    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+                if (m & 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+            } else {
+                if (m & 2)
+#pragma unroll
+                    for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+                if (m & 1)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = w[i + 1];
             }
         }
+        uint32_t eight[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) eight[i] = i < kWords ? w[i] : 0u;
+        widen(eight, v, T());
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] = e + i * step < H ? to_f32(p[e + i * step]) : 0.f;
+        for (int i = 0; i < kVec; ++i) {
+            const int at = L == kStrided ? e + i * step : e + i;
+            v[i] = at >= 0 && at < H ? to_f32(p[at]) : 0.f;
+        }
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, Layout L>
 __device__ __forceinline__ void store8(T* p, int e, int step, int H, const float (&v)[kVec]) {
-    if constexpr (VEC) {
+    if (L == kAligned || (L == kShifted && e >= 0 && e + kVec <= H && (reinterpret_cast<uintptr_t>(p + e) & 15) == 0)) {
         p += e;
         if constexpr (sizeof(T) == 4) {
             *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
@@ -71,28 +119,32 @@ __device__ __forceinline__ void store8(T* p, int e, int step, int H, const float
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (e + i * step < H) p[e + i * step] = from_f32<T>(v[i]);
+        for (int i = 0; i < kVec; ++i) {
+            const int at = L == kStrided ? e + i * step : e + i;
+            if (at >= 0 && at < H) p[at] = from_f32<T>(v[i]);
+        }
     }
 }
 
-template <bool VEC>
+template <Layout L>
 __device__ __forceinline__ void store8_e4m3(uint8_t* p, int e, int step, int H, const float (&v)[kVec]) {
     uint16_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)  // round to nearest even, saturating; NaN stays NaN
         h[i] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
-    if constexpr (VEC) {
+    if (L == kAligned || (L == kShifted && e >= 0 && e + kVec <= H && (reinterpret_cast<uintptr_t>(p + e) & 7) == 0)) {
         *reinterpret_cast<uint2*>(p + e) = make_uint2(h[0] | ((uint32_t)h[1] << 16), h[2] | ((uint32_t)h[3] << 16));
     } else {
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
-            if (e + i * step < H) p[e + i * step] = (uint8_t)(h[i / 2] >> (8 * (i & 1)));
+        for (int i = 0; i < kVec; ++i) {
+            const int at = L == kStrided ? e + i * step : e + i;
+            if (at >= 0 && at < H) p[at] = (uint8_t)(h[i / 2] >> (8 * (i & 1)));
+        }
     }
 }
 
 // One row by `threads` threads (a warp, or the CTA when WARP is false), this thread `tid`.
-template <typename T, typename O, bool VEC, bool WARP, int NV>
+template <typename T, typename O, Layout L, bool WARP, int NV>
 __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int tid, int threads, float (*red)[2]) {
     constexpr bool kQuant = sizeof(O) == 1;
     uint32_t i = o;
@@ -109,18 +161,20 @@ __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int ti
     const T* r = p.residual ? static_cast<const T*>(p.residual) + (uint64_t)i * p.residual_stride : nullptr;
     const int H = (int)p.H;
     const auto load_weight = [&](int e, float (&g)[kVec]) {
-        if (sizeof(T) < 4 && !p.weight_f32) load8<T, VEC>(static_cast<const T*>(p.weight), e, threads, H, g);
-        else load8<float, VEC>(static_cast<const float*>(p.weight), e, threads, H, g);
+        if (sizeof(T) < 4 && !p.weight_f32) load8<T, L>(static_cast<const T*>(p.weight), e, threads, H, g);
+        else load8<float, L>(static_cast<const float*>(p.weight), e, threads, H, g);
     };
-    // the thread's k-th group of eight: where it begins, and whether element j is in the row
-    const auto begin = [&](int k) { return VEC ? (tid + k * threads) * kVec : tid + k * kVec * threads; };
-    const auto in_row = [&](int e, int j) { return VEC || e + j * threads < H; };
+    O* out = static_cast<O*>(p.out) + (uint64_t)o * p.out_stride;
+    // Where the thread's k-th eight begin. Shifted groups follow the output's boundaries (which in
+    // one layout are those of x and residual too).
+    const int shift = L == kShifted && p.shift ? (int)(reinterpret_cast<uintptr_t>(out) / sizeof(O) % kVec) : 0;
+    const auto begin = [&](int k) { return L == kStrided ? tid + k * kVec * threads : (tid + k * threads) * kVec - shift; };
     float h[NV][kVec];
     float sum = 0.f, top = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = begin(k);
-        if (e < H) load8<T, VEC>(x, e, threads, H, h[k]);
+        if (e < H) load8<T, L>(x, e, threads, H, h[k]);
     }
     if (r) {
 #pragma unroll
@@ -128,7 +182,7 @@ __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int ti
             const int e = begin(k);
             float v[kVec];
             if (e < H) {
-                load8<T, VEC>(r, e, threads, H, v);
+                load8<T, L>(r, e, threads, H, v);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) h[k][j] += v[j];
             }
@@ -146,13 +200,13 @@ __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int ti
         if (e < H) {
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                if (in_row(e, j)) sum = fmaf(h[k][j], h[k][j], sum);
+                sum = fmaf(h[k][j], h[k][j], sum);
             if constexpr (kQuant) {
                 float g[kVec];
                 load_weight(e, g);
 #pragma unroll
                 for (int j = 0; j < kVec; ++j)
-                    if (in_row(e, j)) top = max_nan(top, fabsf(h[k][j] * g[j]));
+                    top = max_nan(top, fabsf(h[k][j] * g[j]));
             }
         }
     }
@@ -183,54 +237,57 @@ __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int ti
         per_scale = 1.f / scale;
         if (tid == 0) p.out_scale[o] = scale;
     }
-    O* out = static_cast<O*>(p.out) + (uint64_t)o * p.out_stride;
     T* kept = p.residual_out ? static_cast<T*>(p.residual_out) + (uint64_t)o * p.residual_out_stride : nullptr;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = begin(k);
         if (e >= H) continue;
-        if (kept) store8<T, VEC>(kept, e, threads, H, h[k]);
+        if (kept) store8<T, L>(kept, e, threads, H, h[k]);
         float g[kVec], y[kVec];
         load_weight(e, g);
 #pragma unroll
         for (int j = 0; j < kVec; ++j) y[j] = h[k][j] * inv * g[j] * per_scale;
         if constexpr (kQuant)
-            store8_e4m3<VEC>(reinterpret_cast<uint8_t*>(out), e, threads, H, y);
+            store8_e4m3<L>(reinterpret_cast<uint8_t*>(out), e, threads, H, y);
         else
-            store8<O, VEC>(out, e, threads, H, y);
+            store8<O, L>(out, e, threads, H, y);
     }
 }
 
-template <typename T, typename O, bool VEC, bool WARP, int NV>
+template <typename T, typename O, Layout L, bool WARP, int NV>
 __global__ void __launch_bounds__(WARP ? kWarpRows * 32 : (NV == 4 ? 1024 : 512)) k_norm(NormParams p) {
     __shared__ float red[32][2];
     pdl_trigger();
     pdl_wait();
     if constexpr (WARP) {
         const uint32_t o = blockIdx.x * kWarpRows + (threadIdx.x >> 5);
-        if (o < p.n) norm_row<T, O, VEC, true, NV>(p, o, threadIdx.x & 31, 32, nullptr);
+        if (o < p.n) norm_row<T, O, L, true, NV>(p, o, threadIdx.x & 31, 32, nullptr);
     } else {
-        norm_row<T, O, VEC, false, NV>(p, blockIdx.x, threadIdx.x, blockDim.x, red);
+        norm_row<T, O, L, false, NV>(p, blockIdx.x, threadIdx.x, blockDim.x, red);
     }
 }
 
 template <typename T, typename O, bool VEC>
-lp_status launch_norm(const NormParams& p, lp_stream_t s) {
-    const uint32_t vecs = (p.H + kVec - 1) / kVec;
+lp_status launch_norm(NormParams p, lp_stream_t s) {
+    uint32_t vecs = (p.H + kVec - 1) / kVec;
     if (vecs <= kWarpRowVecs) {
+        constexpr Layout L = VEC ? kAligned : kStrided;
         const dim3 grid((p.n + kWarpRows - 1) / kWarpRows);
-        if (vecs <= 32) return launch(k_norm<T, O, VEC, true, 1>, grid, kWarpRows * 32, 0, s, 1, p);
-        return launch(k_norm<T, O, VEC, true, 4>, grid, kWarpRows * 32, 0, s, 1, p);
+        if (vecs <= 32) return launch(k_norm<T, O, L, true, 1>, grid, kWarpRows * 32, 0, s, 1, p);
+        return launch(k_norm<T, O, L, true, 4>, grid, kWarpRows * 32, 0, s, 1, p);
     }
+    constexpr Layout L = VEC ? kAligned : kShifted;
+    p.shift = !VEC && vecs < LP_MAX_HIDDEN / kVec;  // (one group more, for which the longest rows have no room)
+    if (p.shift) ++vecs;
     const auto warps_for = [&](uint32_t nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; };
     // Few rows: as many threads a row as it has vectors (the row's latency counts). Many: fewer
     // threads with more vectors each, so that several rows share an SM and their loads, sums and
     // stores overlap (16384 rows of 8192 bf16 -> e4m3 and residual: 153 us with 512 threads a row,
     // 141 with 256; of 4096: 94 with 512, 75 with 128).
     const bool few = p.n <= 2u * (uint32_t)sm_count();
-    if (vecs <= (few ? 512u : 128u)) return launch(k_norm<T, O, VEC, false, 1>, dim3(p.n), warps_for(1), 0, s, 1, p);
-    if (vecs <= (few ? 1024u : 256u)) return launch(k_norm<T, O, VEC, false, 2>, dim3(p.n), warps_for(2), 0, s, 1, p);
-    return launch(k_norm<T, O, VEC, false, 4>, dim3(p.n), warps_for(4), 0, s, 1, p);
+    if (vecs <= (few ? 512u : 128u)) return launch(k_norm<T, O, L, false, 1>, dim3(p.n), warps_for(1), 0, s, 1, p);
+    if (vecs <= (few ? 1024u : 256u)) return launch(k_norm<T, O, L, false, 2>, dim3(p.n), warps_for(2), 0, s, 1, p);
+    return launch(k_norm<T, O, L, false, 4>, dim3(p.n), warps_for(4), 0, s, 1, p);
 }
 
 template <typename T>
