@@ -37,7 +37,8 @@ typedef enum lp_dtype {
 
 /*
  * Bytes of scratch the calls below need: a 256-byte header with the status word, and for
- * lp_head_project with adapters, one f32 vector of `rank` values a row and the rows' order.
+ * lp_head_project with adapters, u of every row in f32 and as 16-bit parts, and a list of its
+ * adapters for every 32 rows.
  * lp_head_norm only uses the header (T = rank = 0); lp_head_process has a size of its own.
  */
 size_t lp_head_workspace_size(uint32_t T, uint32_t rank);

@@ -42,10 +42,7 @@ constexpr uint32_t kCopyWarp = kEpilogueWarps, kMmaWarp = kEpilogueWarps + 1, kB
 constexpr uint32_t kThreads = (kEpilogueWarps + 3) * 32;
 constexpr uint32_t kSmemBudget = 227 * 1024;
 constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the alignment of the ring
-#ifndef LP_PROMOTE_SLICES
-#define LP_PROMOTE_SLICES 8
-#endif
-constexpr uint32_t kPromoteSlices = LP_PROMOTE_SLICES;            // slices summed in the tensor core before an f32 addition
+constexpr uint32_t kPromoteSlices = 8;            // slices summed in the tensor core before an f32 addition
 
 struct ProjectParams {
     const float* x_scale;
@@ -922,6 +919,14 @@ bool encode(CUtensorMap* map, const void* ptr, uint32_t dtype, uint64_t rows, ui
 // Clocks of one SM that a cut takes, counted roughly: a stage of the ring costs its products
 // (N / 256 x 512 clocks), its bytes at 55 a clock from L2, W's at 23.5 from HBM, or 120; a tile
 // an epilogue of 8 per row and 1000, of which the last tile's is not hidden.
+// Times of single CTAs and of pairs with tiles of so many rows of x, us (bf16, H = 4096; * is
+// the choice):
+//     48 rows on V = 152064    48: 212* | 212    32: 296
+//     64 rows on V = 128256    64: 181* | 183    32: 261 | 265
+//    128                      128: 177* | 179    64: 263 | 267
+//    256                      256: 199 | 183*   128: 267 | 271
+//   2048 rows on V = 32000    256: 312 | 294*   128: - | 523
+//    256 rows on V = 4096     256: 29.3 | 29.3   64: 27.3 | 29.3   32: 45.7 (chosen: 29.3)
 struct Cut {
     uint32_t cg, tile_t;
 };
