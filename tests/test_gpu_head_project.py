@@ -273,3 +273,40 @@ def test_many_tiles_of_mixed_requests():
     c = Case(off[-1], 128, 700, BF16, A=6, rank=32, off=off, seed=17)
     c.check(c.run())
     c.check(c.run(BF16))
+
+
+# Sizes for which pairs of CTAs are taken, whose tensor cores also multiply the adapters of
+# blocks of 32 rows with one adapter or two.
+SEGMENTS = {
+    # blocks of one adapter, of two, of one and none; tiles of 160 rows
+    "ragged": ([0, 3, 130, 200, 232, 296, 300], [0, 2, -1, 1, 1, 0], 64),
+    "one tile": ([0, 40, 96, 160, 168, 256], [0, 1, 2, 0, 1], 16),
+    # two or three adapters in every block: more second ones than there are free columns
+    "short": (list(range(0, 241, 20)) + [256], [b % 3 for b in range(13)], 24),
+    "a row aside": ([0, 63, 64, 65, 200], [1, 0, -1, 1], 8),
+}
+
+
+@pytest.mark.parametrize("dtype,lora_dtype", [(BF16, BF16), (F16, F16), (E4M3, BF16), (E4M3, F16)])
+@pytest.mark.parametrize("name", sorted(SEGMENTS))
+def test_segments_on_pairs(name, dtype, lora_dtype):
+    off, ids, rank = SEGMENTS[name]
+    c = Case(off[-1], 512, 20001, dtype, A=3, rank=rank, ids=ids, off=off, seed=18, lora_dtype=lora_dtype)
+    for out_dtype in (F32, BF16, F16):
+        c.check(c.run(out_dtype))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, E4M3])
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+def test_infinities_of_one_adapter_on_pairs(dtype, out_dtype):
+    off, ids, rank = SEGMENTS["one tile"]
+    c = Case(256, 512, 20001, dtype, A=3, rank=rank, ids=ids, off=off, seed=19, lora_dtype=BF16 if dtype == E4M3 else None)
+    lb = c.lb.clone()
+    lb[1, 7, 3] = float("inf")
+    lb[1, 19999, 0] = float("nan")
+    out = c.run(out_dtype, lora_b=lb.cuda()).cpu()
+    mine = torch.tensor([ids[b] == 1 for b in range(len(ids)) for _ in range(off[b], off[b + 1])])
+    assert torch.isfinite(out[~mine]).all()
+    assert not torch.isfinite(out[mine][:, [7, 19999]]).any()
+    cols = [v for v in range(20001) if v not in (7, 19999)]
+    assert torch.isfinite(out[mine][:, cols]).all()
