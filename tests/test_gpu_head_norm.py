@@ -206,3 +206,50 @@ def test_refusals_of_the_binding():
         lp.rms_norm(xc, wc, EPS, rows=torch.zeros(2, dtype=torch.int32, device="cuda"))
     with pytest.raises(lp.LpError):
         lp.rms_norm(xc.int(), wc.int().float(), EPS)
+
+
+@pytest.mark.parametrize("H", [1025, 1026, 1031, 2049, 4095, 32761, 32767, 32768])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_unaligned_rows(H, dtype):
+    # rows that begin at every boundary, and each tensor at another one
+    T = 9
+    x, r, w = inputs(T, H, dtype, seed=3)
+    buf = torch.full((4, T, H + 16), 9.0, dtype=dtype, device="cuda")
+    xv, rv, ov, kv = (buf[i].flatten()[i:i + T * (H + 5)].view(T, H + 5)[:, :H] for i in range(4))
+    xv.copy_(x)
+    rv.copy_(r)
+    lp.rms_norm(xv, w.cuda(), EPS, residual=rv, out=ov, residual_out=kv)
+    h, y = ref.norm(x, w, EPS, r)[:2]
+    check(ov, y, dtype)
+    check(kv, h, dtype)
+    for t in range(T - 1):  # the elements between the rows
+        assert (buf[2].flatten()[2 + t * (H + 5) + H:2 + (t + 1) * (H + 5)] == 9).all()
+        assert (buf[3].flatten()[3 + t * (H + 5) + H:3 + (t + 1) * (H + 5)] == 9).all()
+    q = torch.zeros(T * (H + 3) + 1, dtype=torch.uint8, device="cuda")
+    qv = q[1:].view(T, H + 3)[:, :H].view(torch.float8_e4m3fn)
+    qv, scale = lp.rms_norm(xv, w.cuda(), EPS, residual=rv, out=qv, out_scale=torch.empty(T, device="cuda"))
+    check_e4m3(qv, scale, y)
+    assert (q[1:].view(T, H + 3)[:, H:] == 0).all() and q[0] == 0
+
+
+def test_unaligned_rows_in_place():
+    x, r, w = inputs(40, 5003, torch.bfloat16, seed=4)
+    xc, rc, wc = cuda(x, r, w)
+    lp.rms_norm(xc, wc, EPS, residual=rc, out=xc, residual_out=rc)
+    h, y = ref.norm(x, w, EPS, r)[:2]
+    check(xc, y, torch.bfloat16)
+    check(rc, h, torch.bfloat16)
+
+
+@pytest.mark.parametrize("H", [64, 1608, 1609])
+def test_rows_far_apart(H):
+    # the third row begins past 2^32 elements
+    T, step = 3, 2 ** 31 + 24
+    x, r, w = inputs(T, H, torch.bfloat16, seed=5)
+    far = torch.empty(2 * step + H, dtype=torch.bfloat16, device="cuda")
+    xv = far.as_strided((T, H), (step, 1))
+    xv.copy_(x)
+    lp.rms_norm(xv, w.cuda(), EPS, residual=r.cuda(), out=xv)
+    check(xv, ref.norm(x, w, EPS, r)[1], torch.bfloat16)
+    del far, xv
+    torch.cuda.empty_cache()

@@ -323,3 +323,37 @@ def test_workspace_for_long_histories_is_checked():
     c["history"], c["prompt"] = [[1, 2, 3] * 3000] * 2, [0, 0]
     with pytest.raises(lp.LpError):
         call(c, workspace=lp.new_head_workspace())
+
+
+def test_long_histories_in_place():
+    c = make(20, 40001, 20, hist=12000, n_bias=50, seed=21)
+    x = c["x"].cuda()
+    _, status = call(c, x=x, out=x)
+    assert status == 0
+    check(x, want_of(c))
+
+
+def test_long_history_of_few_tokens_sorted():
+    # more than 15 bits of the output part, in slices of a table of 32 bits
+    c = make(2, 60000, 2, seed=22)
+    c["history"] = [[7] * 70000 + [8, 59999] * 1000, [1999] * 9000]
+    c["prompt"] = [100, 9000]
+    c["rep"], c["freq"], c["pres"] = [1.5, 2.0], [0.25, -0.5], [1.0, 0.0]
+    out, status = call(c)
+    assert status == 0
+    check(out, want_of(c))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_far_apart(dtype):
+    # the third row begins past 2^32 elements
+    T, V, step = 3, 3001, 2 ** 31 + 20
+    c = make(T, V, 2, dtype, hist=100, seed=23)
+    far = torch.empty(2 * step + V, dtype=dtype, device="cuda")
+    xv = far.as_strided((T, V), (step, 1))
+    xv.copy_(c["x"])
+    out, status = call(c, x=xv, out=xv if dtype == torch.float32 else None)
+    assert status == 0
+    check(out, want_of(c))
+    del far, xv, out
+    torch.cuda.empty_cache()

@@ -310,3 +310,16 @@ def test_infinities_of_one_adapter_on_pairs(dtype, out_dtype):
     assert not torch.isfinite(out[mine][:, [7, 19999]]).any()
     cols = [v for v in range(20001) if v not in (7, 19999)]
     assert torch.isfinite(out[mine][:, cols]).all()
+
+
+def test_rows_far_apart():
+    # x's and out's third row begin past 2^32 elements
+    T, step = 3, 2 ** 31 + 64
+    c = Case(T, 128, 300, BF16, A=2, rank=8, ids=[0, 1, -1], seed=20)
+    far, fo = (torch.empty(2 * step + 300, dtype=BF16, device="cuda") for _ in range(2))
+    xv, ov = far.as_strided((T, 128), (step, 1)), fo.as_strided((T, 300), (step, 1))
+    xv.copy_(c.x)
+    c.run(out=ov, x=xv)
+    c.check(ov)
+    del far, fo, xv, ov
+    torch.cuda.empty_cache()
