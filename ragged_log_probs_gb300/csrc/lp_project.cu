@@ -19,7 +19,7 @@
 // Bound by HBM (W) up to about 128 rows, by the tensor cores above. Measured, us (W at HBM's
 // measured rate, or the products at a large library product's): one row, V = 128256, H = 4096
 // bf16 162 (155); 256 rows 183 (144); 2048 rows, V = 32000 bf16 286 and f32 327 (287); e4m3 48
-// rows of V = 152064 with 12 adapters of rank 32 134 (114).
+// rows of V = 152064 with 12 adapters of rank 32 127-130 (114).
 #include <cuda.h>
 
 #include "lp_adapters.h"
@@ -284,7 +284,8 @@ struct RunList {
 // adds up to 4.4e-6 of the result, against 6e-7 of rounded f32 sums. So the accumulator is
 // emptied into registers every kPromoteSlices slices (8, 512 products; the first time after
 // half as many again), and those are summed with rounding: 4.8e-7 (4 slices 2.4e-7, 16 1.0e-6).
-// It costs 2048 rows on V = 32000 327 us instead of 286. Rounded outputs (16 bits) and e4m3 products (few bits) do not need it.
+// It costs 2048 rows on V = 32000 327 us instead of 286. Rounded outputs (16 bits) and e4m3
+// products (few bits) do not need it.
 template <bool FP8, typename OUT, int CG, bool PROMOTE, bool LORA>
 __global__ void __launch_bounds__(kThreads, 1)
 k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
