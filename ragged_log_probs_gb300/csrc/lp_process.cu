@@ -15,8 +15,9 @@
 // would take 41 us for 256 rows of 128256 f32, and without lists this takes that. What costs is
 // the time before the copy (who the row belongs to, its parameters, its history: reads that wait
 // for each other, about 6 of a CTA's 17 us), and the copy's look at the table (8 against 4 us).
-// So the slice is asked for in L2 at the very start (57 -> 41 us), the histories are sorted while
-// the first CTAs begin, and four CTAs share an SM. With histories of up to 30000: 66 us.
+// So the slice is asked for in L2 at the very start (57 -> 41 us) and the mask read while one warp
+// finds the row's request (66 -> 62 us with histories of up to 30000), the histories are sorted
+// while the first CTAs begin, and four or five CTAs share an SM.
 // Slices held in shared memory as values, loaded and stored by bulk copies, were measured too:
 // 36000 tokens per SM at a time instead of 98000 hide less of those waits (85 us).
 #include "lp_head_common.h"
@@ -88,39 +89,39 @@ __device__ __forceinline__ float penalised(float x, uint32_t count, const Penalt
 struct Row {
     int32_t request;         // -1: the row's values are NaN
     uint32_t counted;        // the history has an effect
-    int64_t mask;            // first word of the row's mask, -1: none
     uint32_t h0, h1, prompt; // its history, and how much of that is the prompt
     uint32_t b0, b1;         // its biases
     Penalty q;
 };
 
-// The request of row t, found by one warp: 32 offsets at a time, the row's own number first
-// (a request a row). off[0] <= t < off[B] or -1; ends for any contents of off.
+// The request of row t, found by one warp: 32 offsets at a time, and with the first 32 of them
+// the row's own number (a request a row). off[0] <= t < off[B] or -1; ends for any contents of off.
 __device__ __forceinline__ int32_t request_by_warp(const uint32_t* off, uint32_t B, uint32_t t) {
     if (!off) return (int32_t)t;
     const uint32_t lane = threadIdx.x & 31, guess = min(t, B - 1);
+    uint32_t lo = 0, n = B, step = (n + 31) / 32;  // off[lo] <= t < off[lo + n]
     const uint32_t probe = off[lane == 0 ? guess : lane == 1 ? guess + 1 : lane == 2 ? 0 : B];
+    uint32_t first = off[min(lane * step, B)];
     const uint32_t at = __shfl_sync(0xFFFFFFFFu, probe, 0), after = __shfl_sync(0xFFFFFFFFu, probe, 1);
     if (at <= t && t < after) return (int32_t)guess;
     if (__shfl_sync(0xFFFFFFFFu, probe, 2) > t || __shfl_sync(0xFFFFFFFFu, probe, 3) <= t) return -1;
-    uint32_t lo = 0, n = B;  // off[lo] <= t < off[lo + n]
     while (n > 1) {
-        const uint32_t step = (n + 31) / 32, i = lane * step;
-        const uint32_t below = __ballot_sync(0xFFFFFFFFu, i < n && off[lo + (i < n ? i : 0)] <= t);
+        const uint32_t below = __ballot_sync(0xFFFFFFFFu, lane * step < n && first <= t);
         const uint32_t k = 31 - __clz(below | 1u);  // the last probe that is not past t
         lo += k * step;
         n = min(step, n - k * step);
+        step = (n + 31) / 32;
+        if (n > 1) first = off[lo + (lane * step < n ? lane * step : 0)];
     }
     return (int32_t)lo;
 }
 
 // One warp describes row t; loads that do not need each other's values are started together.
-__device__ __forceinline__ void describe(const ProcessParams& p, uint32_t t, Row* row, bool report) {
+__device__ __forceinline__ void describe(const ProcessParams& p, uint32_t t, Row* row, bool mask_fits, bool report) {
     const uint32_t lane = threadIdx.x & 31;
-    const int64_t m = !p.mask ? -1 : p.mask_index ? (int64_t)p.mask_index[t] : (int64_t)t;
     const int32_t b = request_by_warp(p.row_offsets, p.B, t);
     if (lane != 0) return;
-    Row r = {b, 0u, -1, 0u, 0u, 0u, 0u, 0u, {1.f, 1.f, 0.f, 0.f}};
+    Row r = {b, 0u, 0u, 0u, 0u, 0u, 0u, {1.f, 1.f, 0.f, 0.f}};
     uint32_t code = LP_ERR_OFFSETS;
     if (b >= 0) {
         if (p.repetition) r.q.rep = p.repetition[b];
@@ -143,8 +144,7 @@ __device__ __forceinline__ void describe(const ProcessParams& p, uint32_t t, Row
             r.request = -1;
             code = LP_ERR_PENALTY;
         }
-        if (m >= (int64_t)p.mask_rows) r.request = -1;
-        else if (m >= 0) r.mask = m * (int64_t)p.mask_stride;
+        if (!mask_fits) r.request = -1;
         if (r.prompt > r.h1 - r.h0) r.prompt = r.h1 - r.h0;
     }
     if (r.request < 0 && report) flag(p.status, code);
@@ -189,13 +189,13 @@ struct Table {
     }
 };
 
-// Ask for a row's slice in L2.
+// Ask for a row's slice in L2, thread `k` of `threads`.
 template <typename T>
-__device__ __forceinline__ void prefetch_slice(const T* row, uint32_t lo, uint32_t hi, uint32_t threads) {
+__device__ __forceinline__ void prefetch_slice(const T* row, uint32_t lo, uint32_t hi, uint32_t k, uint32_t threads) {
     constexpr uint32_t kPiece = 4096;
     const uintptr_t from = (reinterpret_cast<uintptr_t>(row + lo) + 15) & ~(uintptr_t)15;
     const uintptr_t to = reinterpret_cast<uintptr_t>(row + hi) & ~(uintptr_t)15;
-    for (uintptr_t at = from + threadIdx.x * kPiece; at < to; at += threads * kPiece) {
+    for (uintptr_t at = from + k * kPiece; at < to; at += threads * kPiece) {
         const uint32_t bytes = to - at < kPiece ? (uint32_t)(to - at) : kPiece;
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
     }
@@ -293,8 +293,10 @@ __host__ __device__ constexpr uint32_t threads(bool sorted) { return sorted ? 38
 // grid: T x slices CTAs, all rows' first slices first: a vocabulary's frequent tokens mostly have
 // its low numbers, and the CTAs with the most to count should not be the last to start (256 rows
 // with histories of 30000: 80 us row by row, 69 so).
+// Without sorted histories at most 48 registers, so that five CTAs share an SM where the slices are
+// short enough (240 x 152064 bf16: 52.8 us with 55 registers, 45.3 so).
 template <typename T, bool VEC, bool SORTED>
-__global__ void __launch_bounds__(threads(SORTED), kResident) k_process(ProcessParams p) {
+__global__ void __launch_bounds__(threads(SORTED), SORTED ? kResident : kResident + 1) k_process(ProcessParams p) {
     constexpr uint32_t kThreads = threads(SORTED);
     extern __shared__ __align__(16) uint32_t table[];  // slice / 2 words
     __shared__ Row s_row;
@@ -311,22 +313,26 @@ __global__ void __launch_bounds__(threads(SORTED), kResident) k_process(ProcessP
         for (uint32_t i = tid; i < (p.slice + 7) / 8; i += kThreads) reinterpret_cast<uint4*>(table)[i] = make_uint4(0, 0, 0, 0);
     if (tid == 0) s_in_slice = 0;
     if constexpr (!SORTED) pdl_wait();  // (the sort has waited for what logits and the lists come from)
-    if (!p.mask) prefetch_slice(in, lo, hi, kThreads);
-    if (tid < 32) describe(p, t, &s_row, part == 0);
+    // One warp finds out whose the row is; the others, at the same time, whether it is masked, and
+    // read its mask or ask for the slice.
+    const int64_t m = !p.mask ? -1 : p.mask_index ? (int64_t)p.mask_index[t] : (int64_t)t;
+    const bool mask_fits = m < (int64_t)p.mask_rows, masked = m >= 0 && mask_fits;
+    const uint32_t word0 = lo >> 5, words = ((hi - 1) >> 5) - word0 + 1;
+    if (tid < 32) {
+        describe(p, t, &s_row, mask_fits, part == 0);
+    } else if (masked) {
+        const uint32_t* mask = p.mask + m * (int64_t)p.mask_stride + word0;
+        for (uint32_t i = tid - 32; i <= words; i += kThreads - 32)  // (the last is read beside the one before)
+            s_mask[i] = i < words ? mask[i] : 0u;
+    } else {
+        prefetch_slice(in, lo, hi, tid - 32, kThreads - 32);
+    }
     __syncthreads();
     const Row row = s_row;
     if constexpr (SORTED) pdl_wait();
     if (row.request < 0) {
         for (uint32_t v = lo + tid; v < hi; v += kThreads) out[v] = __int_as_float(0x7fffffff);
         return;
-    }
-    const bool masked = row.mask >= 0;
-    const uint32_t word0 = lo >> 5, words = ((hi - 1) >> 5) - word0 + 1;
-    if (masked) {
-        for (uint32_t i = tid; i <= words; i += kThreads)  // (the last is read beside the one before)
-            s_mask[i] = i < words ? p.mask[row.mask + word0 + i] : 0u;
-    } else if (p.mask) {
-        prefetch_slice(in, lo, hi, kThreads);
     }
     const auto allowed = [&](uint32_t v) { return !masked || ((s_mask[(v >> 5) - word0] >> (v & 31)) & 1u); };
     // 15 bits hold any count of an output part of up to 32767 tokens
@@ -377,7 +383,6 @@ __global__ void __launch_bounds__(threads(SORTED), kResident) k_process(ProcessP
     const bool biased = row.b1 - row.b0 > tid;
     const uint32_t bias_at = biased ? p.bias_tokens[row.b0 + tid] : 0u;
     const float bias = biased ? p.bias_values[row.b0 + tid] : 0.f;
-    if (masked) __syncthreads();
 
     // the copy
     const uint32_t first = VEC ? min(lo + ((-(uint32_t)(reinterpret_cast<uintptr_t>(out + lo) >> 2)) & 3u), hi) : hi;
