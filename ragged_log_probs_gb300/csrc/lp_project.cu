@@ -42,7 +42,10 @@ constexpr uint32_t kCopyWarp = kEpilogueWarps, kMmaWarp = kEpilogueWarps + 1, kB
 constexpr uint32_t kThreads = (kEpilogueWarps + 3) * 32;
 constexpr uint32_t kSmemBudget = 227 * 1024;
 constexpr uint32_t kControlBytes = 1024 + 512;    // barriers and words, and the alignment of the ring
-constexpr uint32_t kPromoteSlices = 8;            // slices summed in the tensor core before an f32 addition
+// Slices summed in the tensor core before an f32 addition: f32 logits of 16-bit inputs. Half as
+// many for tiles of few rows, which wait for HBM (64 rows on V = 128256, H = 4096: 180.9 us both
+// ways, and half the error; with 256 rows 207.5 against 199.3).
+constexpr uint32_t kPromoteSlices = 8, kPromoteFewRows = 64;
 
 struct ProjectParams {
     const float* x_scale;
@@ -282,8 +285,9 @@ struct RunList {
 // PROMOTE: f32 logits of 16-bit inputs. The tensor core's f32 accumulator drops the bits
 // below its last place at every step, always towards zero: over a contraction of 4096 that
 // adds up to 4.4e-6 of the result, against 6e-7 of rounded f32 sums. So the accumulator is
-// emptied into registers every kPromoteSlices slices (8, 512 products; the first time after
-// half as many again), and those are summed with rounding: 4.8e-7 (4 slices 2.4e-7, 16 1.0e-6).
+// emptied into registers every 8 slices (512 products; 4 for tiles of few rows; the first time
+// after half as many again), and those are summed with rounding: 4.8e-7 (4 slices 2.5e-7, 2
+// 1.6e-7, 16 1.0e-6).
 // It costs 2048 rows on V = 32000 327 us instead of 286. Rounded outputs (16 bits) and e4m3
 // products (few bits) do not need it.
 template <bool FP8, typename OUT, int CG, bool PROMOTE, bool LORA>
@@ -1065,7 +1069,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.tensor = cg == 2 && p.lora_tma && rank != 0;
     p.apart = fp8 || dtype == LP_F16;
     p.part_stride = (uint32_t)space.rows;
-    p.chunk = !fp8 && out_dtype == LP_F32 ? kPromoteSlices : p.slices;
+    p.chunk = fp8 || out_dtype != LP_F32 ? p.slices : p.tile_t <= kPromoteFewRows ? kPromoteSlices / 2 : kPromoteSlices;
     for (p.acc_cols = 32; p.acc_cols < p.tile_t; p.acc_cols *= 2) {}
     for (p.acc_shift = 1; p.acc_shift < 3 && p.acc_cols << (p.acc_shift + 1) <= 512; ++p.acc_shift) {}
     // instruction: f32 accumulator, K-major operands, M = 128 lanes a CTA, N = tile_t
