@@ -35,6 +35,7 @@ constexpr uint32_t kBatch = 4;         // vectors a thread has in flight
 constexpr uint32_t kChunk = 4096;      // tokens of a history sorted together
 constexpr uint32_t kSortFrom = 4096;   // mean length from which histories are sorted first
 constexpr uint32_t kMaxSlices = 256;
+constexpr uint32_t kOrderedWord = 32;  // of the workspace's header: see k_sort_history
 
 struct ProcessParams {
     const void* logits;
@@ -52,6 +53,7 @@ struct ProcessParams {
     const int32_t* mask_index;
     uint32_t* sorted;  // [history_total], NULL: histories are not sorted
     uint32_t* bounds;  // [chunks][slices + 1]
+    uint32_t* ordered; // one word: history_offsets nowhere decrease, so that the sort is sound
     float* out;
     uint32_t* status;
     uint64_t stride, out_stride, mask_stride;
@@ -206,20 +208,31 @@ constexpr uint32_t kSortEach = kChunk / kSortThreads;
 constexpr uint32_t kNowhere = 0xFFFF0000u;
 
 // Histories are sorted in chunks of kChunk tokens. Request b's chunk c has number
-// b + h0 / kChunk + c: no two have the same, and there are at most B + total / kChunk + 1.
+// b + h0 / kChunk + c: no two have the same, and there are at most B + total / kChunk + 1, as long
+// as the offsets nowhere decrease. Where they do, two requests may claim one number, or a part of
+// `sorted` each, and a chunk may have no CTA that finds it (its bounds would be an earlier call's).
+// So one CTA looks at all offsets and writes the verdict into a word of the workspace, and where
+// they are bad every row reads its history as it is, as without the sort.
 __device__ __forceinline__ uint32_t first_chunk(const ProcessParams& p, uint32_t b) {
     return b + p.history_offsets[b] / kChunk;
 }
 
 // Sort a chunk by slices: sorted[h0 + c kChunk ...] gets its tokens (bit 31: of the prompt),
 // bounds[chunk][k] where slice k's begin. A warp takes the places of its tokens of one slice
-// together; their order within a slice is left open. grid: a CTA a chunk
+// together; their order within a slice is left open. grid: a CTA a chunk, and one for the verdict
 __global__ void __launch_bounds__(kSortThreads, 3) k_sort_history(ProcessParams p) {
     __shared__ uint32_t place[kMaxSlices + 1];
     __shared__ uint32_t s_request;
     pdl_wait();
     pdl_trigger();  // after the wait: the copy may read logits, which are complete now
     const uint32_t tid = threadIdx.x, lane = tid & 31, chunk = blockIdx.x;
+    if (chunk == gridDim.x - 1) {
+        bool falls = false;
+        for (uint32_t b = tid; b < p.B; b += kSortThreads) falls |= p.history_offsets[b] > p.history_offsets[b + 1];
+        falls = __syncthreads_or(falls);
+        if (tid == 0) *p.ordered = !falls;
+        return;
+    }
     for (uint32_t k = tid; k <= p.slices; k += kSortThreads) place[k] = 0;
     if (tid < 32) {  // the last request whose first chunk is not past this one, 32 at a time
         uint32_t lo = 0, n = p.B;
@@ -330,6 +343,7 @@ __global__ void __launch_bounds__(threads(SORTED), SORTED ? kResident : kResiden
     __syncthreads();
     const Row row = s_row;
     if constexpr (SORTED) pdl_wait();
+    const bool ordered = !SORTED || __ldcg(p.ordered) != 0;
     if (row.request < 0) {
         for (uint32_t v = lo + tid; v < hi; v += kThreads) out[v] = __int_as_float(0x7fffffff);
         return;
@@ -341,6 +355,10 @@ __global__ void __launch_bounds__(threads(SORTED), SORTED ? kResident : kResiden
     const uint32_t pieces = !row.counted ? 0 : SORTED ? (row.h1 - row.h0 + kChunk - 1) / kChunk : 1;
     const auto piece = [&](uint32_t c) -> Tokens {
         if (!SORTED) return {p.history + row.h0, row.h1 - row.h0, row.prompt, false};
+        if (!ordered) {  // (in the same pieces)
+            const uint32_t from = c * kChunk;
+            return {p.history + row.h0 + from, min(kChunk, row.h1 - row.h0 - from), row.prompt - min(row.prompt, from), false};
+        }
         const uint32_t* bounds = p.bounds + (uint64_t)(row.request + row.h0 / kChunk + c) * (p.slices + 1) + part;
         const uint32_t limit = min(kChunk, row.h1 - row.h0 - c * kChunk);
         const uint32_t from = min(bounds[0], limit), to = min(bounds[1], limit);
@@ -588,7 +606,8 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
         p.bounds = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
         const uint32_t chunks = B + history_total / kChunk + 1;
         p.sorted = p.bounds + (size_t)chunks * (p.slices + 1);
-        const lp_status st = launch(k_sort_history, dim3(chunks), kSortThreads, 0, stream, 1, p);
+        p.ordered = p.status + kOrderedWord;
+        const lp_status st = launch(k_sort_history, dim3(chunks + 1), kSortThreads, 0, stream, 1, p);
         if (st != LP_OK) return st;
     }
     // 4 values at a time where logits and out have their 4-value boundaries at the same tokens
