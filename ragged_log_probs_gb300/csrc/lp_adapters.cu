@@ -169,20 +169,45 @@ __device__ void list_tile(const ShrinkParams& p, uint32_t tile) {
     if (c == 0 && total == 0) g->items = 0;
 }
 
+// The part-th of the three 16-bit values whose sum is v: rounded towards zero, so that all have v's
+// sign, and none is zero while v is not: a value that rounds to itself leaves its last place to the
+// next part. An infinite element of B then gives u B's infinity (a part of zero would give 0 x inf =
+// NaN), and so does an infinite u. bf16 parts hold v's 24 bits. f16 parts hold it to 2^-24 at least,
+// v's largest in the row being 2^13 or more: elements below 2^-38 of the row's largest are lost, and
+// below 2^-35 the parts can be zero.
+__device__ __forceinline__ uint16_t part_of(float v, uint32_t part, bool f16) {
+    const uint32_t sign = __float_as_uint(v) >> 16 & 0x8000u;
+    float m = fabsf(v);
+    if (!(m < __int_as_float(0x7f800000)))
+        return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+    if (f16 && m < 1.f) m = rintf(m * 16777216.f) * 5.9604644775390625e-8f;  // whole multiples of 2^-24
+    for (uint32_t n = 0;; ++n) {
+        uint32_t h = f16 ? __half_as_ushort(__float2half_rz(m)) : __float_as_uint(m) >> 16;
+        const auto value = [&] { return f16 ? __half2float(__ushort_as_half((uint16_t)h)) : __uint_as_float(h << 16); };
+        // what the others need: the second and third f16 part 2^-24 each
+        if (n < 2 && m - value() < (f16 && n == 0 ? 1.1920928955078125e-7f : 1.0e-45f)) {
+            const uint32_t step = f16 && n == 0 && h <= 0x0800u ? 2 : 1;  // (places of 2^-24 up to there)
+            if (h > step) h -= step;
+        }
+        if (n == part) return (uint16_t)(h | sign);
+        m -= value();
+    }
+}
+
 // One warp writes row t's u (u[0, rank) in shared memory, zero past the rank), and its parts.
 __device__ void write_row(const ShrinkParams& p, uint32_t t, const float* u) {
     const uint32_t lane = threadIdx.x & 31, cols = rank_cols(p.rank);
     float top = 0.f;
     for (uint32_t j = lane; j < cols; j += 32) {
         p.u[(uint64_t)t * cols + j] = u[j];
-        top = fmaxf(top, fabsf(u[j]));
+        if (fabsf(u[j]) < __int_as_float(0x7f800000)) top = fmaxf(top, fabsf(u[j]));
     }
     if (!p.tensor) return;
-    // f16 parts: u as a value in [2^13, 2^14) times a power of two, so that neither its size
-    // nor the third part leaves f16's range. bf16 has f32's.
+    // f16 parts: u as values times a power of two, the row's largest (that is finite) in [2^13,
+    // 2^14), so that neither their size nor the third part leaves f16's range. bf16 has f32's.
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    const int e = p.lora_f16 && top > 0.f && top < 3.0e38f ? ilogbf(top) - 13 : 0;
+    const int e = p.lora_f16 && top > 0.f ? ilogbf(top) - 13 : 0;
     if (lane == 0) p.factor[t] = ldexpf(1.f, e);
     const uint32_t width = part_cols(p.rank);
     if (lane >= part_rows(p.rank) * 8) return;
@@ -191,23 +216,7 @@ __device__ void write_row(const ShrinkParams& p, uint32_t t, const float* u) {
     uint16_t piece[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-        piece[q] = 0;
-        if (part > 2 || j0 + q >= p.rank) continue;
-        float v = ldexpf(u[j0 + q], -e);
-        for (uint32_t n = 0;; ++n) {
-            float rounded;
-            if (p.lora_f16) {
-                const __half h = __float2half_rn(v);
-                piece[q] = __half_as_ushort(h);
-                rounded = __half2float(h);
-            } else {
-                const __nv_bfloat16 h = __float2bfloat16_rn(v);
-                piece[q] = __bfloat16_as_ushort(h);
-                rounded = __bfloat162float(h);
-            }
-            if (n == part) break;
-            v -= rounded;
-        }
+        piece[q] = part > 2 || j0 + q >= p.rank ? 0 : part_of(ldexpf(u[j0 + q], -e), part, p.lora_f16);
     }
     *reinterpret_cast<uint4*>(p.parts + ((uint64_t)line * p.part_stride + t) * 64 + lane % 8 * 8) =
         make_uint4(piece[0] | (uint32_t)piece[1] << 16, piece[2] | (uint32_t)piece[3] << 16,

@@ -44,8 +44,9 @@ struct TileGroups {
 constexpr size_t kGroupBytes = 2560;  // of one tile in the workspace
 static_assert(sizeof(TileGroups) % 16 == 0 && sizeof(TileGroups) <= kGroupBytes, "read as 16-byte words");
 
-// u of a row for the tensor cores: three 16-bit parts (a value, what rounding it left, and
-// what rounding that left), each padded to b_cols columns, packed into rows of 64 columns.
+// u of a row for the tensor cores: three 16-bit parts (the value rounded towards zero, what that
+// left, rounded the same way, and the rest), each padded to b_cols columns, packed into rows of 64
+// columns.
 __host__ __device__ constexpr uint32_t rank_cols(uint32_t rank) { return (rank + 15) & ~15u; }
 __host__ __device__ constexpr uint32_t part_cols(uint32_t rank) { return rank <= 16 ? 16 : rank <= 32 ? 32 : 64; }
 __host__ __device__ constexpr uint32_t part_rows(uint32_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : 3; }
