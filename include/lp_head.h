@@ -63,7 +63,7 @@ lp_status lp_head_clear_status(void *workspace, lp_stream_t stream);
  *                   residual_out may be x or residual themselves (same type and stride).
  *   workspace       the status word; required with rows, else may be NULL
  * A row holding NaN or an infinity becomes NaN where the formula does (LP_E4M3: the row's
- * scale is NaN). Device check: rows[o] < T (LP_ERR_OFFSETS; that output row gets NaN).
+ * scale is NaN). Only h, y and out_scale have to fit f32, not h^2 or its sum. Device check: rows[o] < T (LP_ERR_OFFSETS; that output row gets NaN).
  * Host checks: H in 1..LP_MAX_HIDDEN, strides >= H, pointers aligned to their type.
  */
 lp_status lp_head_norm(const void *x, const void *residual, const void *weight, uint32_t dtype,

@@ -210,34 +210,77 @@ __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int ti
             }
         }
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if constexpr (kQuant) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-    }
-    if constexpr (!WARP) {
-        const int warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
-        if (lane == 0) {
-            red[warp][0] = sum;
-            red[warp][1] = top;
-        }
-        __syncthreads();
-        sum = lane < warps ? red[lane][0] : 0.f;
-        top = lane < warps ? red[lane][1] : 0.f;
+    const auto over_row = [&](float& sum, float& top) {  // every thread gets the same bits
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) {
             sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
             if constexpr (kQuant) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
         }
+        if constexpr (!WARP) {
+            const int warp = tid >> 5, lane = tid & 31, warps = threads >> 5;
+            if (lane == 0) {
+                red[warp][0] = sum;
+                red[warp][1] = top;
+            }
+            __syncthreads();
+            sum = lane < warps ? red[lane][0] : 0.f;
+            top = lane < warps ? red[lane][1] : 0.f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) {
+                sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                if constexpr (kQuant) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            }
+        }
+    };
+    over_row(sum, top);
+    float mean = sum / (float)p.H + p.eps, inv = rsqrtf(mean);
+    T* kept = p.residual_out ? static_cast<T*>(p.residual_out) + (uint64_t)o * p.residual_out_stride : nullptr;
+    // A row whose squares or products h w leave f32 (or hold a NaN or an infinity): once more, of
+    // h times a power of two that brings them back, with the largest |y| itself.
+    const bool large = !(mean < 0x1p120f), small = mean < 0x1p-90f;
+    if (large || small || (kQuant && sum > 0.f && !(top > 0x1p-100f && top < 0x1p120f))) {
+        if (kept) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (begin(k) < H) store8<T, L>(kept, begin(k), threads, H, h[k]);
+            kept = nullptr;
+        }
+        const float by = large ? 0x1p-80f : small ? 0x1p100f : 1.f;
+        sum = top = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (begin(k) < H)
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    h[k][j] *= by;
+                    sum = fmaf(h[k][j], h[k][j], sum);
+                }
+        if constexpr (!WARP) __syncthreads();  // (the first sums have been read)
+        over_row(sum, top);
+        inv = rsqrtf(sum / (float)p.H + p.eps * by * by);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+            if (begin(k) < H) {
+                float g[kVec];
+                load_weight(begin(k), g);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    h[k][j] *= inv;
+                    top = max_nan(top, fabsf(h[k][j] * g[j]));
+                }
+            }
+        inv = 1.f;
+        if constexpr (kQuant) {
+            if constexpr (!WARP) __syncthreads();
+            over_row(sum, top);
+        }
     }
-    const float inv = rsqrtf(sum / (float)p.H + p.eps);
     float per_scale = 1.f;  // applied after inv: their product may overflow (a row of zeros)
     if constexpr (kQuant) {
         const float scale = max_nan(inv * top / 448.f, 1.17549435e-38f);
         per_scale = 1.f / scale;
         if (tid == 0) p.out_scale[o] = scale;
     }
-    T* kept = p.residual_out ? static_cast<T*>(p.residual_out) + (uint64_t)o * p.residual_out_stride : nullptr;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int e = begin(k);
