@@ -35,7 +35,7 @@ constexpr uint32_t kBatch = 4;         // vectors a thread has in flight
 constexpr uint32_t kChunk = 4096;      // tokens of a history sorted together
 constexpr uint32_t kSortFrom = 4096;   // mean length from which histories are sorted first
 constexpr uint32_t kMaxSlices = 256;
-constexpr uint32_t kOrderedWord = 32;  // of the workspace's header: see k_sort_history
+constexpr uint32_t kOrderedWord = 32;  // of the workspace's header: 1 where history_offsets nowhere decrease
 
 struct ProcessParams {
     const void* logits;
@@ -53,7 +53,6 @@ struct ProcessParams {
     const int32_t* mask_index;
     uint32_t* sorted;  // [history_total], NULL: histories are not sorted
     uint32_t* bounds;  // [chunks][slices + 1]
-    uint32_t* ordered; // one word: history_offsets nowhere decrease, so that the sort is sound
     float* out;
     uint32_t* status;
     uint64_t stride, out_stride, mask_stride;
@@ -230,7 +229,7 @@ __global__ void __launch_bounds__(kSortThreads, 3) k_sort_history(ProcessParams 
         bool falls = false;
         for (uint32_t b = tid; b < p.B; b += kSortThreads) falls |= p.history_offsets[b] > p.history_offsets[b + 1];
         falls = __syncthreads_or(falls);
-        if (tid == 0) *p.ordered = !falls;
+        if (tid == 0) p.status[kOrderedWord] = !falls;
         return;
     }
     for (uint32_t k = tid; k <= p.slices; k += kSortThreads) place[k] = 0;
@@ -343,7 +342,7 @@ __global__ void __launch_bounds__(threads(SORTED), SORTED ? kResident : kResiden
     __syncthreads();
     const Row row = s_row;
     if constexpr (SORTED) pdl_wait();
-    const bool ordered = !SORTED || __ldcg(p.ordered) != 0;
+    const bool ordered = !SORTED || __ldcg(p.status + kOrderedWord) != 0;
     if (row.request < 0) {
         for (uint32_t v = lo + tid; v < hi; v += kThreads) out[v] = __int_as_float(0x7fffffff);
         return;
@@ -606,7 +605,6 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
         p.bounds = reinterpret_cast<uint32_t*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
         const uint32_t chunks = B + history_total / kChunk + 1;
         p.sorted = p.bounds + (size_t)chunks * (p.slices + 1);
-        p.ordered = p.status + kOrderedWord;
         const lp_status st = launch(k_sort_history, dim3(chunks + 1), kSortThreads, 0, stream, 1, p);
         if (st != LP_OK) return st;
     }
