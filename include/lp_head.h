@@ -11,7 +11,8 @@
  * leave nothing enqueued, and errors found on the device set bits of the workspace's
  * status word (bit c <=> code c; read it with lp_ragged_read_status) and never trap.
  * These entry points only ever add bits: lp_head_clear_status (or lp_ragged_plan on the
- * same workspace) clears the word. Strides are in elements. Row counts, sizes and ids are
+ * same workspace) clears the word. Workspaces are aligned to 256 bytes, every other pointer to
+ * its type at least (else LP_ERR_SHAPE). Strides are in elements. Row counts, sizes and ids are
  * uint32; row strides and totals may pass 32 bits.
  */
 #ifndef LP_HEAD_H

@@ -346,7 +346,7 @@ lp_status launch_norm(const NormParams& p, uint32_t out_dtype, uint32_t dtype, b
 extern "C" {
 
 lp_status lp_head_clear_status(void* workspace, lp_stream_t stream) {
-    if (!workspace) return LP_ERR_WORKSPACE;
+    if (!workspace || !aligned_to(workspace, 256)) return LP_ERR_WORKSPACE;
     if (cudaMemsetAsync(workspace, 0, 4, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) {
         (void)cudaGetLastError();
         return LP_ERR_CUDA;

@@ -547,7 +547,15 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
                  (!mask_index && mask_rows < T)))
         return LP_ERR_SHAPE;
     const size_t e = dtype_bytes(dtype);
-    if (!aligned_to(logits, e) || !aligned_to(out, 4)) return LP_ERR_SHAPE;
+    if (!aligned_to(logits, e)) return LP_ERR_SHAPE;
+    for (const void* ptr : {static_cast<const void*>(out), static_cast<const void*>(row_offsets),
+                            static_cast<const void*>(history), static_cast<const void*>(history_offsets),
+                            static_cast<const void*>(prompt_lens), static_cast<const void*>(repetition),
+                            static_cast<const void*>(frequency), static_cast<const void*>(presence),
+                            static_cast<const void*>(bias_tokens), static_cast<const void*>(bias_values),
+                            static_cast<const void*>(bias_offsets), static_cast<const void*>(mask),
+                            static_cast<const void*>(mask_index)})
+        if (!aligned_to(ptr, 4)) return LP_ERR_SHAPE;
     if (static_cast<const void*>(out) == logits && (dtype != LP_F32 || stride != out_stride)) return LP_ERR_SHAPE;
     const int sms = sm_count();
     if (sms == 0) return LP_ERR_CUDA;

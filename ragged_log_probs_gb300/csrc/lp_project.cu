@@ -1023,6 +1023,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
         if (!fp8 && lora_dtype != dtype) return LP_ERR_DTYPE;
         if (B == 0 || (!row_offsets && B != T)) return LP_ERR_SHAPE;
         if (!aligned_to(lora_a, 16) || !aligned_to(lora_b, 16)) return LP_ERR_SHAPE;
+        if (!aligned_to(adapter_scale, 4) || !aligned_to(adapter_ids, 4) || !aligned_to(row_offsets, 4)) return LP_ERR_SHAPE;
     } else {
         rank = 0;
     }
