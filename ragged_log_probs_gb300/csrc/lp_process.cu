@@ -603,6 +603,8 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     }
     p.slice = (uint32_t)(((V + slices - 1) / slices + 7) / 8 * 8);
     p.slices = (V + p.slice - 1) / p.slice;
+    const uint64_t ctas = (uint64_t)p.slices * T;
+    if (ctas > 0x7FFFFFFFull) return LP_ERR_SHAPE;
     // Long histories are sorted by slices first; below that, reading them in every CTA costs less
     // than a second kernel. Rows of 128256 f32, all histories of one length, us (sorted | not):
     //     256 rows  2000: 60 | 59    4000: 64 | 70    8000: 72 | 89   16000: 78 | 113
@@ -619,8 +621,6 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     // 4 values at a time where logits and out have their 4-value boundaries at the same tokens
     const bool vec = stride % 4 == out_stride % 4 &&
                      (reinterpret_cast<uintptr_t>(logits) / e) % 4 == (reinterpret_cast<uintptr_t>(out) / 4) % 4;
-    const uint64_t ctas = (uint64_t)p.slices * T;
-    if (ctas > 0x7FFFFFFFull) return LP_ERR_SHAPE;
     if (dtype == LP_F32) return launch_process<float>(p, vec, (unsigned)ctas, stream);
     if (dtype == LP_BF16) return launch_process<__nv_bfloat16>(p, vec, (unsigned)ctas, stream);
     return launch_process<__half>(p, vec, (unsigned)ctas, stream);

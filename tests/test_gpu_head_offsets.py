@@ -57,3 +57,16 @@ def test_decreasing_history_offsets_where_histories_are_sorted(name, neutral):
     else:
         assert torch.isnan(out[wrong]).all() and lp.read_status(ws) == bits(4)
     check(out[right], (want[0][right], want[1][right]))
+
+
+def test_a_refused_call_leaves_nothing_enqueued():
+    # more rows times slices than a grid holds: refused on the host before the histories' sort
+    B, total = 1, 9000
+    ws = lp.new_head_workspace(requests=B, history=total)
+    history, off = torch.zeros(total, dtype=torch.int32).cuda(), i32([0, total])
+    rep, rows = torch.full((1,), 1.5).cuda(), i32([0, 4])
+    rc = lp.load().lp_head_process(0x10000, 0, 0xF0000000, 64, 64, rows.data_ptr(), B, history.data_ptr(), off.data_ptr(),
+                                   total, None, rep.data_ptr(), None, None, None, None, None, 0, None, 0, 0, None, 0x20000,
+                                   64, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 3 and not ws.any()
