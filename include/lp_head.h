@@ -126,7 +126,8 @@ lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H,
  *   mask_index      device, int32[T]: row t's mask row, negative: row t is not masked;
  *                   NULL: row t has mask row t (mask_rows >= T)
  *   workspace       lp_head_process_workspace_size(B, history_total) bytes: the status word
- *                   and, for histories of some thousand tokens, room to sort them
+ *                   and, for histories of some thousand tokens, room to sort them. The size
+ *                   grows with both, so that the largest call's workspace serves them all
  * A row whose mask allows nothing is all -inf. A masked value is -inf whatever it was.
  * The history of a request with repetition 1 and frequency = presence = 0 is not read.
  * Device checks, each giving the rows concerned NaN: row, history and bias offsets within

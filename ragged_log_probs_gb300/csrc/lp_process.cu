@@ -522,8 +522,11 @@ lp_status launch_process(const ProcessParams& p, bool vec, unsigned ctas, lp_str
 }  // namespace
 
 extern "C" size_t lp_head_process_workspace_size(uint32_t B, uint32_t history_total) {
-    if (B == 0 || history_total / B < kSortFrom) return kHeaderBytes;
-    return kHeaderBytes + (((size_t)B + history_total / kChunk + 1) * (kMaxSlices + 1) + history_total) * 4;
+    // Of the calls of up to so many requests and tokens the one that needs most: histories are sorted
+    // where their mean is kSortFrom, so the requests that count are at most total / kSortFrom.
+    const size_t requests = history_total / kSortFrom < B ? history_total / kSortFrom : B;
+    if (requests == 0) return kHeaderBytes;
+    return kHeaderBytes + ((requests + history_total / kChunk + 1) * (kMaxSlices + 1) + history_total) * 4;
 }
 
 extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,

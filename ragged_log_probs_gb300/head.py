@@ -71,7 +71,7 @@ def _load():
 
 
 def head_workspace_size(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0) -> int:
-    """Bytes of scratch that serve every call of these sizes: ``project`` with adapters of
+    """Bytes of scratch that serve every call of up to these sizes: ``project`` with adapters of
     that rank over T rows, ``process_logits`` of that many requests with that many history
     tokens in all (0: only the status word)."""
     lib = _pkg().load()

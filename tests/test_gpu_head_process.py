@@ -357,3 +357,14 @@ def test_rows_far_apart(dtype):
     check(out, want_of(c))
     del far, xv, out
     torch.cuda.empty_cache()
+
+
+def test_a_smaller_call_in_a_larger_ones_workspace():
+    # sized for a batch of short histories, used by the few long ones that are left of it
+    c = make(4, 9000, 4, hist=10, seed=24)
+    g = torch.Generator().manual_seed(24)
+    c["history"] = [torch.randint(0, 9000, (10000 + 7 * b,), generator=g).tolist() for b in range(4)]
+    ws = lp.new_head_workspace(requests=64, history=60000)
+    out, status = call(c, workspace=ws)
+    assert status == 0
+    check(out, want_of(c))
