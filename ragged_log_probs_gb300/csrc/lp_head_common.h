@@ -16,8 +16,11 @@ namespace lph {
 constexpr size_t kHeaderBytes = 256;  // the status word is the header's first word
 
 // Programmatic dependent launch: let the next kernel on the stream start launching, and
-// wait until the previous one has finished and its writes are visible. Every kernel here
-// waits before it touches global memory, so the chain stays ordered.
+// wait until the previous one has finished and its writes are visible. A call's first kernel
+// waits before it touches global memory, and where the call has a second one it triggers only
+// after that wait. So the second kernel may read the call's inputs, and set status bits, before
+// its own wait: what came before the call is complete then. What the first kernel writes, and
+// the call's outputs, are touched after it.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -416,6 +416,9 @@ k_project(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUt
         }
     } else if (warp == kMmaWarp) {
         if (lane == 0 && rank == 0) {
+            // (nothing to wait for before the copies begin; the bounded waits below are for this
+            // kernel's own work, not for an earlier one that let this one launch early)
+            if (!p.early) pdl_wait();
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
