@@ -130,10 +130,10 @@ lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H,
  *                   grows with both, so that the largest call's workspace serves them all
  * A row whose mask allows nothing is all -inf. A masked value is -inf whatever it was.
  * The history of a request with repetition 1 and frequency = presence = 0 is not read.
- * Device checks, each giving the rows concerned NaN: row, history and bias offsets within
- * their totals, nondecreasing, every row in a request, mask_index < mask_rows
- * (LP_ERR_OFFSETS); repetition within LP_MIN_REPETITION ... LP_MAX_REPETITION, frequency and
- * presence finite (LP_ERR_PENALTY). A history or bias token >= V is skipped (LP_ERR_TOKEN_RANGE), bias
+ * Device checks: the row, history and bias offsets as a whole nondecreasing and within T and
+ * their totals (LP_ERR_OFFSETS; a row gets NaN if it is in no request, or if its own request's
+ * list of tokens or biases is wrong), mask_index < mask_rows (LP_ERR_OFFSETS, NaN); repetition within LP_MIN_REPETITION ... LP_MAX_REPETITION, frequency and
+ * presence finite (LP_ERR_PENALTY, NaN). A history or bias token >= V is skipped (LP_ERR_TOKEN_RANGE), bias
  * ids not strictly ascending set LP_ERR_OFFSETS (that request's biases are unspecified).
  */
 size_t lp_head_process_workspace_size(uint32_t B, uint32_t history_total);

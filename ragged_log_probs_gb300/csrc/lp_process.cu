@@ -297,12 +297,20 @@ __global__ void __launch_bounds__(kSortThreads, 3) k_sort_history(ProcessParams 
     if (outside) flag(p.status, LP_ERR_TOKEN_RANGE);
 }
 
+// Offsets of n lists within `total`, by a whole CTA: LP_ERR_OFFSETS where they decrease or pass it.
+__device__ __forceinline__ void check_offsets(const uint32_t* off, uint32_t n, uint32_t total, uint32_t* status) {
+    bool bad = threadIdx.x == 0 && off[n] > total;
+    for (uint32_t i = threadIdx.x; i < n; i += blockDim.x) bad |= off[i] > off[i + 1];
+    if (bad) flag(status, LP_ERR_OFFSETS);
+}
+
 // Threads of a CTA. With sorted histories more, which overlap better (256 x 128256 f32, histories
 // of 30000: 256 threads 69.0 us, 384 66.1); without, the registers they leave cost more (240 x
 // 152064 bf16, histories of 1000: 47.1 and 51.2 us).
 __host__ __device__ constexpr uint32_t threads(bool sorted) { return sorted ? 384 : 256; }
 
-// grid: T x slices CTAs, all rows' first slices first: a vocabulary's frequent tokens mostly have
+// grid: T x slices CTAs, and one more that looks at the lists' offsets as a whole (a row's CTAs only
+// see its own request's). All rows' first slices first: a vocabulary's frequent tokens mostly have
 // its low numbers, and the CTAs with the most to count should not be the last to start (256 rows
 // with histories of 30000: 80 us row by row, 69 so).
 // Without sorted histories at most 48 registers, so that five CTAs share an SM where the slices are
@@ -317,6 +325,13 @@ __global__ void __launch_bounds__(threads(SORTED), SORTED ? kResident : kResiden
     pdl_trigger();
     const uint32_t tid = threadIdx.x;
     const uint32_t part = blockIdx.x / p.T, t = blockIdx.x - part * p.T;
+    if (part == p.slices) {
+        if constexpr (!SORTED) pdl_wait();
+        if (p.row_offsets) check_offsets(p.row_offsets, p.B, p.T, p.status);
+        if (p.history) check_offsets(p.history_offsets, p.B, p.history_total, p.status);
+        if (p.bias_tokens) check_offsets(p.bias_offsets, p.B, p.bias_total, p.status);
+        return;
+    }
     const uint32_t lo = part * p.slice, hi = min(lo + p.slice, p.V);  // this CTA's tokens
     const T* in = static_cast<const T*>(p.logits) + (uint64_t)t * p.stride;
     float* out = p.out + (uint64_t)t * p.out_stride;
@@ -606,7 +621,7 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
     }
     p.slice = (uint32_t)(((V + slices - 1) / slices + 7) / 8 * 8);
     p.slices = (V + p.slice - 1) / p.slice;
-    const uint64_t ctas = (uint64_t)p.slices * T;
+    const uint64_t ctas = (uint64_t)p.slices * T + (row_offsets || p.history || p.bias_tokens);
     if (ctas > 0x7FFFFFFFull) return LP_ERR_SHAPE;
     // Long histories are sorted by slices first; below that, reading them in every CTA costs less
     // than a second kernel. Rows of 128256 f32, all histories of one length, us (sorted | not):

@@ -1,5 +1,6 @@
-"""Processing of logits with history offsets that decrease: what a row gets does not depend on
-whether histories were sorted by slices first, and nothing of an earlier call comes back."""
+"""Processing of logits with offsets that are wrong: what a row gets does not depend on whether
+histories were sorted by slices first, nothing of an earlier call comes back, and the status word
+tells."""
 
 import pytest
 import torch
@@ -70,3 +71,22 @@ def test_a_refused_call_leaves_nothing_enqueued():
                                    64, ws.data_ptr(), ws.numel(), torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert rc == 3 and not ws.any()
+
+
+@pytest.mark.parametrize("mean", [10, 5000])
+@pytest.mark.parametrize("name,off", [("row_offsets", [0, 2, 1, 3]), ("row_offsets", [0, 1, 2, 4]), ("row_offsets", [0, 3, 3, 2]),
+                                      ("bias_offsets", [0, 2, 1, 2]), ("bias_offsets", [0, 0, 1, 9]),
+                                      ("history_offsets", [0, 2, 1, 3]), ("history_offsets", [0, 1, 2, 4])])
+def test_offsets_wrong_anywhere_set_a_bit(name, off, mean):
+    # also of requests that have no rows, or whose history has no effect
+    B, V, total = 3, 700, 3 * mean
+    if name == "history_offsets":
+        off = [mean * o for o in off]
+    args = dict(history=torch.zeros(total, dtype=torch.int32).cuda(), history_offsets=i32([0, mean, 2 * mean, total]),
+                repetition=torch.ones(3).cuda(), bias_tokens=i32([4, 5]), bias_values=torch.zeros(2).cuda(),
+                bias_offsets=i32([0, 1, 1, 2]), row_offsets=i32([0, 3, 3, 3]))
+    x = torch.randn(3, V).cuda()
+    ws = lp.new_head_workspace(requests=B, history=total)
+    assert torch.equal(lp.process_logits(x, workspace=ws, **args), x) and lp.read_status(ws) == 0
+    lp.process_logits(x, workspace=ws, **dict(args, **{name: i32(off)}))
+    assert lp.read_status(ws) == bits(4)
