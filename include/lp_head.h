@@ -61,7 +61,9 @@ lp_status lp_head_clear_status(void *workspace, lp_stream_t stream);
  *   out             device out, [n][H] of out_dtype (dtype, LP_F32 or LP_E4M3)
  *   out_scale       device out, float[n], for LP_E4M3 only
  *   residual_out    device out, [n][H] of dtype, or NULL. Without rows, out and
- *                   residual_out may be x or residual themselves (same type and stride).
+ *                   residual_out may be x or residual themselves (same type and stride);
+ *                   otherwise outputs and inputs lie apart (LP_ERR_SHAPE where they begin
+ *                   at one place)
  *   workspace       the status word; required with rows, else may be NULL
  * A row holding NaN or an infinity becomes NaN where the formula does (LP_E4M3: the row's
  * scale is NaN). Only h, y and out_scale have to fit f32, not h^2 or its sum. Device check: rows[o] < T (LP_ERR_OFFSETS; that output row gets NaN).

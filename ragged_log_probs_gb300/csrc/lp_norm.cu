@@ -374,6 +374,14 @@ lp_status lp_head_norm(const void* x, const void* residual, const void* weight, 
     if (!(eps >= 0.f) || eps > 3.0e38f) return LP_ERR_SHAPE;
     if (rows && (!workspace || workspace_bytes < lph::kHeaderBytes)) return LP_ERR_WORKSPACE;
     if (workspace && !aligned_to(workspace, 256)) return LP_ERR_WORKSPACE;
+    // An output in an input's place: row for row, so that no row is read after its place was written.
+    const auto apart = [&](const void* to, uint32_t type, uint64_t to_stride, const void* from, uint64_t from_stride) {
+        return to != from || !to || (!rows && type == dtype && (to_stride == from_stride || T == 1));
+    };
+    if (!apart(out, out_dtype, out_stride, x, x_stride) || !apart(out, out_dtype, out_stride, residual, residual_stride) ||
+        !apart(residual_out, dtype, residual_out_stride, x, x_stride) ||
+        !apart(residual_out, dtype, residual_out_stride, residual, residual_stride) || out == residual_out)
+        return LP_ERR_SHAPE;
     NormParams p;
     p.x = x;
     p.residual = residual;

@@ -1,9 +1,10 @@
-"""Pointers that are not aligned to their type are refused on the host: a kernel that read them
-would fault. Without a GPU; no pointer is dereferenced."""
+"""Pointers that are not aligned to their type are refused on the host (a kernel that read them
+would fault), and so are outputs that other rows are still read from. Without a GPU; no pointer is
+dereferenced."""
 
 import pytest
 
-from tests.test_head_host import FAKE, SHAPE, WORKSPACE, _process, _project, lib  # noqa: F401 (a fixture)
+from tests.test_head_host import BF16, E4M3, F32, FAKE, SHAPE, WORKSPACE, _norm, _process, _project, lib  # noqa: F401 (a fixture)
 
 LISTS = dict(off=FAKE, B=4, hist=FAKE, hoff=FAKE, total=40, prompt=FAKE, rep=FAKE, freq=FAKE, pres=FAKE, bt=FAKE, bv=FAKE,
              bo=FAKE, nb=10, mask=FAKE, mi=FAKE)
@@ -24,3 +25,18 @@ def test_project_refuses_unaligned_lists(lib, name):  # noqa: F811
 
 def test_clear_status_refuses_what_is_no_workspace(lib):  # noqa: F811
     assert lib.lp_head_clear_status(FAKE + 4, None) == WORKSPACE
+
+
+def test_norm_refuses_what_cannot_be_done_in_place(lib):  # noqa: F811
+    other, more = 2 * FAKE, 3 * FAKE
+    picked = dict(rows=4 * FAKE, n=2, ws=FAKE, wsb=256)
+    # picked rows: a row may be read after another one has been written over it
+    assert _norm(lib, x=other, out=other, **picked) == SHAPE
+    assert _norm(lib, x=other, residual=more, out=more, **picked) == SHAPE
+    assert _norm(lib, x=other, kept=other, **picked) == SHAPE
+    assert _norm(lib, x=other, residual=more, kept=more, **picked) == SHAPE
+    # another type or stride
+    assert _norm(lib, x=other, out=other, odtype=F32) == SHAPE
+    assert _norm(lib, x=other, out=other, odtype=E4M3, scale=more) == SHAPE
+    assert _norm(lib, x=other, out=other, os_=72) == SHAPE and _norm(lib, x=other, kept=other, ks=72) == SHAPE
+    assert _norm(lib, x=other, out=more, kept=more) == SHAPE                # two outputs in one place
