@@ -11,6 +11,7 @@ import sys
 import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
+from importlib import metadata
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -31,7 +32,9 @@ def lib_path() -> str:
 
 
 def binding_path() -> str:
-    return os.path.join(LIB_DIR, "lp_head_binding.so")
+    """Where the binding is: named after the interpreter and the torch whose C++ ABI it has, so that
+    after an upgrade of either none is found, instead of one that does not fit."""
+    return os.path.join(LIB_DIR, f"lp_head_binding.torch-{metadata.version('torch')}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _binding_commands(work: str):
