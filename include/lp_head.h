@@ -107,6 +107,15 @@ lp_status lp_head_project(const void *x, uint32_t dtype, uint32_t T, uint32_t H,
                           void *workspace, size_t workspace_bytes, lp_stream_t stream);
 
 /*
+ * How lp_head_project cuts a product of these sizes on a device of `sms` SMs (0: the current
+ * one's), for diagnostics: *ctas = 1 or 2 (a pair) to a tile, *rows = rows of x in a tile,
+ * *on_tensor_cores = 1 where the adapters of 32 neighbouring rows that have one or two are
+ * multiplied there (0: all by the epilogue). adapters, rank: 0 without.
+ */
+lp_status lp_head_project_cut(uint32_t T, uint32_t H, uint32_t V, uint32_t dtype, uint32_t adapters, uint32_t rank,
+                              uint32_t sms, uint32_t *ctas, uint32_t *rows, uint32_t *on_tensor_cores);
+
+/*
  * Processing of logits. Logits row t belongs to the request b with
  * row_offsets[b] <= t < row_offsets[b+1] (row_offsets NULL: request t, B == T). With
  * `seen` = the token is in the request's history, `count` = how often it is in the

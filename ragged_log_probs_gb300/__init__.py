@@ -20,7 +20,7 @@ import torch
 from . import _build
 from . import head as _head
 from .head import (clear_status, head_workspace_size, new_head_workspace, process_logits, project,  # noqa: F401
-                   rms_norm)
+                   project_cut, rms_norm)
 from .results import LogProbabilities, assemble  # noqa: F401  (host-side result assembly)
 
 __all__ = [

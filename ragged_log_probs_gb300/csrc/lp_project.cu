@@ -969,6 +969,17 @@ Cut choose_cut(uint32_t T, uint32_t V, uint32_t slices, uint32_t sms, bool adapt
     return best;
 }
 
+// B's rows go through a tensor map, as whole 16-byte pieces.
+bool lora_by_tma(uint32_t rank, uint64_t adapters, uint32_t V) { return rank % 8 == 0 && adapters * V <= 0x7FFFFFFFu; }
+
+// Blocks of rows with one adapter or two run on the tensor cores (pairs only: the tiles of fewer
+// rows wait for memory, and the epilogue's arithmetic is hidden).
+bool adapters_on_tensor_cores(const Cut& cut, uint32_t rank, uint64_t adapters, uint32_t V) {
+    return cut.cg == 2 && rank != 0 && lora_by_tma(rank, adapters, V);
+}
+
+uint32_t slices_of(uint64_t H, uint32_t dtype) { return (uint32_t)((H * dtype_bytes(dtype) + kSliceBytes - 1) / kSliceBytes); }
+
 struct ProjectLaunch {
     CUtensorMap w, x, b, lora_b, parts;
     ProjectParams p;
@@ -1055,12 +1066,12 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     p.b_cols = part_cols(rank);
     p.lora_f16 = lora_dtype == LP_F16;
     p.lora_bytes = (uint64_t)adapters * V * rank * 2;
-    p.lora_tma = rank % 8 == 0 && (uint64_t)adapters * V <= 0x7FFFFFFFu;
+    p.lora_tma = lora_by_tma(rank, adapters, V);
     p.early = rank != 0;
     // How the product is cut: the rows of x into even tiles of at most 256, a multiple of 16, for
     // single CTAs or (a multiple of 32) for pairs, which read each row of x once for two tiles of
     // the vocabulary. The choice is the cheapest of a few by a rough count of clocks.
-    p.slices = (uint32_t)((H * e + kSliceBytes - 1) / kSliceBytes);
+    p.slices = slices_of(H, dtype);
     const Cut cut = choose_cut(T, V, p.slices, (uint32_t)sms, rank != 0);
     const uint32_t cg = cut.cg;
     p.tile_t = cut.tile_t;
@@ -1068,9 +1079,7 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     const uint64_t tiles = (uint64_t)((V + cg * kTileV - 1) / (cg * kTileV)) * p.tiles_t;
     if (tiles > 0x7FFFFFFFu) return LP_ERR_SHAPE;
     p.tiles = (uint32_t)tiles;
-    // Blocks of rows with one adapter run on the tensor cores (pairs only: the tiles of fewer
-    // rows wait for memory, and the epilogue's arithmetic is hidden).
-    p.tensor = cg == 2 && p.lora_tma && rank != 0;
+    p.tensor = adapters_on_tensor_cores(cut, rank, adapters, V);
     p.apart = fp8 || dtype == LP_F16;
     p.part_stride = (uint32_t)space.rows;
     p.chunk = fp8 || out_dtype != LP_F32 ? p.slices : p.tile_t <= kPromoteFewRows ? kPromoteSlices / 2 : kPromoteSlices;
@@ -1135,4 +1144,21 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
     const uint32_t units = (uint32_t)sms / cg;  // CTAs, or pairs
     l.grid = cg * (p.tiles < units ? p.tiles : units);
     return fp8 ? launch_project<true>(l, out_dtype, cg, stream) : launch_project<false>(l, out_dtype, cg, stream);
+}
+
+extern "C" lp_status lp_head_project_cut(uint32_t T, uint32_t H, uint32_t V, uint32_t dtype, uint32_t adapters,
+                                         uint32_t rank, uint32_t sms, uint32_t* ctas, uint32_t* rows,
+                                         uint32_t* on_tensor_cores) {
+    if (!ctas || !rows || !on_tensor_cores) return LP_ERR_NULL;
+    if (dtype != LP_BF16 && dtype != LP_F16 && dtype != LP_E4M3) return LP_ERR_DTYPE;
+    if (T == 0 || H == 0 || V == 0 || T > 0x7FFFFF00u || V > 0x7FFFFF00u || H > 0x7FFFFF00u || rank > LP_MAX_RANK)
+        return LP_ERR_SHAPE;
+    if (adapters == 0) rank = 0;
+    if (sms == 0) sms = (uint32_t)sm_count();
+    if (sms < 2) return LP_ERR_CUDA;
+    const Cut cut = choose_cut(T, V, slices_of(H, dtype), sms, rank != 0);
+    *ctas = cut.cg;
+    *rows = cut.tile_t;
+    *on_tensor_cores = adapters_on_tensor_cores(cut, rank, adapters, V);
+    return LP_OK;
 }

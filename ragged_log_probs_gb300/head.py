@@ -18,7 +18,8 @@ import torch
 
 from . import _build
 
-__all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "project", "process_logits"]
+__all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "project", "project_cut",
+           "process_logits"]
 
 LP_MAX_HIDDEN = 32768
 LP_MAX_RANK = 64
@@ -36,6 +37,8 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.lp_head_project.argtypes = [vp, u32, u32, u32, u64, vp, vp, u32, u64, vp, vp, vp, u32, u32, u32, vp, vp, vp,
                                     u32, vp, u32, u64, vp, sz, vp]
     lib.lp_head_project.restype = ctypes.c_int
+    lib.lp_head_project_cut.argtypes = [u32] * 7 + [vp] * 3
+    lib.lp_head_project_cut.restype = ctypes.c_int
     lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
                                     vp, u64, u32, vp, vp, u64, vp, sz, vp]
     lib.lp_head_process.restype = ctypes.c_int
@@ -136,6 +139,19 @@ def project(x: torch.Tensor, weight: torch.Tensor, x_scale: Optional[torch.Tenso
                                   row_offsets, out, out_dtype, workspace)
     return native.project(x, weight, x_scale, weight_scale, lora_a, lora_b, adapter_scale, adapter_ids, row_offsets,
                           out, out_dtype, workspace)
+
+
+def project_cut(T: int, H: int, V: int, dtype: torch.dtype, adapters: int = 0, rank: int = 0, sms: int = 0):
+    """How ``project`` cuts a product of these sizes on a device of ``sms`` SMs (0: the current
+    one's): (CTAs of a tile, rows of ``x`` in a tile, whether blocks of rows with one adapter or
+    two are multiplied on the tensor cores)."""
+    codes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3}
+    got = (ctypes.c_uint32 * 3)()
+    at = ctypes.addressof(got)
+    rc = _pkg().load().lp_head_project_cut(T, H, V, codes.get(dtype, 99), adapters, rank, sms, at, at + 4, at + 8)
+    if rc:
+        _failed(rc, "lp_head_project_cut")
+    return got[0], got[1], bool(got[2])
 
 
 def process_logits(logits: torch.Tensor, row_offsets: Optional[torch.Tensor] = None,

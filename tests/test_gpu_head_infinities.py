@@ -4,6 +4,7 @@ projection has for adapters."""
 import pytest
 import torch
 
+import ragged_log_probs_gb300 as lp
 from tests import parity
 from tests.test_gpu_head_project import BF16, E4M3, F16, F32, Case
 
@@ -27,8 +28,9 @@ FORMS = {"one a block": ([0, 64, 256], [0, 1]), "two a block": ([0, 48, 170, 256
 def test_an_infinite_b_gives_what_the_formula_gives(name, out_dtype, dtype):
     off, ids = FORMS[name]
     T = off[-1] if off else len(ids)
-    c = Case(T, 256, 20001, dtype, A=5, rank=16, ids=ids, off=off, seed=31, unit=True,
+    c = Case(T, 512, 20001, dtype, A=5, rank=16, ids=ids, off=off, seed=31, unit=True,
              lora_dtype=BF16 if dtype == E4M3 else None)
+    assert lp.project_cut(T, 512, 20001, dtype, 5, 16)[2] == (T > 128)
     # u[t, 0] one value of 16 bits (1, -2, 0 or 0.5), u[t, 1] another of few bits
     x, la, lb = c.x.clone(), c.la.clone(), c.lb.clone()
     x[:, :2] = torch.tensor([[1.0, 1.5], [-2.0, 1.0], [0.0, -3.0], [0.5, 0.0]]).repeat((T + 3) // 4, 1)[:T].to(dtype)
@@ -59,6 +61,7 @@ def test_an_infinite_u_gives_what_the_formula_gives(name, dtype):
     la[:, 1:] = c.la          # eight equal columns: infinities of one sign
     lb[:, :, 1:] = c.lb
     c.rank = 8
+    assert lp.project_cut(T, 256, 20001, dtype, 5, 8)[2] == (T > 128)
     scale = torch.ones(5)
     scale[1] = float("inf")
     out = c.run(F32, lora_a=la.cuda(), lora_b=lb.cuda(), adapter_scale=scale.cuda()).cpu()
