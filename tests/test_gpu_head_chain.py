@@ -92,3 +92,19 @@ def test_the_chain_in_a_graph(example):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(head.logits, want[0]) and torch.equal(head.out_lp, want[1]) and torch.equal(head.out_tok, want[2])
+
+
+def test_every_row_leads_with_its_chosen_token(example):
+    # the best token is the first of the top and the row's own, in every row; the first row's is even
+    B = 6
+    head = example.Head(B, 256, 2001, adapters=2, rank=4, seed=3)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(8)
+    for _ in range(3):
+        x, r = (torch.randn(B, 256, generator=g, device="cuda").bfloat16() for _ in range(2))
+        best, logprobs, tokens = head.step(x, r)
+        K = tokens.shape[1] - 1
+        for b in range(B):
+            assert int(tokens[b, 0]) == int(tokens[b, K]) == int(best[b])
+            assert float(logprobs[b, 0]) == float(logprobs[b, K])
+        assert int(best[0]) % 2 == 0
