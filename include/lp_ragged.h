@@ -50,7 +50,8 @@ typedef enum lp_status {
     LP_OK = 0,
     LP_ERR_NULL = 1,         /* a required pointer is NULL                                  */
     LP_ERR_LEVELS = 2,       /* levels > LP_MAX_LEVELS                                      */
-    LP_ERR_SHAPE = 3,        /* B, T or V is 0 or too large, or logits not 4-byte aligned   */
+    LP_ERR_SHAPE = 3,        /* B, T or V is 0 or too large, or logits not 4-byte aligned; of the
+                                head's operators also another size, a stride or an alignment */
     LP_ERR_OFFSETS = 4,      /* device: empty or decreasing batch range, a range past T, or
                                 output offsets that disagree with the echo flags           */
     LP_ERR_TOKEN_RANGE = 5,  /* device: an actual or sampled token >= V                     */

@@ -359,11 +359,12 @@ lp_status lp_head_norm(const void* x, const void* residual, const void* weight, 
                        const uint32_t* rows, uint32_t n, float eps, void* out, uint32_t out_dtype,
                        uint64_t out_stride, float* out_scale, void* residual_out, uint64_t residual_out_stride,
                        void* workspace, size_t workspace_bytes, lp_stream_t stream) {
+    if (T == 0 || n == 0) return LP_ERR_SHAPE;  // (before the pointers: an empty tensor has none)
     if (!x || !weight || !out) return LP_ERR_NULL;
     if (dtype > LP_F16 || (weight_dtype != dtype && weight_dtype != LP_F32)) return LP_ERR_DTYPE;
     if (out_dtype != dtype && out_dtype != LP_F32 && out_dtype != LP_E4M3) return LP_ERR_DTYPE;
     if (out_dtype == LP_E4M3 && !out_scale) return LP_ERR_NULL;
-    if (T == 0 || n == 0 || n > 0x7FFFFFFFu || H == 0 || H > LP_MAX_HIDDEN || (!rows && n != T)) return LP_ERR_SHAPE;
+    if (n > 0x7FFFFFFFu || H == 0 || H > LP_MAX_HIDDEN || (!rows && n != T)) return LP_ERR_SHAPE;
     if (x_stride < H || out_stride < H || (residual && residual_stride < H) ||
         (residual_out && residual_out_stride < H))
         return LP_ERR_SHAPE;

@@ -553,12 +553,13 @@ extern "C" lp_status lp_head_process(const void* logits, uint32_t dtype, uint32_
                                      uint64_t mask_stride, uint32_t mask_rows, const int32_t* mask_index, float* out,
                                      uint64_t out_stride, void* workspace, size_t workspace_bytes,
                                      lp_stream_t stream) {
+    if (T == 0 || V == 0 || B == 0) return LP_ERR_SHAPE;  // (before the pointers: an empty tensor has none)
     if (!logits || !out || (history && !history_offsets) ||
         (bias_tokens && (!bias_values || !bias_offsets)))
         return LP_ERR_NULL;
     if (!workspace || workspace_bytes < kHeaderBytes || !aligned_to(workspace, 256)) return LP_ERR_WORKSPACE;
     if (dtype > LP_F16) return LP_ERR_DTYPE;
-    if (T == 0 || V == 0 || B == 0 || V >= 0x7FFFFFFFu || stride < V || out_stride < V)
+    if (V >= 0x7FFFFFFFu || stride < V || out_stride < V)
         return LP_ERR_SHAPE;
     if (!row_offsets && B != T) return LP_ERR_SHAPE;
     if (mask && (mask_rows == 0 || mask_rows > 0x7FFFFFFFu || mask_stride < ((uint64_t)V + 31) / 32 ||

@@ -1017,13 +1017,14 @@ extern "C" lp_status lp_head_project(const void* x, uint32_t dtype, uint32_t T, 
                                      const uint32_t* row_offsets, uint32_t B, void* out, uint32_t out_dtype,
                                      uint64_t out_stride, void* workspace, size_t workspace_bytes,
                                      lp_stream_t stream) {
+    if (T == 0 || V == 0) return LP_ERR_SHAPE;  // (before the pointers: an empty tensor has none)
     if (!x || !weight || !out) return LP_ERR_NULL;
     if (dtype != LP_BF16 && dtype != LP_F16 && dtype != LP_E4M3) return LP_ERR_DTYPE;
     if (out_dtype != LP_F32 && out_dtype != LP_BF16 && out_dtype != LP_F16) return LP_ERR_DTYPE;
     const bool fp8 = dtype == LP_E4M3, adapted = adapters != 0;
     if (fp8 && (!x_scale || !weight_scale)) return LP_ERR_NULL;
     if (!fp8 && (x_scale || weight_scale)) return LP_ERR_DTYPE;
-    if (T == 0 || H == 0 || V == 0 || T > 0x7FFFFF00u || V > 0x7FFFFF00u || H > 0x7FFFFF00u) return LP_ERR_SHAPE;
+    if (H == 0 || T > 0x7FFFFF00u || V > 0x7FFFFF00u || H > 0x7FFFFF00u) return LP_ERR_SHAPE;
     if (x_stride < H || weight_stride < H || out_stride < V) return LP_ERR_SHAPE;
     const size_t e = dtype_bytes(dtype), eo = dtype_bytes(out_dtype);
     // the copies start on 16-byte boundaries and move whole 16 bytes

@@ -521,7 +521,7 @@ const char* lp_ragged_strerror(lp_status status) {
         case LP_OK: return "ok";
         case LP_ERR_NULL: return "a required pointer is NULL";
         case LP_ERR_LEVELS: return "levels exceeds 6 (top-k capacity 63)";
-        case LP_ERR_SHAPE: return "B, T or V is zero or too large, or logits are not 4-byte aligned";
+        case LP_ERR_SHAPE: return "B, T, V or another size is zero or too large, a stride is too small, or a pointer or row is not aligned";
         case LP_ERR_OFFSETS:
             return "row offsets invalid: empty/decreasing batch, range past T, echo mismatch, or fewer logits "
                    "rows than scored positions";

@@ -40,3 +40,10 @@ def test_norm_refuses_what_cannot_be_done_in_place(lib):  # noqa: F811
     assert _norm(lib, x=other, out=other, odtype=E4M3, scale=more) == SHAPE
     assert _norm(lib, x=other, out=other, os_=72) == SHAPE and _norm(lib, x=other, kept=other, ks=72) == SHAPE
     assert _norm(lib, x=other, out=more, kept=more) == SHAPE                # two outputs in one place
+
+
+def test_no_rows_is_a_size_and_not_a_missing_pointer(lib):  # noqa: F811
+    assert _norm(lib, x=None, out=None, T=0, n=0) == SHAPE and _norm(lib, out=None, rows=FAKE, n=0, ws=FAKE, wsb=256) == SHAPE
+    assert _project(lib, x=None, out=None, T=0) == SHAPE and _project(lib, w=None, out=None, V=0) == SHAPE
+    assert _process(lib, x=None, out=None, T=0, B=0) == SHAPE
+    assert "aligned" in lib.lp_ragged_strerror(SHAPE).decode() and "stride" in lib.lp_ragged_strerror(SHAPE).decode()
