@@ -53,6 +53,8 @@ lp_status lp_head_clear_status(void *workspace, lp_stream_t stream);
  *     y = h / sqrt(mean(h^2) + eps) * weight      (f32)
  *     out[o] = y rounded to out_dtype, or for LP_E4M3
  *     out_scale[o] = max(max|y| / 448, 2^-126),  out[o] = e4m3(y / out_scale[o])
+ *                    (y times the rounded reciprocal: a value next to the middle of two
+ *                    codes may take the other one)
  *     residual_out[o] = h rounded to dtype        (optional)
  * The norm reads h before its rounding.
  *   x, residual     device, [T][H] of dtype (LP_F32, LP_BF16, LP_F16); residual may be NULL
@@ -80,8 +82,11 @@ lp_status lp_head_norm(const void *x, const void *residual, const void *weight, 
  *     out[t, v] = sx[t] sw[v] sum_h x[t, h] W[v, h]  +  sum_j u[t, j] B_a[v, j]
  *     u[t, j]   = s_a sx[t] sum_h x[t, h] A_a[j, h]
  * with a = adapter_ids[b] for the request b of row t (rows as in lp_head_process); a
- * negative id means no adapter. Products are exact, sums are f32, u stays f32; the result
- * is rounded once to out_dtype.
+ * negative id means no adapter. Products are exact and sums f32: on the tensor cores, whose
+ * f32 sums drop what is below their last place, for f32 logits of 16-bit inputs over 768
+ * products at most at a time, which are added with rounding, else over all of H. u is a f32
+ * sum that enters the second product with its 24 bits (or, LP_F16 adapters on the tensor
+ * cores, to 2^-38 of the row's largest). The result is rounded once to out_dtype.
  *   x               device, [T][H] of dtype (LP_BF16, LP_F16, LP_E4M3)
  *   x_scale         device, float[T], sx, for LP_E4M3 only (else NULL, and sx = 1)
  *   weight          device, [V][H] of dtype; weight_scale: device, float[V], as x_scale
@@ -120,7 +125,8 @@ lp_status lp_head_project_cut(uint32_t T, uint32_t H, uint32_t V, uint32_t dtype
  * row_offsets[b] <= t < row_offsets[b+1] (row_offsets NULL: request t, B == T). With
  * `seen` = the token is in the request's history, `count` = how often it is in the
  * history's output part, every value becomes, in f32 and in this order,
- *     x = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x
+ *     x = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x   (x / r as x times
+ *                                                                       the rounded 1 / r)
  *     x = x - frequency[b] * count - (count > 0 ? presence[b] : 0)
  *     x = x + bias                                  (tokens of the request's bias list)
  *     x = -inf                                      (tokens whose mask bit is 0)

