@@ -4,7 +4,9 @@
  * an 8-bit output), the vocabulary projection with low-rank adapters, and the processing
  * of logits (repetition, frequency and presence penalties, biases, grammar masks).
  *
- *     hidden -> lp_head_norm -> lp_head_project -> lp_head_process -> lp_ragged_step
+ *     hidden -> lp_head_norm -> lp_head_project -> lp_head_process -> lp_head_sample -> lp_ragged_step
+ *
+ * The projection also takes 4-bit operands: lp_head_quantize4 -> lp_head_project4.
  *
  * Conventions are those of lp_ragged.h: the caller owns every buffer and the stream, the
  * library allocates nothing, LP_OK means "validated and enqueued", host-checked errors
@@ -163,6 +165,64 @@ lp_status lp_head_process(const void *logits, uint32_t dtype, uint32_t T, uint32
                           uint32_t bias_total, const uint32_t *mask, uint64_t mask_stride, uint32_t mask_rows,
                           const int32_t *mask_index, float *out, uint64_t out_stride, void *workspace,
                           size_t workspace_bytes, lp_stream_t stream);
+
+/*
+ * Rows in microscaled 4-bit floating point: e2m1 codes (sign, then 0, 0.5, 1, 1.5, 2, 3, 4, 6), two
+ * to a byte, the first of them in the low half, and one scale for every block of 16 or 32
+ * neighbours; H is a multiple of 32.
+ *   block 16: scales are e4m3, and every row has a scale in f32 besides;
+ *             value = code * scale * row_scale
+ *   block 32: scales are e8m0 (2^(byte - 127), 255 is NaN); value = code * scale
+ * Scales lie in tiles of 128 rows by 4 blocks, 512 bytes each, row by row of tiles; in a tile
+ * that of row i and block j is byte (i % 32) * 16 + (i / 32) * 4 + j. What is left of the last
+ * tiles in a row of blocks has to be 0; of the rows past the last one it may be anything.
+ * lp_head_fp4_scale_bytes: their size (0: no such block).
+ */
+size_t lp_head_fp4_scale_bytes(uint32_t rows, uint32_t H, uint32_t block);
+
+/*
+ * Quantise rows.
+ *   block 16: row_scale = the smallest power of two r with max|x[t]| <= 6 * 448 r, at least 2^-100;
+ *             scale = e4m3(max|block| / (6 r)), code = e2m1(x / (scale r))
+ *   block 32: scale = 2^(floor(log2 max|block|) - 2), from 2^-127 on, code = e2m1(x / scale)
+ * each to the nearest, of two as near to the even code, codes saturated at 6; a block whose scale
+ * rounds to 0 (block 16), or that is all 0, has codes of value 0. In a row (block 16), or a block of
+ * 32, that holds a NaN or an infinity, the scales are NaN.
+ *   x            device, [T][H] of dtype (LP_F32, LP_BF16, LP_F16), H <= LP_MAX_HIDDEN
+ *   codes        device out, [T][H / 2] bytes, 16-byte aligned, stride in bytes, of whole 16 bytes
+ *   scales       device out, lp_head_fp4_scale_bytes(T, H, block) bytes, 16-byte aligned; the
+ *                tiles' remainders are written too (0)
+ *   row_scale    device out, float[T], for block 16 only (else NULL)
+ */
+lp_status lp_head_quantize4(const void *x, uint32_t dtype, uint32_t T, uint32_t H, uint64_t x_stride, uint32_t block,
+                            void *codes, uint64_t codes_stride, void *scales, float *row_scale, lp_stream_t stream);
+
+/*
+ * Values of quantised rows: out[o] = row rows[o] (rows NULL: row o, n == V), rounded once to
+ * out_dtype; a lookup of tokens in a 4-bit embedding. row_scale may be NULL (1), for either block.
+ *   workspace    the status word; required with rows, else may be NULL
+ * Device check: rows[o] < V (LP_ERR_OFFSETS; that output row gets NaN).
+ */
+lp_status lp_head_dequantize4(const void *codes, uint64_t codes_stride, const void *scales, const float *row_scale,
+                              uint32_t V, uint32_t H, uint32_t block, const uint32_t *rows, uint32_t n, void *out,
+                              uint32_t out_dtype, uint64_t out_stride, void *workspace, size_t workspace_bytes,
+                              lp_stream_t stream);
+
+/*
+ * Projection of quantised rows to logits, without adapters:
+ *     out[t, v] = x_row_scale[t] weight_row_scale[v] sum_h (code scale)[t, h] (code scale)[v, h]
+ * Products are exact and sums f32, on the tensor cores; the result is rounded once to out_dtype.
+ *   x, x_scales, x_row_scale                 T rows as above; row scales may be NULL (1)
+ *   weight, weight_scales, weight_row_scale  V rows
+ *   out          device out, [T][V] of out_dtype (LP_F32, LP_BF16, LP_F16)
+ *   workspace    256 bytes: the status word
+ * LP_ERR_TIMEOUT: a wait inside the kernel ran out (out is not complete).
+ */
+lp_status lp_head_project4(const void *x, uint64_t x_stride, const void *x_scales, const float *x_row_scale, uint32_t T,
+                           uint32_t H, uint32_t block, const void *weight, uint64_t weight_stride,
+                           const void *weight_scales, const float *weight_row_scale, uint32_t V, void *out,
+                           uint32_t out_dtype, uint64_t out_stride, void *workspace, size_t workspace_bytes,
+                           lp_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -19,7 +19,8 @@ import torch
 
 from . import _build
 from . import head as _head
-from .head import (clear_status, head_workspace_size, new_head_workspace, process_logits, project,  # noqa: F401
+from .head import (clear_status, dequantize_fp4, fp4_scale_bytes, head_workspace_size,  # noqa: F401
+                   new_head_workspace, process_logits, project, project_fp4, quantize_fp4, tile_fp4_scales,
                    project_cut, rms_norm)
 from .results import LogProbabilities, assemble  # noqa: F401  (host-side result assembly)
 

@@ -322,6 +322,136 @@ PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
+// Bytes of a tensor that holds 4-bit codes, two to a byte, or 8-bit scales.
+bool holds_codes(c10::ScalarType t) { return t == c10::ScalarType::Byte || t == c10::ScalarType::Float4_e2m1fn_x2; }
+bool holds_scales(c10::ScalarType t, uint32_t block) {
+    return t == c10::ScalarType::Byte ||
+           t == (block == 16 ? c10::ScalarType::Float8_e4m3fn : c10::ScalarType::Float8_e8m0fnu);
+}
+
+uint32_t block_of(PyObject* o) {
+    const long b = PyLong_AsLong(o);
+    if (b == -1 && PyErr_Occurred()) throw Refused();
+    if (b != 16 && b != 32) refuse(PyExc_ValueError, "block must be 16 or 32, is " + std::to_string(b));
+    return static_cast<uint32_t>(b);
+}
+
+// 4-bit rows: codes [rows, H / 2] and their scales.
+struct Fp4 {
+    Call::Matrix codes;
+    void* scales = nullptr;
+    float* row_scale = nullptr;
+    int64_t rows = 0, H = 0;
+};
+void check_scales(const at::Tensor& s, const char* name, int64_t rows, int64_t H, uint32_t block) {
+    const size_t want = lp_head_fp4_scale_bytes(size32(rows, name), size32(H, name), block);
+    if (!holds_scales(s.scalar_type(), block))
+        refuse(PyExc_TypeError, std::string(name) + " must be uint8 or " + (block == 16 ? "float8_e4m3fn" : "float8_e8m0fnu") +
+                                    ", is " + c10::toString(s.scalar_type()));
+    if (!s.is_contiguous() || static_cast<size_t>(s.numel()) != want)
+        refuse(PyExc_ValueError, std::string(name) + " must be contiguous with " + std::to_string(want) +
+                                     " elements (see fp4_scale_bytes), is " + dims(s));
+}
+Fp4 fp4_rows(const Call& c, PyObject* codes, PyObject* scales, PyObject* row_scale, uint32_t block, const char* name) {
+    const std::string n = name;
+    const at::Tensor& t = c.two_dims(codes, name);
+    if (!holds_codes(t.scalar_type()))
+        refuse(PyExc_TypeError, n + " must be uint8 or float4_e2m1fn_x2, is " + c10::toString(t.scalar_type()));
+    Fp4 f;
+    f.rows = t.size(0);
+    f.H = 2 * t.size(1);
+    f.codes = c.matrix(t, name, t.size(0), t.size(1), t.scalar_type());
+    if (f.rows <= 1) f.codes.stride = (f.codes.stride + 15) / 16 * 16;  // (no second row)
+    const at::Tensor& s = c.tensor(scales, (n + "'s scales").c_str());
+    check_scales(s, (n + "'s scales").c_str(), f.rows, f.H, block);
+    f.scales = s.data_ptr();
+    f.row_scale = c.floats(row_scale, (n + "'s row_scale").c_str(), f.rows);
+    return f;
+}
+
+// (x, block, out, out_scales, out_row_scale)
+PyObject* quantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 5, [&]() -> PyObject* {
+        const Call c;
+        const at::Tensor& x = c.two_dims(a[0], "x");
+        const uint32_t block = block_of(a[1]);
+        const int64_t T = x.size(0), H = x.size(1);
+        const Call::Matrix xm = c.matrix(x, "x", T, H, x.scalar_type());
+        if (H % 32) refuse(PyExc_ValueError, "x's rows must have a multiple of 32 elements, have " + std::to_string(H));
+        const at::TensorOptions bytes = x.options().dtype(c10::ScalarType::Byte);
+        const at::Tensor codes = a[2] == Py_None ? at::empty({T, H / 2}, bytes) : c.tensor(a[2], "out");
+        if (!holds_codes(codes.scalar_type()))
+            refuse(PyExc_TypeError, std::string("out must be uint8 or float4_e2m1fn_x2, is ") + c10::toString(codes.scalar_type()));
+        Call::Matrix cm = c.matrix(codes, "out", T, H / 2, codes.scalar_type());
+        if (T <= 1) cm.stride = (cm.stride + 15) / 16 * 16;
+        const at::Tensor scales =
+            a[3] == Py_None
+                ? at::empty({static_cast<int64_t>(lp_head_fp4_scale_bytes(size32(T, "x"), size32(H, "x"), block))}, bytes)
+                : c.tensor(a[3], "out_scales");
+        check_scales(scales, "out_scales", T, H, block);
+        if (block == 32 && a[4] != Py_None) refuse(PyExc_ValueError, "blocks of 32 have no row scales");
+        at::Tensor row;
+        float* row_ptr = c.floats(a[4], "out_row_scale", T);
+        if (block == 16 && !row_ptr) {
+            row = at::empty({T}, x.options().dtype(c10::ScalarType::Float));
+            row_ptr = static_cast<float*>(row.data_ptr());
+        }
+        check(lp_head_quantize4(xm.ptr, dtype_code(x.scalar_type()), size32(T, "x"), size32(H, "x"), xm.stride, block,
+                                cm.ptr, cm.stride, scales.data_ptr(), row_ptr, c.stream()),
+              "lp_head_quantize4");
+        PyObject *r0 = THPVariable_Wrap(codes), *r1 = THPVariable_Wrap(scales), *r2 = a[4];
+        if (row.defined()) r2 = THPVariable_Wrap(row);
+        else Py_INCREF(r2);
+        PyObject* all = PyTuple_Pack(3, r0, r1, r2);
+        Py_DECREF(r0);
+        Py_DECREF(r1);
+        Py_DECREF(r2);
+        return all;
+    });
+}
+
+// (codes, scales, row_scale, block, rows, out, out_dtype, workspace)
+PyObject* dequantize_fp4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 8, [&]() -> PyObject* {
+        const Call c;
+        const uint32_t block = block_of(a[3]);
+        const Fp4 f = fp4_rows(c, a[0], a[1], a[2], block, "codes");
+        int64_t n = f.rows;
+        const uint32_t* rows = nullptr;
+        if (a[4] != Py_None) {
+            rows = c.ints(a[4], "rows", -1);
+            n = THPVariable_Unpack(a[4]).size(0);
+        }
+        const at::Tensor out = c.output(a[5], a[6], c10::ScalarType::BFloat16, n, f.H, THPVariable_Unpack(a[0]));
+        const Call::Matrix om = c.matrix(out, "out", n, f.H, out.scalar_type());
+        const Call::Scratch ws = c.scratch(a[7]);
+        check(lp_head_dequantize4(f.codes.ptr, f.codes.stride, f.scales, f.row_scale, size32(f.rows, "codes"),
+                                  size32(f.H, "codes"), block, rows, size32(n, "rows"), om.ptr, dtype_code(out.scalar_type()),
+                                  om.stride, ws.ptr, ws.bytes, c.stream()),
+              "lp_head_dequantize4");
+        return THPVariable_Wrap(out);
+    });
+}
+
+// (x, x_scales, weight, weight_scales, block, x_row_scale, weight_row_scale, out, out_dtype, workspace)
+PyObject* project_fp4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 10, [&]() -> PyObject* {
+        const Call c;
+        const uint32_t block = block_of(a[4]);
+        const Fp4 x = fp4_rows(c, a[0], a[1], a[5], block, "x"), w = fp4_rows(c, a[2], a[3], a[6], block, "weight");
+        if (x.H != w.H)
+            refuse(PyExc_ValueError, "x has " + std::to_string(x.H) + " elements a row, weight has " + std::to_string(w.H));
+        const at::Tensor out = c.output(a[7], a[8], c10::ScalarType::Float, x.rows, w.rows, THPVariable_Unpack(a[0]));
+        const Call::Matrix om = c.matrix(out, "out", x.rows, w.rows, out.scalar_type());
+        const Call::Scratch ws = c.scratch(a[9]);
+        check(lp_head_project4(x.codes.ptr, x.codes.stride, x.scales, x.row_scale, size32(x.rows, "x"), size32(x.H, "x"), block,
+                               w.codes.ptr, w.codes.stride, w.scales, w.row_scale, size32(w.rows, "weight"), om.ptr,
+                               dtype_code(out.scalar_type()), om.stride, ws.ptr, ws.bytes, c.stream()),
+              "lp_head_project4");
+        return THPVariable_Wrap(out);
+    });
+}
+
 // (workspace,)
 PyObject* clear_status(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return guarded(n_args, 1, [&]() -> PyObject* {
@@ -345,6 +475,9 @@ PyCFunction fast(Fast f) { return reinterpret_cast<PyCFunction>(reinterpret_cast
 PyMethodDef g_methods[] = {{"rms_norm", fast(rms_norm), METH_FASTCALL, nullptr},
                            {"project", fast(project), METH_FASTCALL, nullptr},
                            {"process_logits", fast(process_logits), METH_FASTCALL, nullptr},
+                           {"quantize_fp4", fast(quantize_fp4), METH_FASTCALL, nullptr},
+                           {"dequantize_fp4", fast(dequantize_fp4), METH_FASTCALL, nullptr},
+                           {"project_fp4", fast(project_fp4), METH_FASTCALL, nullptr},
                            {"clear_status", fast(clear_status), METH_FASTCALL, nullptr},
                            {"on_failure", on_failure, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

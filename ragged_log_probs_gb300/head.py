@@ -1,5 +1,6 @@
 """The operators of a served model's head around the ragged log-probability path: final
-norm, vocabulary projection with low-rank adapters, processing of logits.
+norm, vocabulary projection with low-rank adapters or in microscaled 4-bit floating point,
+processing of logits.
 
 Signatures and documentation only. The checks and the call are compiled
 (``csrc/lp_head_binding.cpp``), since these functions run once a token; every operator runs in
@@ -19,7 +20,7 @@ import torch
 from . import _build
 
 __all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "project", "project_cut",
-           "process_logits"]
+           "process_logits", "fp4_scale_bytes", "tile_fp4_scales", "quantize_fp4", "dequantize_fp4", "project_fp4"]
 
 LP_MAX_HIDDEN = 32768
 LP_MAX_RANK = 64
@@ -42,6 +43,14 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
                                     vp, u64, u32, vp, vp, u64, vp, sz, vp]
     lib.lp_head_process.restype = ctypes.c_int
+    lib.lp_head_fp4_scale_bytes.argtypes = [u32, u32, u32]
+    lib.lp_head_fp4_scale_bytes.restype = sz
+    lib.lp_head_quantize4.argtypes = [vp, u32, u32, u32, u64, u32, vp, u64, vp, vp, vp]
+    lib.lp_head_quantize4.restype = ctypes.c_int
+    lib.lp_head_dequantize4.argtypes = [vp, u64, vp, vp, u32, u32, u32, vp, u32, vp, u32, u64, vp, sz, vp]
+    lib.lp_head_dequantize4.restype = ctypes.c_int
+    lib.lp_head_project4.argtypes = [vp, u64, vp, vp, u32, u32, u32, vp, u64, vp, vp, u32, vp, u32, u64, vp, sz, vp]
+    lib.lp_head_project4.restype = ctypes.c_int
     lib.lp_head_process_workspace_size.argtypes = [u32, u32]
     lib.lp_head_process_workspace_size.restype = sz
 
@@ -180,3 +189,69 @@ def process_logits(logits: torch.Tensor, row_offsets: Optional[torch.Tensor] = N
                                          out, workspace)
     return native.process_logits(logits, row_offsets, history, history_offsets, prompt_lens, repetition, frequency,
                                  presence, bias_tokens, bias_values, bias_offsets, mask, mask_index, out, workspace)
+
+
+def fp4_scale_bytes(rows: int, H: int, block: int = 16) -> int:
+    """Bytes of the block scales of ``rows`` 4-bit rows of ``H`` elements, in their tiles."""
+    if block not in (16, 32):
+        raise ValueError(f"block must be 16 or 32, is {block}")
+    return int(_pkg().load().lp_head_fp4_scale_bytes(rows, H, block))
+
+
+def tile_fp4_scales(scales: torch.Tensor) -> torch.Tensor:
+    """Block scales [rows, blocks] (uint8, float8_e4m3fn or float8_e8m0fnu, on any device) laid out in
+    tiles of 128 rows by 4 blocks, as the functions below take them; for weights that were
+    quantised elsewhere. Done once: a copy of torch's."""
+    if scales.dim() != 2 or scales.element_size() != 1:
+        raise ValueError("scales must be [rows, blocks] of 8-bit elements")
+    rows, n = scales.shape
+    rb, cb = -(-rows // 128), -(-n // 4)
+    full = torch.zeros(rb * 128, cb * 4, dtype=torch.uint8, device=scales.device)
+    full[:rows, :n] = scales.view(torch.uint8)
+    return full.view(rb, 4, 32, cb, 4).permute(0, 3, 2, 1, 4).reshape(-1)
+
+
+def quantize_fp4(x: torch.Tensor, block: int = 16, out: Optional[torch.Tensor] = None,
+                 out_scales: Optional[torch.Tensor] = None, out_row_scale: Optional[torch.Tensor] = None, stream=None):
+    """Rows of ``x`` [T, H] (float32, bfloat16, float16; H a multiple of 32) in 4 bits, with a scale
+    for every block of 16 elements (float8_e4m3fn, and a power of two a row) or of 32 (float8_e8m0fnu).
+
+    Returns ``(codes, scales, row_scale)``: uint8 [T, H / 2], two codes to a byte, the first in the
+    low half; the scales' bytes in tiles (``fp4_scale_bytes`` of them); float32 [T], or None for
+    blocks of 32."""
+    native = _native or _load()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return native.quantize_fp4(x, block, out, out_scales, out_row_scale)
+    return native.quantize_fp4(x, block, out, out_scales, out_row_scale)
+
+
+def dequantize_fp4(codes: torch.Tensor, scales: torch.Tensor, row_scale: Optional[torch.Tensor] = None,
+                   block: int = 16, rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                   out_dtype: Optional[torch.dtype] = None, workspace: Optional[torch.Tensor] = None,
+                   stream=None) -> torch.Tensor:
+    """Values of 4-bit rows (as ``quantize_fp4`` returns them): of all, or of those that ``rows`` [n]
+    names, such as the tokens to look up in a 4-bit embedding. ``out`` is float32, bfloat16 (by
+    default) or float16. With ``rows`` a workspace is needed: a row past the last sets
+    LP_ERR_OFFSETS in its status and gives NaN."""
+    native = _native or _load()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return native.dequantize_fp4(codes, scales, row_scale, block, rows, out, out_dtype, workspace)
+    return native.dequantize_fp4(codes, scales, row_scale, block, rows, out, out_dtype, workspace)
+
+
+def project_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.Tensor, weight_scales: torch.Tensor,
+                block: int = 16, x_row_scale: Optional[torch.Tensor] = None,
+                weight_row_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                out_dtype: Optional[torch.dtype] = None, *, workspace: torch.Tensor, stream=None) -> torch.Tensor:
+    """Logits [T, V] of 4-bit hidden states ``x`` [T, H / 2] and a 4-bit ``weight`` [V, H / 2], both with
+    scales as ``quantize_fp4`` returns them (row scales: None means 1). Returns ``out`` (new by
+    default, of ``out_dtype``, float32 by default). ``workspace``: see ``new_head_workspace``."""
+    native = _native or _load()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return native.project_fp4(x, x_scales, weight, weight_scales, block, x_row_scale, weight_row_scale, out,
+                                      out_dtype, workspace)
+    return native.project_fp4(x, x_scales, weight, weight_scales, block, x_row_scale, weight_row_scale, out, out_dtype,
+                              workspace)
