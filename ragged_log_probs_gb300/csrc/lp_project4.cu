@@ -41,7 +41,6 @@ struct Project4Params {
     uint32_t tile_t, tiles_t, tiles, slices, stages;
     uint32_t chunk;        // slices summed in the accumulator
     uint32_t col_tiles;    // tiles of scales in a row of them
-    uint32_t x_blocks;     // blocks of 128 rows of x in a tile: 1 or 2
     uint32_t acc_shift;    // log2 of the number of accumulators
     uint32_t idesc;        // without N and the scales' places
 };
@@ -73,16 +72,23 @@ __device__ __forceinline__ void mma4(uint32_t tmem, uint64_t a, uint64_t b, uint
 #undef LPH_MMA4
 }
 
+__device__ __forceinline__ bool elect_one() {  // the same lane of a whole warp every time
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 template <int BLOCK, typename OUT, int CG>
 __global__ void __launch_bounds__(kThreads, 1)
 k_project4(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
            const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs, const Project4Params p) {
     // tiles of scales in a slice: 4 blocks of 16 or 32 elements each
     constexpr uint32_t kTiles = kSlice / (4 * BLOCK), kScaleBytes = kTiles * 512;
+    constexpr uint32_t kXBlocks = CG;  // blocks of 128 rows of x in a tile
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t stage_x = p.tile_t / CG * kSliceBytes;
-    const uint32_t stage_bytes = kStageW + stage_x + (1 + p.x_blocks) * kScaleBytes;
+    const uint32_t stage_bytes = kStageW + stage_x + (1 + kXBlocks) * kScaleBytes;
     unsigned char* ring = smem_raw + (base - smem_u32(smem_raw));
     uint64_t* bars = reinterpret_cast<uint64_t*>(ring + p.stages * stage_bytes);
     volatile uint32_t* s_abort = reinterpret_cast<uint32_t*>(bars + kBarriers);
@@ -133,43 +139,51 @@ k_project4(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
 
     uint32_t issued = 0;  // stages the producer has started copies into
     if (warp == kCopyWarp) {
-        if (lane == 0) {
-            pdl_wait();
-            uint64_t once, keep;  // W is read once per row of tiles, x by every tile
-            asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-            asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
-            const uint64_t w_policy = p.tiles_t == 1 ? once : keep;
-            const uint32_t w_blocks = (p.V + 127) / 128, all_x_blocks = (p.T + 127) / 128;
-            uint32_t s = 0, phase = 0;
-            bool ok = true;
-            for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
-                const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
-                const uint32_t block = tv * CG + rank, n = rows_of(tt);
-                const int v0 = (int)(block * kTileV), t0 = (int)(tt * p.tile_t + rank * (n / CG));
-                // (scales of blocks of 128 rows past the last: any, their products are not stored)
-                const uint32_t ws_row = min(block, w_blocks - 1) * p.col_tiles;
-                for (uint32_t k = 0; k < p.slices; ++k) {
-                    if (!mbar_wait(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
+        pdl_wait();
+        uint64_t once, keep;  // W is read once per row of tiles, x by every tile
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+        const uint64_t w_policy = p.tiles_t == 1 ? once : keep;
+        const uint32_t w_blocks = (p.V + 127) / 128, all_x_blocks = (p.T + 127) / 128;
+        const bool elected = elect_one();
+        uint32_t s = 0, phase = 0;
+        bool ok = true;
+        for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
+            const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t;
+            const uint32_t block = tv * CG + rank, n = rows_of(tt);
+            const int v0 = (int)(block * kTileV), t0 = (int)(tt * p.tile_t + rank * (n / CG));
+            // (scales of blocks of 128 rows past the last: any, their products are not stored)
+            const uint32_t ws_row = min(block, w_blocks - 1) * p.col_tiles;
+            uint32_t xs_row[kXBlocks];
+#pragma unroll
+            for (uint32_t j = 0; j < kXBlocks; ++j) xs_row[j] = min(tt * kXBlocks + j, all_x_blocks - 1) * p.col_tiles;
+            for (uint32_t k = 0; k < p.slices; ++k) {
+                if (!mbar_wait_warp(empty0 + 8 * s, phase ^ 1, s_abort)) { ok = false; break; }
+                if (elected) {
                     const uint32_t dst = base + s * stage_bytes;
                     const uint32_t bar = CG == 2 ? map_to(full0 + 8 * s, 0) : full0 + 8 * s;
                     if (rank == 0) mbar_expect(full0 + 8 * s, CG * stage_bytes);
                     tma_2d<CG>(dst, &map_w, (int)(k * kSliceBytes), v0, bar, w_policy);
-                    tma_2d<CG>(dst + kStageW, &map_x, (int)(k * kSliceBytes), t0, bar, keep);
                     tma_2d<CG>(dst + kStageW + stage_x, &map_ws, 0, (int)(ws_row + k * kTiles), bar, w_policy);
-                    for (uint32_t j = 0; j < p.x_blocks; ++j) {
-                        const uint32_t xb = min(tt * p.x_blocks + j, all_x_blocks - 1);
+                    tma_2d<CG>(dst + kStageW, &map_x, (int)(k * kSliceBytes), t0, bar, keep);
+#pragma unroll
+                    for (uint32_t j = 0; j < kXBlocks; ++j)
                         tma_2d<CG>(dst + kStageW + stage_x + (1 + j) * kScaleBytes, &map_xs, 0,
-                                   (int)(xb * p.col_tiles + k * kTiles), bar, keep);
-                    }
-                    ++issued;
-                    if (++s == p.stages) { s = 0; phase ^= 1; }
+                                   (int)(xs_row[j] + k * kTiles), bar, keep);
                 }
+                __syncwarp();
+                ++issued;
+                if (++s == p.stages) { s = 0; phase ^= 1; }
             }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0 && rank == 0) {
+        // The whole warp walks the tiles, so that what the instructions take is known to be the same
+        // for its lanes, and an elected one issues them: 8 clocks a copy of scales, against 50 to 180
+        // from a branch of lane 0 (48 rows on V = 152064: 116 us so).
+        if (rank == 0) {
             pdl_wait();  // (the bounded waits below are for this kernel's own work only)
-            const uint32_t slot = kTiles * 4 * (1 + p.x_blocks);  // columns of a stage's scales
+            constexpr uint32_t kSlot = kTiles * 4 * (1 + kXBlocks);  // columns of a stage's scales
+            const bool elected = elect_one();
             uint32_t s = 0, phase = 0, n = 0;
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
@@ -177,38 +191,43 @@ k_project4(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
                 for (uint32_t k0 = 0, k1; ok && k0 < p.slices; k0 = k1) {
                     const uint32_t acc = acc_of(n), d = tmem + acc * (kMaxTileT / 2);
                     k1 = chunk_end(k0);
-                    if (!mbar_wait(acc_empty0 + 8 * acc, acc_phase(n) ^ 1, s_abort)) { ok = false; break; }
+                    if (!mbar_wait_warp(acc_empty0 + 8 * acc, acc_phase(n) ^ 1, s_abort)) { ok = false; break; }
                     fence_after();
                     for (uint32_t k = k0; k < k1; ++k) {
-                        if (!mbar_wait(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
+                        if (!mbar_wait_warp(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
                         fence_after();
                         const uint32_t at = base + s * stage_bytes, scales = at + kStageW + stage_x;
-                        const uint64_t a = matrix_desc(at), b = matrix_desc(at + kStageW);
-                        const uint32_t sa = tmem + kScaleColumns + s * slot, sb = sa + kTiles * 4;
+                        const uint64_t a = matrix_desc(at), b = matrix_desc(at + kStageW), c = scale_desc(scales);
+                        const uint32_t sa = tmem + kScaleColumns + s * kSlot, sb = sa + kTiles * 4;
                         const uint32_t steps = min(4u, (p.H - k * kSlice + 63) / 64);  // of 64 elements
+                        if (elected) {
 #pragma unroll
-                        for (uint32_t j = 0; j < kTiles; ++j) {
-                            copy_scales<CG>(sa + 4 * j, scale_desc(scales + j * 512));
-                            for (uint32_t q = 0; q < p.x_blocks; ++q)
-                                copy_scales<CG>(sb + 4 * (p.x_blocks * j + q), scale_desc(scales + (1 + q) * kScaleBytes + j * 512));
-                        }
+                            for (uint32_t j = 0; j < kTiles; ++j) {
+                                copy_scales<CG>(sa + 4 * j, c + j * (512 >> 4));
 #pragma unroll
-                        for (uint32_t i = 0; i < 4; ++i) {
-                            if (i >= steps) break;
-                            // blocks of 32: a tile's columns hold the scales of two steps
-                            const uint32_t j = BLOCK == 16 ? i : i / 2, id = BLOCK == 16 ? 0 : (i & 1) * 2;
-                            mma4<BLOCK, CG>(d, a + 2 * i, b + 2 * i, idesc | id << 4 | id << 29, sa + 4 * j,
-                                            sb + 4 * p.x_blocks * j, (k - k0) | i);
+                                for (uint32_t q = 0; q < kXBlocks; ++q)
+                                    copy_scales<CG>(sb + 4 * (kXBlocks * j + q), c + ((1 + q) * kScaleBytes + j * 512 >> 4));
+                            }
+#pragma unroll
+                            for (uint32_t i = 0; i < 4; ++i) {
+                                // blocks of 32: a tile's columns hold the scales of two steps
+                                const uint32_t j = BLOCK == 16 ? i : i / 2, id = BLOCK == 16 ? 0 : (i & 1) * 2;
+                                if (i < steps)
+                                    mma4<BLOCK, CG>(d, a + 2 * i, b + 2 * i, idesc | id << 4 | id << 29, sa + 4 * j,
+                                                    sb + 4 * kXBlocks * j, (k - k0) | i);
+                            }
+                            mma_commit<CG>(empty0 + 8 * s);
                         }
-                        mma_commit<CG>(empty0 + 8 * s);
+                        __syncwarp();
                         if (++s == p.stages) { s = 0; phase ^= 1; }
                     }
                     if (!ok) break;
-                    mma_commit<CG>(acc_full0 + 8 * acc);
+                    if (elected) mma_commit<CG>(acc_full0 + 8 * acc);
                     ++n;
                 }
             }
-            mma_commit<CG>(drain);  // arrives once every product issued above has finished
+            if (elected) mma_commit<CG>(drain);  // arrives once every product issued above has finished
+            __syncwarp();
         }
     } else {
         // The quadrant of lanes this warp may read, and its share of the columns: the blocks
@@ -375,13 +394,12 @@ extern "C" lp_status lp_head_project4(const void* x, uint64_t x_stride, const vo
     const uint32_t cg = T > 128 ? 2 : 1, unit = 16 * cg;
     p.tile_t = T > kMaxTileT ? kMaxTileT : (T + unit - 1) / unit * unit;  // (several tiles: whole blocks of 128 rows)
     p.tiles_t = (T + p.tile_t - 1) / p.tile_t;
-    p.x_blocks = (p.tile_t + 127) / 128;
     const uint64_t tiles = (uint64_t)((V + cg * kTileV - 1) / (cg * kTileV)) * p.tiles_t;
     if (tiles > 0x7FFFFFFFu) return LP_ERR_SHAPE;
     p.tiles = (uint32_t)tiles;
     p.acc_shift = p.tile_t <= kMaxTileT / 2;
-    const uint32_t scale_bytes = kSlice / block * 128, columns = scale_bytes / 128 * (1 + p.x_blocks);
-    const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes + (1 + p.x_blocks) * scale_bytes;
+    const uint32_t scale_bytes = kSlice / block * 128, columns = scale_bytes / 128 * (1 + cg);
+    const uint32_t stage_bytes = kStageW + p.tile_t / cg * kSliceBytes + (1 + cg) * scale_bytes;
     p.stages = (kSmemBudget - kControlBytes) / stage_bytes;
     if (p.stages > kMaxStages) p.stages = kMaxStages;
     if (p.stages > (kColumns - kScaleColumns) / columns) p.stages = (kColumns - kScaleColumns) / columns;
