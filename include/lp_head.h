@@ -37,6 +37,7 @@ typedef enum lp_dtype {
 #define LP_MIN_REPETITION 9.5367432e-07f /* 2^-20 */
 #define LP_MAX_REPETITION 1048576.0f     /* 2^20 */
 #define LP_MAX_RANK 64u      /* largest adapter rank of lp_head_project */
+#define LP_MAX_SAMPLE_VOCAB 393216u /* longest row of lp_head_sample */
 
 /*
  * Bytes of scratch the calls below need: a 256-byte header with the status word, and for
@@ -223,6 +224,39 @@ lp_status lp_head_project4(const void *x, uint64_t x_stride, const void *x_scale
                            const void *weight_scales, const float *weight_row_scale, uint32_t V, void *out,
                            uint32_t out_dtype, uint64_t out_stride, void *workspace, size_t workspace_bytes,
                            lp_stream_t stream);
+
+/*
+ * Draw of a token for every logits row, from a given random number. With m the row's largest logit,
+ * tau, k, p and q its request's temperature, top-k, top-p and min-p, and the tokens ranked by
+ * (logit descending, id ascending):
+ *     w    = exp((x - m) / tau), or 0 where (x - m) / tau < -40 ln 2
+ *     top-k  the first k tokens stay                                    (k <= 0 or >= V: all)
+ *     top-p  of these, a token stays while the weights ranked before it add up to less than p times
+ *            those of all k; the first one always does                  (p = 1: all)
+ *     min-p  of these, those with (x - m) / tau >= ln q                 (q = 0: all)
+ *     out[t] = the first id at which the kept weights, added up in the order of the ids, exceed
+ *            uniform[t] times their sum
+ *     out_logprob[t] = ln(w / sum of the kept weights) of that token
+ * tau = 0 takes the first ranked token (k = 1). Weights have about 40 bits and sums more, so that
+ * the token is that of the formula in 64 bits but for a random number within about 2^-38 of the
+ * border between two tokens (temperatures from 2^-100 to 2^100; a difference x - m past f32's
+ * range counts as -inf).
+ *   logits          device, [T][V] of dtype (LP_F32, LP_BF16, LP_F16), V <= LP_MAX_SAMPLE_VOCAB
+ *   uniform         device, float[T], in [0, 1)
+ *   row_offsets, B  rows of the requests, as in lp_head_process
+ *   temperature, top_k, top_p, min_p   device, float[B], int32[B], float[B], float[B], or NULL (1, 0, 1, 0)
+ *   out             device out, uint32[T]
+ *   out_logprob     device out, float[T], or NULL
+ *   workspace       256 bytes: the status word
+ * Device checks: every row in a request (LP_ERR_OFFSETS), temperatures finite and not negative
+ * (LP_ERR_TEMPERATURE), top_p and min_p within 0..1 and uniform in [0, 1) (LP_ERR_SAMPLING), the
+ * row's largest logit finite (LP_ERR_LOGITS: a row of only -inf, or with a NaN or +inf): such a
+ * row's token is LP_PAD_TOKEN, its logprob NaN.
+ */
+lp_status lp_head_sample(const void *logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
+                         const float *uniform, const uint32_t *row_offsets, uint32_t B, const float *temperature,
+                         const int32_t *top_k, const float *top_p, const float *min_p, uint32_t *out,
+                         float *out_logprob, void *workspace, size_t workspace_bytes, lp_stream_t stream);
 
 #ifdef __cplusplus
 }

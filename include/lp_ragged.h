@@ -62,7 +62,10 @@ typedef enum lp_status {
     LP_ERR_ADAPTER = 10,     /* device: an adapter id past the adapters                     */
     LP_ERR_PENALTY = 11,     /* device: a repetition penalty out of range, or another
                                 penalty that is not finite                                  */
-    LP_ERR_TIMEOUT = 12      /* device: a bounded wait inside a kernel ran out              */
+    LP_ERR_TIMEOUT = 12,     /* device: a bounded wait inside a kernel ran out              */
+    LP_ERR_SAMPLING = 13,    /* device: a top-p, a min-p or a random number out of range    */
+    LP_ERR_LOGITS = 14       /* device: a row whose largest logit is not finite: no token
+                                is allowed, or one is NaN or +inf                           */
 } lp_status;
 
 #define LP_MAX_LEVELS 6u

@@ -21,7 +21,7 @@ from . import _build
 from . import head as _head
 from .head import (clear_status, dequantize_fp4, fp4_scale_bytes, head_workspace_size,  # noqa: F401
                    new_head_workspace, process_logits, project, project_fp4, quantize_fp4, tile_fp4_scales,
-                   project_cut, rms_norm)
+                   project_cut, rms_norm, sample)
 from .results import LogProbabilities, assemble  # noqa: F401  (host-side result assembly)
 
 __all__ = [
@@ -37,6 +37,7 @@ STATUS_NAMES = {
     0: "LP_OK", 1: "LP_ERR_NULL", 2: "LP_ERR_LEVELS", 3: "LP_ERR_SHAPE", 4: "LP_ERR_OFFSETS",
     5: "LP_ERR_TOKEN_RANGE", 6: "LP_ERR_WORKSPACE", 7: "LP_ERR_CUDA", 8: "LP_ERR_TEMPERATURE",
     9: "LP_ERR_DTYPE", 10: "LP_ERR_ADAPTER", 11: "LP_ERR_PENALTY", 12: "LP_ERR_TIMEOUT",
+    13: "LP_ERR_SAMPLING", 14: "LP_ERR_LOGITS",
 }
 EXPORTS = ("lp_ragged_workspace_size", "lp_ragged_plan", "lp_ragged_compute", "lp_ragged_compute_ex",
            "lp_ragged_step", "lp_ragged_tuple_bytes", "lp_ragged_shard_partials", "lp_ragged_shard_merge",

@@ -20,7 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_NAME = "liblp_ragged.so"
 SOURCES = ["lp_ragged.cu", "lp_norm.cu", "lp_process.cu", "lp_project.cu", "lp_adapters.cu", "lp_fp4.cu",
-           "lp_project4.cu"]
+           "lp_project4.cu", "lp_sample.cu"]
 HEADERS = ["lp_device.cuh", "lp_kernels.cuh", "lp_head_common.h", "lp_tcgen05.h", "lp_adapters.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

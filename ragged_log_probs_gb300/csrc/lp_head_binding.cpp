@@ -452,6 +452,38 @@ PyObject* project_fp4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     });
 }
 
+// (logits, uniform, row_offsets, temperature, top_k, top_p, min_p, out, out_logprob, workspace)
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+    return guarded(n_args, 10, [&]() -> PyObject* {
+        const Call c;
+        const at::Tensor& x = c.two_dims(a[0], "logits");
+        const int64_t T = x.size(0), V = x.size(1);
+        const Call::Matrix xm = c.matrix(x, "logits", T, V, x.scalar_type());
+        int64_t B = T;
+        const uint32_t* offsets = nullptr;
+        if (a[2] != Py_None) {
+            offsets = c.ints(a[2], "row_offsets", -1);
+            B = THPVariable_Unpack(a[2]).size(0) - 1;
+            if (B < 0) refuse(PyExc_ValueError, "row_offsets must have an element more than there are requests");
+        }
+        const float* uniform = c.floats(a[1], "uniform", T);
+        const int32_t* top_k = nullptr;
+        if (a[4] != Py_None)
+            top_k = static_cast<const int32_t*>(
+                c.vector(a[4], "top_k", B, c10::ScalarType::Int, c10::ScalarType::Int).data_ptr());
+        at::Tensor out;
+        if (a[7] == Py_None) out = at::empty({T}, x.options().dtype(c10::ScalarType::Int));
+        else out = c.vector(a[7], "out", T, c10::ScalarType::Int, c10::ScalarType::UInt32);
+        const Call::Scratch ws = c.scratch(a[9]);
+        check(lp_head_sample(xm.ptr, dtype_code(x.scalar_type()), size32(T, "logits"), size32(V, "logits"), xm.stride, uniform,
+                             offsets, size32(B, "row_offsets"), c.floats(a[3], "temperature", B), top_k,
+                             c.floats(a[5], "top_p", B), c.floats(a[6], "min_p", B), static_cast<uint32_t*>(out.data_ptr()),
+                             c.floats(a[8], "out_logprob", T), ws.ptr, ws.bytes, c.stream()),
+              "lp_head_sample");
+        return THPVariable_Wrap(out);
+    });
+}
+
 // (workspace,)
 PyObject* clear_status(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return guarded(n_args, 1, [&]() -> PyObject* {
@@ -478,6 +510,7 @@ PyMethodDef g_methods[] = {{"rms_norm", fast(rms_norm), METH_FASTCALL, nullptr},
                            {"quantize_fp4", fast(quantize_fp4), METH_FASTCALL, nullptr},
                            {"dequantize_fp4", fast(dequantize_fp4), METH_FASTCALL, nullptr},
                            {"project_fp4", fast(project_fp4), METH_FASTCALL, nullptr},
+                           {"sample", fast(sample), METH_FASTCALL, nullptr},
                            {"clear_status", fast(clear_status), METH_FASTCALL, nullptr},
                            {"on_failure", on_failure, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};

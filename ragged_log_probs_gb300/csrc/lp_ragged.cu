@@ -533,6 +533,8 @@ const char* lp_ragged_strerror(lp_status status) {
         case LP_ERR_ADAPTER: return "an adapter id is not below the number of adapters";
         case LP_ERR_PENALTY: return "a repetition penalty is out of range, or another penalty is not finite";
         case LP_ERR_TIMEOUT: return "a bounded wait inside a kernel ran out";
+        case LP_ERR_SAMPLING: return "a top-p, a min-p or a random number out of range";
+        case LP_ERR_LOGITS: return "a row of logits whose largest value is not finite";
         default: return "unknown lp_status";
     }
 }

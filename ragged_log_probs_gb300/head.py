@@ -1,6 +1,6 @@
 """The operators of a served model's head around the ragged log-probability path: final
 norm, vocabulary projection with low-rank adapters or in microscaled 4-bit floating point,
-processing of logits.
+processing of logits, draw of the next token.
 
 Signatures and documentation only. The checks and the call are compiled
 (``csrc/lp_head_binding.cpp``), since these functions run once a token; every operator runs in
@@ -20,7 +20,8 @@ import torch
 from . import _build
 
 __all__ = ["head_workspace_size", "new_head_workspace", "clear_status", "rms_norm", "project", "project_cut",
-           "process_logits", "fp4_scale_bytes", "tile_fp4_scales", "quantize_fp4", "dequantize_fp4", "project_fp4"]
+           "process_logits", "fp4_scale_bytes", "tile_fp4_scales", "quantize_fp4", "dequantize_fp4", "project_fp4",
+           "sample"]
 
 LP_MAX_HIDDEN = 32768
 LP_MAX_RANK = 64
@@ -43,6 +44,8 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
                                     vp, u64, u32, vp, vp, u64, vp, sz, vp]
     lib.lp_head_process.restype = ctypes.c_int
+    lib.lp_head_sample.argtypes = [vp, u32, u32, u32, u64, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.lp_head_sample.restype = ctypes.c_int
     lib.lp_head_fp4_scale_bytes.argtypes = [u32, u32, u32]
     lib.lp_head_fp4_scale_bytes.restype = sz
     lib.lp_head_quantize4.argtypes = [vp, u32, u32, u32, u64, u32, vp, u64, vp, vp, vp]
@@ -255,3 +258,26 @@ def project_fp4(x: torch.Tensor, x_scales: torch.Tensor, weight: torch.Tensor, w
                                       out_dtype, workspace)
     return native.project_fp4(x, x_scales, weight, weight_scales, block, x_row_scale, weight_row_scale, out, out_dtype,
                               workspace)
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, row_offsets: Optional[torch.Tensor] = None,
+           temperature: Optional[torch.Tensor] = None, top_k: Optional[torch.Tensor] = None,
+           top_p: Optional[torch.Tensor] = None, min_p: Optional[torch.Tensor] = None,
+           out: Optional[torch.Tensor] = None, out_logprob: Optional[torch.Tensor] = None, *, workspace: torch.Tensor,
+           stream=None) -> torch.Tensor:
+    """A token for every row of ``logits`` [T, V] (float32, bfloat16, float16), drawn with the random
+    number ``uniform`` [T] (float32, in [0, 1)) from what the row's request leaves of the
+    distribution; returns ``out`` (int32 [T], new by default).
+
+    ``temperature``, ``top_p``, ``min_p`` (float32) and ``top_k`` (int32) are [B], ``row_offsets`` [B+1]
+    gives each request's rows (default: one row a request). Temperature 0 takes the best token;
+    ``top_k`` 0, ``top_p`` 1 and ``min_p`` 0 (the defaults) leave all. The order: the best ``top_k``
+    tokens; of these the fewest that hold ``top_p`` of their probability; of these those with at
+    least ``min_p`` of the best one's. ``out_logprob`` (float32 [T]) receives the token's logprob in
+    what was left. A row without a distribution (nothing but -inf, or a NaN or +inf) gives
+    -1 and NaN and sets LP_ERR_LOGITS; ``read_status`` reads the workspace's bits."""
+    native = _native or _load()
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return native.sample(logits, uniform, row_offsets, temperature, top_k, top_p, min_p, out, out_logprob, workspace)
+    return native.sample(logits, uniform, row_offsets, temperature, top_k, top_p, min_p, out, out_logprob, workspace)
