@@ -237,9 +237,9 @@ lp_status lp_head_project4(const void *x, uint64_t x_stride, const void *x_scale
  *     out[t] = the first id at which the kept weights, added up in the order of the ids, exceed
  *            uniform[t] times their sum
  *     out_logprob[t] = ln(w / sum of the kept weights) of that token
- * tau = 0 takes the first ranked token (k = 1). Weights have about 40 bits and sums more, so that
- * the token is that of the formula in 64 bits but for a random number within about 2^-38 of the
- * border between two tokens. A tau below 2^-100 or above 2^100 is taken as that.
+ * tau = 0 takes the first ranked token (k = 1). Weights and their sums are within 2^-32 of the
+ * formula's, so that the token is that of the formula in 64 bits unless one of the comparisons
+ * above is nearer than 2^-31 to turning over. A tau below 2^-100 or above 2^100 is taken as that.
  *   logits          device, [T][V] of dtype (LP_F32, LP_BF16, LP_F16), V <= LP_MAX_SAMPLE_VOCAB
  *   uniform         device, float[T], in [0, 1)
  *   row_offsets, B  rows of the requests, as in lp_head_process

@@ -2,8 +2,8 @@
 // random number a row.
 //
 // A row belongs to a cluster of up to eight CTAs, each with a slice of it in shared memory, read
-// from HBM once. Weights exp((x - max) / tau) are formed with about 40 correct bits (a table of 64
-// powers and a short series, in pairs of f32, two tokens to an instruction) and added as pairs or as
+// from HBM once. Weights exp((x - max) / tau) are formed with about 34 correct bits (a table of 256
+// powers, and a short series for what is left of the exponent) and added as pairs of f32 or as
 // integers of 2^-43: the token is a comparison of sums of up to some hundred thousand weights with
 // each other, and f32's rounding would move it in a few rows of a hundred. All three filters keep a
 // prefix of the order (value descending, id ascending), so that what is kept is told by the last
@@ -11,9 +11,10 @@
 //   top-k: each CTA tells a value that enough of its threads' largest reach (a coarse histogram);
 //          what lies above the least of these is listed and ranked by the cluster's first CTA.
 //   top-p: what weighs less than (1 - p) Z / V is never kept. Where Z is small the rest is listed
-//          as well; else, or if it does not fit, a histogram over the values' bits finds the bin
-//          in which p Z is reached, and that bin is listed. A bin of more than fits is cut again;
-//          one that holds a single value is cut by id.
+//          as well. Else, or if it does not fit, a histogram over the values' bits with rounded
+//          weights finds the bins in which p Z can be reached; what lies above them is summed
+//          exactly, what lies in them is listed. Bins of more than fits are cut again; a single
+//          value is cut by id.
 // The draw follows the ids: the kept weights are summed by warp, and the CTA in which u Z falls
 // walks that warp's part once more. CTAs write what the others need into their shared memory
 // before a barrier of the cluster.
@@ -29,17 +30,17 @@ namespace cg = cooperative_groups;
 constexpr uint32_t kThreads = 384, kWarps = kThreads / 32;
 constexpr uint32_t kResident = 3;  // CTAs per SM, with slices of up to 16384 f32
 constexpr uint32_t kMaxCluster = 8;
-constexpr uint32_t kList = 512;    // tokens that are ranked
-constexpr uint32_t kBins = kThreads;
+constexpr uint32_t kList = kThreads;  // tokens that are ranked
+constexpr uint32_t kBins = 2 * kThreads;
 constexpr uint32_t kBound = 256;
-constexpr uint32_t kTable = 64;
+constexpr uint32_t kTable = 256;
 constexpr uint32_t kLowest = 0x00800000u;  // ordered() of the lowest finite value
 constexpr uint32_t kAll = 0xFFFFFFFFu;
-constexpr int kPoint = 43;           // weights as integers: 2^43 is that of the largest
-constexpr float kUnit = 8796093022208.f, kInvUnit = 1.1368683772161603e-13f;  // 2^43, 2^-43
-constexpr float kSmallest = 40.f;    // -log2 of the smallest weight that counts
+constexpr float kUnit = 8796093022208.f;  // 2^43: weights as integers, the largest one is about that
 constexpr float kFewWeights = 8.f;   // Z up to which a top-p row's tokens are listed at once
-constexpr uint32_t kCount = 384;     // tokens up to which ranks are counted, and not sorted
+// Rounded weights of a histogram: all of them make 2^30; what the roundings can add up to.
+constexpr uint32_t kWhole = 1u << 30, kMargin = 1u << 18;
+static_assert(LP_MAX_SAMPLE_VOCAB / 2 + (kWhole >> 16) < kMargin, "half a unit a token, and the weights' f32 errors");
 
 struct SampleParams {
     const void* logits;
@@ -86,9 +87,9 @@ struct Setting {
 
 struct Cut {
     uint32_t key, id;      // kept: a larger key, or this one with an id up to this
-    uint32_t again;        // the search goes on among keys above `above`, for the weight `target`
+    uint32_t again;        // the search goes on among keys above `above`, for the weight `target` of `total`
     uint32_t above;
-    uint64_t target;
+    uint64_t target, total;
 };
 
 struct Told {              // by each CTA
@@ -96,129 +97,88 @@ struct Told {              // by each CTA
     uint32_t share, whole; // keys that ceil(k / CTAs), and k, of its threads' largest reach
 };
 
+struct Draw {              // where the token is
+    uint64_t start, z;     // the kept weights before the warp that has it, and all
+    uint32_t warp;
+};
+
 struct Shared {
     union {
-        uint64_t list[kList];    // key << 32 | ~id
+        uint64_t list[kList];    // key << 32 | ~id; the ranked tokens' weights
         uint32_t bound[kBound];  // (before the list)
     };
     union {
         struct {
-            uint32_t count[kBins], low[kBins], high[kBins];
+            uint32_t weight[kBins];
+            uint32_t count[kBins / 2];  // 16 bits each
         };
-        uint64_t stage[kList + kList / 2];  // a CTA's part of the list; the ranked list, and its keys
+        uint64_t stage[kList];   // a CTA's part of the list; the ranked list
     };
     float2 table[kTable];
     uint64_t scan[kWarps];
     uint64_t warp_sum[kMaxCluster * kWarps];
     uint64_t cta_sum[kMaxCluster];
-    uint64_t words[4];
     Told told[kMaxCluster];
     Setting set;
     Cut cut;
+    Draw draw;
     uint32_t listed, staged, place;
-    uint32_t found_bin, found_count, found_before_count;
-    uint64_t found_before, found_weight;
+    uint32_t first_bin, last_bin, in_bins, in_weight;
 };
 
-// 2^(j / 64) as pairs of f32, at compile time: by repeated products of 2^(1 / 64), whose digits a
-// series of the exponential gives.
+// 2^(j / 256) as pairs of f32, at compile time, by the exponential's series.
 struct Table {
-    float hi[kTable], lo[kTable];
+    float2 at[kTable];
 };
 constexpr Table make_table() {
     Table t = {};
     for (uint32_t j = 0; j < kTable; ++j) {
         const double y = 0.6931471805599453094 * j / kTable;
-        double term = 1.0, sum = 0.0;
-        for (int n = 30; n > 0; --n) {  // smallest terms first
-            term = 1.0;
-            for (int k = 1; k <= n; ++k) term *= y / k;
-            sum += term;
-        }
-        sum += 1.0;
-        t.hi[j] = (float)sum;
-        t.lo[j] = (float)(sum - (double)(float)sum);
+        double sum = 1.0;
+        for (int n = 24; n > 0; --n) sum = 1.0 + sum * y / n;
+        t.at[j].x = (float)sum;
+        t.at[j].y = (float)(sum - (double)(float)sum);
     }
     return t;
 }
-__constant__ Table c_table = make_table();
-
-// Two f32 at a time.
-using f2 = uint64_t;
-__device__ __forceinline__ f2 both(float a, float b) { return (f2)__float_as_uint(a) | (f2)__float_as_uint(b) << 32; }
-__device__ __forceinline__ f2 both(float a) { return both(a, a); }
-__device__ __forceinline__ float first(f2 a) { return __uint_as_float((uint32_t)a); }
-__device__ __forceinline__ float second(f2 a) { return __uint_as_float((uint32_t)(a >> 32)); }
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f2 sub2(f2 a, f2 b) { return fma2(b, both(-1.f), a); }
+__device__ const Table g_table = make_table();
 
 struct Scale {             // of a row
     float m, low;          // largest value; values below `low` weigh 0
-    f2 neg_m, chi, neg_chi, clo;
+    float base, chi, clo;  // exponents are (x - base) (chi + clo) - shift
+    float magic;           // 1.5 * 2^15, of which an ulp is 2^-8, less the shift: a multiple of 2^-8
 };
 __device__ __forceinline__ Scale scale_of(float m, const Setting& s) {
-    // where exp is below 2^-40 (or f32 ends): low - m and its products stay finite
-    const float low = fmaxf(fmaxf(m - 28.5f * s.tau, m - 3e38f), -3.402823466e38f);
-    return {m, low, both(-m), both(s.chi), both(-s.chi), both(s.clo)};
+    // where exp falls below 2^-40 (or f32 ends)
+    const float low = fmaxf(fmaxf(m - 27.725887f * s.tau, m - 3e38f), -3.402823466e38f);
+    // Far out the largest value is subtracted first: exact there, since what weighs more than
+    // 2^-40 is within a factor of two of it.
+    const bool far = !(fabsf(m) * s.chi < 8192.f);
+    const float shift = far ? 0.f : (m * s.chi + 49152.f) - 49152.f;
+    return {m, low, far ? m : 0.f, s.chi, s.clo, 49152.f - shift};
 }
 
-struct Weight2 {
-    f2 hi, lo;  // hi + lo; hi is rounded to 24 bits
+struct Weight {
+    float hi, lo;  // hi + lo, |lo| <= 2^-8 hi
 };
-// exp((x - m) / tau) of two values; 0 below 2^-40.
-__device__ __forceinline__ Weight2 weigh(float x0, float x1, const Scale& r, const float2* table) {
-    const f2 x = both(fmaxf(x0, r.low), fmaxf(x1, r.low));
-    const f2 d = add2(x, r.neg_m), back = sub2(d, x);
-    const f2 err = add2(sub2(x, sub2(d, back)), sub2(r.neg_m, back));  // x - m = d + err
-    const f2 np = mul2(d, r.neg_chi);
-    const f2 rest = fma2(err, r.chi, fma2(d, r.clo, fma2(d, r.chi, np)));
-    // -np + rest = log2 of the weight = k / 64 + g; an ulp of 1.5 * 2^17 is 1 / 64
-    const f2 magic = both(196608.f);
-    const f2 t = sub2(magic, np);
-    const f2 g = sub2(rest, add2(np, sub2(t, magic)));
-    // 2^g - 1 = g ln 2 + (g ln 2)^2 / 2 + ...; the first term as a pair
-    const f2 l1 = both(0.693147180559945f);
-    const f2 qh = mul2(g, l1);
-    f2 ql = fma2(g, l1, mul2(g, both(-0.693147180559945f)));
-    ql = fma2(g, both(-1.9046542e-9f), ql);
-    const f2 series = fma2(g, fma2(g, both(0.00961812910762848f), both(0.0555041086648216f)), both(0.240226506959101f));
-    ql = fma2(mul2(g, g), series, ql);
-    const uint32_t k0 = (uint32_t)t, k1 = (uint32_t)(t >> 32);
-    const float2 t0 = table[k0 & (kTable - 1)], t1 = table[k1 & (kTable - 1)];
-    const f2 th = both(t0.x, t1.x), tl = both(t0.y, t1.y);
-    const f2 a = mul2(th, qh), b = fma2(th, qh, mul2(th, mul2(qh, both(-1.f))));
-    const f2 s = add2(th, a);
-    const f2 e = add2(add2(sub2(th, s), a), fma2(th, ql, fma2(tl, qh, add2(tl, b))));
-    // 2^(k >> 6): the bits of t are 0x48400000 + k
-    const auto power = [&r](uint32_t bits, float neg, float x) {
-        const uint32_t p = ((bits << 17) & 0xFF800000u) + ((127u - 0x1210000u) << 23);
-        return neg <= kSmallest && x >= r.low ? __uint_as_float(p) : 0.f;
-    };
-    const f2 scale = both(power(k0, first(np), x0), power(k1, second(np), x1));
-    return {mul2(s, scale), mul2(e, scale)};
+// exp((x - m) / tau) times a factor between 2^(-1/512) and 2^(1/512) that is the row's; 0 below
+// 2^-40. About 20 operations of f32.
+__device__ __forceinline__ Weight weigh(float x, const Scale& r, const float2* table) {
+    const float y = fmaxf(x, r.low) - r.base;
+    const float t = fmaf(y, r.chi, r.magic), grid = t - r.magic;  // of 2^-8, exact
+    const float g = fmaf(y, r.clo, fmaf(y, r.chi, -grid));        // |g| <= 2^-9
+    const float q = g * fmaf(g, fmaf(g, 0.0555041087f, 0.240226507f), 0.693147181f);  // 2^g - 1
+    const uint32_t bits = __float_as_uint(t);  // 0x47400000 + the exponent in units of 2^-8
+    const float2 e = table[bits & (kTable - 1)];
+    const uint32_t power = ((bits << 15) & 0xFF800000u) + ((127u - 0x474000u) << 23);
+    const float scale = x >= r.low ? __uint_as_float(power) : 0.f;
+    return {e.x * scale, fmaf(e.x, q, e.y) * scale};
 }
-__device__ __forceinline__ uint64_t fixed(float hi, float lo) {
-    return __float2ull_rn(hi * kUnit) + (uint64_t)__float2ll_rn(lo * kUnit);
-}
-__device__ __forceinline__ uint64_t fixed(Weight2 w) { return fixed(first(w.hi), first(w.lo)) + fixed(second(w.hi), second(w.lo)); }
+__device__ __forceinline__ uint64_t fixed(Weight w) { return __float2ull_rn(w.hi * kUnit) + (uint64_t)__float2ll_rn(w.lo * kUnit); }
 // Sums of weights, as pairs.
-__device__ __forceinline__ void add(Weight2& s, Weight2 w) {
-    const f2 t = add2(s.hi, w.hi), z = sub2(t, s.hi);
-    s.lo = add2(s.lo, add2(add2(sub2(s.hi, sub2(t, z)), sub2(w.hi, z)), w.lo));
+__device__ __forceinline__ void add(Weight& s, Weight w) {
+    const float t = s.hi + w.hi, z = t - s.hi;
+    s.lo += ((s.hi - (t - z)) + (w.hi - z)) + w.lo;
     s.hi = t;
 }
 
@@ -273,36 +233,19 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* scratch, ui
     return v + before;
 }
 
-// n keys (n <= kList) of `from` in descending order, to `to`. Few are ranked by counting the
-// larger ones (one to eight threads a key), many by a bitonic sort (384: 3.3 against 3.6 us).
-__device__ __forceinline__ void sort_list(uint64_t* from, uint64_t* to, uint32_t n) {
-    const uint32_t t = threadIdx.x;
-    if (n <= kCount) {
-        const uint32_t shift = n <= kCount / 8 ? 3 : n <= kCount / 4 ? 2 : n <= kCount / 2 ? 1 : 0;
-        const uint32_t at = t >> shift, parts = 1u << shift;
-        const uint64_t key = at < n ? from[at] : 0;
-        uint32_t rank = 0;
-#pragma unroll 4
-        for (uint32_t j = t & (parts - 1); j < n; j += parts) rank += from[j] > key;
-        for (uint32_t k = 1; k < parts; k *= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, k);
-        if (at < n && (t & (parts - 1)) == 0) to[rank] = key;
-        __syncthreads();
-        return;
-    }
-    for (uint32_t i = t; i < kList; i += kThreads) to[i] = i < n ? from[i] : 0;
+// Threads that share a key of a list of n, as a power of two, so that n keys keep the CTA busy.
+__device__ __forceinline__ uint32_t sharing(uint32_t n) { return n <= kList / 8 ? 3 : n <= kList / 4 ? 2 : n <= kList / 2 ? 1 : 0; }
+// n different keys (n <= kList) of `from` in descending order, to `to`, each ranked by counting the
+// larger ones (200 of them: 1 us; a bitonic sort waits for the CTA at each of 36 steps).
+__device__ __forceinline__ void sort_list(const uint64_t* from, uint64_t* to, uint32_t n) {
+    const uint32_t t = threadIdx.x, shift = sharing(n), at = t >> shift, parts = 1u << shift;
+    const uint64_t key = at < n ? from[at] : 0;
+    uint32_t rank = 0;
+#pragma unroll 8
+    for (uint32_t j = t & (parts - 1); j < n; j += parts) rank += from[j] > key;
+    for (uint32_t k = 1; k < parts; k *= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, k);
+    if (at < n && (t & (parts - 1)) == 0) to[rank] = key;
     __syncthreads();
-    for (uint32_t k = 2; k <= kList; k *= 2)
-        for (uint32_t j = k / 2; j > 0; j /= 2) {
-            if (t < kList / 2) {
-                const uint32_t i = 2 * j * (t / j) + t % j;
-                const uint64_t a = to[i], b = to[i + j];
-                if ((a < b) == ((i & k) == 0)) {
-                    to[i] = b;
-                    to[i + j] = a;
-                }
-            }
-            __syncthreads();
-        }
 }
 
 // Vectors of 16 bytes.
@@ -329,14 +272,23 @@ __device__ __forceinline__ void widen(uint4 w, float (&v)[8], T) {
 
 __device__ __forceinline__ Setting setting_of(const SampleParams& p, uint32_t row, bool report) {
     Setting s = {};
-    const int b = request_of(p.row_offsets, p.B, row);
-    if (b < 0) {
+    // (those of request `row`, which it is where every request has one row, are asked for at once)
+    int b = (int)min(row, p.B - 1);
+    float tau = p.temperature ? p.temperature[b] : 1.f, top_p = p.top_p ? p.top_p[b] : 1.f, min_p = p.min_p ? p.min_p[b] : 0.f;
+    int k = p.top_k ? p.top_k[b] : 0;
+    const float u = p.uniform[row];
+    const int found = request_of(p.row_offsets, p.B, row);
+    if (found < 0) {
         if (report) flag(p.status, LP_ERR_OFFSETS);
         return s;
     }
-    float tau = p.temperature ? p.temperature[b] : 1.f;
-    const float top_p = p.top_p ? p.top_p[b] : 1.f, min_p = p.min_p ? p.min_p[b] : 0.f, u = p.uniform[row];
-    const int k = p.top_k ? p.top_k[b] : 0;
+    if (found != b) {
+        b = found;
+        tau = p.temperature ? p.temperature[b] : 1.f;
+        top_p = p.top_p ? p.top_p[b] : 1.f;
+        min_p = p.min_p ? p.min_p[b] : 0.f;
+        k = p.top_k ? p.top_k[b] : 0;
+    }
     s.ok = 1;
     if (!(tau >= 0.f && tau <= 3.402823466e38f)) {
         s.ok = 0;
@@ -373,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t row = blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5;
     pdl_trigger();
-    if (t < kTable) sh.table[t] = make_float2(c_table.hi[t], c_table.lo[t]);
+    const float2 power = t < kTable ? g_table.at[t] : make_float2(0.f, 0.f);
     if (t < kBound) sh.bound[t] = 0;
     if (t == 0) sh.staged = sh.listed = 0;
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // (waited for before others' memory is written to)
@@ -414,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
 #pragma unroll
         for (uint32_t i = 0; i < VEC; ++i) top = max_nan(top, f[i]);
     }
-    __syncthreads();  // the bins are cleared, the setting is there
+    if (t < kTable) sh.table[t] = power;
+    __syncthreads();  // the bins are cleared, the setting and the table are there
     const Setting set = sh.set;
     if (set.k && top > -kInf) atomicAdd(&sh.bound[bound_bin(top)], 1);
 #pragma unroll
@@ -469,6 +422,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
     }
     const Scale scale = scale_of(m, set);
     uint32_t hi = ordered(m);
+    const auto weight_of = [&](float f) { return weigh(f, scale, sh.table); };
+    const Weight most = weight_of(m);
     // min-p: what weighs less than that is not kept. `least` is a key below all that are (room for
     // the roundings here), the weights decide.
     uint32_t least = kLowest;
@@ -476,44 +431,21 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         const float f = m + set.tau * (__logf(set.min_p) - 0.01f) - fabsf(m) * 1e-6f;
         least = f > -3e38f ? min(max(ordered(f + 0.f), kLowest), hi) : kLowest;
     }
-    const auto enough = [&](float w_hi, float w_lo) {  // (hi is the pair rounded to f32)
-        return w_hi > set.min_p || (w_hi == set.min_p && w_lo >= 0.f);
+    const auto enough = [&](Weight w) {
+        return set.min_p == 0.f || (double)w.hi + (double)w.lo >= (double)set.min_p * ((double)most.hi + (double)most.lo);
     };
     const auto token_is = [&](uint32_t id, float value, uint64_t z) {
         p.out[row] = id;
         if (p.out_logprob) {
-            // the largest value is kept: z >= 2^43, and both terms have one sign
-            const float lnz = log1pf((float)(z - (1ull << kPoint)) * kInvUnit);
+            // both terms have one sign: the largest value is kept
+            const uint64_t one = fixed(most);
+            const float lnz = z > one ? log1pf((float)(z - one) / (float)one) : 0.f;
             p.out_logprob[row] = (value - m) / set.tau - lnz;
         }
     };
-    // Weights of places 2 t and 2 t + 1 of the ranked list (0 from `n` on), and whether min-p keeps them.
-    const auto list_weights = [&](uint32_t n, uint64_t (&w)[2], bool (&fine)[2]) {
-        const float f0 = 2 * t < n ? unordered((uint32_t)(sh.stage[2 * t] >> 32)) : -kInf;
-        const float f1 = 2 * t + 1 < n ? unordered((uint32_t)(sh.stage[2 * t + 1] >> 32)) : -kInf;
-        const Weight2 q = weigh(f0, f1, scale, sh.table);
-        w[0] = fixed(first(q.hi), first(q.lo));
-        w[1] = fixed(second(q.hi), second(q.lo));
-        fine[0] = w[0] && enough(first(q.hi), first(q.lo));
-        fine[1] = w[1] && enough(second(q.hi), second(q.lo));
-    };
-    // All weights of the warp's elements.
-    const auto add_all = [&](Weight2& s) {
-#pragma unroll 1
-        for (uint32_t v = lane; v < vecs; v += 32) {
-            float f[VEC];
-            widen(mine[v], f, T());
-            float high = f[0];
-#pragma unroll
-            for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
-            if (!__any_sync(__activemask(), high >= scale.low)) continue;
-#pragma unroll
-            for (uint32_t i = 0; i < VEC; i += 2) add(s, weigh(f[i], f[i + 1], scale, sh.table));
-        }
-    };
-    // Visits the warp's elements whose keys lie in [from, to], two at a time: body(element, element or
+    // Visits the warp's elements with values in [from, to], two at a time: body(element, element or
     // kAll, value, value). Lanes take them out of masks of 32, so that few cost little.
-    const auto visit = [&](uint32_t from, uint32_t to, auto body) {
+    const auto visit = [&](float from, float to, auto body) {
         for (uint32_t v0 = 0; v0 < vecs; v0 += 32 * (32 / VEC)) {
             uint32_t take = 0;
 #pragma unroll
@@ -523,10 +455,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                     float f[VEC];
                     widen(mine[v], f, T());
 #pragma unroll
-                    for (uint32_t i = 0; i < VEC; ++i) {
-                        const uint32_t key = ordered(f[i]);
-                        take |= (key >= from && key <= to ? 1u : 0u) << (j * VEC + i);
-                    }
+                    for (uint32_t i = 0; i < VEC; ++i)
+                        if (f[i] >= from && f[i] <= to) take |= 1u << (j * VEC + i);
                 }
             }
             const auto next = [&] {
@@ -542,11 +472,71 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
             }
         }
     };
+    const auto warp_total = [&](uint64_t v) {
+#pragma unroll
+        for (int k = 16; k > 0; k /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, k);
+        return v;
+    };
+    // All weights of the warp's elements.
+    const auto add_all = [&](Weight& s) {
+#pragma unroll 1
+        for (uint32_t v = lane; v < vecs; v += 32) {
+            float f[VEC];
+            widen(mine[v], f, T());
+            float high = f[0];
+#pragma unroll
+            for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
+            if (!__any_sync(__activemask(), high >= scale.low)) continue;
+#pragma unroll
+            for (uint32_t i = 0; i < VEC; ++i) add(s, weight_of(f[i]));
+        }
+    };
+    // The sum of the CTAs' threads' `v`, told to all; ends with a barrier of the cluster.
+    const auto cluster_total = [&](uint64_t v) {
+        uint64_t all;
+        (void)block_scan(v, sh.scan, &all);
+        if (t < C) cluster.map_shared_rank(&sh, t)->cta_sum[rank] = all;
+        cluster.sync();
+        uint64_t z = 0;
+        for (uint32_t k = 0; k < C; ++k) z += sh.cta_sum[k];
+        return z;
+    };
+    // The warp's sum, told to all.
+    const auto tell_warp = [&](uint64_t sum) {
+        if (lane < C) cluster.map_shared_rank(&sh, lane)->warp_sum[rank * kWarps + warp] = sum;
+    };
+    // Where u Z falls among the warps' sums; by a whole warp.
+    const auto draw_warp = [&] {
+        constexpr uint32_t kEach = kMaxCluster * kWarps / 32;  // of the warps' sums to a lane
+        uint64_t part[kEach], own = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < kEach; ++i) {
+            const uint32_t g = lane * kEach + i;
+            part[i] = g < C * kWarps ? sh.warp_sum[g] : 0;
+            own += part[i];
+        }
+        const uint64_t upto = warp_scan(own);
+        Draw d = {0, __shfl_sync(0xFFFFFFFFu, upto, 31), kAll};
+        bool exact;
+        const uint64_t want = part_of(set.u, d.z, &exact);
+        uint64_t below = upto - own;
+#pragma unroll
+        for (uint32_t i = 0; i < kEach; ++i) {
+            if (below <= want && want < below + part[i]) {
+                d.warp = lane * kEach + i;
+                d.start = below;
+            }
+            below += part[i];
+        }
+        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, d.warp != kAll)) - 1;  // (one lane: want < z)
+        d.warp = __shfl_sync(0xFFFFFFFFu, d.warp, src);
+        d.start = __shfl_sync(0xFFFFFFFFu, d.start, src);
+        return d;
+    };
 
     Shared* lead = cluster.map_shared_rank(&sh, 0);
-    // Tokens with keys in [from, to] into the first CTA's list; true where all of them fit. Ends with a
-    // barrier of the cluster.
-    const auto make_list = [&](uint32_t from, uint32_t to) {
+    // Tokens with values in [from, to] into the first CTA's list; ends with a barrier of the cluster.
+    const auto make_list = [&](float from, float to) {
         visit(from, to, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
             const uint32_t n = (e0 != kAll) + (e1 != kAll), upto = warp_scan(n);
             uint32_t at = 0;
@@ -565,30 +555,28 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         cluster.sync();
     };
 
-    Cut cut = {least, kAll, 0, 0, 0};
+    Cut cut = {least, kAll, 0, 0, 0, 0};
+    bool drawn = false;  // the first CTA has told where the token is
     if (set.k || set.top_p < 1.f) {
         uint64_t target = set.k;
         bool by_count = set.k != 0, few = set.k <= kList;
+        float unit = 0.f;  // of the rounded weights: weights times that
         if (!by_count) {
             // ---- 2. the sum of all weights, and from it a bound
-            Weight2 s = {0, 0};
+            Weight s = {0.f, 0.f};
             add_all(s);
-            uint64_t all;
-            (void)block_scan(fixed(s), sh.scan, &all);
-            if (t < C) cluster.map_shared_rank(&sh, t)->cta_sum[rank] = all;
-            cluster.sync();
-            uint64_t z = 0;
-            for (uint32_t k = 0; k < C; ++k) z += sh.cta_sum[k];
+            const uint64_t z = cluster_total(fixed(s));
             target = reached_at(set.top_p, z);
-            const float sum = (float)z * kInvUnit;
+            const float sum = (float)z / kUnit;
+            unit = (float)kWhole / sum;
             // kept tokens weigh (1 - p) Z / V at least (with room for the roundings here)
-            const float f = m + set.tau * (__logf((1.f - set.top_p) * sum / (float)p.V) - 0.01f) - fabsf(m) * 1e-6f;
+            const float f = m + set.tau * (__logf((1.f - set.top_p) * sum / (float)p.V) - 0.02f) - fabsf(m) * 1e-6f;
             lo = f > -3e38f ? min(max(ordered(f + 0.f), kLowest), hi) : kLowest;
             few = sum < kFewWeights;
         }
         // ---- 3. all that can be kept in one list?
         if (few) {
-            make_list(lo, hi);
+            make_list(unordered(lo), m);
             const uint32_t n = lead->listed;
             if (n <= kList) {
                 // the first CTA does the rest; the others have read its count, and no one reads theirs
@@ -597,309 +585,287 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                     return;
                 }
                 sort_list(sh.list, sh.stage, n);
-                uint64_t w[2], all;
-                bool fine[2];
-                const uint32_t at0 = 2 * t;
-                list_weights(set.k ? min(n, set.k) : n, w, fine);
-                uint64_t below = block_scan(w[0] + w[1], sh.scan, &all) - (w[0] + w[1]);
+                const uint64_t ranked = t < n ? sh.stage[t] : 0;
+                const bool counts = t < n && (!set.k || t < set.k);
+                const Weight weight = weight_of(counts ? unordered((uint32_t)(ranked >> 32)) : -kInf);
+                const uint64_t w = fixed(weight);
+                uint64_t all, kept;
+                const uint64_t below = block_scan(w, sh.scan, &all) - w;
                 if (by_count) target = set.top_p < 1.f ? reached_at(set.top_p, all) : ~0ull;
-                uint32_t keep = 0;
-#pragma unroll
-                for (uint32_t i = 0; i < 2; ++i) {
-                    keep += fine[i] && below < target;
-                    below += w[i];
-                    if (at0 + i < n) sh.list[at0 + i] = w[i];  // (the list is in `stage` now)
-                }
-                uint64_t kept;
-                (void)block_scan(keep, sh.scan, &kept);
+                if (t < n) sh.list[t] = w;  // (the list is in `stage` now)
+                (void)block_scan(w && enough(weight) && below < target, sh.scan, &kept);
                 // The first `kept` of them, in the order of their ids: what lies below each.
-                uint64_t z = 0;
-                bool exact;
-                if (kept <= kCount) {
-                    const uint32_t n_kept = (uint32_t)kept;
-                    const uint32_t shift = n_kept <= kCount / 8 ? 3 : n_kept <= kCount / 4 ? 2 : n_kept <= kCount / 2 ? 1 : 0;
-                    const uint32_t at = t >> shift, parts = 1u << shift;
-                    const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
-                    const uint32_t not_id = (uint32_t)entry;
-                    uint64_t under = 0;
-#pragma unroll 4
-                    for (uint32_t j = t & (parts - 1); j < n_kept; j += parts) {
-                        const uint64_t wj = sh.list[j];
-                        under += (uint32_t)sh.stage[j] > not_id ? wj : 0;
-                        z += wj;
-                    }
-                    for (uint32_t k = 1; k < parts; k *= 2) {
-                        under += __shfl_xor_sync(0xFFFFFFFFu, under, k);
-                        z += __shfl_xor_sync(0xFFFFFFFFu, z, k);
-                    }
-                    const uint64_t want = part_of(set.u, z, &exact);
-                    if (at < n_kept && (t & (parts - 1)) == 0 && under <= want && want < under + sh.list[at])
-                        token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
-                } else {
-                    // sorted by id, with their places; keys and weights are looked up there
-                    uint32_t* keys = reinterpret_cast<uint32_t*>(sh.stage + kList);
-                    uint64_t order[2];
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        const uint32_t at = at0 + i;
-                        order[i] = at < kept ? sh.stage[at] << 32 | at : 0;
-                        if (at < kList) keys[at] = (uint32_t)(sh.stage[at] >> 32);
-                    }
-                    uint64_t mine2[2] = {at0 < kept ? sh.list[at0] : 0, at0 + 1 < kept ? sh.list[at0 + 1] : 0};
-                    __syncthreads();
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i)
-                        if (at0 + i < kList) sh.list[at0 + i] = order[i];
-                    __syncthreads();
-                    sort_list(sh.list, sh.stage, (uint32_t)kept);
-                    // (weights back where their places are)
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i)
-                        if (at0 + i < kList) sh.list[at0 + i] = mine2[i];
-                    __syncthreads();
-                    uint64_t own = 0;
-                    uint32_t place[2];
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        place[i] = at0 + i < kept ? (uint32_t)sh.stage[at0 + i] : 0u;
-                        w[i] = at0 + i < kept ? sh.list[place[i]] : 0;
-                        own += w[i];
-                    }
-                    uint64_t under = block_scan(own, sh.scan, &z) - own;
-                    const uint64_t want = part_of(set.u, z, &exact);
-#pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i) {
-                        if (w[i] && under <= want && want < under + w[i])
-                            token_is(~(uint32_t)(sh.stage[at0 + i] >> 32), unordered(keys[place[i]]), z);
-                        under += w[i];
-                    }
+                const uint32_t n_kept = (uint32_t)kept, shift = sharing(n_kept), at = t >> shift, parts = 1u << shift;
+                const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
+                const uint32_t not_id = (uint32_t)entry;
+                uint64_t under = 0, z = 0;
+#pragma unroll 8
+                for (uint32_t j = t & (parts - 1); j < n_kept; j += parts) {
+                    const uint64_t wj = sh.list[j];
+                    under += (uint32_t)sh.stage[j] > not_id ? wj : 0;
+                    z += wj;
                 }
+                for (uint32_t k = 1; k < parts; k *= 2) {
+                    under += __shfl_xor_sync(0xFFFFFFFFu, under, k);
+                    z += __shfl_xor_sync(0xFFFFFFFFu, z, k);
+                }
+                bool exact;
+                const uint64_t want = part_of(set.u, z, &exact);
+                if (at < n_kept && (t & (parts - 1)) == 0 && under <= want && want < under + sh.list[at])
+                    token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
                 asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
                 return;
             }
         }
         // ---- 4. the value at which the target is reached, by histograms over [lo, hi]
-        bool cut_found = false, read = few;  // whether others may still read the tables and the list
-        for (int round = 0; round < 2 && !cut_found; ++round) {
-            uint64_t above = 0;           // weight of the keys above hi
-            uint32_t above_count = 0;
-            for (;;) {
-                uint32_t shift = 0;
-                while ((hi - lo) >> shift >= kBins) ++shift;
-                if (read) cluster.sync();
-                read = true;
-                sh.count[t] = sh.low[t] = sh.high[t] = 0;
-                if (t == 0) {
-                    sh.listed = sh.staged = 0;
-                    sh.found_bin = kAll;
-                }
-                __syncthreads();
-                visit(lo, hi, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
-                    const Weight2 w = weigh(f0, f1, scale, sh.table);
-                    const auto count = [&](float f, uint64_t fix) {
-                        const uint32_t bin = (hi - ordered(f)) >> shift;
-                        atomicAdd(&sh.count[bin], 1);
-                        const uint32_t was = atomicAdd(&sh.low[bin], (uint32_t)fix);
-                        const uint32_t up = (uint32_t)(fix >> 32) + (was + (uint32_t)fix < was);
-                        if (up) atomicAdd(&sh.high[bin], up);
-                    };
-                    if (e0 != kAll) count(f0, fixed(first(w.hi), first(w.lo)));
-                    if (e1 != kAll) count(f1, fixed(second(w.hi), second(w.lo)));
-                });
-                cluster.sync();
-                uint32_t n = 0;
-                uint64_t w = 0, all_w, all_n;
-                for (uint32_t k = 0; k < C; ++k) {
-                    const Shared* o = cluster.map_shared_rank(&sh, k);
-                    n += o->count[t];
-                    w += (uint64_t)o->high[t] << 32 | o->low[t];
-                }
-                const uint64_t upto = block_scan(w, sh.scan, &all_w), upto_n = block_scan(n, sh.scan, &all_n);
-                const uint64_t have = by_count ? above_count + upto_n : above + upto, step = by_count ? n : w;
-                if (have >= target && have - step < target) {
-                    sh.found_bin = t;
-                    sh.found_count = n;
-                    sh.found_before = above + upto - w;
-                    sh.found_before_count = above_count + (uint32_t)(upto_n - n);
-                    sh.found_weight = w;
-                }
-                __syncthreads();
-                const uint32_t bin = sh.found_bin;
-                if (bin == kAll) {  // all of it is kept (k is more than there are)
-                    if (by_count && set.top_p < 1.f) {
-                        cut.above = lo - 1;
-                        cut.target = reached_at(set.top_p, above + all_w);
-                    } else {
-                        cut = {max(lo, least), kAll, 0, 0, 0};
-                        cut_found = true;
+        bool found = false, read = few;  // whether others may still read the tables and the list
+        uint64_t above = 0;              // weight of the keys above hi, and (by count) their number
+        uint32_t above_count = 0;
+        for (int n_hist = 0; n_hist < 64 && !found; ++n_hist) {  // (a bound only: each cuts the range)
+            uint32_t shift = 0;
+            while ((hi - lo) >> shift >= kBins) ++shift;
+            if (read) cluster.sync();
+            read = true;
+            sh.weight[t] = sh.weight[t + kThreads] = sh.count[t] = 0;
+            if (t == 0) {
+                sh.listed = sh.staged = sh.in_bins = sh.in_weight = 0;
+                sh.first_bin = sh.last_bin = kAll;
+            }
+            __syncthreads();
+            visit(unordered(lo), unordered(hi), [&](uint32_t e0, uint32_t e1, float f0, float f1) {
+                const auto count = [&](float f) {
+                    const uint32_t bin = (hi - ordered(f)) >> shift;
+                    atomicAdd(&sh.count[bin >> 1], bin & 1 ? 65536u : 1u);
+                    if (!by_count) {
+                        float w;
+                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(f - scale.base, scale.chi, scale.magic - 49152.f)));
+                        atomicAdd(&sh.weight[bin], __float2uint_rn(w * unit));
                     }
+                };
+                if (e0 != kAll) count(f0);
+                if (e1 != kAll) count(f1);
+            });
+            cluster.sync();
+            uint32_t n0 = 0, n1 = 0, w0 = 0, w1 = 0;  // of bins 2 t and 2 t + 1
+            for (uint32_t k = 0; k < C; ++k) {
+                const Shared* o = cluster.map_shared_rank(&sh, k);
+                const uint32_t n = o->count[t];
+                const uint2 w = *reinterpret_cast<const uint2*>(&o->weight[2 * t]);
+                n0 += n & 0xFFFFu;
+                n1 += n >> 16;
+                w0 += w.x;
+                w1 += w.y;
+            }
+            uint64_t all;
+            const uint64_t upto = block_scan((uint64_t)(n0 + n1) << 32 | (w0 + w1), sh.scan, &all);  // (neither passes 32 bits)
+            const uint32_t n_before = (uint32_t)(upto >> 32) - n0 - n1, w_before = (uint32_t)upto - w0 - w1;
+            // the first and the last bin in which the target can be reached
+            const uint32_t aim = by_count ? (uint32_t)target - above_count
+                                          : (uint32_t)((target > above ? (float)(target - above) : 0.f) / kUnit * unit);
+            const uint32_t slack = by_count ? 0 : kMargin;
+            const uint32_t x0 = by_count ? n_before : w_before, x1 = x0 + (by_count ? n0 : w0), x2 = x1 + (by_count ? n1 : w1);
+            const auto reach = [&](uint32_t a, uint32_t* bin) {
+                if (x0 < a && x2 >= a) *bin = 2 * t + (x1 < a);
+            };
+            reach(max(aim, slack + 1) - slack, &sh.first_bin);
+            reach(aim + slack, &sh.last_bin);
+            __syncthreads();
+            const uint32_t bins = (hi - lo) >> shift;
+            if (by_count && sh.first_bin == kAll) {  // all of it is kept (k is more than there are)
+                if (set.top_p == 1.f) {
+                    cut = {max(lo, least), kAll, 0, 0, 0, 0};
+                    found = true;
                     break;
                 }
-                above = sh.found_before;
-                above_count = sh.found_before_count;
-                const uint32_t in_bin = sh.found_count;
-                const uint64_t bin_weight = sh.found_weight;
-                hi = hi - (bin << shift);
-                lo = max(lo, hi - (1u << shift) + 1 > hi ? 0u : hi - (1u << shift) + 1);
-                if (in_bin > kList && lo < hi) continue;
-                if (in_bin > kList) {
-                    // one value: its first `j` ids are kept
-                    const uint64_t each = bin_weight / in_bin;
-                    uint64_t j = by_count ? target - above_count : (target - above + each - 1) / each;
-                    if (by_count && set.top_p < 1.f) {
-                        const uint64_t next = reached_at(set.top_p, above + j * each);
-                        if (next <= above) {
-                            cut.above = hi;
-                            cut.target = next;
-                            break;
-                        }
-                        if (each) j = min(j, (next - above + each - 1) / each);
-                    }
-                    // the j-th of them, counted by warp in the order of the ids
-                    uint32_t here = 0;
-                    visit(hi, hi, [&](uint32_t e0, uint32_t e1, float, float) { here += (e0 != kAll) + (e1 != kAll); });
-                    here = __reduce_add_sync(0xFFFFFFFFu, here);
-                    if (lane < C) cluster.map_shared_rank(&sh, lane)->warp_sum[rank * kWarps + warp] = here;
-                    cluster.sync();
-                    uint64_t before_me = 0;
-                    for (uint32_t k = 0; k < rank * kWarps + warp; ++k) before_me += sh.warp_sum[k];
-                    if (before_me < j && j <= before_me + here) {
-                        uint32_t left = (uint32_t)(j - before_me);
-                        for (uint32_t v0 = 0; v0 < vecs && left; v0 += 32) {
-                            const uint32_t v = v0 + lane;
-                            uint32_t take = 0;
-                            if (v < vecs) {
-                                float f[VEC];
-                                widen(mine[v], f, T());
-#pragma unroll
-                                for (uint32_t i = 0; i < VEC; ++i) take |= (ordered(f[i]) == hi ? 1u : 0u) << i;
-                            }
-                            const uint32_t c = __popc(take), cum = warp_scan(c), all = __shfl_sync(0xFFFFFFFFu, cum, 31);
-                            if (left > all) {
-                                left -= all;
-                                continue;
-                            }
-                            if (cum >= left && cum - c < left) {
-                                for (uint32_t skip = left - (cum - c) - 1; skip; --skip) take &= take - 1;
-                                const uint32_t id = id_of(v * VEC + __ffs(take) - 1);
-                                for (uint32_t k = 0; k < C; ++k) cluster.map_shared_rank(&sh, k)->cut.id = id;
-                            }
-                            left = 0;
-                        }
-                    }
-                    cluster.sync();
-                    cut = {hi, sh.cut.id, 0, 0, 0};
-                } else {
-                    // the bin's tokens, ranked by the first CTA (its tables have been read before it stages)
-                    cluster.sync();
-                    make_list(lo, hi);
-                    if (rank == 0) {
-                        sort_list(sh.list, sh.stage, in_bin);
-                        const uint32_t limit = by_count ? (uint32_t)(target - above_count) : kAll, at0 = 2 * t;
-                        uint64_t w2[2], all;
-                        bool fine[2];
-                        list_weights(min(in_bin, limit), w2, fine);
-                        uint64_t below = above + block_scan(w2[0] + w2[1], sh.scan, &all) - (w2[0] + w2[1]);
-                        uint64_t reach = target;
-                        if (by_count) reach = set.top_p < 1.f ? reached_at(set.top_p, above + all) : ~0ull;
-                        uint32_t keep = 0;
-#pragma unroll
-                        for (uint32_t i = 0; i < 2; ++i) {
-                            keep += at0 + i < in_bin && at0 + i < limit && below < reach;
-                            below += w2[i];
-                        }
-                        uint64_t kept;
-                        (void)block_scan(keep, sh.scan, &kept);
-                        if (t < C) {
-                            Cut c = {kAll, 0, 1, hi, reach};  // reached among larger values
-                            if (kept) {
-                                const uint64_t last = sh.stage[kept - 1];
-                                c = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0};
-                            }
-                            cluster.map_shared_rank(&sh, t)->cut = c;
-                        }
-                    }
-                    cluster.sync();
-                    cut = sh.cut;
-                    if (cut.again) break;
-                }
-                cut_found = true;
-                if (least > cut.key) cut = {least, kAll, 0, 0, 0};
-                break;
-            }
-            if (!cut_found) {  // once more, by weight, among the larger values
+                Weight s = {0.f, 0.f};
+                add_all(s);
+                const uint64_t z = cluster_total(fixed(s));
                 by_count = false;
-                target = cut.target;
-                lo = cut.above + 1;
-                hi = ordered(m);
+                target = reached_at(set.top_p, z);
+                unit = (float)kWhole * kUnit / (float)z;
+                continue;
+            }
+            const uint32_t last_bin = min(sh.last_bin, bins), first_bin = min(sh.first_bin, last_bin);
+            const bool in0 = 2 * t >= first_bin && 2 * t <= last_bin, in1 = 2 * t + 1 >= first_bin && 2 * t + 1 <= last_bin;
+            if (in0 || in1) {
+                atomicAdd(&sh.in_bins, (in0 ? n0 : 0) + (in1 ? n1 : 0));
+                atomicAdd(&sh.in_weight, (in0 ? w0 : 0) + (in1 ? w1 : 0));
+            }
+            if (first_bin >> 1 == t) sh.place = n_before + (first_bin & 1 ? n0 : 0);
+            __syncthreads();
+            const uint32_t in_bins = sh.in_bins, end = hi - (((first_bin + 1) << shift) - 1);  // (of the first bin)
+            const bool narrowed = first_bin != 0 || last_bin != bins;
+            above_count += sh.place;
+            lo = last_bin == bins ? lo : hi - (((last_bin + 1) << shift) - 1);
+            hi -= first_bin << shift;
+            // the weights above them, exactly, by warp
+            {
+                Weight s = {0.f, 0.f};
+                const float from = unordered(hi);
+                visit(from, m, [&](uint32_t, uint32_t, float f0, float f1) {
+                    add(s, weight_of(f0 > from ? f0 : -kInf));
+                    add(s, weight_of(f1 > from ? f1 : -kInf));
+                });
+                tell_warp(warp_total(fixed(s)));
+            }
+            cluster.sync();
+            above = 0;
+            for (uint32_t k = 0; k < C * kWarps; ++k) above += sh.warp_sum[k];
+            if (in_bins <= kList) {
+                // ranked by the first CTA
+                make_list(unordered(lo), unordered(hi));
+                if (rank == 0) {
+                    sort_list(sh.list, sh.stage, in_bins);
+                    const uint32_t limit = by_count ? min(in_bins, (uint32_t)target - above_count) : in_bins;
+                    const uint64_t ranked = t < limit ? sh.stage[t] : 0;
+                    const uint32_t key = (uint32_t)(ranked >> 32), id = ~(uint32_t)ranked;
+                    const uint64_t w = fixed(weight_of(t < limit ? unordered(key) : -kInf));
+                    uint64_t sum, kept;
+                    const uint64_t below = above + block_scan(w, sh.scan, &sum) - w;
+                    uint64_t goal = target;
+                    if (by_count) goal = set.top_p < 1.f ? reached_at(set.top_p, above + sum) : ~0ull;
+                    const bool keep = t < limit && below < goal;
+                    (void)block_scan(keep, sh.scan, &kept);
+                    Cut c = {kAll, 0, 1, hi, goal, above + sum};  // reached among larger values
+                    Draw d = {};
+                    if (kept) {
+                        const uint64_t last = sh.stage[kept - 1];
+                        c = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0, 0};
+                        if (set.min_p == 0.f) {  // the warps' sums are complete with these
+                            if (keep && w)
+                                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.warp_sum[(id + before) / p.chunk]), (unsigned long long)w);
+                            __syncthreads();
+                            d = draw_warp();
+                        }
+                    }
+                    if (t < C) {
+                        Shared* o = cluster.map_shared_rank(&sh, t);
+                        o->cut = c;
+                        o->draw = d;
+                    }
+                }
+                cluster.sync();
+                cut = sh.cut;
+                found = cut.again == 0;
+                drawn = found && set.min_p == 0.f;
+                if (cut.again) {  // once more, by weight, among the larger values
+                    by_count = false;
+                    target = cut.target;
+                    unit = (float)kWhole * kUnit / (float)cut.total;
+                    lo = cut.above + 1;
+                    hi = ordered(m);
+                    above = 0;
+                }
+            } else if (lo == hi) {
+                // one value: its first `j` ids are kept
+                const uint64_t one = fixed(weight_of(unordered(hi)));
+                uint64_t j = by_count ? target - above_count : (target - above + one - 1) / one;
+                if (by_count && set.top_p < 1.f) {
+                    const uint64_t z = above + j * one, goal = reached_at(set.top_p, z);
+                    if (goal <= above) {
+                        by_count = false;
+                        target = goal;
+                        unit = (float)kWhole * kUnit / (float)z;
+                        lo = hi + 1;
+                        hi = ordered(m);
+                        above = 0;
+                        continue;
+                    }
+                    if (one) j = min(j, (goal - above + one - 1) / one);
+                }
+                // the j-th of them, counted by warp in the order of the ids
+                uint32_t here = 0;
+                visit(unordered(hi), unordered(hi), [&](uint32_t e0, uint32_t e1, float, float) { here += (e0 != kAll) + (e1 != kAll); });
+                here = __reduce_add_sync(0xFFFFFFFFu, here);
+                cluster.sync();  // (the sums have been read)
+                tell_warp(here);
+                cluster.sync();
+                uint64_t before_me = 0;
+                for (uint32_t k = 0; k < rank * kWarps + warp; ++k) before_me += sh.warp_sum[k];
+                if (before_me < j && j <= before_me + here) {
+                    uint32_t left = (uint32_t)(j - before_me);
+                    for (uint32_t v0 = 0; v0 < vecs && left; v0 += 32) {
+                        const uint32_t v = v0 + lane;
+                        uint32_t take = 0;
+                        if (v < vecs) {
+                            float f[VEC];
+                            widen(mine[v], f, T());
+#pragma unroll
+                            for (uint32_t i = 0; i < VEC; ++i) take |= (ordered(f[i]) == hi ? 1u : 0u) << i;
+                        }
+                        const uint32_t c = __popc(take), cum = warp_scan(c), sum = __shfl_sync(0xFFFFFFFFu, cum, 31);
+                        if (left > sum) {
+                            left -= sum;
+                            continue;
+                        }
+                        if (cum >= left && cum - c < left) {
+                            for (uint32_t skip = left - (cum - c) - 1; skip; --skip) take &= take - 1;
+                            const uint32_t id = id_of(v * VEC + __ffs(take) - 1);
+                            for (uint32_t k = 0; k < C; ++k) cluster.map_shared_rank(&sh, k)->cut.id = id;
+                        }
+                        left = 0;
+                    }
+                }
+                cluster.sync();
+                cut = {hi, sh.cut.id, 0, 0, 0, 0};
+                found = true;
+            } else if (by_count || narrowed) {
+                // once more; what is left of the weights makes the whole
+                unit *= (float)kWhole / ((float)sh.in_weight + 2.f * (float)kMargin);
+            } else {
+                // a few values of many tokens: on which side of the first bin's end? (the weights down to there tell)
+                Weight s = {0.f, 0.f};
+                visit(unordered(end), m, [&](uint32_t, uint32_t, float f0, float f1) {
+                    add(s, weight_of(f0));
+                    add(s, weight_of(f1));
+                });
+                const uint64_t upto_end = cluster_total(fixed(s));
+                if (upto_end >= target) {
+                    lo = end;
+                } else {
+                    hi = end - 1;
+                    above = upto_end;
+                }
             }
         }
+        if (least > cut.key) cut = {least, kAll, 0, 0, 0, 0};
     }
 
     // ---- 5. the kept weights by warp, in the order of the ids, and the draw
-    const auto kept_weight = [&](uint32_t key, uint32_t id, float w_hi, float w_lo) {
-        return key < cut.key || (key == cut.key && id > cut.id) || !enough(w_hi, w_lo) ? 0ull : fixed(w_hi, w_lo);
+    const auto kept = [&](float f, uint32_t id) {
+        const uint32_t key = ordered(f);
+        return !(key < cut.key || (key == cut.key && id > cut.id));
     };
-    uint64_t sum;
-    {
-        Weight2 s = {0, 0};
-        if (cut.key == kLowest && set.min_p == 0.f) {  // all
+    if (!drawn) {
+        Weight s = {0.f, 0.f};
+        if (cut.key == kLowest && set.min_p == 0.f) {
             add_all(s);
         } else {
-            visit(cut.key, kAll, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
-                if (e0 != kAll && ordered(f0) == cut.key && id_of(e0) > cut.id) f0 = -kInf;
-                if (e1 != kAll && ordered(f1) == cut.key && id_of(e1) > cut.id) f1 = -kInf;
-                Weight2 w = weigh(f0, f1, scale, sh.table);
-                if (set.min_p > 0.f) {
-                    const f2 keep = both(enough(first(w.hi), first(w.lo)) ? 1.f : 0.f, enough(second(w.hi), second(w.lo)) ? 1.f : 0.f);
-                    w = {mul2(w.hi, keep), mul2(w.lo, keep)};
-                }
-                add(s, w);
+            visit(unordered(cut.key), m, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
+                const Weight a = weight_of(e0 != kAll && kept(f0, id_of(e0)) ? f0 : -kInf);
+                const Weight b = weight_of(e1 != kAll && kept(f1, id_of(e1)) ? f1 : -kInf);
+                if (enough(a)) add(s, a);
+                if (enough(b)) add(s, b);
             });
         }
-        sum = fixed(s);
-#pragma unroll
-        for (int k = 16; k > 0; k /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+        const uint64_t sum = warp_total(fixed(s));
+        tell_warp(sum);
+        cluster.sync();
     }
-    if (lane < C) cluster.map_shared_rank(&sh, lane)->warp_sum[rank * kWarps + warp] = sum;
-    cluster.sync();
     // (no one writes to or reads from other CTAs from here on)
-    constexpr uint32_t kEach = kMaxCluster * kWarps / 32;  // of the warps' sums to a lane
-    uint64_t part[kEach], own = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i) {
-        const uint32_t g = lane * kEach + i;
-        part[i] = g < C * kWarps ? sh.warp_sum[g] : 0;
-        own += part[i];
-    }
-    const uint64_t upto = warp_scan(own), z = __shfl_sync(0xFFFFFFFFu, upto, 31);
-    bool exact;
-    const uint64_t want = part_of(set.u, z, &exact);
-    uint64_t below = upto - own, start = 0;
-    uint32_t hit = kAll;
-#pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i) {
-        if (below <= want && want < below + part[i]) {
-            hit = lane * kEach + i;
-            start = below;
-        }
-        below += part[i];
-    }
-    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, hit != kAll)) - 1;  // (one lane: want < z)
-    hit = __shfl_sync(0xFFFFFFFFu, hit, src);
-    start = __shfl_sync(0xFFFFFFFFu, start, src);
-    if (hit / kWarps != rank) return;
+    const Draw draw = drawn ? sh.draw : draw_warp();
+    if (draw.warp / kWarps != rank) return;
     // The CTA that has it walks the warp's part, a few neighbours to a thread.
-    const uint32_t each = (vecs + kThreads - 1) / kThreads, from = (hit % kWarps) * vecs, number = hit * p.chunk - before;
+    bool exact;
+    const uint64_t want = part_of(set.u, draw.z, &exact) - draw.start;
+    const uint32_t each = (vecs + kThreads - 1) / kThreads, from = (draw.warp % kWarps) * vecs, number = draw.warp * p.chunk - before;
     const uint32_t v_begin = min(t * each, vecs), v_end = min(v_begin + each, vecs);
     const auto weights = [&](uint32_t v, uint64_t (&w)[VEC], float (&f)[VEC]) {
         widen(slice[from + v], f, T());
 #pragma unroll
-        for (uint32_t i = 0; i < VEC; i += 2) {
-            const Weight2 q = weigh(f[i], f[i + 1], scale, sh.table);
-            const uint32_t id = number + v * VEC + i;
-            w[i] = kept_weight(ordered(f[i]), id, first(q.hi), first(q.lo));
-            w[i + 1] = kept_weight(ordered(f[i + 1]), id + 1, second(q.hi), second(q.lo));
+        for (uint32_t i = 0; i < VEC; ++i) {
+            const Weight q = weight_of(kept(f[i], number + v * VEC + i) ? f[i] : -kInf);
+            w[i] = enough(q) ? fixed(q) : 0;
         }
     };
     uint64_t here = 0, all;
@@ -910,9 +876,9 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
 #pragma unroll
         for (uint32_t i = 0; i < VEC; ++i) here += w[i];
     }
-    below = block_scan(here, sh.scan, &all) - here;
+    const uint64_t below = block_scan(here, sh.scan, &all) - here;
     // (these sums are rounded another way than the warp's: at its very end the last kept is meant)
-    uint64_t left = min(want - start, all - 1);
+    uint64_t left = min(want, all - 1);
     if (left < below || left >= below + here) return;
     left -= below;
     for (uint32_t v = v_begin; v < v_end; ++v) {
@@ -922,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
 #pragma unroll
         for (uint32_t i = 0; i < VEC; ++i) {
             if (left < w[i]) {
-                token_is(number + v * VEC + i, f[i], z);
+                token_is(number + v * VEC + i, f[i], draw.z);
                 return;
             }
             left -= w[i];

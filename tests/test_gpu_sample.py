@@ -14,8 +14,10 @@ pytestmark = pytest.mark.gpu
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 LAST = 1.0 - 2.0 ** -24  # the largest random number
-# The kernel's weights have about 40 bits: a comparison nearer than this may turn over.
-NEAR = 2.0 ** -36
+# A weight is within 2^-32 of the formula's: three roundings of f32 to what is left of a power of two after a
+# table of 256 (2^-8.5 of the weight, so 3 * 2^-33.5) and the table's own 2^-49. A comparison of sums of such
+# weights that is nearer than twice that may turn over.
+NEAR = 2.0 ** -31
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -79,7 +81,7 @@ SETTINGS = {
 def test_settings(name, V, dtype):
     s, T = SETTINGS[name], 5
     x = logits(T, V, dtype, seed=1)
-    # (p next to 1 ends among tokens of a share of 2^-33 or less: the margin is often below 2^-36 there)
+    # (p next to 1 ends among tokens of a share of 2^-30 or less: the margin is often below 2^-31 there)
     check(x, uniforms(T - 2) + [0.0, LAST], skipped=1.0 if name == "p_last" else 0.02, **{n: [v] * T for n, v in s.items()})
 
 
