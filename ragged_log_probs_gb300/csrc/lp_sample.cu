@@ -20,6 +20,8 @@
 // before a barrier of the cluster.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "lp_head_common.h"
 
 namespace {
@@ -93,8 +95,18 @@ struct Cut {
 };
 
 struct Told {              // by each CTA
-    float top;             // its largest value
+    uint32_t top;          // ordered() of its largest value (a NaN's is above all)
     uint32_t share, whole; // keys that ceil(k / CTAs), and k, of its threads' largest reach
+};
+
+struct Range {             // keys among which the cut is
+    uint32_t lo, hi;
+    uint32_t end;          // the least key of the first bin
+    uint32_t in;           // how many they hold
+    uint32_t above_count;  // how many lie above them, in the histogram's range
+    uint32_t none;         // by count: there are not as many
+    uint32_t narrowed, more;  // than before; than one bin
+    float grow;            // what the rounded weights may be multiplied with
 };
 
 struct Draw {              // where the token is
@@ -109,21 +121,20 @@ struct Shared {
     };
     union {
         struct {
-            uint32_t weight[kBins];
-            uint32_t count[kBins / 2];  // 16 bits each
+            uint32_t weight[kBins], count[kBins];
         };
         uint64_t stage[kList];   // a CTA's part of the list; the ranked list
     };
     float2 table[kTable];
     uint64_t scan[kWarps];
     uint64_t warp_sum[kMaxCluster * kWarps];
-    uint64_t cta_sum[kMaxCluster];
     Told told[kMaxCluster];
     Setting set;
     Cut cut;
     Draw draw;
-    uint32_t listed, staged, place;
-    uint32_t first_bin, last_bin, in_bins, in_weight;
+    Range range;
+    uint32_t listed, staged, place, top;
+    uint32_t first_bin, last_bin, in_bins, in_weight, above_bins;
 };
 
 // 2^(j / 256) as pairs of f32, at compile time, by the exponential's series.
@@ -314,6 +325,12 @@ __device__ __forceinline__ Setting setting_of(const SampleParams& p, uint32_t ro
     return s;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SampleParams p) {
     constexpr uint32_t VEC = Vec<T>::kElems;
@@ -327,8 +344,9 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
     pdl_trigger();
     const float2 power = t < kTable ? g_table.at[t] : make_float2(0.f, 0.f);
     if (t < kBound) sh.bound[t] = 0;
-    if (t == 0) sh.staged = sh.listed = 0;
-    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // (waited for before others' memory is written to)
+    if (t == 0) sh.staged = sh.listed = sh.top = 0;
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before others' memory is written to)
     pdl_wait();
 
     // The row in units of aligned vectors: element i of the row is number i + before. Slices and the
@@ -341,9 +359,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
     const T* values = reinterpret_cast<const T*>(mine);
     const auto id_of = [&](uint32_t element) { return begin + element - before; };  // of the warp's part
 
-    // ---- 1. read; the setting, by the last warp; the largest value, threads' largest in coarse bins
-    if (t == kThreads - 1) sh.set = setting_of(p, row, rank == 0);
-    __syncwarp();
+    // ---- 1. read; the largest value, and threads' largest in coarse bins; the setting, by one thread
     float top = -kInf;
 #pragma unroll 8
     for (uint32_t v = lane; v < vecs; v += 32) {
@@ -364,24 +380,19 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         float f[VEC];
         widen(w, f, T());
 #pragma unroll
-        for (uint32_t i = 0; i < VEC; ++i) top = max_nan(top, f[i]);
+        for (uint32_t i = 0; i < VEC; i += 2) top = max_nan(top, f[i], f[i + 1]);
     }
+    if (t == kThreads - 1) sh.set = setting_of(p, row, rank == 0);
+    __syncwarp();
     if (t < kTable) sh.table[t] = power;
-    __syncthreads();  // the bins are cleared, the setting and the table are there
-    const Setting set = sh.set;
-    if (set.k && top > -kInf) atomicAdd(&sh.bound[bound_bin(top)], 1);
-#pragma unroll
-    for (int k = 16; k > 0; k /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-    if (lane == 0) reinterpret_cast<float*>(sh.scan)[warp] = top;
+    if (top > -kInf) atomicAdd(&sh.bound[bound_bin(top)], 1);
+    const uint32_t warp_top = __reduce_max_sync(0xFFFFFFFFu, ordered(top));  // (max.NaN's NaN is positive)
+    if (lane == 0) atomicMax(&sh.top, warp_top);
     __syncthreads();
+    const Setting set = sh.set;
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (warp == 0) {
-        Told told;
-        top = lane < kWarps ? reinterpret_cast<float*>(sh.scan)[lane] : -kInf;
-#pragma unroll
-        for (int k = 8; k > 0; k /= 2) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-        told.top = __shfl_sync(0xFFFFFFFFu, top, 0);
-        told.share = told.whole = kLowest;
+        Told told = {sh.top, kLowest, kLowest};
         if (set.k) {
             // from the top: lane 0 has the largest bins
             uint32_t n[kBound / 32], sum = 0;
@@ -404,15 +415,10 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         if (lane < C) cluster.map_shared_rank(&sh, lane)->told[rank] = told;
     }
     cluster.sync();
-    float m = -kInf;
-    uint32_t lo = kAll, lo_whole = kLowest;  // keys below `lo` are not kept
-    for (uint32_t k = 0; k < C; ++k) {
-        m = max_nan(m, sh.told[k].top);
-        lo = min(lo, sh.told[k].share);
-        lo_whole = max(lo_whole, sh.told[k].whole);
-    }
-    lo = max(lo, lo_whole);
-    if (!set.ok || !(m > -kInf && m < kInf)) {
+    const Told told = lane < C ? sh.told[lane] : Told{0, kAll, 0};
+    uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, told.top);
+    uint32_t lo = max(__reduce_min_sync(0xFFFFFFFFu, told.share), __reduce_max_sync(0xFFFFFFFFu, told.whole));  // keys below are not kept
+    if (!set.ok || hi < kLowest || hi >= ordered(kInf)) {
         if (rank == 0 && t == 0) {
             if (set.ok) flag(p.status, LP_ERR_LOGITS);
             p.out[row] = kAll;
@@ -420,8 +426,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         }
         return;
     }
+    const float m = unordered(hi);
     const Scale scale = scale_of(m, set);
-    uint32_t hi = ordered(m);
     const auto weight_of = [&](float f) { return weigh(f, scale, sh.table); };
     const Weight most = weight_of(m);
     // min-p: what weighs less than that is not kept. `least` is a key below all that are (room for
@@ -454,6 +460,10 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                 if (v < vecs) {
                     float f[VEC];
                     widen(mine[v], f, T());
+                    float high = f[0];
+#pragma unroll
+                    for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
+                    if (!__any_sync(__activemask(), high >= from)) continue;
 #pragma unroll
                     for (uint32_t i = 0; i < VEC; ++i)
                         if (f[i] >= from && f[i] <= to) take |= 1u << (j * VEC + i);
@@ -491,19 +501,21 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
             for (uint32_t i = 0; i < VEC; ++i) add(s, weight_of(f[i]));
         }
     };
-    // The sum of the CTAs' threads' `v`, told to all; ends with a barrier of the cluster.
-    const auto cluster_total = [&](uint64_t v) {
-        uint64_t all;
-        (void)block_scan(v, sh.scan, &all);
-        if (t < C) cluster.map_shared_rank(&sh, t)->cta_sum[rank] = all;
-        cluster.sync();
-        uint64_t z = 0;
-        for (uint32_t k = 0; k < C; ++k) z += sh.cta_sum[k];
-        return z;
-    };
     // The warp's sum, told to all.
     const auto tell_warp = [&](uint64_t sum) {
         if (lane < C) cluster.map_shared_rank(&sh, lane)->warp_sum[rank * kWarps + warp] = sum;
+    };
+    const auto told_total = [&] {  // of what all warps told
+        uint64_t sum = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < kMaxCluster * kWarps; i += 32) sum += i + lane < C * kWarps ? sh.warp_sum[i + lane] : 0;
+        return warp_total(sum);
+    };
+    // The sum over all threads of the cluster.
+    const auto cluster_total = [&](uint64_t v) {
+        tell_warp(warp_total(v));
+        cluster.sync();
+        return told_total();
     };
     // Where u Z falls among the warps' sums; by a whole warp.
     const auto draw_warp = [&] {
@@ -535,16 +547,21 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
     };
 
     Shared* lead = cluster.map_shared_rank(&sh, 0);
-    // Tokens with values in [from, to] into the first CTA's list; ends with a barrier of the cluster.
-    const auto make_list = [&](float from, float to) {
-        visit(from, to, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
-            const uint32_t n = (e0 != kAll) + (e1 != kAll), upto = warp_scan(n);
+    // Tokens into the CTA's part of the list, and the parts into the first CTA's, which ends with a barrier of
+    // the cluster.
+    const auto stage = [&](uint32_t e0, uint32_t e1, float f0, float f1) {
+        const auto one = [&](uint32_t e, float f) {
+            const uint32_t take = __ballot_sync(0xFFFFFFFFu, e != kAll);
+            if (!take) return;
             uint32_t at = 0;
-            if (lane == 31) at = atomicAdd(&sh.staged, upto);
-            at = __shfl_sync(0xFFFFFFFFu, at, 31) + upto - n;
-            if (e0 != kAll && at < kList) sh.stage[at] = (uint64_t)ordered(f0) << 32 | (uint32_t)~id_of(e0);
-            if (e1 != kAll && at + 1 < kList) sh.stage[at + 1] = (uint64_t)ordered(f1) << 32 | (uint32_t)~id_of(e1);
-        });
+            if (lane == 0) at = atomicAdd(&sh.staged, __popc(take));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(take & ((1u << lane) - 1));
+            if (e != kAll && at < kList) sh.stage[at] = (uint64_t)ordered(f) << 32 | (uint32_t)~id_of(e);
+        };
+        one(e0, f0);
+        one(e1, f1);
+    };
+    const auto send_list = [&] {
         __syncthreads();
         const uint32_t n = sh.staged;
         if (t == 0) sh.place = n ? atomicAdd(&lead->listed, n) : 0u;
@@ -560,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
     if (set.k || set.top_p < 1.f) {
         uint64_t target = set.k;
         bool by_count = set.k != 0, few = set.k <= kList;
-        float unit = 0.f;  // of the rounded weights: weights times that
+        float unit = 1.f;  // of the rounded weights: weights times that
         if (!by_count) {
             // ---- 2. the sum of all weights, and from it a bound
             Weight s = {0.f, 0.f};
@@ -576,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         }
         // ---- 3. all that can be kept in one list?
         if (few) {
-            make_list(unordered(lo), m);
+            visit(unordered(lo), m, stage);
+            send_list();
             const uint32_t n = lead->listed;
             if (n <= kList) {
                 // the first CTA does the rest; the others have read its count, and no one reads theirs
@@ -626,52 +644,97 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
             while ((hi - lo) >> shift >= kBins) ++shift;
             if (read) cluster.sync();
             read = true;
-            sh.weight[t] = sh.weight[t + kThreads] = sh.count[t] = 0;
+            for (uint32_t i = t; i < kBins; i += kThreads) sh.weight[i] = sh.count[i] = 0;
             if (t == 0) {
                 sh.listed = sh.staged = sh.in_bins = sh.in_weight = 0;
                 sh.first_bin = sh.last_bin = kAll;
             }
             __syncthreads();
-            visit(unordered(lo), unordered(hi), [&](uint32_t e0, uint32_t e1, float f0, float f1) {
-                const auto count = [&](float f) {
-                    const uint32_t bin = (hi - ordered(f)) >> shift;
-                    atomicAdd(&sh.count[bin >> 1], bin & 1 ? 65536u : 1u);
-                    if (!by_count) {
-                        float w;
-                        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(f - scale.base, scale.chi, scale.magic - 49152.f)));
-                        atomicAdd(&sh.weight[bin], __float2uint_rn(w * unit));
+            {
+                const float from = unordered(lo), to = unordered(hi), chi = scale.chi, log_unit = scale.magic - 49152.f + __log2f(unit);
+                const auto fill = [&](auto weighted) {
+#pragma unroll 1
+                    for (uint32_t v = lane; v < vecs; v += 32) {
+                        float f[VEC];
+                        widen(mine[v], f, T());
+#pragma unroll
+                        for (uint32_t i = 0; i < VEC; ++i) {
+                            if (!(f[i] >= from && f[i] <= to)) continue;
+                            const uint32_t bin = (hi - ordered(f[i])) >> shift;
+                            atomicAdd(&sh.count[bin], 1);
+                            if constexpr (decltype(weighted)::value) {
+                                float w;
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(f[i] - scale.base, chi, log_unit)));
+                                atomicAdd(&sh.weight[bin], __float2uint_rn(w));
+                            }
+                        }
                     }
                 };
-                if (e0 != kAll) count(f0);
-                if (e1 != kAll) count(f1);
-            });
-            cluster.sync();
-            uint32_t n0 = 0, n1 = 0, w0 = 0, w1 = 0;  // of bins 2 t and 2 t + 1
-            for (uint32_t k = 0; k < C; ++k) {
-                const Shared* o = cluster.map_shared_rank(&sh, k);
-                const uint32_t n = o->count[t];
-                const uint2 w = *reinterpret_cast<const uint2*>(&o->weight[2 * t]);
-                n0 += n & 0xFFFFu;
-                n1 += n >> 16;
-                w0 += w.x;
-                w1 += w.y;
+                if (by_count) fill(std::false_type()); else fill(std::true_type());
             }
-            uint64_t all;
-            const uint64_t upto = block_scan((uint64_t)(n0 + n1) << 32 | (w0 + w1), sh.scan, &all);  // (neither passes 32 bits)
-            const uint32_t n_before = (uint32_t)(upto >> 32) - n0 - n1, w_before = (uint32_t)upto - w0 - w1;
-            // the first and the last bin in which the target can be reached
-            const uint32_t aim = by_count ? (uint32_t)target - above_count
-                                          : (uint32_t)((target > above ? (float)(target - above) : 0.f) / kUnit * unit);
-            const uint32_t slack = by_count ? 0 : kMargin;
-            const uint32_t x0 = by_count ? n_before : w_before, x1 = x0 + (by_count ? n0 : w0), x2 = x1 + (by_count ? n1 : w1);
-            const auto reach = [&](uint32_t a, uint32_t* bin) {
-                if (x0 < a && x2 >= a) *bin = 2 * t + (x1 < a);
-            };
-            reach(max(aim, slack + 1) - slack, &sh.first_bin);
-            reach(aim + slack, &sh.last_bin);
-            __syncthreads();
-            const uint32_t bins = (hi - lo) >> shift;
-            if (by_count && sh.first_bin == kAll) {  // all of it is kept (k is more than there are)
+            cluster.sync();
+            // The first CTA adds the tables up and finds the bins in which the target can be reached.
+            if (rank == 0) {
+                constexpr uint32_t kEach = kBins / kThreads;
+                uint32_t n[kEach] = {}, w[kEach] = {}, n_all = 0, w_all = 0;
+                for (uint32_t k = 0; k < C; ++k) {
+                    const Shared* o = cluster.map_shared_rank(&sh, k);
+#pragma unroll
+                    for (uint32_t i = 0; i < kEach; ++i) {
+                        n[i] += o->count[kEach * t + i];
+                        w[i] += o->weight[kEach * t + i];
+                    }
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < kEach; ++i) {
+                    n_all += n[i];
+                    w_all += w[i];
+                }
+                uint64_t all;
+                const uint64_t upto = block_scan((uint64_t)n_all << 32 | w_all, sh.scan, &all);  // (neither passes 32 bits)
+                const uint32_t n_before = (uint32_t)(upto >> 32) - n_all, w_before = (uint32_t)upto - w_all;
+                const uint32_t aim = by_count ? (uint32_t)target - above_count
+                                              : (uint32_t)((target > above ? (float)(target - above) : 0.f) / kUnit * unit);
+                const uint32_t slack = by_count ? 0 : kMargin, from = max(aim, slack + 1) - slack, to = aim + slack;
+                uint32_t have = by_count ? n_before : w_before;
+#pragma unroll
+                for (uint32_t i = 0; i < kEach; ++i) {
+                    const uint32_t next = have + (by_count ? n[i] : w[i]);
+                    if (have < from && next >= from) sh.first_bin = kEach * t + i;
+                    if (have < to && next >= to) sh.last_bin = kEach * t + i;
+                    have = next;
+                }
+                __syncthreads();
+                const uint32_t bins = (hi - lo) >> shift, last = min(sh.last_bin, bins), first = min(sh.first_bin, last);
+                uint32_t in_n = 0, in_w = 0, below = n_before;
+#pragma unroll
+                for (uint32_t i = 0; i < kEach; ++i) {
+                    const uint32_t bin = kEach * t + i;
+                    if (bin == first) sh.above_bins = below;
+                    in_n += bin >= first && bin <= last ? n[i] : 0;
+                    in_w += bin >= first && bin <= last ? w[i] : 0;
+                    below += n[i];
+                }
+                if (in_n) atomicAdd(&sh.in_bins, in_n);
+                if (in_w) atomicAdd(&sh.in_weight, in_w);
+                __syncthreads();
+                if (t < C) {
+                    Range r;
+                    r.lo = last == bins ? lo : hi - (((last + 1) << shift) - 1);
+                    r.hi = hi - (first << shift);
+                    r.end = hi - (((first + 1) << shift) - 1);
+                    r.in = sh.in_bins;
+                    r.above_count = sh.above_bins;
+                    r.none = by_count && sh.first_bin == kAll;
+                    r.narrowed = first != 0 || last != bins;
+                    r.more = first != last;
+                    r.grow = (float)kWhole / ((float)sh.in_weight + 2.f * (float)kMargin);
+                    cluster.map_shared_rank(&sh, t)->range = r;
+                }
+            }
+            cluster.sync();  // (the tables have been read, too: the list takes their place)
+            const Range range = sh.range;
+            if (range.none) {  // all of it is kept
                 if (set.top_p == 1.f) {
                     cut = {max(lo, least), kAll, 0, 0, 0, 0};
                     found = true;
@@ -685,38 +748,28 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                 unit = (float)kWhole * kUnit / (float)z;
                 continue;
             }
-            const uint32_t last_bin = min(sh.last_bin, bins), first_bin = min(sh.first_bin, last_bin);
-            const bool in0 = 2 * t >= first_bin && 2 * t <= last_bin, in1 = 2 * t + 1 >= first_bin && 2 * t + 1 <= last_bin;
-            if (in0 || in1) {
-                atomicAdd(&sh.in_bins, (in0 ? n0 : 0) + (in1 ? n1 : 0));
-                atomicAdd(&sh.in_weight, (in0 ? w0 : 0) + (in1 ? w1 : 0));
-            }
-            if (first_bin >> 1 == t) sh.place = n_before + (first_bin & 1 ? n0 : 0);
-            __syncthreads();
-            const uint32_t in_bins = sh.in_bins, end = hi - (((first_bin + 1) << shift) - 1);  // (of the first bin)
-            const bool narrowed = first_bin != 0 || last_bin != bins;
-            above_count += sh.place;
-            lo = last_bin == bins ? lo : hi - (((last_bin + 1) << shift) - 1);
-            hi -= first_bin << shift;
-            // the weights above them, exactly, by warp
+            above_count += range.above_count;
+            lo = range.lo;
+            hi = range.hi;
+            // the weights above them, exactly, by warp; what lies in them is listed, where it fits
+            const bool fits = range.in <= kList;
             {
                 Weight s = {0.f, 0.f};
-                const float from = unordered(hi);
-                visit(from, m, [&](uint32_t, uint32_t, float f0, float f1) {
-                    add(s, weight_of(f0 > from ? f0 : -kInf));
-                    add(s, weight_of(f1 > from ? f1 : -kInf));
+                const float to = unordered(hi);
+                visit(fits ? unordered(lo) : to, m, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
+                    add(s, weight_of(f0 > to ? f0 : -kInf));
+                    add(s, weight_of(f1 > to ? f1 : -kInf));
+                    if (fits) stage(f0 > to ? kAll : e0, f1 > to ? kAll : e1, f0, f1);
                 });
                 tell_warp(warp_total(fixed(s)));
             }
-            cluster.sync();
-            above = 0;
-            for (uint32_t k = 0; k < C * kWarps; ++k) above += sh.warp_sum[k];
-            if (in_bins <= kList) {
+            if (fits) send_list(); else cluster.sync();
+            above = told_total();
+            if (fits) {
                 // ranked by the first CTA
-                make_list(unordered(lo), unordered(hi));
                 if (rank == 0) {
-                    sort_list(sh.list, sh.stage, in_bins);
-                    const uint32_t limit = by_count ? min(in_bins, (uint32_t)target - above_count) : in_bins;
+                    sort_list(sh.list, sh.stage, range.in);
+                    const uint32_t limit = by_count ? min(range.in, (uint32_t)target - above_count) : range.in;
                     const uint64_t ranked = t < limit ? sh.stage[t] : 0;
                     const uint32_t key = (uint32_t)(ranked >> 32), id = ~(uint32_t)ranked;
                     const uint64_t w = fixed(weight_of(t < limit ? unordered(key) : -kInf));
@@ -809,21 +862,22 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                 cluster.sync();
                 cut = {hi, sh.cut.id, 0, 0, 0, 0};
                 found = true;
-            } else if (by_count || narrowed) {
+            } else if (by_count || range.narrowed || !range.more) {
                 // once more; what is left of the weights makes the whole
-                unit *= (float)kWhole / ((float)sh.in_weight + 2.f * (float)kMargin);
+                unit *= range.grow;
             } else {
                 // a few values of many tokens: on which side of the first bin's end? (the weights down to there tell)
                 Weight s = {0.f, 0.f};
-                visit(unordered(end), m, [&](uint32_t, uint32_t, float f0, float f1) {
+                visit(unordered(range.end), m, [&](uint32_t, uint32_t, float f0, float f1) {
                     add(s, weight_of(f0));
                     add(s, weight_of(f1));
                 });
+                cluster.sync();  // (the sums told before have been read)
                 const uint64_t upto_end = cluster_total(fixed(s));
                 if (upto_end >= target) {
-                    lo = end;
+                    lo = range.end;
                 } else {
-                    hi = end - 1;
+                    hi = range.end - 1;
                     above = upto_end;
                 }
             }
