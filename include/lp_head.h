@@ -229,7 +229,8 @@ lp_status lp_head_project4(const void *x, uint64_t x_stride, const void *x_scale
  * Draw of a token for every logits row, from a given random number. With m the row's largest logit,
  * tau, k, p and q its request's temperature, top-k, top-p and min-p, and the tokens ranked by
  * (logit descending, id ascending):
- *     w    = exp((x - m) / tau), or 0 where (x - m) / tau < -40 ln 2
+ *     w    = exp((x - m) / tau), or 0 where (x - m) / tau < -40 ln 2 (never drawn; in sums over all
+ *            tokens some of these may be left in)
  *     top-k  the first k tokens stay                                    (k <= 0 or >= V: all)
  *     top-p  of these, a token stays while the weights ranked before it add up to less than p times
  *            those of all k; the first one always does                  (p = 1: all)
@@ -239,19 +240,21 @@ lp_status lp_head_project4(const void *x, uint64_t x_stride, const void *x_scale
  *     out_logprob[t] = ln(w / sum of the kept weights) of that token
  * tau = 0 takes the first ranked token (k = 1). Weights and their sums are within 2^-32 of the
  * formula's, so that the token is that of the formula in 64 bits unless one of the comparisons
- * above is nearer than 2^-31 to turning over. A tau below 2^-100 or above 2^100 is taken as that.
+ * above is nearer than 2^-31 (and the weights below 2^-40) to turning over. A tau below 2^-100 or above 2^100 is taken as that.
  *   logits          device, [T][V] of dtype (LP_F32, LP_BF16, LP_F16), V <= LP_MAX_SAMPLE_VOCAB
  *   uniform         device, float[T], in [0, 1)
  *   row_offsets, B  rows of the requests, as in lp_head_process
  *   temperature, top_k, top_p, min_p   device, float[B], int32[B], float[B], float[B], or NULL (1, 0, 1, 0)
  *   out             device out, uint32[T]
  *   out_logprob     device out, float[T], or NULL
- *   workspace       256 bytes: the status word
+ *   workspace       lp_head_sample_workspace_size(T, V) bytes, which grows with both
  * Device checks: every row in a request (LP_ERR_OFFSETS), temperatures finite and not negative
  * (LP_ERR_TEMPERATURE), top_p and min_p within 0..1 and uniform in [0, 1) (LP_ERR_SAMPLING), the
  * row's largest logit finite (LP_ERR_LOGITS: a row of only -inf, or with a NaN or +inf): such a
  * row's token is LP_PAD_TOKEN, its logprob NaN.
  */
+size_t lp_head_sample_workspace_size(uint32_t T, uint32_t V);
+
 lp_status lp_head_sample(const void *logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
                          const float *uniform, const uint32_t *row_offsets, uint32_t B, const float *temperature,
                          const int32_t *top_k, const float *top_p, const float *min_p, uint32_t *out,

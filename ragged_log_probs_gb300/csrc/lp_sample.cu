@@ -1,23 +1,28 @@
 // Draw of the next token (include/lp_head.h): temperature, top-k, top-p and min-p, from a given
 // random number a row.
 //
-// A row belongs to a cluster of up to eight CTAs, each with a slice of it in shared memory, read
-// from HBM once. Weights exp((x - max) / tau) are formed with about 34 correct bits (a table of 256
-// powers, and a short series for what is left of the exponent) and added as pairs of f32 or as
-// integers of 2^-43: the token is a comparison of sums of up to some hundred thousand weights with
-// each other, and f32's rounding would move it in a few rows of a hundred. All three filters keep a
-// prefix of the order (value descending, id ascending), so that what is kept is told by the last
-// kept (value, id):
-//   top-k: each CTA tells a value that enough of its threads' largest reach (a coarse histogram);
-//          what lies above the least of these is listed and ranked by the cluster's first CTA.
+// Two kernels. The first reads the logits once, at HBM's rate: a warp takes a part of 1024 tokens
+// and writes down its largest value, and what the row's setting asks for: the sum of its weights
+// (top-p, or no filter) or some of its lanes' largest values in order (top-k). The second kernel, a
+// cluster of up to eight CTAs a row, decides from that what can be kept, and reads again only the
+// parts that hold some of it, from L2 for the most part; without a filter that is the one part
+// in which the token lies.
+//
+// Weights exp((x - max) / tau) are formed with about 34 correct bits (a table of 256 powers, and a
+// short series for what is left of the exponent) and added as pairs of f32 or as integers of 2^-43:
+// the token is a comparison of sums of up to some hundred thousand weights with each other, and
+// f32's rounding would move it in a few rows of a hundred. All three filters keep a prefix of the
+// order (value descending, id ascending), so that what is kept is told by the last kept (value, id):
+//   top-k: a value that k tokens reach for sure is read from the parts' ordered values; what
+//          lies above it is listed and ranked by the cluster's first CTA.
 //   top-p: what weighs less than (1 - p) Z / V is never kept. Where Z is small the rest is listed
 //          as well. Else, or if it does not fit, a histogram over the values' bits with rounded
 //          weights finds the bins in which p Z can be reached; what lies above them is summed
 //          exactly, what lies in them is listed. Bins of more than fits are cut again; a single
 //          value is cut by id.
-// The draw follows the ids: the kept weights are summed by warp, and the CTA in which u Z falls
-// walks that warp's part once more. CTAs write what the others need into their shared memory
-// before a barrier of the cluster.
+// The draw follows the ids: the kept weights are summed by part, and the first CTA walks the part
+// in which u Z falls. CTAs write what the others need into their shared memory before a barrier
+// of the cluster.
 #include <cooperative_groups.h>
 
 #include <type_traits>
@@ -29,11 +34,13 @@ namespace {
 using namespace lph;
 namespace cg = cooperative_groups;
 
-constexpr uint32_t kThreads = 384, kWarps = kThreads / 32;
-constexpr uint32_t kResident = 3;  // CTAs per SM, with slices of up to 16384 f32
+constexpr uint32_t kPart = 1024;     // tokens of a part
+constexpr uint32_t kMaxParts = (LP_MAX_SAMPLE_VOCAB + 7 + kPart - 1) / kPart;
+constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kScanResident = 4, kDrawResident = 3;  // CTAs per SM
 constexpr uint32_t kMaxCluster = 8;
-constexpr uint32_t kList = kThreads;  // tokens that are ranked
-constexpr uint32_t kBins = 2 * kThreads;
+constexpr uint32_t kList = 384;      // tokens that are ranked
+constexpr uint32_t kBins = 3 * kThreads;
 constexpr uint32_t kBound = 256;
 constexpr uint32_t kTable = 256;
 constexpr uint32_t kLowest = 0x00800000u;  // ordered() of the lowest finite value
@@ -43,6 +50,18 @@ constexpr float kFewWeights = 8.f;   // Z up to which a top-p row's tokens are l
 // Rounded weights of a histogram: all of them make 2^30; what the roundings can add up to.
 constexpr uint32_t kWhole = 1u << 30, kMargin = 1u << 18;
 static_assert(LP_MAX_SAMPLE_VOCAB / 2 + (kWhole >> 16) < kMargin, "half a unit a token, and the weights' f32 errors");
+
+// What the first kernel tells of a part.
+struct Part {
+    uint32_t top;                // ordered() of its largest value (a NaN's is above all)
+    union {
+        uint32_t lanes[3];       // keys that the 4, 16 and 32 largest of its lanes' largest reach (top-k)
+        struct {
+            uint32_t unused, sum_low, sum_high;  // its weights, relative to its own largest value
+        };
+    };
+};
+static_assert(sizeof(Part) == 16, "one access");
 
 struct SampleParams {
     const void* logits;
@@ -55,9 +74,9 @@ struct SampleParams {
     uint32_t* out;
     float* out_logprob;
     uint32_t* status;
+    Part* told;      // [T][parts]
     uint64_t stride;
-    uint32_t T, V, B;
-    uint32_t chunk;  // elements of a warp: whole vectors
+    uint32_t T, V, B, parts;
 };
 
 // A value's bits in the order of the values (both zeros were made one before).
@@ -85,6 +104,7 @@ struct Setting {
     float tau, chi, clo;   // chi + clo = log2(e) / tau
     float top_p, min_p, u;
     uint32_t k;            // 0: off
+    __device__ __forceinline__ bool weighed() const { return ok && !k && (top_p < 1.f || min_p == 0.f); }  // all weights are needed
 };
 
 struct Cut {
@@ -92,11 +112,6 @@ struct Cut {
     uint32_t again;        // the search goes on among keys above `above`, for the weight `target` of `total`
     uint32_t above;
     uint64_t target, total;
-};
-
-struct Told {              // by each CTA
-    uint32_t top;          // ordered() of its largest value (a NaN's is above all)
-    uint32_t share, whole; // keys that ceil(k / CTAs), and k, of its threads' largest reach
 };
 
 struct Range {             // keys among which the cut is
@@ -107,11 +122,6 @@ struct Range {             // keys among which the cut is
     uint32_t none;         // by count: there are not as many
     uint32_t narrowed, more;  // than before; than one bin
     float grow;            // what the rounded weights may be multiplied with
-};
-
-struct Draw {              // where the token is
-    uint64_t start, z;     // the kept weights before the warp that has it, and all
-    uint32_t warp;
 };
 
 struct Shared {
@@ -126,12 +136,11 @@ struct Shared {
         uint64_t stage[kList];   // a CTA's part of the list; the ranked list
     };
     float2 table[kTable];
+    uint64_t part_sum[kMaxParts];  // kept weights (or numbers) of the parts
+    uint32_t part_top[kMaxParts];
     uint64_t scan[kWarps];
-    uint64_t warp_sum[kMaxCluster * kWarps];
-    Told told[kMaxCluster];
     Setting set;
     Cut cut;
-    Draw draw;
     Range range;
     uint32_t listed, staged, place, top;
     uint32_t first_bin, last_bin, in_bins, in_weight, above_bins;
@@ -245,17 +254,20 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* scratch, ui
 }
 
 // Threads that share a key of a list of n, as a power of two, so that n keys keep the CTA busy.
-__device__ __forceinline__ uint32_t sharing(uint32_t n) { return n <= kList / 8 ? 3 : n <= kList / 4 ? 2 : n <= kList / 2 ? 1 : 0; }
+__device__ __forceinline__ uint32_t sharing(uint32_t n) { return n <= kThreads / 8 ? 3 : n <= kThreads / 4 ? 2 : n <= kThreads / 2 ? 1 : 0; }
 // n different keys (n <= kList) of `from` in descending order, to `to`, each ranked by counting the
 // larger ones (200 of them: 1 us; a bitonic sort waits for the CTA at each of 36 steps).
 __device__ __forceinline__ void sort_list(const uint64_t* from, uint64_t* to, uint32_t n) {
-    const uint32_t t = threadIdx.x, shift = sharing(n), at = t >> shift, parts = 1u << shift;
-    const uint64_t key = at < n ? from[at] : 0;
-    uint32_t rank = 0;
+    const uint32_t t = threadIdx.x, shift = sharing(n), parts = 1u << shift;
+    for (uint32_t at = t >> shift; at < n || shift; at += kThreads) {
+        const uint64_t key = at < n ? from[at] : 0;
+        uint32_t rank = 0;
 #pragma unroll 8
-    for (uint32_t j = t & (parts - 1); j < n; j += parts) rank += from[j] > key;
-    for (uint32_t k = 1; k < parts; k *= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, k);
-    if (at < n && (t & (parts - 1)) == 0) to[rank] = key;
+        for (uint32_t j = t & (parts - 1); j < n; j += parts) rank += from[j] > key;
+        for (uint32_t k = 1; k < parts; k *= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, k);
+        if (at < n && (t & (parts - 1)) == 0) to[rank] = key;
+        if (shift) break;  // (all of them: whole warps came here)
+    }
     __syncthreads();
 }
 
@@ -280,6 +292,38 @@ __device__ __forceinline__ void widen(uint4 w, float (&v)[8], T) {
         v[2 * i + 1] = f.y + 0.f;
     }
 }
+
+// A part of a row, in units of aligned vectors: element i of the row is number i + before, a part is
+// 1024 numbers, and what lies outside the row is -inf.
+template <typename T>
+struct Row {
+    static constexpr uint32_t VEC = Vec<T>::kElems, kVecs = kPart / 32 / VEC;  // vectors of a lane
+    const T* x;
+    uint32_t before, V;
+    __device__ __forceinline__ Row(const SampleParams& p, uint32_t row)
+        : x(static_cast<const T*>(p.logits) + (uint64_t)row * p.stride),
+          before((uint32_t)(reinterpret_cast<uintptr_t>(x) / sizeof(T)) % VEC), V(p.V) {}
+    __device__ __forceinline__ T element(uint32_t number) const {
+        return number >= before && number < V + before ? x[number - before] : from_f32<T>(-__builtin_huge_valf());
+    }
+    // vector j of a lane: elements (32 j + lane) VEC + 0, 1, ... of the part
+    __device__ __forceinline__ void load(uint32_t part, uint4 (&w)[kVecs]) const {
+        const uint32_t lane = threadIdx.x & 31, begin = part * kPart;
+        if (begin >= before && begin + kPart <= V + before) {
+            const uint4* from = reinterpret_cast<const uint4*>(x + (begin - before)) + lane;
+#pragma unroll
+            for (uint32_t j = 0; j < kVecs; ++j) w[j] = from[32 * j];
+        } else {
+#pragma unroll
+            for (uint32_t j = 0; j < kVecs; ++j) {
+                T e[VEC];
+#pragma unroll
+                for (uint32_t i = 0; i < VEC; ++i) e[i] = element(begin + (32 * j + lane) * VEC + i);
+                memcpy(&w[j], e, 16);
+            }
+        }
+    }
+};
 
 __device__ __forceinline__ Setting setting_of(const SampleParams& p, uint32_t row, bool report) {
     Setting s = {};
@@ -331,93 +375,111 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return r;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, kResident) k_sample(const SampleParams p) {
-    constexpr uint32_t VEC = Vec<T>::kElems;
-    constexpr float kInf = __builtin_huge_valf();
-    extern __shared__ __align__(16) unsigned char smem_raw[];
-    __shared__ Shared sh;
-    uint4* slice = reinterpret_cast<uint4*>(smem_raw);
-    const cg::cluster_group cluster = cg::this_cluster();
-    const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
-    const uint32_t row = blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    pdl_trigger();
-    const float2 power = t < kTable ? g_table.at[t] : make_float2(0.f, 0.f);
-    if (t < kBound) sh.bound[t] = 0;
-    if (t == 0) sh.staged = sh.listed = sh.top = 0;
-    __syncthreads();
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before others' memory is written to)
-    pdl_wait();
-
-    // The row in units of aligned vectors: element i of the row is number i + before. Slices and the
-    // warps' parts of them are whole vectors; what lies outside the row becomes -inf.
-    const T* x = static_cast<const T*>(p.logits) + (uint64_t)row * p.stride;
-    const uint32_t before = (uint32_t)(reinterpret_cast<uintptr_t>(x) / sizeof(T)) % VEC;
-    const uint32_t vecs = p.chunk / VEC;                     // of a warp
-    const uint32_t begin = (rank * kWarps + warp) * p.chunk; // number of the warp's first element
-    uint4* mine = slice + warp * vecs;
-    const T* values = reinterpret_cast<const T*>(mine);
-    const auto id_of = [&](uint32_t element) { return begin + element - before; };  // of the warp's part
-
-    // ---- 1. read; the largest value, and threads' largest in coarse bins; the setting, by one thread
-    float top = -kInf;
-#pragma unroll 8
-    for (uint32_t v = lane; v < vecs; v += 32) {
-        const uint32_t at = begin + v * VEC;
-        uint4 w;
-        if (at >= before && at + VEC <= p.V + before) {
-            w = *reinterpret_cast<const uint4*>(x + (at - before));
-        } else {
-            T e[VEC];
+__device__ __forceinline__ uint64_t warp_total(uint64_t v) {
 #pragma unroll
-            for (uint32_t i = 0; i < VEC; ++i) {
-                const uint32_t n = at + i;
-                e[i] = n >= before && n < p.V + before ? x[n - before] : from_f32<T>(-kInf);
-            }
-            memcpy(&w, e, 16);
-        }
-        mine[v] = w;
+    for (int k = 16; k > 0; k /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, k);
+    return v;
+}
+
+// ---------------------------------------------------------------- the first kernel: a part a warp
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kScanResident) k_sample_scan(const SampleParams p) {
+    constexpr uint32_t VEC = Row<T>::VEC, kVecs = Row<T>::kVecs;
+    __shared__ float2 table[kTable];
+    const uint32_t t = threadIdx.x, lane = t & 31;
+    table[t] = g_table.at[t];
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();  // (the second kernel waits for this one before it reads what it tells)
+    const uint32_t at = blockIdx.x * kWarps + (t >> 5), row = at / p.parts, part = at - row * p.parts;
+    if (row >= p.T) return;
+    const Row<T> r(p, row);
+    uint4 w[kVecs];
+    r.load(part, w);
+    const Setting set = setting_of(p, row, false);
+    float top = -__builtin_huge_valf();
+#pragma unroll
+    for (uint32_t j = 0; j < kVecs; ++j) {
         float f[VEC];
-        widen(w, f, T());
+        widen(w[j], f, T());
 #pragma unroll
         for (uint32_t i = 0; i < VEC; i += 2) top = max_nan(top, f[i], f[i + 1]);
     }
-    if (t == kThreads - 1) sh.set = setting_of(p, row, rank == 0);
-    __syncwarp();
-    if (t < kTable) sh.table[t] = power;
-    if (top > -kInf) atomicAdd(&sh.bound[bound_bin(top)], 1);
-    const uint32_t warp_top = __reduce_max_sync(0xFFFFFFFFu, ordered(top));  // (max.NaN's NaN is positive)
-    if (lane == 0) atomicMax(&sh.top, warp_top);
+    Part told = {};
+    const uint32_t mine = ordered(top);
+    told.top = __reduce_max_sync(0xFFFFFFFFu, mine);  // (max.NaN's NaN is positive)
+    if (set.k) {
+        // the lanes' largest, sorted
+        uint32_t v = mine;
+#pragma unroll
+        for (uint32_t k = 2; k <= 32; k *= 2)
+#pragma unroll
+            for (uint32_t j = k / 2; j > 0; j /= 2) {
+                const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, v, j);
+                v = ((lane & j) == 0) == ((lane & k) == 0) ? max(v, o) : min(v, o);
+            }
+        told.lanes[0] = __shfl_sync(0xFFFFFFFFu, v, 3);
+        told.lanes[1] = __shfl_sync(0xFFFFFFFFu, v, 15);
+        told.lanes[2] = __shfl_sync(0xFFFFFFFFu, v, 31);
+    } else if (set.weighed() && told.top >= kLowest && told.top < ordered(__builtin_huge_valf())) {
+        const Scale scale = scale_of(unordered(told.top), set);
+        Weight s = {0.f, 0.f};
+#pragma unroll
+        for (uint32_t j = 0; j < kVecs; ++j) {
+            float f[VEC];
+            widen(w[j], f, T());
+            float high = f[0];
+#pragma unroll
+            for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
+            if (!__any_sync(0xFFFFFFFFu, high >= scale.low)) continue;
+#pragma unroll
+            for (uint32_t i = 0; i < VEC; ++i) add(s, weigh(f[i], scale, table));
+        }
+        const uint64_t sum = warp_total(fixed(s));
+        told.sum_low = (uint32_t)sum;
+        told.sum_high = (uint32_t)(sum >> 32);
+    }
+    if (lane == 0) *reinterpret_cast<uint4*>(&p.told[at]) = *reinterpret_cast<const uint4*>(&told);
+}
+
+// ---------------------------------------------------------------- the second kernel: a row a cluster
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const SampleParams p) {
+    constexpr uint32_t VEC = Row<T>::VEC, kVecs = Row<T>::kVecs;
+    constexpr float kInf = __builtin_huge_valf();
+    __shared__ Shared sh;
+    __shared__ __align__(16) T buffers[kWarps][kPart];  // a part each
+    const cg::cluster_group cluster = cg::this_cluster();
+    const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
+    const uint32_t row = blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before others' memory is written to)
+    sh.table[t] = g_table.at[t];
+    sh.bound[t] = 0;
+    if (t == 0) sh.staged = sh.listed = sh.top = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const Row<T> r(p, row);
+    const auto id_of = [&](uint32_t part, uint32_t element) { return part * kPart + element - r.before; };
+
+    // ---- 1. what the parts tell
+    const uint4* told = reinterpret_cast<const uint4*>(p.told + (uint64_t)row * parts);
+    uint4 info[(kMaxParts + kThreads - 1) / kThreads];
+    uint32_t top = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < (kMaxParts + kThreads - 1) / kThreads; ++i) {
+        info[i] = t + i * kThreads < parts ? __ldcg(told + t + i * kThreads) : make_uint4(0, 0, 0, 0);
+        top = max(top, info[i].x);
+    }
+    if (t == 0) sh.set = setting_of(p, row, rank == 0);
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) atomicMax(&sh.top, top);
     __syncthreads();
     const Setting set = sh.set;
+    uint32_t hi = sh.top, lo = kLowest;  // keys below `lo` are not kept
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (warp == 0) {
-        Told told = {sh.top, kLowest, kLowest};
-        if (set.k) {
-            // from the top: lane 0 has the largest bins
-            uint32_t n[kBound / 32], sum = 0;
-#pragma unroll
-            for (uint32_t i = 0; i < kBound / 32; ++i) sum += n[i] = sh.bound[kBound - 1 - (lane * (kBound / 32) + i)];
-            const uint32_t upto = warp_scan(sum), share = (set.k + C - 1) / C;
-            uint32_t have = upto - sum, s = kAll, w = kAll;
-#pragma unroll
-            for (uint32_t i = 0; i < kBound / 32; ++i) {
-                const uint32_t bin = kBound - 1 - (lane * (kBound / 32) + i);
-                if (have < share && have + n[i] >= share) s = bin;
-                if (have < set.k && have + n[i] >= set.k) w = bin;
-                have += n[i];
-            }
-            s = __reduce_min_sync(0xFFFFFFFFu, s);
-            w = __reduce_min_sync(0xFFFFFFFFu, w);
-            told.share = s == kAll ? kLowest : bound_edge(s);
-            told.whole = w == kAll ? kLowest : bound_edge(w);
-        }
-        if (lane < C) cluster.map_shared_rank(&sh, lane)->told[rank] = told;
-    }
-    cluster.sync();
-    const Told told = lane < C ? sh.told[lane] : Told{0, kAll, 0};
-    uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, told.top);
-    uint32_t lo = max(__reduce_min_sync(0xFFFFFFFFu, told.share), __reduce_max_sync(0xFFFFFFFFu, told.whole));  // keys below are not kept
     if (!set.ok || hi < kLowest || hi >= ordered(kInf)) {
         if (rank == 0 && t == 0) {
             if (set.ok) flag(p.status, LP_ERR_LOGITS);
@@ -426,6 +488,8 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         }
         return;
     }
+    // (without a filter, and for the best token, the first CTA is enough)
+    if (rank != 0 && (set.k == 1 || (!set.k && set.top_p == 1.f && set.min_p == 0.f))) return;
     const float m = unordered(hi);
     const Scale scale = scale_of(m, set);
     const auto weight_of = [&](float f) { return weigh(f, scale, sh.table); };
@@ -449,114 +513,197 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
             p.out_logprob[row] = (value - m) / set.tau - lnz;
         }
     };
-    // Visits the warp's elements with values in [from, to], two at a time: body(element, element or
-    // kAll, value, value). Lanes take them out of masks of 32, so that few cost little.
-    const auto visit = [&](float from, float to, auto body) {
-        for (uint32_t v0 = 0; v0 < vecs; v0 += 32 * (32 / VEC)) {
+    // The elements of the parts that hold values of [from, ...], for the warps of the cluster in turn:
+    // body(part, values of a lane's vectors).
+    const auto for_parts = [&](float from, auto body) {
+        const uint32_t key = ordered(from);
+        for (uint32_t part = rank * kWarps + warp; part < parts; part += C * kWarps) {
+            if (sh.part_top[part] < key) continue;
+            uint4 w[kVecs];
+            r.load(part, w);
+            body(part, w);
+        }
+    };
+    // Visits the elements with values in [from, to], two at a time: body(part, element, element or kAll,
+    // value, value), then after(part). Lanes take them out of masks of 32, so that few cost little.
+    const auto visit = [&](float from, float to, auto body, auto after) {
+        for_parts(from, [&](uint32_t part, const uint4 (&w)[kVecs]) {
             uint32_t take = 0;
+            __syncwarp();
 #pragma unroll
-            for (uint32_t j = 0; j < 32 / VEC; ++j) {
-                const uint32_t v = v0 + j * 32 + lane;
-                if (v < vecs) {
-                    float f[VEC];
-                    widen(mine[v], f, T());
-                    float high = f[0];
+            for (uint32_t j = 0; j < kVecs; ++j) {
+                float f[VEC];
+                widen(w[j], f, T());
+                float high = f[0];
 #pragma unroll
-                    for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
-                    if (!__any_sync(__activemask(), high >= from)) continue;
+                for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
+                if (!__any_sync(0xFFFFFFFFu, high >= from)) continue;
+                reinterpret_cast<uint4*>(buffers[warp])[j * 32 + lane] = w[j];
 #pragma unroll
-                    for (uint32_t i = 0; i < VEC; ++i)
-                        if (f[i] >= from && f[i] <= to) take |= 1u << (j * VEC + i);
-                }
+                for (uint32_t i = 0; i < VEC; ++i)
+                    if (f[i] >= from && f[i] <= to) take |= 1u << (j * VEC + i);
             }
+            __syncwarp();
             const auto next = [&] {
                 if (!take) return kAll;
                 const uint32_t b = __ffs(take) - 1;
                 take &= take - 1;
-                return (v0 + b / VEC * 32 + lane) * VEC + b % VEC;
+                return (b / VEC * 32 + lane) * VEC + b % VEC;
             };
             while (__any_sync(0xFFFFFFFFu, take)) {
                 const uint32_t e0 = next(), e1 = next();
-                const float f0 = e0 == kAll ? -kInf : to_f32(values[e0]) + 0.f, f1 = e1 == kAll ? -kInf : to_f32(values[e1]) + 0.f;
-                body(e0, e1, f0, f1);
+                const float f0 = e0 == kAll ? -kInf : to_f32(buffers[warp][e0]) + 0.f, f1 = e1 == kAll ? -kInf : to_f32(buffers[warp][e1]) + 0.f;
+                body(part, e0, e1, f0, f1);
             }
-        }
+            after(part);
+        });
     };
-    const auto warp_total = [&](uint64_t v) {
-#pragma unroll
-        for (int k = 16; k > 0; k /= 2) v += __shfl_xor_sync(0xFFFFFFFFu, v, k);
-        return v;
+    const auto no_more = [](uint32_t) {};
+    // A part's sum, told to all CTAs; those of parts that are not visited stay 0.
+    const auto clear_sums = [&] {
+        for (uint32_t i = t; i < parts; i += kThreads) sh.part_sum[i] = 0;
     };
-    // All weights of the warp's elements.
-    const auto add_all = [&](Weight& s) {
-#pragma unroll 1
-        for (uint32_t v = lane; v < vecs; v += 32) {
-            float f[VEC];
-            widen(mine[v], f, T());
-            float high = f[0];
-#pragma unroll
-            for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
-            if (!__any_sync(__activemask(), high >= scale.low)) continue;
-#pragma unroll
-            for (uint32_t i = 0; i < VEC; ++i) add(s, weight_of(f[i]));
-        }
+    const auto tell = [&](uint32_t part, uint64_t sum) {
+        if (lane < C) cluster.map_shared_rank(&sh, lane)->part_sum[part] = sum;
     };
-    // The warp's sum, told to all.
-    const auto tell_warp = [&](uint64_t sum) {
-        if (lane < C) cluster.map_shared_rank(&sh, lane)->warp_sum[rank * kWarps + warp] = sum;
-    };
-    const auto told_total = [&] {  // of what all warps told
+    const auto told_total = [&] {
         uint64_t sum = 0;
-#pragma unroll
-        for (uint32_t i = 0; i < kMaxCluster * kWarps; i += 32) sum += i + lane < C * kWarps ? sh.warp_sum[i + lane] : 0;
+        for (uint32_t i = lane; i < parts; i += 32) sum += sh.part_sum[i];
         return warp_total(sum);
     };
-    // The sum over all threads of the cluster.
-    const auto cluster_total = [&](uint64_t v) {
-        tell_warp(warp_total(v));
+    // The sum of the weights of values of at least `from`; begins and ends with a barrier of the cluster.
+    const auto sum_from = [&](float from) {
+        cluster.sync();  // (the sums told before have been read)
+        clear_sums();
+        cluster.sync();
+        Weight s = {0.f, 0.f};
+        visit(from, m, [&](uint32_t, uint32_t, uint32_t, float f0, float f1) {
+            add(s, weight_of(f0));
+            add(s, weight_of(f1));
+        }, [&](uint32_t part) {
+            tell(part, warp_total(fixed(s)));
+            s = {0.f, 0.f};
+        });
         cluster.sync();
         return told_total();
     };
-    // Where u Z falls among the warps' sums; by a whole warp.
-    const auto draw_warp = [&] {
-        constexpr uint32_t kEach = kMaxCluster * kWarps / 32;  // of the warps' sums to a lane
-        uint64_t part[kEach], own = 0;
+
+    // ---- 2. the parts' largest; their weights, relative to the row's largest; a bound for the k-th value
 #pragma unroll
-        for (uint32_t i = 0; i < kEach; ++i) {
-            const uint32_t g = lane * kEach + i;
-            part[i] = g < C * kWarps ? sh.warp_sum[g] : 0;
-            own += part[i];
-        }
-        const uint64_t upto = warp_scan(own);
-        Draw d = {0, __shfl_sync(0xFFFFFFFFu, upto, 31), kAll};
-        bool exact;
-        const uint64_t want = part_of(set.u, d.z, &exact);
-        uint64_t below = upto - own;
-#pragma unroll
-        for (uint32_t i = 0; i < kEach; ++i) {
-            if (below <= want && want < below + part[i]) {
-                d.warp = lane * kEach + i;
-                d.start = below;
+    for (uint32_t i = 0; i < (kMaxParts + kThreads - 1) / kThreads; ++i) {
+        const uint32_t part = t + i * kThreads;
+        if (part >= parts) continue;
+        sh.part_top[part] = info[i].x;
+        uint64_t sum = 0;
+        if (set.weighed() && info[i].x >= ordered(scale.low)) {  // (one at least of its tokens can be drawn)
+            // sums are in units of 2^(x (chi + clo) - shift) each: shift of the part, and of the row
+            const Scale own = scale_of(unordered(info[i].x), set);
+            const bool far = own.base != 0.f || scale.base != 0.f;
+            double factor;
+            if (far) {
+                const double c = (double)set.chi + (double)set.clo;
+                const auto origin = [&](const Scale& q) { return q.base != 0.f ? (double)q.base * c : 49152.0 - (double)q.magic; };
+                factor = exp2(origin(own) - origin(scale));
+            } else {
+                const int k = (int)((scale.magic - own.magic) * 256.f);  // shift of the part less that of the row
+                const float2 e = sh.table[k & (kTable - 1)];
+                factor = k < -126 * 256 ? 0.0 : ((double)e.x + (double)e.y) * (double)__uint_as_float((uint32_t)((k >> 8) + 127) << 23);
             }
-            below += part[i];
+            sum = __double2ull_rn((double)((uint64_t)info[i].w << 32 | info[i].z) * factor);
         }
-        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, d.warp != kAll)) - 1;  // (one lane: want < z)
-        d.warp = __shfl_sync(0xFFFFFFFFu, d.warp, src);
-        d.start = __shfl_sync(0xFFFFFFFFu, d.start, src);
-        return d;
-    };
+        sh.part_sum[part] = sum;
+        if (set.k && info[i].x >= kLowest) {
+            // one value of `x`, three more of `y`, twelve of `z` and sixteen of `w` at least
+            const uint32_t key[4] = {info[i].x, info[i].y, info[i].z, info[i].w}, more[4] = {1, 3, 12, 16};
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+                if (key[k] >= kLowest) atomicAdd(&sh.bound[bound_bin(unordered(key[k]))], more[k]);
+        }
+    }
+    __syncthreads();
 
     Shared* lead = cluster.map_shared_rank(&sh, 0);
+    Cut cut = {least, kAll, 0, 0, 0, 0};
+    const auto kept = [&](float f, uint32_t id) {
+        const uint32_t key = ordered(f);
+        return !(key < cut.key || (key == cut.key && id > cut.id));
+    };
+    // The draw, by one CTA, from the parts' sums of kept weights: the part in which u Z falls, and in it
+    // the token, four neighbours to a thread.
+    const auto finish = [&] {
+        const uint32_t each = (parts + 31) / 32;
+        uint64_t own = 0;
+        for (uint32_t i = lane * each; i < min(lane * each + each, parts); ++i) own += sh.part_sum[i];
+        const uint64_t upto = warp_scan(own), z = __shfl_sync(0xFFFFFFFFu, upto, 31);
+        bool exact;
+        const uint64_t want = part_of(set.u, z, &exact);
+        uint64_t below = upto - own;
+        uint32_t part = kAll;
+        if (below <= want && want < upto)
+            for (uint32_t i = lane * each; i < min(lane * each + each, parts); ++i) {
+                if (want < below + sh.part_sum[i]) {
+                    part = i;
+                    break;
+                }
+                below += sh.part_sum[i];
+            }
+        const int src = __ffs(__ballot_sync(0xFFFFFFFFu, part != kAll)) - 1;  // (one lane: want < z)
+        part = __shfl_sync(0xFFFFFFFFu, part, src);
+        below = __shfl_sync(0xFFFFFFFFu, below, src);
+        float f[kPart / kThreads];
+        uint64_t w[kPart / kThreads], here = 0, all;
+#pragma unroll
+        for (uint32_t i = 0; i < kPart / kThreads; ++i) {
+            const uint32_t e = t * (kPart / kThreads) + i;
+            f[i] = to_f32(r.element(part * kPart + e)) + 0.f;
+            const Weight q = weight_of(kept(f[i], id_of(part, e)) ? f[i] : -kInf);
+            w[i] = enough(q) ? fixed(q) : 0;
+            here += w[i];
+        }
+        uint64_t under = block_scan(here, sh.scan, &all) - here;
+        // (these sums are rounded another way than the part's: at its very end the last kept is meant)
+        const uint64_t left = min(want - below, all - 1);
+#pragma unroll
+        for (uint32_t i = 0; i < kPart / kThreads; ++i) {
+            if (under <= left && left < under + w[i]) token_is(id_of(part, t * (kPart / kThreads) + i), f[i], z);
+            under += w[i];
+        }
+    };
+    if (set.k == 1) {
+        // the first token that has the largest value
+        uint32_t first = kAll;
+        for (uint32_t i = lane; i < parts; i += 32)
+            if (sh.part_top[i] == hi) first = min(first, i);
+        first = __reduce_min_sync(0xFFFFFFFFu, first);
+        uint32_t id = kAll;
+#pragma unroll
+        for (uint32_t i = 0; i < kPart / kThreads; ++i) {
+            const uint32_t e = t + i * kThreads;
+            if (to_f32(r.element(first * kPart + e)) + 0.f == m) id = min(id, id_of(first, e));
+        }
+        id = __reduce_min_sync(0xFFFFFFFFu, id);
+        if (lane == 0) sh.scan[warp] = id;
+        __syncthreads();
+        if (t == 0) {
+            for (uint32_t k = 1; k < kWarps; ++k) id = min(id, (uint32_t)sh.scan[k]);
+            token_is(id, m, fixed(most));
+        }
+        return;
+    }
+    if (!set.k && set.top_p == 1.f && set.min_p == 0.f) {
+        finish();
+        return;
+    }
     // Tokens into the CTA's part of the list, and the parts into the first CTA's, which ends with a barrier of
     // the cluster.
-    const auto stage = [&](uint32_t e0, uint32_t e1, float f0, float f1) {
+    const auto stage = [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
         const auto one = [&](uint32_t e, float f) {
             const uint32_t take = __ballot_sync(0xFFFFFFFFu, e != kAll);
             if (!take) return;
             uint32_t at = 0;
             if (lane == 0) at = atomicAdd(&sh.staged, __popc(take));
             at = __shfl_sync(0xFFFFFFFFu, at, 0) + __popc(take & ((1u << lane) - 1));
-            if (e != kAll && at < kList) sh.stage[at] = (uint64_t)ordered(f) << 32 | (uint32_t)~id_of(e);
+            if (e != kAll && at < kList) sh.stage[at] = (uint64_t)ordered(f) << 32 | (uint32_t)~id_of(part, e);
         };
         one(e0, f0);
         one(e1, f1);
@@ -572,17 +719,30 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         cluster.sync();
     };
 
-    Cut cut = {least, kAll, 0, 0, 0, 0};
-    bool drawn = false;  // the first CTA has told where the token is
     if (set.k || set.top_p < 1.f) {
         uint64_t target = set.k;
         bool by_count = set.k != 0, few = set.k <= kList;
         float unit = 1.f;  // of the rounded weights: weights times that
-        if (!by_count) {
-            // ---- 2. the sum of all weights, and from it a bound
-            Weight s = {0.f, 0.f};
-            add_all(s);
-            const uint64_t z = cluster_total(fixed(s));
+        if (by_count) {
+            // from the top: lane 0 has the largest bins
+            if (warp == 0) {
+                uint32_t n[kBound / 32], sum = 0, bin = kAll;
+#pragma unroll
+                for (uint32_t i = 0; i < kBound / 32; ++i) sum += n[i] = sh.bound[kBound - 1 - (lane * (kBound / 32) + i)];
+                uint32_t have = warp_scan(sum) - sum;
+#pragma unroll
+                for (uint32_t i = 0; i < kBound / 32; ++i) {
+                    if (have < set.k && have + n[i] >= set.k) bin = kBound - 1 - (lane * (kBound / 32) + i);
+                    have += n[i];
+                }
+                bin = __reduce_min_sync(0xFFFFFFFFu, bin);
+                if (lane == 0) sh.place = bin == kAll ? kLowest : bound_edge(bin);
+            }
+            __syncthreads();
+            lo = sh.place;
+            cluster.sync();  // (the bins: the list takes their place)
+        } else {
+            const uint64_t z = told_total();
             target = reached_at(set.top_p, z);
             const float sum = (float)z / kUnit;
             unit = (float)kWhole / sum;
@@ -593,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         }
         // ---- 3. all that can be kept in one list?
         if (few) {
-            visit(unordered(lo), m, stage);
+            visit(unordered(lo), m, stage, no_more);
             send_list();
             const uint32_t n = lead->listed;
             if (n <= kList) {
@@ -603,34 +763,45 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                     return;
                 }
                 sort_list(sh.list, sh.stage, n);
-                const uint64_t ranked = t < n ? sh.stage[t] : 0;
-                const bool counts = t < n && (!set.k || t < set.k);
-                const Weight weight = weight_of(counts ? unordered((uint32_t)(ranked >> 32)) : -kInf);
-                const uint64_t w = fixed(weight);
-                uint64_t all, kept;
-                const uint64_t below = block_scan(w, sh.scan, &all) - w;
+                // (two ranks to a thread, neighbours)
+                uint64_t w[2], all, kept_all;
+                bool fine[2];
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i) {
+                    const uint32_t at = 2 * t + i;
+                    const Weight q = weight_of(at < n && (!set.k || at < set.k) ? unordered((uint32_t)(sh.stage[at] >> 32)) : -kInf);
+                    w[i] = fixed(q);
+                    fine[i] = w[i] && enough(q);
+                }
+                const uint64_t below = block_scan(w[0] + w[1], sh.scan, &all) - w[0] - w[1];
                 if (by_count) target = set.top_p < 1.f ? reached_at(set.top_p, all) : ~0ull;
-                if (t < n) sh.list[t] = w;  // (the list is in `stage` now)
-                (void)block_scan(w && enough(weight) && below < target, sh.scan, &kept);
-                // The first `kept` of them, in the order of their ids: what lies below each.
-                const uint32_t n_kept = (uint32_t)kept, shift = sharing(n_kept), at = t >> shift, parts = 1u << shift;
-                const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
-                const uint32_t not_id = (uint32_t)entry;
-                uint64_t under = 0, z = 0;
+                const uint32_t keep = (fine[0] && below < target) + (fine[1] && below + w[0] < target);
+#pragma unroll
+                for (uint32_t i = 0; i < 2; ++i)
+                    if (2 * t + i < n) sh.list[2 * t + i] = w[i];  // (the list is in `stage` now)
+                (void)block_scan(keep, sh.scan, &kept_all);
+                // The first of them, in the order of their ids: what lies below each.
+                const uint32_t n_kept = (uint32_t)kept_all, shift = sharing(n_kept), share = 1u << shift;
+                for (uint32_t at = t >> shift; at < n_kept || shift; at += kThreads) {
+                    const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
+                    const uint32_t not_id = (uint32_t)entry;
+                    uint64_t under = 0, z = 0;
 #pragma unroll 8
-                for (uint32_t j = t & (parts - 1); j < n_kept; j += parts) {
-                    const uint64_t wj = sh.list[j];
-                    under += (uint32_t)sh.stage[j] > not_id ? wj : 0;
-                    z += wj;
+                    for (uint32_t j = t & (share - 1); j < n_kept; j += share) {
+                        const uint64_t wj = sh.list[j];
+                        under += (uint32_t)sh.stage[j] > not_id ? wj : 0;
+                        z += wj;
+                    }
+                    for (uint32_t k = 1; k < share; k *= 2) {
+                        under += __shfl_xor_sync(0xFFFFFFFFu, under, k);
+                        z += __shfl_xor_sync(0xFFFFFFFFu, z, k);
+                    }
+                    bool exact;
+                    const uint64_t want = part_of(set.u, z, &exact);
+                    if (at < n_kept && (t & (share - 1)) == 0 && under <= want && want < under + sh.list[at])
+                        token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
+                    if (shift) break;
                 }
-                for (uint32_t k = 1; k < parts; k *= 2) {
-                    under += __shfl_xor_sync(0xFFFFFFFFu, under, k);
-                    z += __shfl_xor_sync(0xFFFFFFFFu, z, k);
-                }
-                bool exact;
-                const uint64_t want = part_of(set.u, z, &exact);
-                if (at < n_kept && (t & (parts - 1)) == 0 && under <= want && want < under + sh.list[at])
-                    token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
                 asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
                 return;
             }
@@ -642,8 +813,9 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         for (int n_hist = 0; n_hist < 64 && !found; ++n_hist) {  // (a bound only: each cuts the range)
             uint32_t shift = 0;
             while ((hi - lo) >> shift >= kBins) ++shift;
-            if (read) cluster.sync();
+            if (read) cluster.sync(); else __syncthreads();
             read = true;
+            clear_sums();
             for (uint32_t i = t; i < kBins; i += kThreads) sh.weight[i] = sh.count[i] = 0;
             if (t == 0) {
                 sh.listed = sh.staged = sh.in_bins = sh.in_weight = 0;
@@ -653,22 +825,24 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
             {
                 const float from = unordered(lo), to = unordered(hi), chi = scale.chi, log_unit = scale.magic - 49152.f + __log2f(unit);
                 const auto fill = [&](auto weighted) {
-#pragma unroll 1
-                    for (uint32_t v = lane; v < vecs; v += 32) {
-                        float f[VEC];
-                        widen(mine[v], f, T());
+                    for_parts(from, [&](uint32_t, const uint4 (&w)[kVecs]) {
 #pragma unroll
-                        for (uint32_t i = 0; i < VEC; ++i) {
-                            if (!(f[i] >= from && f[i] <= to)) continue;
-                            const uint32_t bin = (hi - ordered(f[i])) >> shift;
-                            atomicAdd(&sh.count[bin], 1);
-                            if constexpr (decltype(weighted)::value) {
-                                float w;
-                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fmaf(f[i] - scale.base, chi, log_unit)));
-                                atomicAdd(&sh.weight[bin], __float2uint_rn(w));
+                        for (uint32_t j = 0; j < kVecs; ++j) {
+                            float f[VEC];
+                            widen(w[j], f, T());
+#pragma unroll
+                            for (uint32_t i = 0; i < VEC; ++i) {
+                                if (!(f[i] >= from && f[i] <= to)) continue;
+                                const uint32_t bin = (hi - ordered(f[i])) >> shift;
+                                atomicAdd(&sh.count[bin], 1);
+                                if constexpr (decltype(weighted)::value) {
+                                    float e;
+                                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(f[i] - scale.base, chi, log_unit)));
+                                    atomicAdd(&sh.weight[bin], __float2uint_rn(e));
+                                }
                             }
                         }
-                    }
+                    });
                 };
                 if (by_count) fill(std::false_type()); else fill(std::true_type());
             }
@@ -740,9 +914,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                     found = true;
                     break;
                 }
-                Weight s = {0.f, 0.f};
-                add_all(s);
-                const uint64_t z = cluster_total(fixed(s));
+                const uint64_t z = sum_from(unordered(kLowest));
                 by_count = false;
                 target = reached_at(set.top_p, z);
                 unit = (float)kWhole * kUnit / (float)z;
@@ -756,12 +928,14 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
             {
                 Weight s = {0.f, 0.f};
                 const float to = unordered(hi);
-                visit(fits ? unordered(lo) : to, m, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
+                visit(fits ? unordered(lo) : to, m, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
                     add(s, weight_of(f0 > to ? f0 : -kInf));
                     add(s, weight_of(f1 > to ? f1 : -kInf));
-                    if (fits) stage(f0 > to ? kAll : e0, f1 > to ? kAll : e1, f0, f1);
+                    if (fits) stage(part, f0 > to ? kAll : e0, f1 > to ? kAll : e1, f0, f1);
+                }, [&](uint32_t part) {
+                    tell(part, warp_total(fixed(s)));
+                    s = {0.f, 0.f};
                 });
-                tell_warp(warp_total(fixed(s)));
             }
             if (fits) send_list(); else cluster.sync();
             above = told_total();
@@ -770,37 +944,36 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                 if (rank == 0) {
                     sort_list(sh.list, sh.stage, range.in);
                     const uint32_t limit = by_count ? min(range.in, (uint32_t)target - above_count) : range.in;
-                    const uint64_t ranked = t < limit ? sh.stage[t] : 0;
-                    const uint32_t key = (uint32_t)(ranked >> 32), id = ~(uint32_t)ranked;
-                    const uint64_t w = fixed(weight_of(t < limit ? unordered(key) : -kInf));
-                    uint64_t sum, kept;
-                    const uint64_t below = above + block_scan(w, sh.scan, &sum) - w;
+                    uint64_t w[2], sum, kept_all;
+#pragma unroll
+                    for (uint32_t i = 0; i < 2; ++i)
+                        w[i] = fixed(weight_of(2 * t + i < limit ? unordered((uint32_t)(sh.stage[2 * t + i] >> 32)) : -kInf));
+                    const uint64_t below = above + block_scan(w[0] + w[1], sh.scan, &sum) - w[0] - w[1];
                     uint64_t goal = target;
                     if (by_count) goal = set.top_p < 1.f ? reached_at(set.top_p, above + sum) : ~0ull;
-                    const bool keep = t < limit && below < goal;
-                    (void)block_scan(keep, sh.scan, &kept);
-                    Cut c = {kAll, 0, 1, hi, goal, above + sum};  // reached among larger values
-                    Draw d = {};
-                    if (kept) {
-                        const uint64_t last = sh.stage[kept - 1];
-                        c = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0, 0};
-                        if (set.min_p == 0.f) {  // the warps' sums are complete with these
-                            if (keep && w)
-                                atomicAdd(reinterpret_cast<unsigned long long*>(&sh.warp_sum[(id + before) / p.chunk]), (unsigned long long)w);
-                            __syncthreads();
-                            d = draw_warp();
+                    const bool keep[2] = {2 * t < limit && below < goal, 2 * t + 1 < limit && below + w[0] < goal};
+                    (void)block_scan(keep[0] + keep[1], sh.scan, &kept_all);
+                    cut = {kAll, 0, 1, hi, goal, above + sum};  // reached among larger values
+                    if (kept_all) {
+                        const uint64_t last = sh.stage[kept_all - 1];
+                        cut = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0, 0};
+                        if (set.min_p == 0.f) {  // the parts' sums are complete with these
+#pragma unroll
+                            for (uint32_t i = 0; i < 2; ++i)
+                                if (keep[i] && w[i])
+                                    atomicAdd(reinterpret_cast<unsigned long long*>(&sh.part_sum[(~(uint32_t)sh.stage[2 * t + i] + r.before) / kPart]),
+                                              (unsigned long long)w[i]);
                         }
                     }
-                    if (t < C) {
-                        Shared* o = cluster.map_shared_rank(&sh, t);
-                        o->cut = c;
-                        o->draw = d;
-                    }
+                    if (t < C) cluster.map_shared_rank(&sh, t)->cut = cut;
                 }
                 cluster.sync();
                 cut = sh.cut;
                 found = cut.again == 0;
-                drawn = found && set.min_p == 0.f;
+                if (found && set.min_p == 0.f) {
+                    if (rank == 0) finish();
+                    return;
+                }
                 if (cut.again) {  // once more, by weight, among the larger values
                     by_count = false;
                     target = cut.target;
@@ -827,37 +1000,34 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                     if (one) j = min(j, (goal - above + one - 1) / one);
                 }
                 // the j-th of them, counted by warp in the order of the ids
-                uint32_t here = 0;
-                visit(unordered(hi), unordered(hi), [&](uint32_t e0, uint32_t e1, float, float) { here += (e0 != kAll) + (e1 != kAll); });
-                here = __reduce_add_sync(0xFFFFFFFFu, here);
                 cluster.sync();  // (the sums have been read)
-                tell_warp(here);
+                clear_sums();
                 cluster.sync();
-                uint64_t before_me = 0;
-                for (uint32_t k = 0; k < rank * kWarps + warp; ++k) before_me += sh.warp_sum[k];
-                if (before_me < j && j <= before_me + here) {
-                    uint32_t left = (uint32_t)(j - before_me);
-                    for (uint32_t v0 = 0; v0 < vecs && left; v0 += 32) {
-                        const uint32_t v = v0 + lane;
-                        uint32_t take = 0;
-                        if (v < vecs) {
-                            float f[VEC];
-                            widen(mine[v], f, T());
-#pragma unroll
-                            for (uint32_t i = 0; i < VEC; ++i) take |= (ordered(f[i]) == hi ? 1u : 0u) << i;
-                        }
-                        const uint32_t c = __popc(take), cum = warp_scan(c), sum = __shfl_sync(0xFFFFFFFFu, cum, 31);
-                        if (left > sum) {
-                            left -= sum;
+                uint32_t here = 0;
+                visit(unordered(hi), unordered(hi), [&](uint32_t, uint32_t e0, uint32_t e1, float, float) { here += (e0 != kAll) + (e1 != kAll); },
+                      [&](uint32_t part) {
+                          tell(part, __reduce_add_sync(0xFFFFFFFFu, here));
+                          here = 0;
+                      });
+                cluster.sync();
+                if (rank == 0 && warp == 0) {
+                    // the part that has it, and its place there
+                    uint64_t left = j;
+                    uint32_t part = 0;
+                    while (part < parts && left > sh.part_sum[part]) left -= sh.part_sum[part++];
+                    uint32_t id = kAll;
+                    for (uint32_t e0 = 0; part < parts && e0 < kPart; e0 += 32) {
+                        const bool is = to_f32(r.element(part * kPart + e0 + lane)) + 0.f == unordered(hi);
+                        const uint32_t who = __ballot_sync(0xFFFFFFFFu, is), n = __popc(who);
+                        if (left > n) {
+                            left -= n;
                             continue;
                         }
-                        if (cum >= left && cum - c < left) {
-                            for (uint32_t skip = left - (cum - c) - 1; skip; --skip) take &= take - 1;
-                            const uint32_t id = id_of(v * VEC + __ffs(take) - 1);
-                            for (uint32_t k = 0; k < C; ++k) cluster.map_shared_rank(&sh, k)->cut.id = id;
-                        }
-                        left = 0;
+                        if (is && __popc(who & ((2u << lane) - 1)) == (uint32_t)left) id = id_of(part, e0 + lane);
+                        break;
                     }
+                    id = __reduce_min_sync(0xFFFFFFFFu, id);
+                    if (lane < C) cluster.map_shared_rank(&sh, lane)->cut.id = id;
                 }
                 cluster.sync();
                 cut = {hi, sh.cut.id, 0, 0, 0, 0};
@@ -867,13 +1037,7 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
                 unit *= range.grow;
             } else {
                 // a few values of many tokens: on which side of the first bin's end? (the weights down to there tell)
-                Weight s = {0.f, 0.f};
-                visit(unordered(range.end), m, [&](uint32_t, uint32_t, float f0, float f1) {
-                    add(s, weight_of(f0));
-                    add(s, weight_of(f1));
-                });
-                cluster.sync();  // (the sums told before have been read)
-                const uint64_t upto_end = cluster_total(fixed(s));
+                const uint64_t upto_end = sum_from(unordered(range.end));
                 if (upto_end >= target) {
                     lo = range.end;
                 } else {
@@ -885,92 +1049,42 @@ __global__ void __launch_bounds__(kThreads, kResident) k_sample(const SamplePara
         if (least > cut.key) cut = {least, kAll, 0, 0, 0, 0};
     }
 
-    // ---- 5. the kept weights by warp, in the order of the ids, and the draw
-    const auto kept = [&](float f, uint32_t id) {
-        const uint32_t key = ordered(f);
-        return !(key < cut.key || (key == cut.key && id > cut.id));
-    };
-    if (!drawn) {
-        Weight s = {0.f, 0.f};
-        if (cut.key == kLowest && set.min_p == 0.f) {
-            add_all(s);
-        } else {
-            visit(unordered(cut.key), m, [&](uint32_t e0, uint32_t e1, float f0, float f1) {
-                const Weight a = weight_of(e0 != kAll && kept(f0, id_of(e0)) ? f0 : -kInf);
-                const Weight b = weight_of(e1 != kAll && kept(f1, id_of(e1)) ? f1 : -kInf);
-                if (enough(a)) add(s, a);
-                if (enough(b)) add(s, b);
-            });
-        }
-        const uint64_t sum = warp_total(fixed(s));
-        tell_warp(sum);
-        cluster.sync();
-    }
-    // (no one writes to or reads from other CTAs from here on)
-    const Draw draw = drawn ? sh.draw : draw_warp();
-    if (draw.warp / kWarps != rank) return;
-    // The CTA that has it walks the warp's part, a few neighbours to a thread.
-    bool exact;
-    const uint64_t want = part_of(set.u, draw.z, &exact) - draw.start;
-    const uint32_t each = (vecs + kThreads - 1) / kThreads, from = (draw.warp % kWarps) * vecs, number = draw.warp * p.chunk - before;
-    const uint32_t v_begin = min(t * each, vecs), v_end = min(v_begin + each, vecs);
-    const auto weights = [&](uint32_t v, uint64_t (&w)[VEC], float (&f)[VEC]) {
-        widen(slice[from + v], f, T());
-#pragma unroll
-        for (uint32_t i = 0; i < VEC; ++i) {
-            const Weight q = weight_of(kept(f[i], number + v * VEC + i) ? f[i] : -kInf);
-            w[i] = enough(q) ? fixed(q) : 0;
-        }
-    };
-    uint64_t here = 0, all;
-    for (uint32_t v = v_begin; v < v_end; ++v) {
-        float f[VEC];
-        uint64_t w[VEC];
-        weights(v, w, f);
-#pragma unroll
-        for (uint32_t i = 0; i < VEC; ++i) here += w[i];
-    }
-    const uint64_t below = block_scan(here, sh.scan, &all) - here;
-    // (these sums are rounded another way than the warp's: at its very end the last kept is meant)
-    uint64_t left = min(want, all - 1);
-    if (left < below || left >= below + here) return;
-    left -= below;
-    for (uint32_t v = v_begin; v < v_end; ++v) {
-        float f[VEC];
-        uint64_t w[VEC];
-        weights(v, w, f);
-#pragma unroll
-        for (uint32_t i = 0; i < VEC; ++i) {
-            if (left < w[i]) {
-                token_is(number + v * VEC + i, f[i], draw.z);
-                return;
-            }
-            left -= w[i];
-        }
-    }
+    // ---- 5. the kept weights by part
+    cluster.sync();  // (the sums told before have been read)
+    clear_sums();
+    cluster.sync();
+    Weight s = {0.f, 0.f};
+    visit(unordered(cut.key), m, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
+        const Weight a = weight_of(e0 != kAll && kept(f0, id_of(part, e0)) ? f0 : -kInf);
+        const Weight b = weight_of(e1 != kAll && kept(f1, id_of(part, e1)) ? f1 : -kInf);
+        if (enough(a)) add(s, a);
+        if (enough(b)) add(s, b);
+    }, [&](uint32_t part) {
+        tell(part, warp_total(fixed(s)));
+        s = {0.f, 0.f};
+    });
+    cluster.sync();
+    if (rank == 0) finish();
 }
 
-constexpr uint32_t vecs_of(uint32_t V, uint32_t ctas, uint32_t vec) {  // of a warp
-    return (V + vec - 1 + ctas * kWarps * vec - 1) / (ctas * kWarps * vec);
-}
-static_assert(vecs_of(LP_MAX_SAMPLE_VOCAB, kMaxCluster, 4) * kWarps * 16 + sizeof(Shared) <= 227 * 1024, "the longest rows fit");
+uint32_t parts_of(uint32_t V) { return (V + 7 + kPart - 1) / kPart; }  // (rows begin up to seven elements past a boundary)
 
 template <typename T>
-lp_status launch_sample(SampleParams p, lp_stream_t stream) {
-    constexpr uint32_t kVec = Vec<T>::kElems;
-    static std::atomic<uint64_t> smem_set;
-    // CTAs of a row: slices of about 16384 elements at most (the smallest number that gives them), eight at most
+lp_status launch_sample(const SampleParams& p, lp_stream_t stream) {
+    const uint64_t warps = (uint64_t)p.T * p.parts;
+    const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), kThreads, 0, stream, 1, p);
+    if (st != LP_OK) return st;
+    // CTAs of a row: two parts to a warp, eight CTAs at most
     uint32_t c = 1;
-    while (c < kMaxCluster && p.V > c * 16384) c *= 2;
-    const uint32_t vecs = vecs_of(p.V, c, kVec);
-    p.chunk = vecs * kVec;
-    auto kernel = k_sample<T>;
-    constexpr size_t kMost = (size_t)vecs_of(LP_MAX_SAMPLE_VOCAB, kMaxCluster, kVec) * kWarps * 16;
-    if (!allow_smem(reinterpret_cast<const void*>(kernel), kMost, &smem_set)) return LP_ERR_CUDA;
-    return launch(kernel, dim3(p.T * c), kThreads, (size_t)vecs * kWarps * 16, stream, c, p);
+    while (c < kMaxCluster && c * kWarps * 2 < p.parts) c *= 2;
+    return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, 0, stream, c, p);
 }
 
 }  // namespace
+
+extern "C" size_t lp_head_sample_workspace_size(uint32_t T, uint32_t V) {
+    return kHeaderBytes + (size_t)T * parts_of(V) * sizeof(Part);
+}
 
 extern "C" lp_status lp_head_sample(const void* logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
                                     const float* uniform, const uint32_t* row_offsets, uint32_t B,
@@ -986,7 +1100,8 @@ extern "C" lp_status lp_head_sample(const void* logits, uint32_t dtype, uint32_t
         !aligned_to(temperature, 4) || !aligned_to(top_k, 4) || !aligned_to(top_p, 4) || !aligned_to(min_p, 4) ||
         !aligned_to(out, 4) || !aligned_to(out_logprob, 4))
         return LP_ERR_SHAPE;
-    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < kHeaderBytes) return LP_ERR_WORKSPACE;
+    if ((uint64_t)T * parts_of(V) > 0x7FFFFFFFu) return LP_ERR_SHAPE;
+    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < lp_head_sample_workspace_size(T, V)) return LP_ERR_WORKSPACE;
     SampleParams p = {};
     p.logits = logits;
     p.uniform = uniform;
@@ -998,6 +1113,8 @@ extern "C" lp_status lp_head_sample(const void* logits, uint32_t dtype, uint32_t
     p.out = out;
     p.out_logprob = out_logprob;
     p.status = static_cast<uint32_t*>(workspace);
+    p.told = reinterpret_cast<Part*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
+    p.parts = parts_of(V);
     p.stride = stride;
     p.T = T;
     p.V = V;

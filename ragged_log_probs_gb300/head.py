@@ -44,6 +44,8 @@ def _declare(lib: ctypes.CDLL) -> None:
     lib.lp_head_process.argtypes = [vp, u32, u32, u32, u64, vp, u32, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, u32,
                                     vp, u64, u32, vp, vp, u64, vp, sz, vp]
     lib.lp_head_process.restype = ctypes.c_int
+    lib.lp_head_sample_workspace_size.argtypes = [u32, u32]
+    lib.lp_head_sample_workspace_size.restype = sz
     lib.lp_head_sample.argtypes = [vp, u32, u32, u32, u64, vp, vp, u32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.lp_head_sample.restype = ctypes.c_int
     lib.lp_head_fp4_scale_bytes.argtypes = [u32, u32, u32]
@@ -85,21 +87,25 @@ def _load():
     return module
 
 
-def head_workspace_size(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0) -> int:
+def head_workspace_size(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0, draws: int = 0,
+                        vocab: int = 0) -> int:
     """Bytes of scratch that serve every call of up to these sizes: ``project`` with adapters of
     that rank over T rows, ``process_logits`` of that many requests with that many history
-    tokens in all (0: only the status word)."""
+    tokens in all, ``sample`` of that many rows of logits of that vocabulary (0: only the status
+    word)."""
     lib = _pkg().load()
     n = int(lib.lp_head_workspace_size(T, rank))
     if n == 0:
         raise ValueError(f"rank {rank} exceeds {LP_MAX_RANK}")
-    return max(n, int(lib.lp_head_process_workspace_size(requests, history)))
+    return max(n, int(lib.lp_head_process_workspace_size(requests, history)),
+               int(lib.lp_head_sample_workspace_size(draws, vocab)))
 
 
-def new_head_workspace(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0, device=None) -> torch.Tensor:
+def new_head_workspace(T: int = 0, rank: int = 0, requests: int = 0, history: int = 0, device=None, draws: int = 0,
+                       vocab: int = 0) -> torch.Tensor:
     """A zeroed workspace (uint8) of ``head_workspace_size``. Its status word collects the
     bits of every call that is given it, until ``clear_status``; ``read_status`` reads it."""
-    return torch.zeros(head_workspace_size(T, rank, requests, history), dtype=torch.uint8,
+    return torch.zeros(head_workspace_size(T, rank, requests, history, draws, vocab), dtype=torch.uint8,
                        device=torch.device("cuda") if device is None else device)
 
 
@@ -275,7 +281,8 @@ def sample(logits: torch.Tensor, uniform: torch.Tensor, row_offsets: Optional[to
     tokens; of these the fewest that hold ``top_p`` of their probability; of these those with at
     least ``min_p`` of the best one's. ``out_logprob`` (float32 [T]) receives the token's logprob in
     what was left. A row without a distribution (nothing but -inf, or a NaN or +inf) gives
-    -1 and NaN and sets LP_ERR_LOGITS; ``read_status`` reads the workspace's bits."""
+    -1 and NaN and sets LP_ERR_LOGITS; ``read_status`` reads the workspace's bits. ``workspace``: see
+    ``new_head_workspace(draws=T, vocab=V)``."""
     native = _native or _load()
     if stream is not None:
         with torch.cuda.stream(stream):

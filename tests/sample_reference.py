@@ -10,7 +10,8 @@ SMALLEST = -40.0 * math.log(2.0)
 
 def draw(x, u, tau=1.0, k=0, p=1.0, q=0.0):
     """(token, logprob, margin) of one row [V]: margin is how far, relative to the sums they are compared with,
-    the nearest comparison that decides the token is from turning over (inf: none could)."""
+    the nearest comparison that decides the token is from turning over (inf: none could), less the share of the
+    weights below the smallest, which sums may hold or not."""
     x = x.double() + 0.0
     V = x.numel()
     m = float(x.max()) if V else math.nan
@@ -21,6 +22,7 @@ def draw(x, u, tau=1.0, k=0, p=1.0, q=0.0):
     margin = math.inf
     d = (x - m) / tau
     w = torch.where(d >= SMALLEST, torch.exp(d), torch.zeros_like(d))
+    light = float(torch.exp(d[d < SMALLEST]).sum()) / float(w.sum())
     order = torch.sort(x, descending=True, stable=True).indices
     if 0 < k < V:
         order = order[:k]
@@ -46,4 +48,4 @@ def draw(x, u, tau=1.0, k=0, p=1.0, q=0.0):
     if inner.numel():
         margin = min(margin, float((inner - u * z).abs().min()) / z if u > 0.0 else math.inf)
     t = int(ids[at])
-    return t, float(d[t]) - math.log(z), margin
+    return t, float(d[t]) - math.log(z), margin - (light if u > 0.0 else 0.0)

@@ -27,7 +27,7 @@ def _built():
 
 def run(x, u, tau=None, k=None, p=None, q=None, off=None, ws=None, **kw):
     t = lambda v, d: None if v is None else torch.tensor(v, dtype=d, device="cuda")
-    ws = lp.new_head_workspace() if ws is None else ws
+    ws = lp.new_head_workspace(draws=x.shape[0], vocab=x.shape[1]) if ws is None else ws
     logprob = torch.full((x.shape[0],), 7.0, device="cuda")
     x = x if x.is_cuda else x.cuda()
     got = lp.sample(x, t(u, F32), t(off, torch.int32), t(tau, F32), t(k, torch.int32), t(p, F32), t(q, F32),
@@ -241,7 +241,7 @@ def test_streams_graphs_and_repetition():
     x = logits(T, V, BF16, seed=12).cuda()
     u = torch.tensor(uniforms(T), device="cuda")
     p, k = torch.full((T,), 0.9, device="cuda"), torch.arange(T, dtype=torch.int32, device="cuda") * 40
-    ws = [lp.new_head_workspace() for _ in range(2)]
+    ws = [lp.new_head_workspace(draws=T, vocab=V) for _ in range(2)]
     want = lp.sample(x, u, top_p=p, top_k=k, workspace=ws[0])
     torch.cuda.synchronize()
     outs, streams = [torch.zeros(T, dtype=torch.int32, device="cuda") for _ in range(2)], [torch.cuda.Stream() for _ in range(2)]
@@ -269,7 +269,7 @@ def test_rows_past_32_bits():
     x.fill_(-3.0)
     x[-2:] = logits(2, V, F16, seed=13).cuda()
     u = torch.full((T,), 0.37, device="cuda")
-    got = lp.sample(x, u, top_p=torch.full((T,), 0.5, device="cuda"), workspace=lp.new_head_workspace()).tolist()
+    got = lp.sample(x, u, top_p=torch.full((T,), 0.5, device="cuda"), workspace=lp.new_head_workspace(draws=T, vocab=V)).tolist()
     for t in (T - 2, T - 1, 0):
         token, _, margin = ref.draw(x[t].cpu(), torch.tensor(0.37).item(), p=0.5)
         assert got[t] == token or margin < NEAR

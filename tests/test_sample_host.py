@@ -11,7 +11,7 @@ from tests.test_head_host import DTYPE, E4M3, F32, FAKE, NULL, SHAPE, WORKSPACE,
 
 
 def _sample(lib, x=FAKE, dtype=F32, T=4, V=100, xs=100, u=FAKE, off=None, B=4, tau=FAKE, k=FAKE, p=FAKE, q=FAKE, out=FAKE,  # noqa: F811
-            lw=FAKE, ws=FAKE, wsb=256):
+            lw=FAKE, ws=FAKE, wsb=4096):
     return lib.lp_head_sample(x, dtype, T, V, xs, u, off, B, tau, k, p, q, out, lw, ws, wsb, None)
 
 
@@ -26,7 +26,13 @@ def test_refusals(lib):  # noqa: F811
     for name in ("x", "u", "off", "tau", "k", "p", "q", "out", "lw"):
         for by in (1, 2, 3):
             assert _sample(lib, **{name: FAKE + by}) == SHAPE
-    assert _sample(lib, ws=None) == WORKSPACE and _sample(lib, wsb=255) == WORKSPACE and _sample(lib, ws=FAKE + 128) == WORKSPACE
+    assert _sample(lib, ws=None) == WORKSPACE and _sample(lib, wsb=319) == WORKSPACE and _sample(lib, ws=FAKE + 128) == WORKSPACE
+
+
+def test_workspace_size(lib):  # noqa: F811
+    f = lib.lp_head_sample_workspace_size
+    assert f(0, 0) == 256 and f(4, 100) == 256 + 4 * 16 and f(1, 1017) == 256 + 16 and f(1, 1018) == 256 + 32
+    assert f(2 ** 31, 393216) == 256 + 2 ** 31 * 385 * 16
 
 
 def test_new_error_codes(lib):  # noqa: F811
