@@ -824,6 +824,8 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             __syncthreads();
             {
                 const float from = unordered(lo), to = unordered(hi), chi = scale.chi, log_unit = scale.magic - 49152.f + __log2f(unit);
+                const uint32_t tables = (uint32_t)__cvta_generic_to_shared(sh.weight);
+                // (the additions are predicated: no branch for a token that is not counted)
                 const auto fill = [&](auto weighted) {
                     for_parts(from, [&](uint32_t, const uint4 (&w)[kVecs]) {
 #pragma unroll
@@ -832,13 +834,16 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                             widen(w[j], f, T());
 #pragma unroll
                             for (uint32_t i = 0; i < VEC; ++i) {
-                                if (!(f[i] >= from && f[i] <= to)) continue;
-                                const uint32_t bin = (hi - ordered(f[i])) >> shift;
-                                atomicAdd(&sh.count[bin], 1);
+                                const uint32_t in = f[i] >= from && f[i] <= to, at = tables + ((hi - ordered(f[i])) >> shift) * 4;
                                 if constexpr (decltype(weighted)::value) {
                                     float e;
                                     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(f[i] - scale.base, chi, log_unit)));
-                                    atomicAdd(&sh.weight[bin], __float2uint_rn(e));
+                                    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+                                                 "@p red.shared.add.u32 [%0], %1;\n\t@p red.shared.add.u32 [%0 + %4], %2;\n\t}"
+                                                 ::"r"(at), "r"(__float2uint_rn(e)), "r"(1), "r"(in), "n"(kBins * 4) : "memory");
+                                } else {
+                                    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.add.u32 [%0 + %3], %1;\n\t}"
+                                                 ::"r"(at), "r"(1), "r"(in), "n"(kBins * 4) : "memory");
                                 }
                             }
                         }
@@ -940,7 +945,9 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             if (fits) send_list(); else cluster.sync();
             above = told_total();
             if (fits) {
-                // ranked by the first CTA
+                // ranked by the first CTA (by weight it ends there: the bins hold the cut for sure)
+                const bool last = !by_count && set.min_p == 0.f;
+                if (last && rank != 0) return;
                 if (rank == 0) {
                     sort_list(sh.list, sh.stage, range.in);
                     const uint32_t limit = by_count ? min(range.in, (uint32_t)target - above_count) : range.in;
@@ -953,6 +960,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     if (by_count) goal = set.top_p < 1.f ? reached_at(set.top_p, above + sum) : ~0ull;
                     const bool keep[2] = {2 * t < limit && below < goal, 2 * t + 1 < limit && below + w[0] < goal};
                     (void)block_scan(keep[0] + keep[1], sh.scan, &kept_all);
+                    if (!by_count && kept_all == 0) kept_all = 1;  // (the margin would have been passed: cannot be)
                     cut = {kAll, 0, 1, hi, goal, above + sum};  // reached among larger values
                     if (kept_all) {
                         const uint64_t last = sh.stage[kept_all - 1];
@@ -964,6 +972,11 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                                     atomicAdd(reinterpret_cast<unsigned long long*>(&sh.part_sum[(~(uint32_t)sh.stage[2 * t + i] + r.before) / kPart]),
                                               (unsigned long long)w[i]);
                         }
+                    }
+                    if (last) {
+                        __syncthreads();
+                        finish();
+                        return;
                     }
                     if (t < C) cluster.map_shared_rank(&sh, t)->cut = cut;
                 }
@@ -1074,9 +1087,11 @@ lp_status launch_sample(const SampleParams& p, lp_stream_t stream) {
     const uint64_t warps = (uint64_t)p.T * p.parts;
     const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), kThreads, 0, stream, 1, p);
     if (st != LP_OK) return st;
-    // CTAs of a row: two parts to a warp, eight CTAs at most
+    // CTAs of a row: two parts to a warp, eight CTAs at most; of many rows, so many that all CTAs are twice
+    // what the device holds at once (256 rows of 128256, all with top-p: 8 CTAs 221 us, 4 198, 2 239; one row 32, 38, 52).
+    const uint32_t slots = 2 * kDrawResident * (uint32_t)sm_count();
     uint32_t c = 1;
-    while (c < kMaxCluster && c * kWarps * 2 < p.parts) c *= 2;
+    while (c < kMaxCluster && c * kWarps * 2 < p.parts && 2 * (uint64_t)c * p.T <= slots + slots / 4) c *= 2;
     return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, 0, stream, c, p);
 }
 
