@@ -40,16 +40,16 @@ constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kScanResident = 4, kDrawResident = 3;  // CTAs per SM
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kList = 384;      // tokens that are ranked
-constexpr uint32_t kBins = 3 * kThreads;
+constexpr uint32_t kBins = 32;
 constexpr uint32_t kBound = 256;
 constexpr uint32_t kTable = 256;
 constexpr uint32_t kLowest = 0x00800000u;  // ordered() of the lowest finite value
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kUnit = 8796093022208.f;  // 2^43: weights as integers, the largest one is about that
 constexpr float kFewWeights = 8.f;   // Z up to which a top-p row's tokens are listed at once
-// Rounded weights of a histogram: all of them make 2^30; what the roundings can add up to.
-constexpr uint32_t kWhole = 1u << 30, kMargin = 1u << 18;
-static_assert(LP_MAX_SAMPLE_VOCAB / 2 + (kWhole >> 16) < kMargin, "half a unit a token, and the weights' f32 errors");
+// What a histogram's sums of f32 weights can be off by, of the whole: 2^-18 and less (an exponent of 40
+// rounded to 2^-19, times ln 2, and the sums of some hundred).
+constexpr float kSlack = 1.f / 65536.f;
 
 // What the first kernel tells of a part.
 struct Part {
@@ -109,19 +109,19 @@ struct Setting {
 
 struct Cut {
     uint32_t key, id;      // kept: a larger key, or this one with an id up to this
-    uint32_t again;        // the search goes on among keys above `above`, for the weight `target` of `total`
+    uint32_t again;        // the search goes on among keys above `above`, for the weight `target`
     uint32_t above;
-    uint64_t target, total;
+    uint64_t target;
 };
 
 struct Range {             // keys among which the cut is
     uint32_t lo, hi;
     uint32_t end;          // the least key of the first bin
-    uint32_t in;           // how many they hold
-    uint32_t above_count;  // how many lie above them, in the histogram's range
+    uint32_t above_count;  // how many lie above them, in the histogram's range (by count)
     uint32_t none;         // by count: there are not as many
+    uint32_t fits;         // no more than a list holds
     uint32_t narrowed, more;  // than before; than one bin
-    float grow;            // what the rounded weights may be multiplied with
+    float above, slip;     // by weight: what lies above them, and what that can be off by
 };
 
 struct Shared {
@@ -129,12 +129,8 @@ struct Shared {
         uint64_t list[kList];    // key << 32 | ~id; the ranked tokens' weights
         uint32_t bound[kBound];  // (before the list)
     };
-    union {
-        struct {
-            uint32_t weight[kBins], count[kBins];
-        };
-        uint64_t stage[kList];   // a CTA's part of the list; the ranked list
-    };
+    uint64_t stage[kList];       // a CTA's part of the list; the ranked list
+    float bin_sum[kMaxCluster][kBins];
     float2 table[kTable];
     uint64_t part_sum[kMaxParts];  // kept weights (or numbers) of the parts
     uint32_t part_top[kMaxParts];
@@ -142,8 +138,8 @@ struct Shared {
     Setting set;
     Cut cut;
     Range range;
+    uint32_t edge[3];
     uint32_t listed, staged, place, top;
-    uint32_t first_bin, last_bin, in_bins, in_weight, above_bins;
 };
 
 // 2^(j / 256) as pairs of f32, at compile time, by the exponential's series.
@@ -450,7 +446,8 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     constexpr uint32_t VEC = Row<T>::VEC, kVecs = Row<T>::kVecs;
     constexpr float kInf = __builtin_huge_valf();
     __shared__ Shared sh;
-    __shared__ __align__(16) T buffers[kWarps][kPart];  // a part each
+    __shared__ __align__(16) unsigned char buffers[kWarps][4 * kPart];  // a part each, or 32 sums of each lane
+    T* const buffer = reinterpret_cast<T*>(buffers[threadIdx.x >> 5]);
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t row = blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
@@ -538,21 +535,22 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
 #pragma unroll
                 for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
                 if (!__any_sync(0xFFFFFFFFu, high >= from)) continue;
-                reinterpret_cast<uint4*>(buffers[warp])[j * 32 + lane] = w[j];
+                reinterpret_cast<uint4*>(buffer)[j * 32 + lane] = w[j];
 #pragma unroll
                 for (uint32_t i = 0; i < VEC; ++i)
-                    if (f[i] >= from && f[i] <= to) take |= 1u << (j * VEC + i);
+                    if ((f[i] >= from) & (f[i] <= to)) take |= 1u << (j * VEC + i);
             }
             __syncwarp();
-            const auto next = [&] {
-                if (!take) return kAll;
-                const uint32_t b = __ffs(take) - 1;
+            const auto next = [&] {  // (without branches)
+                const uint32_t b = __ffs(take) - 1, e = (b / VEC * 32 + lane) * VEC + b % VEC;
+                const bool some = take != 0;
                 take &= take - 1;
-                return (b / VEC * 32 + lane) * VEC + b % VEC;
+                return some ? e : kAll;
             };
             while (__any_sync(0xFFFFFFFFu, take)) {
                 const uint32_t e0 = next(), e1 = next();
-                const float f0 = e0 == kAll ? -kInf : to_f32(buffers[warp][e0]) + 0.f, f1 = e1 == kAll ? -kInf : to_f32(buffers[warp][e1]) + 0.f;
+                const float x0 = to_f32(buffer[min(e0, kPart - 1)]) + 0.f, x1 = to_f32(buffer[min(e1, kPart - 1)]) + 0.f;
+                const float f0 = e0 == kAll ? -kInf : x0, f1 = e1 == kAll ? -kInf : x1;
                 body(part, e0, e1, f0, f1);
             }
             after(part);
@@ -623,10 +621,10 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     __syncthreads();
 
     Shared* lead = cluster.map_shared_rank(&sh, 0);
-    Cut cut = {least, kAll, 0, 0, 0, 0};
+    Cut cut = {least, kAll, 0, 0, 0};
     const auto kept = [&](float f, uint32_t id) {
         const uint32_t key = ordered(f);
-        return !(key < cut.key || (key == cut.key && id > cut.id));
+        return (key > cut.key) | ((key == cut.key) & (id <= cut.id));
     };
     // The draw, by one CTA, from the parts' sums of kept weights: the part in which u Z falls, and in it
     // the token, four neighbours to a thread.
@@ -722,7 +720,6 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     if (set.k || set.top_p < 1.f) {
         uint64_t target = set.k;
         bool by_count = set.k != 0, few = set.k <= kList;
-        float unit = 1.f;  // of the rounded weights: weights times that
         if (by_count) {
             // from the top: lane 0 has the largest bins
             if (warp == 0) {
@@ -745,7 +742,6 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             const uint64_t z = told_total();
             target = reached_at(set.top_p, z);
             const float sum = (float)z / kUnit;
-            unit = (float)kWhole / sum;
             // kept tokens weigh (1 - p) Z / V at least (with room for the roundings here)
             const float f = m + set.tau * (__logf((1.f - set.top_p) * sum / (float)p.V) - 0.02f) - fabsf(m) * 1e-6f;
             lo = f > -3e38f ? min(max(ordered(f + 0.f), kLowest), hi) : kLowest;
@@ -808,149 +804,172 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
         }
         // ---- 4. the value at which the target is reached, by histograms over [lo, hi]
         bool found = false, read = few;  // whether others may still read the tables and the list
-        uint64_t above = 0;              // weight of the keys above hi, and (by count) their number
-        uint32_t above_count = 0;
+        uint32_t above_count = 0;        // by count: of the keys above hi
+        float rough = 0.f, slip = 0.f;   // by weight: their weight, and what that can be off by
         for (int n_hist = 0; n_hist < 64 && !found; ++n_hist) {  // (a bound only: each cuts the range)
-            uint32_t shift = 0;
-            while ((hi - lo) >> shift >= kBins) ++shift;
+            // 32 bins of equal width, and from the second time on (or where that is all of f32) of equally many
+            // keys: what is left is within an octave mostly, and a cut at 0 would be neared 32-fold at a time.
+            const float from = unordered(lo), to = unordered(hi), per_bin = 31.99f / (to - from);
+            const bool even = n_hist == 0 && to - from < 1e38f && to - from > 1e-30f && !(by_count && lo == kLowest);
+            const uint32_t shift = 27 - min(__clz(hi - lo | 1), 27);
+            const auto bin_of = [&](float f, auto equal_width) {  // (decreasing in f)
+                if constexpr (decltype(equal_width)::value) return min((uint32_t)((to - f) * per_bin), kBins - 1);
+                else return min((hi - ordered(f)) >> shift, kBins - 1);
+            };
+            const auto bin_at = [&](float f) { return even ? bin_of(f, std::true_type()) : bin_of(f, std::false_type()); };
             if (read) cluster.sync(); else __syncthreads();
             read = true;
             clear_sums();
-            for (uint32_t i = t; i < kBins; i += kThreads) sh.weight[i] = sh.count[i] = 0;
-            if (t == 0) {
-                sh.listed = sh.staged = sh.in_bins = sh.in_weight = 0;
-                sh.first_bin = sh.last_bin = kAll;
-            }
-            __syncthreads();
+            if (t == 0) sh.listed = sh.staged = 0;
             {
-                const float from = unordered(lo), to = unordered(hi), chi = scale.chi, log_unit = scale.magic - 49152.f + __log2f(unit);
-                const uint32_t tables = (uint32_t)__cvta_generic_to_shared(sh.weight);
-                // (the additions are predicated: no branch for a token that is not counted)
-                const auto fill = [&](auto weighted) {
+                // A lane adds to sums of its own (bin by lane: each in the lane's bank), without atomics, which
+                // take two clocks a lane: 27000 tokens that can be kept, 13500 clocks of eight CTAs with them.
+                // (by count: 2^0; no branches below, which cost this loop as much as all the rest)
+                const float chi = by_count ? 0.f : scale.chi, shift_of = by_count ? 0.f : scale.magic - 49152.f;
+                float* const sums = reinterpret_cast<float*>(buffers[warp]) + lane;
+#pragma unroll
+                for (uint32_t i = 0; i < kBins / 4; ++i) reinterpret_cast<uint4*>(buffers[warp])[i * 32 + lane] = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+                const auto fill = [&](auto equal_width) {
                     for_parts(from, [&](uint32_t, const uint4 (&w)[kVecs]) {
 #pragma unroll
                         for (uint32_t j = 0; j < kVecs; ++j) {
                             float f[VEC];
                             widen(w[j], f, T());
+                            float high = f[0];
+#pragma unroll
+                            for (uint32_t i = 1; i < VEC; ++i) high = fmaxf(high, f[i]);
+                            if (!__any_sync(0xFFFFFFFFu, high >= from)) continue;
 #pragma unroll
                             for (uint32_t i = 0; i < VEC; ++i) {
-                                const uint32_t in = f[i] >= from && f[i] <= to, at = tables + ((hi - ordered(f[i])) >> shift) * 4;
-                                if constexpr (decltype(weighted)::value) {
-                                    float e;
-                                    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(f[i] - scale.base, chi, log_unit)));
-                                    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\t"
-                                                 "@p red.shared.add.u32 [%0], %1;\n\t@p red.shared.add.u32 [%0 + %4], %2;\n\t}"
-                                                 ::"r"(at), "r"(__float2uint_rn(e)), "r"(1), "r"(in), "n"(kBins * 4) : "memory");
-                                } else {
-                                    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p red.shared.add.u32 [%0 + %3], %1;\n\t}"
-                                                 ::"r"(at), "r"(1), "r"(in), "n"(kBins * 4) : "memory");
-                                }
+                                float e;
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(f[i] - scale.base, chi, shift_of)));
+                                const bool in = (f[i] >= from) & (f[i] <= to);
+                                sums[bin_of(f[i], equal_width) * 32] += in ? e : 0.f;
                             }
                         }
                     });
                 };
-                if (by_count) fill(std::false_type()); else fill(std::true_type());
+                if (even) fill(std::true_type()); else fill(std::false_type());
+                __syncthreads();
+                // the CTA's, four bins a warp, to the first CTA
+#pragma unroll
+                for (uint32_t b = 0; b < kBins / kWarps; ++b) {
+                    const uint32_t bin = warp * (kBins / kWarps) + b;
+                    float sum = 0.f;
+#pragma unroll
+                    for (uint32_t k = 0; k < kWarps; ++k) sum += reinterpret_cast<const float*>(buffers[k])[bin * 32 + lane];
+#pragma unroll
+                    for (int k = 16; k > 0; k /= 2) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
+                    if (lane == 0) lead->bin_sum[rank][bin] = sum;
+                }
             }
             cluster.sync();
-            // The first CTA adds the tables up and finds the bins in which the target can be reached.
+            // The first CTA finds the bins in which the target can be reached.
             if (rank == 0) {
-                constexpr uint32_t kEach = kBins / kThreads;
-                uint32_t n[kEach] = {}, w[kEach] = {}, n_all = 0, w_all = 0;
-                for (uint32_t k = 0; k < C; ++k) {
-                    const Shared* o = cluster.map_shared_rank(&sh, k);
+                float own = 0.f;
+                for (uint32_t k = 0; k < C; ++k) own += sh.bin_sum[k][lane];
+                float upto = own;
 #pragma unroll
-                    for (uint32_t i = 0; i < kEach; ++i) {
-                        n[i] += o->count[kEach * t + i];
-                        w[i] += o->weight[kEach * t + i];
+                for (int k = 1; k < 32; k *= 2) {
+                    const float o = __shfl_up_sync(0xFFFFFFFFu, upto, k);
+                    if (lane >= k) upto += o;
+                }
+                // (numbers are exact: fewer than 2^24)
+                const float aim = by_count ? (float)((uint32_t)target - above_count) : fmaxf((float)target / kUnit - rough, 0.f);
+                const float slack = by_count ? 0.f : slip + kSlack * (__shfl_sync(0xFFFFFFFFu, upto, 31) + rough / 64.f);  // (the aim is a difference of f32)
+                const uint32_t bins = bin_at(from);
+                const uint32_t can = __ballot_sync(0xFFFFFFFFu, upto >= aim - slack), must = __ballot_sync(0xFFFFFFFFu, upto >= aim + slack);
+                const uint32_t last = min(must ? __ffs(must) - 1 : bins, bins), first = min(can ? __ffs(can) - 1 : last, last);
+                // The least keys of bins `last`, `first` and the one above it, by a warp each: 32 keys at a time.
+                if (warp < 3) {
+                    const uint32_t bin = warp == 0 ? last : warp == 1 ? first : first - 1;
+                    uint32_t low = lo, n = hi - lo + 1;  // it is among n keys from `low` on
+                    while (n > 1) {
+                        const uint32_t step = (n - 1) / 32 + 1, key = low + min(lane * step, n - 1);
+                        const uint32_t below = __popc(__ballot_sync(0xFFFFFFFFu, lane * step < n && bin_at(unordered(key)) > bin));
+                        if (below == 0) break;
+                        const uint32_t past = (below - 1) * step + 1;  // (the next key looked at is one that has it)
+                        low += past;
+                        n = min(step, n - past);
                     }
+                    if (lane == 0) sh.edge[warp] = low;
                 }
-#pragma unroll
-                for (uint32_t i = 0; i < kEach; ++i) {
-                    n_all += n[i];
-                    w_all += w[i];
-                }
-                uint64_t all;
-                const uint64_t upto = block_scan((uint64_t)n_all << 32 | w_all, sh.scan, &all);  // (neither passes 32 bits)
-                const uint32_t n_before = (uint32_t)(upto >> 32) - n_all, w_before = (uint32_t)upto - w_all;
-                const uint32_t aim = by_count ? (uint32_t)target - above_count
-                                              : (uint32_t)((target > above ? (float)(target - above) : 0.f) / kUnit * unit);
-                const uint32_t slack = by_count ? 0 : kMargin, from = max(aim, slack + 1) - slack, to = aim + slack;
-                uint32_t have = by_count ? n_before : w_before;
-#pragma unroll
-                for (uint32_t i = 0; i < kEach; ++i) {
-                    const uint32_t next = have + (by_count ? n[i] : w[i]);
-                    if (have < from && next >= from) sh.first_bin = kEach * t + i;
-                    if (have < to && next >= to) sh.last_bin = kEach * t + i;
-                    have = next;
-                }
-                __syncthreads();
-                const uint32_t bins = (hi - lo) >> shift, last = min(sh.last_bin, bins), first = min(sh.first_bin, last);
-                uint32_t in_n = 0, in_w = 0, below = n_before;
-#pragma unroll
-                for (uint32_t i = 0; i < kEach; ++i) {
-                    const uint32_t bin = kEach * t + i;
-                    if (bin == first) sh.above_bins = below;
-                    in_n += bin >= first && bin <= last ? n[i] : 0;
-                    in_w += bin >= first && bin <= last ? w[i] : 0;
-                    below += n[i];
-                }
-                if (in_n) atomicAdd(&sh.in_bins, in_n);
-                if (in_w) atomicAdd(&sh.in_weight, in_w);
+                const float before = __shfl_sync(0xFFFFFFFFu, upto, first ? first - 1 : 0), below = first ? before : 0.f;
+                const float in = __shfl_sync(0xFFFFFFFFu, upto, last) - below;
                 __syncthreads();
                 if (t < C) {
-                    Range r;
-                    r.lo = last == bins ? lo : hi - (((last + 1) << shift) - 1);
-                    r.hi = hi - (first << shift);
-                    r.end = hi - (((first + 1) << shift) - 1);
-                    r.in = sh.in_bins;
-                    r.above_count = sh.above_bins;
-                    r.none = by_count && sh.first_bin == kAll;
-                    r.narrowed = first != 0 || last != bins;
-                    r.more = first != last;
-                    r.grow = (float)kWhole / ((float)sh.in_weight + 2.f * (float)kMargin);
-                    cluster.map_shared_rank(&sh, t)->range = r;
+                    Range q;
+                    q.lo = last == bins ? lo : sh.edge[0];
+                    q.end = sh.edge[1];
+                    q.hi = first ? sh.edge[2] - 1 : hi;
+                    q.above_count = by_count ? (uint32_t)below : 0u;
+                    q.none = by_count && !can;
+                    // (by weight: as many as the lightest of them would make)
+                    q.fits = by_count ? in <= (float)kList : in * 1.001f <= (float)kList * weight_of(unordered(q.lo)).hi;
+                    q.narrowed = first != 0 || last != bins;
+                    q.more = first != last;
+                    q.above = rough + below;
+                    q.slip = first ? slack : slip;
+                    cluster.map_shared_rank(&sh, t)->range = q;
                 }
             }
-            cluster.sync();  // (the tables have been read, too: the list takes their place)
+            cluster.sync();
             const Range range = sh.range;
             if (range.none) {  // all of it is kept
                 if (set.top_p == 1.f) {
-                    cut = {max(lo, least), kAll, 0, 0, 0, 0};
+                    cut = {max(lo, least), kAll, 0, 0, 0};
                     found = true;
                     break;
                 }
                 const uint64_t z = sum_from(unordered(kLowest));
                 by_count = false;
                 target = reached_at(set.top_p, z);
-                unit = (float)kWhole * kUnit / (float)z;
                 continue;
             }
             above_count += range.above_count;
             lo = range.lo;
             hi = range.hi;
-            // the weights above them, exactly, by warp; what lies in them is listed, where it fits
-            const bool fits = range.in <= kList;
+            const bool fits = range.fits, exact = slip == 0.f && range.slip == 0.f;
+            rough = range.above;
+            slip = range.slip;
+            if (!fits && lo != hi) {
+                if (by_count || range.narrowed || !range.more) continue;  // once more
+                // A few values of many tokens, or few of the weights. On which side of the first bin's end?
+                // (first, what lies above, exactly)
+                const uint64_t upto_there = sum_from(unordered(exact ? range.end : hi + 1));
+                if (exact && upto_there >= target) {
+                    lo = range.end;
+                    continue;
+                }
+                if (exact) hi = range.end - 1;
+                rough = (float)upto_there / kUnit;
+                slip = 0.f;
+                continue;
+            }
+            // the weights above them, exactly, by part; what lies in them is listed, where it fits
             {
                 Weight s = {0.f, 0.f};
-                const float to = unordered(hi);
-                visit(fits ? unordered(lo) : to, m, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
-                    add(s, weight_of(f0 > to ? f0 : -kInf));
-                    add(s, weight_of(f1 > to ? f1 : -kInf));
-                    if (fits) stage(part, f0 > to ? kAll : e0, f1 > to ? kAll : e1, f0, f1);
+                const float border = unordered(hi);
+                visit(fits ? unordered(lo) : border, m, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
+                    add(s, weight_of(f0 > border ? f0 : -kInf));
+                    add(s, weight_of(f1 > border ? f1 : -kInf));
+                    if (fits) stage(part, f0 > border ? kAll : e0, f1 > border ? kAll : e1, f0, f1);
                 }, [&](uint32_t part) {
                     tell(part, warp_total(fixed(s)));
                     s = {0.f, 0.f};
                 });
             }
             if (fits) send_list(); else cluster.sync();
-            above = told_total();
+            const uint64_t above = told_total();
             if (fits) {
                 // ranked by the first CTA (by weight it ends there: the bins hold the cut for sure)
                 const bool last = !by_count && set.min_p == 0.f;
                 if (last && rank != 0) return;
                 if (rank == 0) {
-                    sort_list(sh.list, sh.stage, range.in);
-                    const uint32_t limit = by_count ? min(range.in, (uint32_t)target - above_count) : range.in;
+                    const uint32_t listed = min(sh.listed, kList);
+                    sort_list(sh.list, sh.stage, listed);
+                    const uint32_t limit = by_count ? min(listed, (uint32_t)target - above_count) : listed;
                     uint64_t w[2], sum, kept_all;
 #pragma unroll
                     for (uint32_t i = 0; i < 2; ++i)
@@ -961,10 +980,10 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     const bool keep[2] = {2 * t < limit && below < goal, 2 * t + 1 < limit && below + w[0] < goal};
                     (void)block_scan(keep[0] + keep[1], sh.scan, &kept_all);
                     if (!by_count && kept_all == 0) kept_all = 1;  // (the margin would have been passed: cannot be)
-                    cut = {kAll, 0, 1, hi, goal, above + sum};  // reached among larger values
+                    cut = {kAll, 0, 1, hi, goal};  // reached among larger values
                     if (kept_all) {
                         const uint64_t last = sh.stage[kept_all - 1];
-                        cut = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0, 0};
+                        cut = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0};
                         if (set.min_p == 0.f) {  // the parts' sums are complete with these
 #pragma unroll
                             for (uint32_t i = 0; i < 2; ++i)
@@ -990,12 +1009,11 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                 if (cut.again) {  // once more, by weight, among the larger values
                     by_count = false;
                     target = cut.target;
-                    unit = (float)kWhole * kUnit / (float)cut.total;
                     lo = cut.above + 1;
                     hi = ordered(m);
-                    above = 0;
+                    rough = slip = 0.f;
                 }
-            } else if (lo == hi) {
+            } else {
                 // one value: its first `j` ids are kept
                 const uint64_t one = fixed(weight_of(unordered(hi)));
                 uint64_t j = by_count ? target - above_count : (target - above + one - 1) / one;
@@ -1004,10 +1022,9 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     if (goal <= above) {
                         by_count = false;
                         target = goal;
-                        unit = (float)kWhole * kUnit / (float)z;
-                        lo = hi + 1;
+                                lo = hi + 1;
                         hi = ordered(m);
-                        above = 0;
+                        rough = slip = 0.f;
                         continue;
                     }
                     if (one) j = min(j, (goal - above + one - 1) / one);
@@ -1043,23 +1060,11 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     if (lane < C) cluster.map_shared_rank(&sh, lane)->cut.id = id;
                 }
                 cluster.sync();
-                cut = {hi, sh.cut.id, 0, 0, 0, 0};
+                cut = {hi, sh.cut.id, 0, 0, 0};
                 found = true;
-            } else if (by_count || range.narrowed || !range.more) {
-                // once more; what is left of the weights makes the whole
-                unit *= range.grow;
-            } else {
-                // a few values of many tokens: on which side of the first bin's end? (the weights down to there tell)
-                const uint64_t upto_end = sum_from(unordered(range.end));
-                if (upto_end >= target) {
-                    lo = range.end;
-                } else {
-                    hi = range.end - 1;
-                    above = upto_end;
-                }
             }
         }
-        if (least > cut.key) cut = {least, kAll, 0, 0, 0, 0};
+        if (least > cut.key) cut = {least, kAll, 0, 0, 0};
     }
 
     // ---- 5. the kept weights by part
