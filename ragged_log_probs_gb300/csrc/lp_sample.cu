@@ -39,9 +39,12 @@ constexpr uint32_t kMaxParts = (LP_MAX_SAMPLE_VOCAB + 7 + kPart - 1) / kPart;
 constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kScanResident = 4, kDrawResident = 3;  // CTAs per SM
 constexpr uint32_t kMaxCluster = 8;
-constexpr uint32_t kList = 384;      // tokens that are ranked
+constexpr uint32_t kList = 1024;     // tokens that are ranked
+constexpr uint32_t kRanks = kList / kThreads;  // of a thread, neighbours
+constexpr uint32_t kCounted = 384;   // tokens up to which ranks are counted, and not sorted
+constexpr uint32_t kDrawnByList = 128;  // tokens up to which the draw is made from the list
 constexpr uint32_t kBins = 32;
-constexpr uint32_t kBound = 256;
+constexpr uint32_t kBound = 512;
 constexpr uint32_t kTable = 256;
 constexpr uint32_t kLowest = 0x00800000u;  // ordered() of the lowest finite value
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -86,16 +89,16 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 
-// The coarse bins of the values: eight to an octave from 2^-3 to 2^13 on both sides of 0.
+// The coarse bins of the values: sixteen to an octave from 2^-3 to 2^13 on both sides of 0.
 __device__ __forceinline__ uint32_t bound_bin(float x) {
-    const uint32_t a = (__float_as_uint(x) & 0x7FFFFFFFu) >> 20;
-    const uint32_t i = min(max(a, 992u) - 992u, 127u);
-    return x < 0.f ? 127 - i : 128 + i;
+    const uint32_t a = (__float_as_uint(x) & 0x7FFFFFFFu) >> 19;
+    const uint32_t i = min(max(a, 1984u) - 1984u, 255u);
+    return x < 0.f ? 255 - i : 256 + i;
 }
 __device__ __forceinline__ uint32_t bound_edge(uint32_t bin) {  // ordered() of the least value in it
-    if (bin > 128) return ordered(__uint_as_float((bin - 128 + 992) << 20));
-    if (bin == 128) return ordered(0.f);
-    return bin == 0 ? kLowest : ordered(-__uint_as_float(((993 + 127 - bin) << 20) - 1));
+    if (bin > 256) return ordered(__uint_as_float((bin - 256 + 1984) << 19));
+    if (bin == 256) return ordered(0.f);
+    return bin == 0 ? kLowest : ordered(-__uint_as_float(((1985 + 255 - bin) << 19) - 1));
 }
 
 // What a row is drawn with.
@@ -251,10 +254,29 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* scratch, ui
 
 // Threads that share a key of a list of n, as a power of two, so that n keys keep the CTA busy.
 __device__ __forceinline__ uint32_t sharing(uint32_t n) { return n <= kThreads / 8 ? 3 : n <= kThreads / 4 ? 2 : n <= kThreads / 2 ? 1 : 0; }
-// n different keys (n <= kList) of `from` in descending order, to `to`, each ranked by counting the
-// larger ones (200 of them: 1 us; a bitonic sort waits for the CTA at each of 36 steps).
+// n different keys (n <= kList) of `from` in descending order, to `to`: few are ranked by counting
+// the larger ones (the steps of a sort wait for the CTA), many are sorted in steps of a bitonic network.
 __device__ __forceinline__ void sort_list(const uint64_t* from, uint64_t* to, uint32_t n) {
-    const uint32_t t = threadIdx.x, shift = sharing(n), parts = 1u << shift;
+    const uint32_t t = threadIdx.x;
+    if (n > kCounted) {
+        for (uint32_t i = t; i < kList; i += kThreads) to[i] = i < n ? from[i] : 0;
+        __syncthreads();
+        for (uint32_t k = 1; k < 11 && (1u << (k - 1)) < n; ++k)  // (up to the power of two that holds n)
+            for (uint32_t j = k; j-- > 0;) {
+#pragma unroll
+                for (uint32_t q = t; q < kList / 2; q += kThreads) {
+                    const uint32_t i = (q >> j << (j + 1)) | (q & ((1u << j) - 1)), o = i + (1u << j);
+                    const uint64_t a = to[i], b = to[o];
+                    if ((a < b) == ((i >> k & 1) == 0)) {
+                        to[i] = b;
+                        to[o] = a;
+                    }
+                }
+                __syncthreads();
+            }
+        return;
+    }
+    const uint32_t shift = sharing(n), parts = 1u << shift;
     for (uint32_t at = t >> shift; at < n || shift; at += kThreads) {
         const uint64_t key = at < n ? from[at] : 0;
         uint32_t rank = 0;
@@ -446,14 +468,15 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     constexpr uint32_t VEC = Row<T>::VEC, kVecs = Row<T>::kVecs;
     constexpr float kInf = __builtin_huge_valf();
     __shared__ Shared sh;
-    __shared__ __align__(16) unsigned char buffers[kWarps][4 * kPart];  // a part each, or 32 sums of each lane
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    unsigned char (*const buffers)[4 * kPart] = reinterpret_cast<unsigned char (*)[4 * kPart]>(smem_raw);  // of a warp: a part, or 32 sums a lane
     T* const buffer = reinterpret_cast<T*>(buffers[threadIdx.x >> 5]);
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
     const uint32_t row = blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before others' memory is written to)
     sh.table[t] = g_table.at[t];
-    sh.bound[t] = 0;
+    for (uint32_t i = t; i < kBound; i += kThreads) sh.bound[i] = 0;
     if (t == 0) sh.staged = sh.listed = sh.top = 0;
     __syncthreads();
     pdl_wait();
@@ -626,6 +649,10 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
         const uint32_t key = ordered(f);
         return (key > cut.key) | ((key == cut.key) & (id <= cut.id));
     };
+    const auto add_to_part = [&](uint64_t entry, uint64_t w) {  // of a ranked token
+        if (w)
+            atomicAdd(reinterpret_cast<unsigned long long*>(&sh.part_sum[(~(uint32_t)entry + r.before) / kPart]), (unsigned long long)w);
+    };
     // The draw, by one CTA, from the parts' sums of kept weights: the part in which u Z falls, and in it
     // the token, four neighbours to a thread.
     const auto finish = [&] {
@@ -759,26 +786,41 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     return;
                 }
                 sort_list(sh.list, sh.stage, n);
-                // (two ranks to a thread, neighbours)
-                uint64_t w[2], all, kept_all;
-                bool fine[2];
+                uint64_t w[kRanks], all, kept_all, sum = 0;
+                bool fine[kRanks];
 #pragma unroll
-                for (uint32_t i = 0; i < 2; ++i) {
-                    const uint32_t at = 2 * t + i;
+                for (uint32_t i = 0; i < kRanks; ++i) {
+                    const uint32_t at = kRanks * t + i;
                     const Weight q = weight_of(at < n && (!set.k || at < set.k) ? unordered((uint32_t)(sh.stage[at] >> 32)) : -kInf);
                     w[i] = fixed(q);
                     fine[i] = w[i] && enough(q);
+                    sum += w[i];
                 }
-                const uint64_t below = block_scan(w[0] + w[1], sh.scan, &all) - w[0] - w[1];
+                uint64_t below = block_scan(sum, sh.scan, &all) - sum;
                 if (by_count) target = set.top_p < 1.f ? reached_at(set.top_p, all) : ~0ull;
-                const uint32_t keep = (fine[0] && below < target) + (fine[1] && below + w[0] < target);
+                uint32_t keep = 0;
 #pragma unroll
-                for (uint32_t i = 0; i < 2; ++i)
-                    if (2 * t + i < n) sh.list[2 * t + i] = w[i];  // (the list is in `stage` now)
+                for (uint32_t i = 0; i < kRanks; ++i) {
+                    keep += fine[i] && below < target;
+                    below += w[i];
+                    if (kRanks * t + i < n) sh.list[kRanks * t + i] = w[i];  // (the list is in `stage` now)
+                }
                 (void)block_scan(keep, sh.scan, &kept_all);
-                // The first of them, in the order of their ids: what lies below each.
-                const uint32_t n_kept = (uint32_t)kept_all, shift = sharing(n_kept), share = 1u << shift;
-                for (uint32_t at = t >> shift; at < n_kept || shift; at += kThreads) {
+                const uint32_t n_kept = (uint32_t)kept_all;
+                if (n_kept > kDrawnByList) {
+                    // by the parts' sums, as where there is no list
+                    const uint64_t least_kept = sh.stage[n_kept - 1];
+                    cut = {(uint32_t)(least_kept >> 32), ~(uint32_t)least_kept, 0, 0, 0};
+                    clear_sums();
+                    __syncthreads();
+#pragma unroll
+                    for (uint32_t i = 0; i < kRanks; ++i)
+                        if (kRanks * t + i < n_kept) add_to_part(sh.stage[kRanks * t + i], w[i]);
+                    __syncthreads();
+                    finish();
+                } else {
+                    // The kept in the order of their ids: what lies below each.
+                    const uint32_t shift = sharing(n_kept), share = 1u << shift, at = t >> shift;
                     const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
                     const uint32_t not_id = (uint32_t)entry;
                     uint64_t under = 0, z = 0;
@@ -796,7 +838,6 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     const uint64_t want = part_of(set.u, z, &exact);
                     if (at < n_kept && (t & (share - 1)) == 0 && under <= want && want < under + sh.list[at])
                         token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
-                    if (shift) break;
                 }
                 asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
                 return;
@@ -970,26 +1011,32 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     const uint32_t listed = min(sh.listed, kList);
                     sort_list(sh.list, sh.stage, listed);
                     const uint32_t limit = by_count ? min(listed, (uint32_t)target - above_count) : listed;
-                    uint64_t w[2], sum, kept_all;
+                    uint64_t w[kRanks], own = 0, sum, kept_all;
 #pragma unroll
-                    for (uint32_t i = 0; i < 2; ++i)
-                        w[i] = fixed(weight_of(2 * t + i < limit ? unordered((uint32_t)(sh.stage[2 * t + i] >> 32)) : -kInf));
-                    const uint64_t below = above + block_scan(w[0] + w[1], sh.scan, &sum) - w[0] - w[1];
+                    for (uint32_t i = 0; i < kRanks; ++i) {
+                        const uint32_t at = kRanks * t + i;
+                        w[i] = fixed(weight_of(at < limit ? unordered((uint32_t)(sh.stage[at] >> 32)) : -kInf));
+                        own += w[i];
+                    }
+                    uint64_t below = above + block_scan(own, sh.scan, &sum) - own;
                     uint64_t goal = target;
                     if (by_count) goal = set.top_p < 1.f ? reached_at(set.top_p, above + sum) : ~0ull;
-                    const bool keep[2] = {2 * t < limit && below < goal, 2 * t + 1 < limit && below + w[0] < goal};
-                    (void)block_scan(keep[0] + keep[1], sh.scan, &kept_all);
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (uint32_t i = 0; i < kRanks; ++i) {
+                        keep += kRanks * t + i < limit && below < goal;
+                        below += w[i];
+                    }
+                    (void)block_scan(keep, sh.scan, &kept_all);
                     if (!by_count && kept_all == 0) kept_all = 1;  // (the margin would have been passed: cannot be)
                     cut = {kAll, 0, 1, hi, goal};  // reached among larger values
                     if (kept_all) {
-                        const uint64_t last = sh.stage[kept_all - 1];
-                        cut = {(uint32_t)(last >> 32), ~(uint32_t)last, 0, 0, 0};
+                        const uint64_t least_kept = sh.stage[kept_all - 1];
+                        cut = {(uint32_t)(least_kept >> 32), ~(uint32_t)least_kept, 0, 0, 0};
                         if (set.min_p == 0.f) {  // the parts' sums are complete with these
 #pragma unroll
-                            for (uint32_t i = 0; i < 2; ++i)
-                                if (keep[i] && w[i])
-                                    atomicAdd(reinterpret_cast<unsigned long long*>(&sh.part_sum[(~(uint32_t)sh.stage[2 * t + i] + r.before) / kPart]),
-                                              (unsigned long long)w[i]);
+                            for (uint32_t i = 0; i < kRanks; ++i)
+                                if (kRanks * t + i < kept_all) add_to_part(sh.stage[kRanks * t + i], w[i]);
                         }
                     }
                     if (last) {
@@ -1097,7 +1144,10 @@ lp_status launch_sample(const SampleParams& p, lp_stream_t stream) {
     const uint32_t slots = 2 * kDrawResident * (uint32_t)sm_count();
     uint32_t c = 1;
     while (c < kMaxCluster && c * kWarps * 2 < p.parts && 2 * (uint64_t)c * p.T <= slots + slots / 4) c *= 2;
-    return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, 0, stream, c, p);
+    static std::atomic<uint64_t> smem_set;
+    constexpr size_t kBuffers = (size_t)kWarps * 4 * kPart;
+    if (!allow_smem(reinterpret_cast<const void*>(k_sample_draw<T>), kBuffers, &smem_set)) return LP_ERR_CUDA;
+    return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, kBuffers, stream, c, p);
 }
 
 }  // namespace
