@@ -1,18 +1,19 @@
 // Rows in microscaled 4-bit floating point (include/lp_head.h): quantised in blocks of 16 or
 // 32, and read back as values, all of them or those that an index picks.
 //
-// Quantising is one pass: a thread holds groups of eight neighbouring elements in registers, a
-// block is two or four neighbouring lanes, and (blocks of 16) the row's largest magnitude is
+// Quantising is one pass: a thread holds groups of sixteen neighbouring elements in registers, a
+// block is one or two neighbouring lanes, and (blocks of 16) the row's largest magnitude is
 // reduced before the first scale is formed. Scales are powers of two or have four significant
 // bits, so every quotient below is either exact or rounded once, and a value half way between two
-// codes goes where the formula says. Bound by HBM.
+// codes goes where the formula says. Bound by HBM, and for blocks of 16 nearly as much by the
+// quotients (three operations each).
 #include "lp_head_common.h"
 
 namespace {
 
 using namespace lph;
 
-constexpr int kVec = 8;  // elements of a group: 16 bytes of 16-bit input, 4 bytes of codes
+constexpr int kVec = 16;  // elements of a group: 8 bytes of codes
 
 struct QuantParams {
     const void* x;
@@ -30,27 +31,32 @@ __device__ __forceinline__ uint64_t scale_at(uint32_t row, uint32_t col, uint32_
     return ((uint64_t)(row >> 7) * col_tiles + (col >> 2)) * 512 + (row & 31) * 16 + (row >> 5 & 3) * 4 + (col & 3);
 }
 
-// Eight elements as floats.
-__device__ __forceinline__ void load8(const float* p, bool aligned, float (&v)[kVec]) {
+// Sixteen elements as floats.
+__device__ __forceinline__ void load16(const float* p, bool aligned, float (&v)[kVec]) {
     if (aligned) {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4) {
+            const float4 a = *reinterpret_cast<const float4*>(p + i);
+            v[i] = a.x; v[i + 1] = a.y; v[i + 2] = a.z; v[i + 3] = a.w;
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[i] = p[i];
     }
 }
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool aligned, float (&v)[kVec]) {
+__device__ __forceinline__ void load16(const T* p, bool aligned, float (&v)[kVec]) {
     if (aligned) {
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2(u[i], T());
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+        for (int k = 0; k < kVec; k += 8) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + k);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(u[i], T());
+                v[k + 2 * i] = f.x;
+                v[k + 2 * i + 1] = f.y;
+            }
         }
     } else {
 #pragma unroll
@@ -58,7 +64,7 @@ __device__ __forceinline__ void load8(const T* p, bool aligned, float (&v)[kVec]
     }
 }
 
-__device__ __forceinline__ uint32_t codes_of(const float (&q)[kVec]) {  // nearest even, saturated, low half first
+__device__ __forceinline__ uint32_t codes_of(const float* q) {  // of eight: nearest even, saturated, low half first
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -88,7 +94,7 @@ __global__ void __launch_bounds__(CTA) k_quantize4(const QuantParams p) {
         const uint32_t g = u * TPR + t;
 #pragma unroll
         for (int i = 0; i < kVec; ++i) v[u][i] = 0.f;
-        if (live && g < groups) load8(x + (uint64_t)g * kVec, p.aligned, v[u]);
+        if (live && g < groups) load16(x + (uint64_t)g * kVec, p.aligned, v[u]);
     }
     float top[U];  // of the block that a group is part of
 #pragma unroll
@@ -127,16 +133,15 @@ __global__ void __launch_bounds__(CTA) k_quantize4(const QuantParams p) {
         uint32_t byte;
         float q[kVec];
         if constexpr (BLOCK == 16) {
-            const float inv = power_of_two(-e);
-            const float want = __fdiv_rn(top[u] * inv, 6.f);
+            const float want = __fdiv_rn(top[u] * power_of_two(-e), 6.f);
             byte = finite ? (uint32_t)__nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3) : 0x7Fu;
-            // 1 / scale rounded, and quotients corrected by their remainder: rounded once
+            // The quotient by s = scale * 2^e: by the rounded 1 / s, and corrected by its remainder: rounded once.
             const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
-            const float r1 = byte ? __frcp_rn(s) : 0.f;
+            const float whole = s * power_of_two(e), inv = byte ? __frcp_rn(s) * power_of_two(-e) : 0.f;
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                const float y = v[u][i] * inv, a = y * r1;
-                q[i] = fmaf(fmaf(-a, s, y), r1, a);
+                const float a = v[u][i] * inv;
+                q[i] = fmaf(fmaf(-a, whole, v[u][i]), inv, a);
             }
         } else {
             const uint32_t bits = __float_as_uint(top[u]);
@@ -148,7 +153,7 @@ __global__ void __launch_bounds__(CTA) k_quantize4(const QuantParams p) {
             for (int i = 0; i < kVec; ++i) q[i] = v[u][i] * inv;
         }
         if (live && g < groups) {
-            *reinterpret_cast<uint32_t*>(p.codes + (uint64_t)row * p.codes_stride + (uint64_t)g * (kVec / 2)) = codes_of(q);
+            *reinterpret_cast<uint2*>(p.codes + (uint64_t)row * p.codes_stride + (uint64_t)g * (kVec / 2)) = make_uint2(codes_of(q), codes_of(q + 8));
             if (g % kLanes == 0) p.scales[scale_at(row, g / kLanes, p.col_tiles)] = (unsigned char)byte;
         }
     }
@@ -159,11 +164,10 @@ __global__ void __launch_bounds__(CTA) k_quantize4(const QuantParams p) {
 template <typename T, int BLOCK>
 lp_status launch_quantize(const QuantParams& p, lp_stream_t stream) {
     const uint32_t groups = p.H / kVec, rows = (p.T + 127) / 128 * 128;
-    if (groups <= 128)
-        return launch(k_quantize4<T, BLOCK, 32, 4, 128>, dim3(rows / 4), 128, 0, stream, 1, p);
-    if (groups <= 512) return launch(k_quantize4<T, BLOCK, 128, 4, 128>, dim3(rows), 128, 0, stream, 1, p);
-    if (groups <= 1024) return launch(k_quantize4<T, BLOCK, 256, 4, 256>, dim3(rows), 256, 0, stream, 1, p);
-    return launch(k_quantize4<T, BLOCK, 512, 8, 512>, dim3(rows), 512, 0, stream, 1, p);
+    if (groups <= 64) return launch(k_quantize4<T, BLOCK, 32, 2, 128>, dim3(rows / 4), 128, 0, stream, 1, p);
+    if (groups <= 256) return launch(k_quantize4<T, BLOCK, 128, 2, 128>, dim3(rows), 128, 0, stream, 1, p);
+    if (groups <= 512) return launch(k_quantize4<T, BLOCK, 256, 2, 256>, dim3(rows), 256, 0, stream, 1, p);
+    return launch(k_quantize4<T, BLOCK, 512, 4, 512>, dim3(rows), 512, 0, stream, 1, p);
 }
 template <typename T>
 lp_status launch_quantize(const QuantParams& p, uint32_t block, lp_stream_t stream) {
@@ -183,62 +187,83 @@ struct DequantParams {
 };
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, bool aligned, const float (&v)[kVec]) {
+__device__ __forceinline__ void store16(T* p, bool aligned, const float (&v)[kVec]) {
     if (!aligned) {
 #pragma unroll
         for (int i = 0; i < kVec; ++i) p[i] = from_f32<T>(v[i]);
     } else if constexpr (sizeof(T) == 4) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+        for (int i = 0; i < kVec; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
     } else {
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack2(v[0], v[1], T()), pack2(v[2], v[3], T()), pack2(v[4], v[5], T()),
-                                                  pack2(v[6], v[7], T()));
+#pragma unroll
+        for (int i = 0; i < kVec; i += 8)
+            *reinterpret_cast<uint4*>(p + i) = make_uint4(pack2(v[i], v[i + 1], T()), pack2(v[i + 2], v[i + 3], T()),
+                                                          pack2(v[i + 4], v[i + 5], T()), pack2(v[i + 6], v[i + 7], T()));
     }
 }
+// The levels of eight codes, as pairs of halves.
+__device__ __forceinline__ void levels_of(uint32_t codes, __half2 (&l)[4]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(l);
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(codes));
+}
 
-constexpr int kDequantThreads = 128;
+constexpr uint32_t kDequantThreads = 256, kDequantItems = 2 * kDequantThreads;  // groups of a CTA
 
-// A CTA takes a piece of a row: kDequantThreads groups of eight codes, four times.
+// A CTA takes kDequantItems groups: of a row's piece, or of several short rows.
 template <typename T, int BLOCK>
 __global__ void __launch_bounds__(kDequantThreads) k_dequantize4(const DequantParams p) {
     pdl_trigger();
     pdl_wait();
-    const uint32_t o = blockIdx.x, groups = p.H / kVec;
-    const uint32_t row = p.rows ? p.rows[o] : o;
-    T* out = static_cast<T*>(p.out) + (uint64_t)o * p.out_stride;
-    const bool bad = row >= p.V;
-    if (bad && threadIdx.x == 0 && blockIdx.y == 0) flag(p.status, LP_ERR_OFFSETS);
+    const uint32_t groups = p.H / kVec, several = kDequantItems / groups;  // rows of a CTA, 0: pieces of one
     const float nan = __uint_as_float(0x7FC00000u);
-    const float rs = bad ? nan : p.row_scale ? p.row_scale[row] : 1.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t g = (blockIdx.y * 4 + k) * kDequantThreads + threadIdx.x;
-        if (g >= groups) return;
+    for (uint32_t k = 0; k < kDequantItems / kDequantThreads; ++k) {
+        uint32_t o = blockIdx.x, g = blockIdx.y * kDequantItems + k * kDequantThreads + threadIdx.x;
+        if (several) {
+            const uint32_t r = g / groups;
+            if (r >= several) return;
+            o = o * several + r;
+            g -= r * groups;
+        }
+        if (o >= p.n || g >= groups) return;
+        const uint32_t row = p.rows ? p.rows[o] : o;
         float v[kVec];
-        if (bad) {
+        if (row >= p.V) {
+            if (g == 0) flag(p.status, LP_ERR_OFFSETS);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) v[i] = nan;
         } else {
-            const uint32_t c = *reinterpret_cast<const uint32_t*>(p.codes + (uint64_t)row * p.codes_stride + (uint64_t)g * 4);
+            const uint2 c = *reinterpret_cast<const uint2*>(p.codes + (uint64_t)row * p.codes_stride + (uint64_t)g * 8);
             const uint32_t byte = p.scales[scale_at(row, g * kVec / BLOCK, p.col_tiles)];
-            float s;
-            if constexpr (BLOCK == 16) s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
-            else s = byte == 255 ? nan : byte ? power_of_two((int)byte - 127) : __uint_as_float(0x00400000u);  // 2^-127
+            const float rs = p.row_scale ? p.row_scale[row] : 1.f;
+            __half2 l[8];
+            levels_of(c.x, reinterpret_cast<__half2(&)[4]>(l[0]));
+            levels_of(c.y, reinterpret_cast<__half2(&)[4]>(l[4]));
+            float s = 1.f;
+            if constexpr (BLOCK == 16) {  // six bits and exponents from -10 to 11: exact in f16
+                const __half2 s2 = __half2half2(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                // the three bits below the sign: exponent and mantissa of 0, 0.5, 1, 1.5, 2, 3, 4, 6
-                const uint32_t m = c >> (4 * i) & 7, sign = (c >> (4 * i + 3) & 1) << 31;
-                const float level = __uint_as_float((m < 2 ? m * 0x3F000000u : ((m + 252u) << 22)) | sign);
-                v[i] = level * s * rs;  // (the first product is exact)
+                for (int i = 0; i < 8; ++i) l[i] = __hmul2(l[i], s2);
+            } else {
+                s = byte == 255 ? nan : byte ? power_of_two((int)byte - 127) : __uint_as_float(0x00400000u);  // 2^-127
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 f = __half22float2(l[i]);
+                v[2 * i] = BLOCK == 16 ? f.x * rs : f.x * s * rs;  // (the product with s is exact)
+                v[2 * i + 1] = BLOCK == 16 ? f.y * rs : f.y * s * rs;
             }
         }
-        store8(out + (uint64_t)g * kVec, p.aligned, v);
+        store16(static_cast<T*>(p.out) + (uint64_t)o * p.out_stride + (uint64_t)g * kVec, p.aligned, v);
     }
 }
 
 template <typename T>
 lp_status launch_dequantize(const DequantParams& p, uint32_t block, lp_stream_t stream) {
-    const dim3 grid(p.n, (p.H / kVec + 4 * kDequantThreads - 1) / (4 * kDequantThreads));
+    const uint32_t groups = p.H / kVec, several = kDequantItems / groups;
+    const dim3 grid(several ? (p.n + several - 1) / several : p.n, several ? 1 : (groups + kDequantItems - 1) / kDequantItems);
     return block == 16 ? launch(k_dequantize4<T, 16>, grid, kDequantThreads, 0, stream, 1, p)
                        : launch(k_dequantize4<T, 32>, grid, kDequantThreads, 0, stream, 1, p);
 }
