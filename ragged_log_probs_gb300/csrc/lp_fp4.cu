@@ -165,8 +165,10 @@ template <typename T, int BLOCK>
 lp_status launch_quantize(const QuantParams& p, lp_stream_t stream) {
     const uint32_t groups = p.H / kVec, rows = (p.T + 127) / 128 * 128;
     if (groups <= 64) return launch(k_quantize4<T, BLOCK, 32, 2, 128>, dim3(rows / 4), 128, 0, stream, 1, p);
-    if (groups <= 256) return launch(k_quantize4<T, BLOCK, 128, 2, 128>, dim3(rows), 128, 0, stream, 1, p);
-    if (groups <= 512) return launch(k_quantize4<T, BLOCK, 256, 2, 256>, dim3(rows), 256, 0, stream, 1, p);
+    // one group a thread (32000 rows of 4096 bf16: 70 us and, blocks of 32, 51; two a thread 73 and 56, a row a
+    // warp 77 and 67)
+    if (groups <= 256) return launch(k_quantize4<T, BLOCK, 256, 1, 256>, dim3(rows), 256, 0, stream, 1, p);
+    if (groups <= 512) return launch(k_quantize4<T, BLOCK, 512, 1, 512>, dim3(rows), 512, 0, stream, 1, p);
     return launch(k_quantize4<T, BLOCK, 512, 4, 512>, dim3(rows), 512, 0, stream, 1, p);
 }
 template <typename T>
