@@ -15,8 +15,8 @@
 // order (value descending, id ascending), so that what is kept is told by the last kept (value, id):
 //   top-k: a value that k tokens reach for sure is read from the parts' ordered values; what
 //          lies above it is listed and ranked by the cluster's first CTA.
-//   top-p: what weighs less than (1 - p) Z / V is never kept. Where Z is small the rest is listed
-//          as well. Else, or if it does not fit, a histogram over the values' bits with rounded
+//   top-p: what weighs less than (1 - p) Z / V is never kept. Where that leaves few tokens they are
+//          listed as well. Else, or if it does not fit, a histogram over the values' bits with rounded
 //          weights finds the bins in which p Z can be reached; what lies above them is summed
 //          exactly, what lies in them is listed. Bins of more than fits are cut again; a single
 //          value is cut by id.
@@ -40,8 +40,7 @@ constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
 constexpr uint32_t kScanResident = 4, kDrawResident = 3;  // CTAs per SM
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kList = 1024;     // tokens that are ranked
-constexpr uint32_t kRanks = kList / kThreads;  // of a thread, neighbours
-constexpr uint32_t kCounted = 384;   // tokens up to which ranks are counted, and not sorted
+constexpr uint32_t kRanks = kList / kThreads;  // of a thread
 constexpr uint32_t kDrawnByList = 128;  // tokens up to which the draw is made from the list
 constexpr uint32_t kBins = 32;
 constexpr uint32_t kBound = 512;
@@ -49,7 +48,6 @@ constexpr uint32_t kTable = 256;
 constexpr uint32_t kLowest = 0x00800000u;  // ordered() of the lowest finite value
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr float kUnit = 8796093022208.f;  // 2^43: weights as integers, the largest one is about that
-constexpr float kFewWeights = 8.f;   // Z up to which a top-p row's tokens are listed at once
 // What a histogram's sums of f32 weights can be off by, of the whole: 2^-18 and less (an exponent of 40
 // rounded to 2^-19, times ln 2, and the sums of some hundred).
 constexpr float kSlack = 1.f / 65536.f;
@@ -254,37 +252,64 @@ __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* scratch, ui
 
 // Threads that share a key of a list of n, as a power of two, so that n keys keep the CTA busy.
 __device__ __forceinline__ uint32_t sharing(uint32_t n) { return n <= kThreads / 8 ? 3 : n <= kThreads / 4 ? 2 : n <= kThreads / 2 ? 1 : 0; }
-// n different keys (n <= kList) of `from` in descending order, to `to`: few are ranked by counting
-// the larger ones (the steps of a sort wait for the CTA), many are sorted in steps of a bitonic network.
-__device__ __forceinline__ void sort_list(const uint64_t* from, uint64_t* to, uint32_t n) {
+// n different keys (n <= kList) of `from` in descending order, to `to`. They are put into a bucket a
+// thread by value, and ranked among those of their bucket (300 keys: 0.9 us; counted among all, 7).
+// `scratch`: kList keys and kThreads + 1 words.
+__device__ __forceinline__ void sort_list(const uint64_t* from, uint64_t* to, uint32_t n, uint64_t* scratch, uint64_t* scan) {
+    uint64_t* const by_bucket = scratch;
+    uint32_t* const count = reinterpret_cast<uint32_t*>(scratch + kList);
     const uint32_t t = threadIdx.x;
-    if (n > kCounted) {
-        for (uint32_t i = t; i < kList; i += kThreads) to[i] = i < n ? from[i] : 0;
-        __syncthreads();
-        for (uint32_t k = 1; k < 11 && (1u << (k - 1)) < n; ++k)  // (up to the power of two that holds n)
-            for (uint32_t j = k; j-- > 0;) {
+    uint64_t key[kRanks];
+    uint32_t low = kAll, high = 0;
 #pragma unroll
-                for (uint32_t q = t; q < kList / 2; q += kThreads) {
-                    const uint32_t i = (q >> j << (j + 1)) | (q & ((1u << j) - 1)), o = i + (1u << j);
-                    const uint64_t a = to[i], b = to[o];
-                    if ((a < b) == ((i >> k & 1) == 0)) {
-                        to[i] = b;
-                        to[o] = a;
-                    }
-                }
-                __syncthreads();
-            }
-        return;
+    for (uint32_t i = 0; i < kRanks; ++i) {
+        const uint32_t at = t + i * kThreads;
+        key[i] = at < n ? from[at] : 0;
+        if (at < n) {
+            low = min(low, (uint32_t)(key[i] >> 32));
+            high = max(high, (uint32_t)(key[i] >> 32));
+        }
     }
-    const uint32_t shift = sharing(n), parts = 1u << shift;
-    for (uint32_t at = t >> shift; at < n || shift; at += kThreads) {
-        const uint64_t key = at < n ? from[at] : 0;
-        uint32_t rank = 0;
-#pragma unroll 8
-        for (uint32_t j = t & (parts - 1); j < n; j += parts) rank += from[j] > key;
-        for (uint32_t k = 1; k < parts; k *= 2) rank += __shfl_xor_sync(0xFFFFFFFFu, rank, k);
-        if (at < n && (t & (parts - 1)) == 0) to[rank] = key;
-        if (shift) break;  // (all of them: whole warps came here)
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    high = __reduce_max_sync(0xFFFFFFFFu, high);
+    uint32_t* const ends = reinterpret_cast<uint32_t*>(scan);
+    if ((t & 31) == 0) {
+        ends[t / 32] = low;
+        ends[kWarps + t / 32] = high;
+    }
+    count[t] = 0;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t k = 0; k < kWarps; ++k) {
+        low = min(low, ends[k]);
+        high = max(high, ends[kWarps + k]);
+    }
+    const float top = unordered(high), per_bucket = ((float)kThreads - 0.01f) / fminf(top - unordered(low), 3e38f);
+    uint32_t bucket[kRanks], place[kRanks];
+#pragma unroll
+    for (uint32_t i = 0; i < kRanks; ++i) {
+        bucket[i] = min((uint32_t)((top - unordered((uint32_t)(key[i] >> 32))) * per_bucket), kThreads - 1);  // (one value: 0)
+        place[i] = t + i * kThreads < n ? atomicAdd(&count[bucket[i]], 1) : 0;
+    }
+    __syncthreads();
+    const uint32_t own = count[t];
+    uint64_t all;
+    const uint32_t start = (uint32_t)block_scan(own, scan, &all) - own;
+    __syncthreads();
+    count[t] = start;
+    if (t == 0) count[kThreads] = n;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kRanks; ++i)
+        if (t + i * kThreads < n) by_bucket[count[bucket[i]] + place[i]] = key[i];
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kRanks; ++i) {
+        if (t + i * kThreads >= n) continue;
+        const uint32_t begin = count[bucket[i]], end = count[bucket[i] + 1];
+        uint32_t rank = begin;
+        for (uint32_t j = begin; j < end; ++j) rank += by_bucket[j] > key[i];
+        to[rank] = key[i];
     }
     __syncthreads();
 }
@@ -473,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     T* const buffer = reinterpret_cast<T*>(buffers[threadIdx.x >> 5]);
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
-    const uint32_t row = blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
+    // (the rows that the first kernel read last come first: they are in L2)
+    const uint32_t row = p.T - 1 - blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before others' memory is written to)
     sh.table[t] = g_table.at[t];
     for (uint32_t i = t; i < kBound; i += kThreads) sh.bound[i] = 0;
@@ -772,7 +798,16 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             // kept tokens weigh (1 - p) Z / V at least (with room for the roundings here)
             const float f = m + set.tau * (__logf((1.f - set.top_p) * sum / (float)p.V) - 0.02f) - fabsf(m) * 1e-6f;
             lo = f > -3e38f ? min(max(ordered(f + 0.f), kLowest), hi) : kLowest;
-            few = sum < kFewWeights;
+            // Tokens are few where not nearly every part has one. (Looking for them in vain costs 12 us of a row's 50.)
+            uint32_t with = 0;
+            for (uint32_t i = t; i < parts; i += kThreads) with += sh.part_top[i] >= lo;
+            with = __reduce_add_sync(0xFFFFFFFFu, with);
+            __syncthreads();
+            if (lane == 0) sh.scan[warp] = with;
+            __syncthreads();
+            with = 0;
+            for (uint32_t k = 0; k < kWarps; ++k) with += (uint32_t)sh.scan[k];
+            few = p.V <= kList || 20 * with < 19 * parts;
         }
         // ---- 3. all that can be kept in one list?
         if (few) {
@@ -785,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
                     return;
                 }
-                sort_list(sh.list, sh.stage, n);
+                sort_list(sh.list, sh.stage, n, reinterpret_cast<uint64_t*>(smem_raw), sh.scan);
                 uint64_t w[kRanks], all, kept_all, sum = 0;
                 bool fine[kRanks];
 #pragma unroll
@@ -1009,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                 if (last && rank != 0) return;
                 if (rank == 0) {
                     const uint32_t listed = min(sh.listed, kList);
-                    sort_list(sh.list, sh.stage, listed);
+                    sort_list(sh.list, sh.stage, listed, reinterpret_cast<uint64_t*>(smem_raw), sh.scan);
                     const uint32_t limit = by_count ? min(listed, (uint32_t)target - above_count) : listed;
                     uint64_t w[kRanks], own = 0, sum, kept_all;
 #pragma unroll
