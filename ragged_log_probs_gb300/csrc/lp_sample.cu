@@ -570,9 +570,9 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             body(part, w);
         }
     };
-    // Visits the elements with values in [from, to], two at a time: body(part, element, element or kAll,
+    // Visits the elements with values of `from` or more, two at a time: body(part, element, element or kAll,
     // value, value), then after(part). Lanes take them out of masks of 32, so that few cost little.
-    const auto visit = [&](float from, float to, auto body, auto after) {
+    const auto visit = [&](float from, auto body, auto after) {
         for_parts(from, [&](uint32_t part, const uint4 (&w)[kVecs]) {
             uint32_t take = 0;
             __syncwarp();
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                 reinterpret_cast<uint4*>(buffer)[j * 32 + lane] = w[j];
 #pragma unroll
                 for (uint32_t i = 0; i < VEC; ++i)
-                    if ((f[i] >= from) & (f[i] <= to)) take |= 1u << (j * VEC + i);
+                    if (f[i] >= from) take |= 1u << (j * VEC + i);
             }
             __syncwarp();
             const auto next = [&] {  // (without branches)
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
         clear_sums();
         cluster.sync();
         Weight s = {0.f, 0.f};
-        visit(from, m, [&](uint32_t, uint32_t, uint32_t, float f0, float f1) {
+        visit(from, [&](uint32_t, uint32_t, uint32_t, float f0, float f1) {
             add(s, weight_of(f0));
             add(s, weight_of(f1));
         }, [&](uint32_t part) {
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
         }
         // ---- 3. all that can be kept in one list?
         if (few) {
-            visit(unordered(lo), m, stage, no_more);
+            visit(unordered(lo), stage, no_more);
             send_list();
             const uint32_t n = lead->listed;
             if (n <= kList) {
@@ -883,13 +883,16 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
         uint32_t above_count = 0;        // by count: of the keys above hi
         float rough = 0.f, slip = 0.f;   // by weight: their weight, and what that can be off by
         for (int n_hist = 0; n_hist < 64 && !found; ++n_hist) {  // (a bound only: each cuts the range)
-            // 32 bins of equal width, and from the second time on (or where that is all of f32) of equally many
+            // 31 bins of equal width, and from the second time on (or where that is all of f32) of equally many
             // keys: what is left is within an octave mostly, and a cut at 0 would be neared 32-fold at a time.
-            const float from = unordered(lo), to = unordered(hi), per_bin = 31.99f / (to - from);
+            // What lies outside has a bin of its own, the last. (Below `lo` some may be in the bin of `lo`.)
+            const float from = unordered(lo), to = unordered(hi), per_bin = 30.49f / (to - from);
             const bool even = n_hist == 0 && to - from < 1e38f && to - from > 1e-30f && !(by_count && lo == kLowest);
-            const uint32_t shift = 27 - min(__clz(hi - lo | 1), 27);
+            uint32_t shift = 27 - min(__clz(hi - lo | 1), 27);
+            shift += (hi - lo) >> shift >= kBins - 1;
             const auto bin_of = [&](float f, auto equal_width) {  // (decreasing in f)
-                if constexpr (decltype(equal_width)::value) return min((uint32_t)((to - f) * per_bin), kBins - 1);
+                // (equal width: `to` is the row's largest; an ulp of 2^23 is 1)
+                if constexpr (decltype(equal_width)::value) return min(__float_as_uint(fmaf(to - f, per_bin, 8388608.f)) - 0x4B000000u, kBins - 1);
                 else return min((hi - ordered(f)) >> shift, kBins - 1);
             };
             const auto bin_at = [&](float f) { return even ? bin_of(f, std::true_type()) : bin_of(f, std::false_type()); };
@@ -901,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                 // A lane adds to sums of its own (bin by lane: each in the lane's bank), without atomics, which
                 // take two clocks a lane: 27000 tokens that can be kept, 13500 clocks of eight CTAs with them.
                 // (by count: 2^0; no branches below, which cost this loop as much as all the rest)
-                const float chi = by_count ? 0.f : scale.chi, shift_of = by_count ? 0.f : scale.magic - 49152.f;
+                const float chi = by_count ? 0.f : -scale.chi, at_to = by_count ? 0.f : fmaf(to - scale.base, scale.chi, scale.magic - 49152.f);
                 float* const sums = reinterpret_cast<float*>(buffers[warp]) + lane;
 #pragma unroll
                 for (uint32_t i = 0; i < kBins / 4; ++i) reinterpret_cast<uint4*>(buffers[warp])[i * 32 + lane] = make_uint4(0, 0, 0, 0);
@@ -919,9 +922,10 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
 #pragma unroll
                             for (uint32_t i = 0; i < VEC; ++i) {
                                 float e;
-                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(f[i] - scale.base, chi, shift_of)));
-                                const bool in = (f[i] >= from) & (f[i] <= to);
-                                sums[bin_of(f[i], equal_width) * 32] += in ? e : 0.f;
+                                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(to - f[i], chi, at_to)));
+                                // (-inf has weight 0, but counts as 1)
+                                if constexpr (!decltype(equal_width)::value) e = f[i] >= from ? e : 0.f;
+                                sums[bin_of(f[i], equal_width) * 32] += e;
                             }
                         }
                     });
@@ -945,6 +949,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             if (rank == 0) {
                 float own = 0.f;
                 for (uint32_t k = 0; k < C; ++k) own += sh.bin_sum[k][lane];
+                if (lane == kBins - 1) own = 0.f;  // (what lies outside)
                 float upto = own;
 #pragma unroll
                 for (int k = 1; k < 32; k *= 2) {
@@ -954,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                 // (numbers are exact: fewer than 2^24)
                 const float aim = by_count ? (float)((uint32_t)target - above_count) : fmaxf((float)target / kUnit - rough, 0.f);
                 const float slack = by_count ? 0.f : slip + kSlack * (__shfl_sync(0xFFFFFFFFu, upto, 31) + rough / 64.f);  // (the aim is a difference of f32)
-                const uint32_t bins = bin_at(from);
+                const uint32_t bins = min(bin_at(from), kBins - 2);
                 const uint32_t can = __ballot_sync(0xFFFFFFFFu, upto >= aim - slack), must = __ballot_sync(0xFFFFFFFFu, upto >= aim + slack);
                 const uint32_t last = min(must ? __ffs(must) - 1 : bins, bins), first = min(can ? __ffs(can) - 1 : last, last);
                 // The least keys of bins `last`, `first` and the one above it, by a warp each: 32 keys at a time.
@@ -1027,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             {
                 Weight s = {0.f, 0.f};
                 const float border = unordered(hi);
-                visit(fits ? unordered(lo) : border, m, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
+                visit(fits ? unordered(lo) : border, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
                     add(s, weight_of(f0 > border ? f0 : -kInf));
                     add(s, weight_of(f1 > border ? f1 : -kInf));
                     if (fits) stage(part, f0 > border ? kAll : e0, f1 > border ? kAll : e1, f0, f1);
@@ -1098,25 +1103,26 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             } else {
                 // one value: its first `j` ids are kept
                 const uint64_t one = fixed(weight_of(unordered(hi)));
-                uint64_t j = by_count ? target - above_count : (target - above + one - 1) / one;
+                uint64_t j = by_count ? target - above_count : one ? (target - above + one - 1) / one : 1;
                 if (by_count && set.top_p < 1.f) {
                     const uint64_t z = above + j * one, goal = reached_at(set.top_p, z);
                     if (goal <= above) {
                         by_count = false;
                         target = goal;
-                                lo = hi + 1;
+                        lo = hi + 1;
                         hi = ordered(m);
                         rough = slip = 0.f;
                         continue;
                     }
                     if (one) j = min(j, (goal - above + one - 1) / one);
                 }
-                // the j-th of them, counted by warp in the order of the ids
+                // the j-th of them, counted by part in the order of the ids
                 cluster.sync();  // (the sums have been read)
                 clear_sums();
                 cluster.sync();
+                const float value = unordered(hi);
                 uint32_t here = 0;
-                visit(unordered(hi), unordered(hi), [&](uint32_t, uint32_t e0, uint32_t e1, float, float) { here += (e0 != kAll) + (e1 != kAll); },
+                visit(unordered(hi), [&](uint32_t, uint32_t, uint32_t, float f0, float f1) { here += (f0 == value) + (f1 == value); },
                       [&](uint32_t part) {
                           tell(part, __reduce_add_sync(0xFFFFFFFFu, here));
                           here = 0;
@@ -1154,7 +1160,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     clear_sums();
     cluster.sync();
     Weight s = {0.f, 0.f};
-    visit(unordered(cut.key), m, [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
+    visit(unordered(cut.key), [&](uint32_t part, uint32_t e0, uint32_t e1, float f0, float f1) {
         const Weight a = weight_of(e0 != kAll && kept(f0, id_of(part, e0)) ? f0 : -kInf);
         const Weight b = weight_of(e1 != kAll && kept(f1, id_of(part, e1)) ? f1 : -kInf);
         if (enough(a)) add(s, a);
@@ -1171,6 +1177,9 @@ uint32_t parts_of(uint32_t V) { return (V + 7 + kPart - 1) / kPart; }  // (rows 
 
 template <typename T>
 lp_status launch_sample(const SampleParams& p, lp_stream_t stream) {
+    static std::atomic<uint64_t> smem_set;
+    constexpr size_t kBuffers = (size_t)kWarps * 4 * kPart;
+    if (!allow_smem(reinterpret_cast<const void*>(k_sample_draw<T>), kBuffers, &smem_set)) return LP_ERR_CUDA;
     const uint64_t warps = (uint64_t)p.T * p.parts;
     const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), kThreads, 0, stream, 1, p);
     if (st != LP_OK) return st;
@@ -1179,9 +1188,6 @@ lp_status launch_sample(const SampleParams& p, lp_stream_t stream) {
     const uint32_t slots = 2 * kDrawResident * (uint32_t)sm_count();
     uint32_t c = 1;
     while (c < kMaxCluster && c * kWarps * 2 < p.parts && 2 * (uint64_t)c * p.T <= slots + slots / 4) c *= 2;
-    static std::atomic<uint64_t> smem_set;
-    constexpr size_t kBuffers = (size_t)kWarps * 4 * kPart;
-    if (!allow_smem(reinterpret_cast<const void*>(k_sample_draw<T>), kBuffers, &smem_set)) return LP_ERR_CUDA;
     return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, kBuffers, stream, c, p);
 }
 
