@@ -39,7 +39,6 @@ struct Project4Params {
     uint64_t out_stride;
     uint32_t T, V, H;
     uint32_t tile_t, tiles_t, tiles, slices, stages;
-    uint32_t chunk;        // slices summed in the accumulator
     uint32_t col_tiles;    // tiles of scales in a row of them
     uint32_t acc_shift;    // log2 of the number of accumulators
     uint32_t idesc;        // without N and the scales' places
@@ -101,7 +100,6 @@ k_project4(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
     const uint32_t first = blockIdx.x / CG, step = gridDim.x / CG;
     const auto acc_of = [&](uint32_t n) { return n & ((1u << p.acc_shift) - 1); };
     const auto acc_phase = [&](uint32_t n) { return n >> p.acc_shift & 1; };
-    const auto chunk_end = [&](uint32_t k0) { return k0 + min(p.slices - k0, p.chunk); };
     // rows of x in tile tt, a whole number of 16 for each CTA
     const auto rows_of = [&](uint32_t tt) { return min(p.tile_t, (p.T - tt * p.tile_t + 16 * CG - 1) / (16 * CG) * (16 * CG)); };
 
@@ -188,43 +186,40 @@ k_project4(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
             bool ok = true;
             for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
                 const uint32_t idesc = p.idesc | ((rows_of(tile % p.tiles_t) >> 3) << 17);
-                for (uint32_t k0 = 0, k1; ok && k0 < p.slices; k0 = k1) {
-                    const uint32_t acc = acc_of(n), d = tmem + acc * (kMaxTileT / 2);
-                    k1 = chunk_end(k0);
-                    if (!mbar_wait_warp(acc_empty0 + 8 * acc, acc_phase(n) ^ 1, s_abort)) { ok = false; break; }
+                const uint32_t acc = acc_of(n), d = tmem + acc * (kMaxTileT / 2);
+                if (!mbar_wait_warp(acc_empty0 + 8 * acc, acc_phase(n) ^ 1, s_abort)) { ok = false; break; }
+                fence_after();
+                for (uint32_t k = 0; k < p.slices; ++k) {
+                    if (!mbar_wait_warp(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
                     fence_after();
-                    for (uint32_t k = k0; k < k1; ++k) {
-                        if (!mbar_wait_warp(full0 + 8 * s, phase, s_abort)) { ok = false; break; }
-                        fence_after();
-                        const uint32_t at = base + s * stage_bytes, scales = at + kStageW + stage_x;
-                        const uint64_t a = matrix_desc(at), b = matrix_desc(at + kStageW), c = scale_desc(scales);
-                        const uint32_t sa = tmem + kScaleColumns + s * kSlot, sb = sa + kTiles * 4;
-                        const uint32_t steps = min(4u, (p.H - k * kSlice + 63) / 64);  // of 64 elements
-                        if (elected) {
+                    const uint32_t at = base + s * stage_bytes, scales = at + kStageW + stage_x;
+                    const uint64_t a = matrix_desc(at), b = matrix_desc(at + kStageW), c = scale_desc(scales);
+                    const uint32_t sa = tmem + kScaleColumns + s * kSlot, sb = sa + kTiles * 4;
+                    const uint32_t steps = min(4u, (p.H - k * kSlice + 63) / 64);  // of 64 elements
+                    if (elected) {
 #pragma unroll
-                            for (uint32_t j = 0; j < kTiles; ++j) {
-                                copy_scales<CG>(sa + 4 * j, c + j * (512 >> 4));
+                        for (uint32_t j = 0; j < kTiles; ++j) {
+                            copy_scales<CG>(sa + 4 * j, c + j * (512 >> 4));
 #pragma unroll
-                                for (uint32_t q = 0; q < kXBlocks; ++q)
-                                    copy_scales<CG>(sb + 4 * (kXBlocks * j + q), c + ((1 + q) * kScaleBytes + j * 512 >> 4));
-                            }
-#pragma unroll
-                            for (uint32_t i = 0; i < 4; ++i) {
-                                // blocks of 32: a tile's columns hold the scales of two steps
-                                const uint32_t j = BLOCK == 16 ? i : i / 2, id = BLOCK == 16 ? 0 : (i & 1) * 2;
-                                if (i < steps)
-                                    mma4<BLOCK, CG>(d, a + 2 * i, b + 2 * i, idesc | id << 4 | id << 29, sa + 4 * j,
-                                                    sb + 4 * kXBlocks * j, (k - k0) | i);
-                            }
-                            mma_commit<CG>(empty0 + 8 * s);
+                            for (uint32_t q = 0; q < kXBlocks; ++q)
+                                copy_scales<CG>(sb + 4 * (kXBlocks * j + q), c + ((1 + q) * kScaleBytes + j * 512 >> 4));
                         }
-                        __syncwarp();
-                        if (++s == p.stages) { s = 0; phase ^= 1; }
+#pragma unroll
+                        for (uint32_t i = 0; i < 4; ++i) {
+                            // blocks of 32: a tile's columns hold the scales of two steps
+                            const uint32_t j = BLOCK == 16 ? i : i / 2, id = BLOCK == 16 ? 0 : (i & 1) * 2;
+                            if (i < steps)
+                                mma4<BLOCK, CG>(d, a + 2 * i, b + 2 * i, idesc | id << 4 | id << 29, sa + 4 * j,
+                                                sb + 4 * kXBlocks * j, k | i);
+                        }
+                        mma_commit<CG>(empty0 + 8 * s);
                     }
-                    if (!ok) break;
-                    if (elected) mma_commit<CG>(acc_full0 + 8 * acc);
-                    ++n;
+                    __syncwarp();
+                    if (++s == p.stages) { s = 0; phase ^= 1; }
                 }
+                if (!ok) break;
+                if (elected) mma_commit<CG>(acc_full0 + 8 * acc);
+                ++n;
             }
             if (elected) mma_commit<CG>(drain);  // arrives once every product issued above has finished
             __syncwarp();
@@ -237,44 +232,27 @@ k_project4(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CU
         uint32_t n = 0;
         const uint32_t acc_empty_at = CG == 2 ? map_to(acc_empty0, 0) : acc_empty0;
         pdl_wait();
-        bool ok = true;
-        for (uint32_t tile = first; ok && tile < p.tiles; tile += step) {
+        for (uint32_t tile = first; tile < p.tiles; tile += step) {
             const uint32_t tv = tile / p.tiles_t, tt = tile - tv * p.tiles_t, t0 = tt * p.tile_t;
             const uint32_t v = (tv * CG + rank) * kTileV + quad * 32 + lane;
             const uint32_t rows = min(p.tile_t, p.T - t0);
             const float sw = p.w_scale && v < p.V ? p.w_scale[v] : 1.f;
             float sum[kMaxBlocks][32];
-            for (uint32_t k0 = 0; k0 < p.slices;) {
-                const uint32_t acc = acc_of(n);
-                if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) { ok = false; break; }
-                ++n;
-                fence_after();
+            const uint32_t acc = acc_of(n);
+            if (!mbar_wait_warp(acc_full0 + 8 * acc, acc_phase(n), s_abort)) break;
+            ++n;
+            fence_after();
 #pragma unroll
-                for (uint32_t i = 0; i < kMaxBlocks; ++i) {
-                    const uint32_t c0 = (share + kShares * i) * 32;
-                    if (c0 >= rows) continue;
-                    const uint32_t at = tmem + ((quad * 32) << 16) + acc * (kMaxTileT / 2) + c0;
-                    if (k0 == 0) {
-                        tmem_load32(at, sum[i]);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 32; q += 16) {
-                            float y[16];
-                            tmem_load16(at + q, y);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) sum[i][q + c] += y[c];
-                        }
-                    }
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2) mbar_arrive_at(acc_empty_at + 8 * acc);
-                    else mbar_arrive(acc_empty0 + 8 * acc);
-                }
-                k0 = chunk_end(k0);
+            for (uint32_t i = 0; i < kMaxBlocks; ++i) {
+                const uint32_t c0 = (share + kShares * i) * 32;
+                if (c0 < rows) tmem_load32(tmem + ((quad * 32) << 16) + acc * (kMaxTileT / 2) + c0, sum[i]);
             }
-            if (!ok) break;
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_at(acc_empty_at + 8 * acc);
+                else mbar_arrive(acc_empty0 + 8 * acc);
+            }
 #pragma unroll
             for (uint32_t i = 0; i < kMaxBlocks; ++i) {
                 const uint32_t c0 = (share + kShares * i) * 32;
@@ -390,7 +368,6 @@ extern "C" lp_status lp_head_project4(const void* x, uint64_t x_stride, const vo
     p.V = V;
     p.H = H;
     p.slices = (H + kSlice - 1) / kSlice;
-    p.chunk = p.slices;
     const uint32_t cg = T > 128 ? 2 : 1, unit = 16 * cg;
     p.tile_t = T > kMaxTileT ? kMaxTileT : (T + unit - 1) / unit * unit;  // (several tiles: whole blocks of 128 rows)
     p.tiles_t = (T + p.tile_t - 1) / p.tile_t;
