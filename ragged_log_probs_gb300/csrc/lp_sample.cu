@@ -41,6 +41,8 @@ constexpr uint32_t kScanResident = 4, kDrawResident = 3;  // CTAs per SM
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kList = 1024;     // tokens that are ranked
 constexpr uint32_t kRanks = kList / kThreads;  // of a thread
+constexpr uint32_t kListedTop = kList * 3 / 8;  // top-k up to which what can be kept is listed at once: the bound lets two to three times as many pass
+constexpr uint32_t kMaxOrdered = 4096;  // rows that are put in order (a class's count has 16 bits)
 constexpr uint32_t kDrawnByList = 128;  // tokens up to which the draw is made from the list
 constexpr uint32_t kBins = 32;
 constexpr uint32_t kBound = 512;
@@ -76,6 +78,7 @@ struct SampleParams {
     float* out_logprob;
     uint32_t* status;
     Part* told;      // [T][parts]
+    uint32_t* order; // [T]: the rows in the order in which they are drawn, or NULL: the last one first
     uint64_t stride;
     uint32_t T, V, B, parts;
 };
@@ -121,6 +124,7 @@ struct Range {             // keys among which the cut is
     uint32_t above_count;  // how many lie above them, in the histogram's range (by count)
     uint32_t none;         // by count: there are not as many
     uint32_t fits;         // no more than a list holds
+    uint32_t all_fit;      // even with what lies above them
     uint32_t narrowed, more;  // than before; than one bin
     float above, slip;     // by weight: what lies above them, and what that can be off by
 };
@@ -424,6 +428,28 @@ __device__ __forceinline__ uint64_t warp_total(uint64_t v) {
     return v;
 }
 
+// The rows in the order in which they are drawn, by one CTA: those that take longest first, and of a kind those
+// that were read last. (Of 256 rows of mixed settings the last to end had begun when half of the time was over.)
+__device__ __forceinline__ void order_rows(const SampleParams& p, uint64_t* scan) {
+    const uint32_t t = threadIdx.x, each = (p.T + kThreads - 1) / kThreads, begin = t * each, end = min(begin + each, p.T);
+    const auto kind = [&](uint32_t i) {  // 0: longest. Row T - 1 - i, in units of bits
+        const Setting s = setting_of(p, p.T - 1 - i, false);
+        if (s.k > kListedTop || (!s.k && s.top_p < 1.f)) return 0u;  // histograms
+        return s.k > kDrawnByList ? 16u : s.k > 1 || (!s.k && s.min_p > 0.f) ? 32u : 48u;
+    };
+    uint64_t own = 0, all;
+    for (uint32_t i = begin; i < end; ++i) own += 1ull << kind(i);
+    uint64_t place = block_scan(own, scan, &all) - own;
+    place += all << 16;  // (of a kind: after all of those before it)
+    place += all << 32;
+    place += all << 48;
+    for (uint32_t i = begin; i < end; ++i) {
+        const uint32_t k = kind(i);
+        p.order[place >> k & 0xFFFFu] = p.T - 1 - i;
+        place += 1ull << k;
+    }
+}
+
 // ---------------------------------------------------------------- the first kernel: a part a warp
 
 template <typename T>
@@ -435,7 +461,12 @@ __global__ void __launch_bounds__(kThreads, kScanResident) k_sample_scan(const S
     __syncthreads();
     pdl_wait();
     pdl_trigger();  // (the second kernel waits for this one before it reads what it tells)
-    const uint32_t at = blockIdx.x * kWarps + (t >> 5), row = at / p.parts, part = at - row * p.parts;
+    if (p.order && blockIdx.x == 0) {
+        __shared__ uint64_t scan[kWarps];
+        order_rows(p, scan);
+        return;
+    }
+    const uint32_t at = (blockIdx.x - (p.order != nullptr)) * kWarps + (t >> 5), row = at / p.parts, part = at - row * p.parts;
     if (row >= p.T) return;
     const Row<T> r(p, row);
     uint4 w[kVecs];
@@ -498,8 +529,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     T* const buffer = reinterpret_cast<T*>(buffers[threadIdx.x >> 5]);
     const cg::cluster_group cluster = cg::this_cluster();
     const uint32_t C = cluster.num_blocks(), rank = cluster.block_rank();
-    // (the rows that the first kernel read last come first: they are in L2)
-    const uint32_t row = p.T - 1 - blockIdx.x / C, t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
+    const uint32_t t = threadIdx.x, lane = t & 31, warp = t >> 5, parts = p.parts;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // (waited for before others' memory is written to)
     sh.table[t] = g_table.at[t];
     for (uint32_t i = t; i < kBound; i += kThreads) sh.bound[i] = 0;
@@ -507,6 +537,8 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     __syncthreads();
     pdl_wait();
     pdl_trigger();
+    // (the rows that the first kernel read last come first: they are in L2)
+    const uint32_t row = p.order ? __ldcg(p.order + blockIdx.x / C) : p.T - 1 - blockIdx.x / C;
     const Row<T> r(p, row);
     const auto id_of = [&](uint32_t part, uint32_t element) { return part * kPart + element - r.before; };
 
@@ -772,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
 
     if (set.k || set.top_p < 1.f) {
         uint64_t target = set.k;
-        bool by_count = set.k != 0, few = set.k <= kList;
+        bool by_count = set.k != 0, few = set.k <= kListedTop;
         if (by_count) {
             // from the top: lane 0 has the largest bins
             if (warp == 0) {
@@ -809,80 +841,82 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             for (uint32_t k = 0; k < kWarps; ++k) with += (uint32_t)sh.scan[k];
             few = p.V <= kList || 20 * with < 19 * parts;
         }
-        // ---- 3. all that can be kept in one list?
-        if (few) {
-            visit(unordered(lo), stage, no_more);
-            send_list();
-            const uint32_t n = lead->listed;
-            if (n <= kList) {
-                // the first CTA does the rest; the others have read its count, and no one reads theirs
-                if (rank != 0) {
-                    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-                    return;
-                }
-                sort_list(sh.list, sh.stage, n, reinterpret_cast<uint64_t*>(smem_raw), sh.scan);
-                uint64_t w[kRanks], all, kept_all, sum = 0;
-                bool fine[kRanks];
-#pragma unroll
-                for (uint32_t i = 0; i < kRanks; ++i) {
-                    const uint32_t at = kRanks * t + i;
-                    const Weight q = weight_of(at < n && (!set.k || at < set.k) ? unordered((uint32_t)(sh.stage[at] >> 32)) : -kInf);
-                    w[i] = fixed(q);
-                    fine[i] = w[i] && enough(q);
-                    sum += w[i];
-                }
-                uint64_t below = block_scan(sum, sh.scan, &all) - sum;
-                if (by_count) target = set.top_p < 1.f ? reached_at(set.top_p, all) : ~0ull;
-                uint32_t keep = 0;
-#pragma unroll
-                for (uint32_t i = 0; i < kRanks; ++i) {
-                    keep += fine[i] && below < target;
-                    below += w[i];
-                    if (kRanks * t + i < n) sh.list[kRanks * t + i] = w[i];  // (the list is in `stage` now)
-                }
-                (void)block_scan(keep, sh.scan, &kept_all);
-                const uint32_t n_kept = (uint32_t)kept_all;
-                if (n_kept > kDrawnByList) {
-                    // by the parts' sums, as where there is no list
-                    const uint64_t least_kept = sh.stage[n_kept - 1];
-                    cut = {(uint32_t)(least_kept >> 32), ~(uint32_t)least_kept, 0, 0, 0};
-                    clear_sums();
-                    __syncthreads();
-#pragma unroll
-                    for (uint32_t i = 0; i < kRanks; ++i)
-                        if (kRanks * t + i < n_kept) add_to_part(sh.stage[kRanks * t + i], w[i]);
-                    __syncthreads();
-                    finish();
-                } else {
-                    // The kept in the order of their ids: what lies below each.
-                    const uint32_t shift = sharing(n_kept), share = 1u << shift, at = t >> shift;
-                    const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
-                    const uint32_t not_id = (uint32_t)entry;
-                    uint64_t under = 0, z = 0;
-#pragma unroll 8
-                    for (uint32_t j = t & (share - 1); j < n_kept; j += share) {
-                        const uint64_t wj = sh.list[j];
-                        under += (uint32_t)sh.stage[j] > not_id ? wj : 0;
-                        z += wj;
-                    }
-                    for (uint32_t k = 1; k < share; k *= 2) {
-                        under += __shfl_xor_sync(0xFFFFFFFFu, under, k);
-                        z += __shfl_xor_sync(0xFFFFFFFFu, z, k);
-                    }
-                    bool exact;
-                    const uint64_t want = part_of(set.u, z, &exact);
-                    if (at < n_kept && (t & (share - 1)) == 0 && under <= want && want < under + sh.list[at])
-                        token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
-                }
-                asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-                return;
-            }
-        }
         // ---- 4. the value at which the target is reached, by histograms over [lo, hi]
-        bool found = false, read = few;  // whether others may still read the tables and the list
+        bool found = false, read = false;  // whether others may still read the tables and the list
         uint32_t above_count = 0;        // by count: of the keys above hi
         float rough = 0.f, slip = 0.f;   // by weight: their weight, and what that can be off by
         for (int n_hist = 0; n_hist < 64 && !found; ++n_hist) {  // (a bound only: each cuts the range)
+            // ---- 3. all that can be kept in one list? (at once, or when a histogram has told so)
+            if (few) {
+                few = false;
+                read = true;
+                visit(unordered(lo), stage, no_more);
+                send_list();
+                const uint32_t n = lead->listed;
+                if (n <= kList) {
+                    // the first CTA does the rest; the others have read its count, and no one reads theirs
+                    if (rank != 0) {
+                        asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+                        return;
+                    }
+                    sort_list(sh.list, sh.stage, n, reinterpret_cast<uint64_t*>(smem_raw), sh.scan);
+                    uint64_t w[kRanks], all, kept_all, sum = 0;
+                    bool fine[kRanks];
+#pragma unroll
+                    for (uint32_t i = 0; i < kRanks; ++i) {
+                        const uint32_t at = kRanks * t + i;
+                        const Weight q = weight_of(at < n && (!set.k || at < set.k) ? unordered((uint32_t)(sh.stage[at] >> 32)) : -kInf);
+                        w[i] = fixed(q);
+                        fine[i] = w[i] && enough(q);
+                        sum += w[i];
+                    }
+                    uint64_t below = block_scan(sum, sh.scan, &all) - sum;
+                    if (by_count) target = set.top_p < 1.f ? reached_at(set.top_p, all) : ~0ull;
+                    uint32_t keep = 0;
+#pragma unroll
+                    for (uint32_t i = 0; i < kRanks; ++i) {
+                        keep += fine[i] && below < target;
+                        below += w[i];
+                        if (kRanks * t + i < n) sh.list[kRanks * t + i] = w[i];  // (the list is in `stage` now)
+                    }
+                    (void)block_scan(keep, sh.scan, &kept_all);
+                    const uint32_t n_kept = (uint32_t)kept_all;
+                    if (n_kept > kDrawnByList) {
+                        // by the parts' sums, as where there is no list
+                        const uint64_t least_kept = sh.stage[n_kept - 1];
+                        cut = {(uint32_t)(least_kept >> 32), ~(uint32_t)least_kept, 0, 0, 0};
+                        clear_sums();
+                        __syncthreads();
+#pragma unroll
+                        for (uint32_t i = 0; i < kRanks; ++i)
+                            if (kRanks * t + i < n_kept) add_to_part(sh.stage[kRanks * t + i], w[i]);
+                        __syncthreads();
+                        finish();
+                    } else {
+                        // The kept in the order of their ids: what lies below each.
+                        const uint32_t shift = sharing(n_kept), share = 1u << shift, at = t >> shift;
+                        const uint64_t entry = at < n_kept ? sh.stage[at] : 0;
+                        const uint32_t not_id = (uint32_t)entry;
+                        uint64_t under = 0, z = 0;
+#pragma unroll 8
+                        for (uint32_t j = t & (share - 1); j < n_kept; j += share) {
+                            const uint64_t wj = sh.list[j];
+                            under += (uint32_t)sh.stage[j] > not_id ? wj : 0;
+                            z += wj;
+                        }
+                        for (uint32_t k = 1; k < share; k *= 2) {
+                            under += __shfl_xor_sync(0xFFFFFFFFu, under, k);
+                            z += __shfl_xor_sync(0xFFFFFFFFu, z, k);
+                        }
+                        bool exact;
+                        const uint64_t want = part_of(set.u, z, &exact);
+                        if (at < n_kept && (t & (share - 1)) == 0 && under <= want && want < under + sh.list[at])
+                            token_is(~not_id, unordered((uint32_t)(entry >> 32)), z);
+                    }
+                    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+                    return;
+                }
+            }
             // 31 bins of equal width, and from the second time on (or where that is all of f32) of equally many
             // keys: what is left is within an octave mostly, and a cut at 0 would be neared 32-fold at a time.
             // What lies outside has a bin of its own, the last. (Below `lo` some may be in the bin of `lo`.)
@@ -988,6 +1022,8 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
                     q.none = by_count && !can;
                     // (by weight: as many as the lightest of them would make)
                     q.fits = by_count ? in <= (float)kList : in * 1.001f <= (float)kList * weight_of(unordered(q.lo)).hi;
+                    // (what lies above weighs more than that each)
+                    q.all_fit = by_count ? (float)above_count + below + in <= (float)kList : (rough + below + in) * 1.001f <= (float)kList * weight_of(unordered(q.lo)).hi;
                     q.narrowed = first != 0 || last != bins;
                     q.more = first != last;
                     q.above = rough + below;
@@ -1014,6 +1050,11 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
             const bool fits = range.fits, exact = slip == 0.f && range.slip == 0.f;
             rough = range.above;
             slip = range.slip;
+            few = range.all_fit;
+            if (few) continue;
+            // (bins of bins, for a list of all: k and p from one ranking instead of one after the other. 256 rows
+            // of 128256 with both, k up to 1000: 85 -> 77 us)
+            if (by_count && n_hist == 0 && set.top_p < 1.f && set.k <= kList - kList / 32 && lo != hi) continue;
             if (!fits && lo != hi) {
                 if (by_count || range.narrowed || !range.more) continue;  // once more
                 // A few values of many tokens, or few of the weights. On which side of the first bin's end?
@@ -1176,25 +1217,27 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
 uint32_t parts_of(uint32_t V) { return (V + 7 + kPart - 1) / kPart; }  // (rows begin up to seven elements past a boundary)
 
 template <typename T>
-lp_status launch_sample(const SampleParams& p, lp_stream_t stream) {
+lp_status launch_sample(SampleParams& p, lp_stream_t stream) {
     static std::atomic<uint64_t> smem_set;
     constexpr size_t kBuffers = (size_t)kWarps * 4 * kPart;
     if (!allow_smem(reinterpret_cast<const void*>(k_sample_draw<T>), kBuffers, &smem_set)) return LP_ERR_CUDA;
-    const uint64_t warps = (uint64_t)p.T * p.parts;
-    const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), kThreads, 0, stream, 1, p);
-    if (st != LP_OK) return st;
     // CTAs of a row: two parts to a warp, eight CTAs at most; of many rows, so many that all CTAs are twice
     // what the device holds at once (256 rows of 128256, all with top-p: 8 CTAs 221 us, 4 198, 2 239; one row 32, 38, 52).
     const uint32_t slots = 2 * kDrawResident * (uint32_t)sm_count();
     uint32_t c = 1;
     while (c < kMaxCluster && c * kWarps * 2 < p.parts && 2 * (uint64_t)c * p.T <= slots + slots / 4) c *= 2;
+    // In order where there are more than the device holds, but not many times that.
+    if (c * p.T <= slots / 2 || p.T > kMaxOrdered) p.order = nullptr;
+    const uint64_t warps = (uint64_t)p.T * p.parts;
+    const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps) + (p.order ? 1 : 0)), kThreads, 0, stream, 1, p);
+    if (st != LP_OK) return st;
     return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, kBuffers, stream, c, p);
 }
 
 }  // namespace
 
 extern "C" size_t lp_head_sample_workspace_size(uint32_t T, uint32_t V) {
-    return kHeaderBytes + (size_t)T * parts_of(V) * sizeof(Part);
+    return kHeaderBytes + (size_t)T * (parts_of(V) * sizeof(Part) + sizeof(uint32_t));
 }
 
 extern "C" lp_status lp_head_sample(const void* logits, uint32_t dtype, uint32_t T, uint32_t V, uint64_t stride,
@@ -1226,6 +1269,7 @@ extern "C" lp_status lp_head_sample(const void* logits, uint32_t dtype, uint32_t
     p.status = static_cast<uint32_t*>(workspace);
     p.told = reinterpret_cast<Part*>(static_cast<unsigned char*>(workspace) + kHeaderBytes);
     p.parts = parts_of(V);
+    p.order = reinterpret_cast<uint32_t*>(p.told + (size_t)T * p.parts);
     p.stride = stride;
     p.T = T;
     p.V = V;
