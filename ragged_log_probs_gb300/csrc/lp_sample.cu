@@ -445,7 +445,8 @@ __device__ __forceinline__ void order_rows(const SampleParams& p, uint64_t* scan
     place += all << 48;
     for (uint32_t i = begin; i < end; ++i) {
         const uint32_t k = kind(i);
-        p.order[place >> k & 0xFFFFu] = p.T - 1 - i;
+        const uint32_t at = (uint32_t)(place >> k) & 0xFFFFu;
+        if (at < p.T) p.order[at] = p.T - 1 - i;  // (always, unless the settings change meanwhile)
         place += 1ull << k;
     }
 }
@@ -538,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, kDrawResident) k_sample_draw(const S
     pdl_wait();
     pdl_trigger();
     // (the rows that the first kernel read last come first: they are in L2)
-    const uint32_t row = p.order ? __ldcg(p.order + blockIdx.x / C) : p.T - 1 - blockIdx.x / C;
+    const uint32_t row = p.order ? min(__ldcg(p.order + blockIdx.x / C), p.T - 1) : p.T - 1 - blockIdx.x / C;
     const Row<T> r(p, row);
     const auto id_of = [&](uint32_t part, uint32_t element) { return part * kPart + element - r.before; };
 

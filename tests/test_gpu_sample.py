@@ -286,3 +286,38 @@ def test_mixed_batches(T, V, dtype):
     p = torch.where(r() < 0.5, 1.0, 0.3 + 0.69 * r()).tolist()
     q = torch.where(r() < 0.8, 0.0, 0.2 * r()).tolist()
     check(x, r().tolist(), tau, k, p, q)
+
+
+@pytest.mark.parametrize("T", [200, 456, 457, 1500, 4096, 4097])
+def test_every_row_of_many_is_drawn(T):
+    # rows of all kinds in turn, some without a token: each is drawn once, whatever the order they are taken in
+    V = 130
+    x = logits(T, V, F32, seed=15)
+    off = [0] + [i for i in range(1, T) if i % 5 in (1, 2)] + [T]  # requests of one row and of four
+    B = len(off) - 1
+    tau = [0.0 if b % 11 == 3 else 0.5 + b % 7 / 7 for b in range(B)]
+    k = [(0, 1, 20, 0, 129, 500)[b % 6] for b in range(B)]
+    p = [(1.0, 0.9, 0.3)[b % 3] for b in range(B)]
+    q = [0.05 if b % 4 == 0 else 0.0 for b in range(B)]
+    u = uniforms(T, 15)
+    check(x, u, tau, k, p, q, off)
+    bad = [b for b in range(B) if b % 13 == 5]
+    of = [b for b in range(B) for _ in range(off[b], off[b + 1])]
+    want, want_logprob, _ = run(x, u, tau, k, p, q, off)
+    got, logprob, status = run(x, u, [math.nan if b in set(bad) else v for b, v in enumerate(tau)], k, p, q, off)
+    assert status == 1 << 8
+    for t in range(T):
+        if of[t] in set(bad):
+            assert got[t] == -1 and math.isnan(logprob[t])
+        else:
+            assert got[t] == want[t] and logprob[t] == want_logprob[t]
+
+
+@pytest.mark.parametrize("V,dtype", [(30001, F16), (128256, F32), (5000, BF16)])
+@pytest.mark.parametrize("scale", [0.5, 3.0])
+def test_large_k_with_top_p(V, dtype, scale):
+    k = [300, 383, 384, 385, 500, 700, 900, 991, 992, 993, 1000, 1023, 1024, 1025, 1500, 3000]
+    x, u = logits(len(k), V, dtype, seed=16, scale=scale), uniforms(len(k), 16)
+    for p in (1.0, 0.999, 0.8, 0.2):
+        check(x, u, k=k, p=[p] * len(k))
+    check(x, u, k=k, p=[0.8] * len(k), q=[0.1] * len(k))
