@@ -200,7 +200,8 @@ lp_status lp_head_quantize4(const void *x, uint32_t dtype, uint32_t T, uint32_t 
 
 /*
  * Values of quantised rows: out[o] = row rows[o] (rows NULL: row o, n == V), rounded once to
- * out_dtype; a lookup of tokens in a 4-bit embedding. row_scale may be NULL (1), for either block.
+ * out_dtype; a lookup of tokens in a 4-bit embedding. row_scale may be NULL (1), for either block;
+ * the product code * scale comes first, and has to fit f32.
  *   workspace    the status word; required with rows, else may be NULL
  * Device check: rows[o] < V (LP_ERR_OFFSETS; that output row gets NaN).
  */

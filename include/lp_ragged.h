@@ -57,7 +57,7 @@ typedef enum lp_status {
     LP_ERR_TOKEN_RANGE = 5,  /* device: an actual or sampled token >= V                     */
     LP_ERR_WORKSPACE = 6,    /* workspace NULL or smaller than lp_ragged_workspace_size     */
     LP_ERR_CUDA = 7,         /* a CUDA launch or copy failed                                */
-    LP_ERR_TEMPERATURE = 8,  /* device: a temperature that is not a positive finite number  */
+    LP_ERR_TEMPERATURE = 8,  /* device: a temperature that is not a positive finite number (lp_head_sample: or 0) */
     LP_ERR_DTYPE = 9,        /* a type, or a combination of types, that the call does not take */
     LP_ERR_ADAPTER = 10,     /* device: an adapter id past the adapters                     */
     LP_ERR_PENALTY = 11,     /* device: a repetition penalty out of range, or another

@@ -11,6 +11,12 @@
 // written again only after the products that read them have been waited for. 256 columns hold
 // the accumulators (two of 128, or one), 256 the scales. The epilogue takes a finished
 // accumulator into registers at once and hands it back before it stores.
+//
+// Few rows are bound by HBM: 48 on V = 152064, H = 4096 66 us (350 MB of W and scales in 5.8 TB/s, 86 %
+// of a copy's rate). Many rows are bound by the tensor cores: 2048 on 32000 x 4096 91 us (5.9 PFLOP/s, the
+// pipe active 65 % of the time); a further 4096 of H cost 64 us (8.3 PFLOP/s), the rest is the start, the
+// last wave of tiles, and 1.2 us a tile for which the one accumulator of 256 columns is being
+// emptied. Loads of all columns before one wait for them were not faster.
 #include "lp_tcgen05.h"
 
 namespace {

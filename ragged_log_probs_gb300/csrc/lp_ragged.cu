@@ -528,7 +528,7 @@ const char* lp_ragged_strerror(lp_status status) {
         case LP_ERR_TOKEN_RANGE: return "an actual or sampled token id is >= V";
         case LP_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
         case LP_ERR_CUDA: return "CUDA launch or copy failed";
-        case LP_ERR_TEMPERATURE: return "a temperature is not a positive finite number";
+        case LP_ERR_TEMPERATURE: return "a temperature is not a positive finite number (or, for a draw, 0)";
         case LP_ERR_DTYPE: return "a type, or a combination of types, that the call does not take";
         case LP_ERR_ADAPTER: return "an adapter id is not below the number of adapters";
         case LP_ERR_PENALTY: return "a repetition penalty is out of range, or another penalty is not finite";

@@ -14,15 +14,23 @@
 // f32's rounding would move it in a few rows of a hundred. All three filters keep a prefix of the
 // order (value descending, id ascending), so that what is kept is told by the last kept (value, id):
 //   top-k: a value that k tokens reach for sure is read from the parts' ordered values; what
-//          lies above it is listed and ranked by the cluster's first CTA.
+//          lies above it is listed and ranked by the cluster's first CTA (k up to 384; above
+//          that a histogram of counts lowers the number of those that pass first).
 //   top-p: what weighs less than (1 - p) Z / V is never kept. Where that leaves few tokens they are
-//          listed as well. Else, or if it does not fit, a histogram over the values' bits with rounded
-//          weights finds the bins in which p Z can be reached; what lies above them is summed
+//          listed as well. Else, or if it does not fit, a histogram of f32 weights (31 bins over the
+//          values) finds the bins in which p Z can be reached; what lies above them is summed
 //          exactly, what lies in them is listed. Bins of more than fits are cut again; a single
 //          value is cut by id.
 // The draw follows the ids: the kept weights are summed by part, and the first CTA walks the part
 // in which u Z falls. CTAs write what the others need into their shared memory before a barrier
 // of the cluster.
+//
+// Measured: 256 rows of 128256 f32: best token 33 us, temperature 59, min-p 58, top-k with top-p 75,
+// top-p alone 165, of every kind 92; the bytes once take 19. The first kernel is bound by HBM without
+// weights (26 us), by its instructions with them (45, 78 % of the issue slots). The second is bound
+// by latency: barriers of the cluster (some 1 us each) and what one CTA does for the others between
+// them, 29 % of the issue slots, 14 % of HBM. One row: 12 to 30 us, of which 9 are the two launches
+// and their reads.
 #include <cooperative_groups.h>
 
 #include <type_traits>
