@@ -26,13 +26,14 @@ def test_refusals(lib):  # noqa: F811
     for name in ("x", "u", "off", "tau", "k", "p", "q", "out", "lw"):
         for by in (1, 2, 3):
             assert _sample(lib, **{name: FAKE + by}) == SHAPE
-    assert _sample(lib, ws=None) == WORKSPACE and _sample(lib, wsb=319) == WORKSPACE and _sample(lib, ws=FAKE + 128) == WORKSPACE
+    assert _sample(lib, ws=None) == WORKSPACE and _sample(lib, wsb=335) == WORKSPACE and _sample(lib, ws=FAKE + 128) == WORKSPACE
 
 
 def test_workspace_size(lib):  # noqa: F811
     f = lib.lp_head_sample_workspace_size
-    assert f(0, 0) == 256 and f(4, 100) == 256 + 4 * 16 and f(1, 1017) == 256 + 16 and f(1, 1018) == 256 + 32
-    assert f(2 ** 31, 393216) == 256 + 2 ** 31 * 385 * 16
+    # 16 bytes for a part of 1024 tokens (up to 7 of them before a row's first), 4 for a row's place in the order
+    assert f(0, 0) == 256 and f(4, 100) == 256 + 4 * 20 and f(1, 1017) == 256 + 16 + 4 and f(1, 1018) == 256 + 32 + 4
+    assert f(2 ** 31, 393216) == 256 + 2 ** 31 * (385 * 16 + 4)
 
 
 def test_new_error_codes(lib):  # noqa: F811
