@@ -50,7 +50,7 @@ constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kList = 1024;     // tokens that are ranked
 constexpr uint32_t kRanks = kList / kThreads;  // of a thread
 constexpr uint32_t kListedTop = kList * 3 / 8;  // top-k up to which what can be kept is listed at once: the bound lets two to three times as many pass
-constexpr uint32_t kMaxOrdered = 4096;  // rows that are put in order (a class's count has 16 bits)
+constexpr uint32_t kOrdered = 8 * kThreads;  // rows that a CTA puts in order
 constexpr uint32_t kDrawnByList = 128;  // tokens up to which the draw is made from the list
 constexpr uint32_t kBins = 32;
 constexpr uint32_t kBound = 512;
@@ -436,26 +436,38 @@ __device__ __forceinline__ uint64_t warp_total(uint64_t v) {
     return v;
 }
 
-// The rows in the order in which they are drawn, by one CTA: those that take longest first, and of a kind those
-// that were read last. (Of 256 rows of mixed settings the last to end had begun when half of the time was over.)
+// The rows in the order in which they are drawn, kOrdered at a time by a CTA: those that take longest first, and
+// of a kind those that were read last. The last rows to be drawn are then short ones, and CTAs that run at a time do
+// the same. (Rows of every kind, without and with: 256 of 128256 109 and 92 us, 2000 of 16000 166 and 123; where all are
+// of one kind it costs 0.5 us, 2 to 4 of thousands of short rows. 1024 rows a CTA: 131 us of the 2000.)
 __device__ __forceinline__ void order_rows(const SampleParams& p, uint64_t* scan) {
-    const uint32_t t = threadIdx.x, each = (p.T + kThreads - 1) / kThreads, begin = t * each, end = min(begin + each, p.T);
-    const auto kind = [&](uint32_t i) {  // 0: longest. Row T - 1 - i, in units of bits
-        const Setting s = setting_of(p, p.T - 1 - i, false);
-        if (s.k > kListedTop || (!s.k && s.top_p < 1.f)) return 0u;  // histograms
-        return s.k > kDrawnByList ? 16u : s.k > 1 || (!s.k && s.min_p > 0.f) ? 32u : 48u;
-    };
+    constexpr uint32_t kEach = kOrdered / kThreads;
+    const uint32_t base = blockIdx.x * kOrdered, each = (min(p.T - base, kOrdered) + kThreads - 1) / kThreads;
+    const uint32_t begin = base + threadIdx.x * each;
+    uint32_t kind[kEach];  // 0: longest; of row T - 1 - i, in units of bits
     uint64_t own = 0, all;
-    for (uint32_t i = begin; i < end; ++i) own += 1ull << kind(i);
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+        if (i >= each || begin + i >= p.T) continue;
+        const uint32_t row = p.T - 1 - (begin + i);
+        int b = (int)min(row, p.B - 1);  // (request `row`, where every one has one row)
+        if (p.row_offsets && !(p.row_offsets[b] <= row && row < p.row_offsets[b + 1])) b = max(request_of(p.row_offsets, p.B, row), 0);
+        const bool best = p.temperature && p.temperature[b] == 0.f, cut = p.top_p && p.top_p[b] < 1.f, low = p.min_p && p.min_p[b] > 0.f;
+        const int k = best ? 1 : p.top_k ? p.top_k[b] : 0;
+        const bool listed = k > 0 && (uint32_t)k < p.V;
+        kind[i] = listed ? ((uint32_t)k > kListedTop ? 0 : (uint32_t)k > kDrawnByList ? 16 : k > 1 ? 32 : 48)
+                         : cut ? 0 : low ? 32 : 48;  // 0: histograms
+        own += 1ull << kind[i];
+    }
     uint64_t place = block_scan(own, scan, &all) - own;
     place += all << 16;  // (of a kind: after all of those before it)
     place += all << 32;
     place += all << 48;
-    for (uint32_t i = begin; i < end; ++i) {
-        const uint32_t k = kind(i);
-        const uint32_t at = (uint32_t)(place >> k) & 0xFFFFu;
-        if (at < p.T) p.order[at] = p.T - 1 - i;  // (always, unless the settings change meanwhile)
-        place += 1ull << k;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+        if (i >= each || begin + i >= p.T) continue;
+        p.order[base + (uint32_t)(place >> kind[i] & 0xFFFFu)] = p.T - 1 - (begin + i);
+        place += 1ull << kind[i];
     }
 }
 
@@ -470,12 +482,13 @@ __global__ void __launch_bounds__(kThreads, kScanResident) k_sample_scan(const S
     __syncthreads();
     pdl_wait();
     pdl_trigger();  // (the second kernel waits for this one before it reads what it tells)
-    if (p.order && blockIdx.x == 0) {
+    const uint32_t ordering = p.order ? (p.T + kOrdered - 1) / kOrdered : 0;  // CTAs that do this
+    if (blockIdx.x < ordering) {
         __shared__ uint64_t scan[kWarps];
         order_rows(p, scan);
         return;
     }
-    const uint32_t at = (blockIdx.x - (p.order != nullptr)) * kWarps + (t >> 5), row = at / p.parts, part = at - row * p.parts;
+    const uint32_t at = (blockIdx.x - ordering) * kWarps + (t >> 5), row = at / p.parts, part = at - row * p.parts;
     if (row >= p.T) return;
     const Row<T> r(p, row);
     uint4 w[kVecs];
@@ -1235,10 +1248,11 @@ lp_status launch_sample(SampleParams& p, lp_stream_t stream) {
     const uint32_t slots = 2 * kDrawResident * (uint32_t)sm_count();
     uint32_t c = 1;
     while (c < kMaxCluster && c * kWarps * 2 < p.parts && 2 * (uint64_t)c * p.T <= slots + slots / 4) c *= 2;
-    // In order where there are more than the device holds, but not many times that.
-    if (c * p.T <= slots / 2 || p.T > kMaxOrdered) p.order = nullptr;
+    // In order where there are more than the device holds.
+    if ((uint64_t)c * p.T <= slots / 2) p.order = nullptr;
+    const uint32_t ordering = p.order ? (p.T + kOrdered - 1) / kOrdered : 0;
     const uint64_t warps = (uint64_t)p.T * p.parts;
-    const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps) + (p.order ? 1 : 0)), kThreads, 0, stream, 1, p);
+    const lp_status st = launch(k_sample_scan<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps) + ordering), kThreads, 0, stream, 1, p);
     if (st != LP_OK) return st;
     return launch(k_sample_draw<T>, dim3(p.T * c), kThreads, kBuffers, stream, c, p);
 }
