@@ -321,3 +321,26 @@ def test_large_k_with_top_p(V, dtype, scale):
     for p in (1.0, 0.999, 0.8, 0.2):
         check(x, u, k=k, p=[p] * len(k))
     check(x, u, k=k, p=[0.8] * len(k), q=[0.1] * len(k))
+
+
+def test_graphs_that_share_a_workspace():
+    # more rows than are drawn at a time: the order is made anew by every call
+    T, V = 500, 9000
+    x = [logits(T, V, BF16, seed=17 + i).cuda() for i in range(2)]
+    u = torch.tensor(uniforms(T, 17), device="cuda")
+    t = torch.arange(T, device="cuda")
+    k = [torch.where(t % 3 == i, 700, 0).int() for i in range(2)]
+    p = [torch.where(t % 5 == i, 0.9, 1.0).float() for i in range(2)]
+    ws = lp.new_head_workspace(draws=T, vocab=V)
+    want = [lp.sample(x[i], u, top_k=k[i], top_p=p[i], workspace=lp.new_head_workspace(draws=T, vocab=V)) for i in range(2)]
+    outs = [torch.zeros(T, dtype=torch.int32, device="cuda") for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i in range(2):
+        with torch.cuda.graph(graphs[i]):
+            lp.sample(x[i], u, top_k=k[i], top_p=p[i], out=outs[i], workspace=ws)
+    for _ in range(5):
+        for i in range(2):
+            graphs[i].replay()
+            lp.sample(x[1 - i], u, top_k=k[1 - i], top_p=p[1 - i], workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want)) and lp.read_status(ws) == 0
